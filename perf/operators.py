@@ -346,7 +346,7 @@ def _exact_weight(st, e):
     v = torch.where(sel.repeat_interleave(S, dim=1) == 1, t[1][q], t[0][q]) * s
     # the stored weight is the product rounded to 8 significant bits, ties to even
     m, ex = torch.frexp(v)
-    return torch.ldexp(torch.round(m * 256.0), ex - 8)
+    return torch.round(m * 256.0) * torch.exp2(ex.double() - 8)
 
 
 def exact(case, seed):
