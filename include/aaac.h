@@ -325,6 +325,79 @@ aaac_status aaac_assign_refine_batch(int count, const uint16_t* const* W, const 
                                      double* err, double* w2, void* ws, size_t ws_bytes,
                                      void* stream);
 
+/*
+ * Element types of the calls below.
+ */
+#define AAAC_BF16 0
+#define AAAC_F16 1
+#define AAAC_F32 2
+#define AAAC_MXFP4 3                    /* matmul input: codes and scale bytes of aaac_mxfp4_quantize */
+
+/*
+ * MXFP4 quantization (OCP Microscaling formats, MXFP4: 4-bit e2m1 elements in blocks of 32 along a
+ * row with one power-of-two scale, e8m0), the other 4-bit weight format beside the dual-codebook
+ * one, and the format of 4-bit activations. The last block of a row is padded with zeros; with
+ * Cp = 32 ceil(C / 32):
+ *   e = clamp(floor(log2 max |x|) - 2, -127, 127) over the block, scale byte e + 127;
+ *   code = the e2m1 value nearest to x 2^-e, ties to the even code, magnitudes above 6 become 6.
+ * A block of zeros has scale byte 0. A block holding an infinity or a NaN has scale byte 255 and
+ * zero codes, and reads back as NaN. Code values by bits 0..2: 0, 1/2, 1, 3/2, 2, 3, 4, 6; bit 3 is
+ * the sign.
+ * X       [M, C] of x_type AAAC_BF16, AAAC_F16 or AAAC_F32, row stride ldx >= C (elements), aligned
+ *         to its element; rows of 16-byte multiples on a 16-byte boundary are read fastest.
+ * codes   u8 [M, Cp / 2], two codes per byte, the low nibble holds the even column; 16-byte aligned.
+ * scales  u8 [M, Cp / 32].
+ * Shapes: M >= 0 (0: nothing is written), 1 <= C < 2^22, M * Cp < 2^40. One kernel.
+ */
+aaac_status aaac_mxfp4_quantize(const void* X, int x_type, int64_t M, int64_t C, int64_t ldx,
+                                uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * The values of MXFP4 codes: y = e2m1[code] 2^(byte - 127), exact in fp32 up to its range, rounded
+ * once to y_type (ties to even); scale byte 255 gives NaN. Y [M, C] with row stride ldy >= C; only
+ * the C columns of a row are written. codes 4-byte aligned. Shapes as aaac_mxfp4_quantize.
+ */
+aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t C,
+                               void* Y, int y_type, int64_t ldy, void* stream);
+
+/*
+ * Matrix products on 4-bit weights for any number of rows of x, grouped by expert:
+ *   y[t, r] = sum_c x[t, c] W_e[r, c]   for offsets[e] <= t < offsets[e + 1],
+ * W_e the values of the e-th of E stacked [R, C] matrices; sums in fp32 in an order fixed by the
+ * call's shapes (bitwise reproducible), rounded once to y_type.
+ * offsets  int32 [E + 1] on the device, ascending: the rows of x sorted by expert; an expert may
+ *          have none. Rows of y outside [offsets[0], offsets[E]) are left as they were. Values are
+ *          not checked on the host: the kernels clamp them to [0, T] and to ascending order, so a
+ *          bad one never leads outside x or y. NULL (then E must be 1): every row belongs to the
+ *          one matrix.
+ * T        rows of x and y, 0 <= T < 2^31; T = 0 launches nothing.
+ * y        [T, R] of y_type AAAC_BF16, AAAC_F16 or AAAC_F32, row stride ldy >= R, aligned to its
+ *          element. y must not overlap an input.
+ * Shapes: 1 <= E <= 65535, 1 <= R < 2^31, 1 <= C < 2^22, E * R * C < 2^40, and at most 2^31 output
+ * tiles. No workspace; one kernel.
+ *
+ * aaac_mxfp4_matmul: weights in MXFP4, w_codes [E, R, Cp / 2] (16-byte aligned) and w_scales
+ * [E, R, Cp / 32] as aaac_mxfp4_quantize writes them for the stacked rows. x_type:
+ *   AAAC_MXFP4  x = codes [T, Cp / 2] (16-byte aligned), x_scales [T, Cp / 32], ldx ignored; products
+ *               of codes and scales are exact.
+ *   AAAC_BF16   x bf16 [T, C], row stride ldx >= C; x 16-byte aligned, C % 8 == 0, ldx % 8 == 0;
+ *               x_scales NULL.
+ *
+ * aaac_matmul: weights in the packed dual-codebook format, stacked: codes [E, R, C / 2] (16-byte
+ * aligned), scales [E, R, C / g], tables_bf16 [E, 2, n], bitmap [E, ceil(R * C / S / 8)] exactly
+ * when S < g, each matrix's part as aaac_assign and aaac_pack write it. The weight is aaac_dequant's
+ * W_hat = bf16(|s| T~_sel[q]) (a product below 2^-126 may differ from it by its rounding); a code
+ * >= n reads entry 0. x bf16 [T, C] as above. g, S, n as for the other calls, and C % 32 == 0.
+ */
+aaac_status aaac_mxfp4_matmul(const uint8_t* w_codes, const uint8_t* w_scales, int64_t E, int64_t R,
+                              int64_t C, const int32_t* offsets, const void* x, int x_type,
+                              const uint8_t* x_scales, int64_t T, int64_t ldx, void* y, int y_type,
+                              int64_t ldy, void* stream);
+aaac_status aaac_matmul(const uint8_t* codes, const uint16_t* scales, const uint8_t* bitmap,
+                        const uint16_t* tables_bf16, int64_t E, int64_t R, int64_t C, int g, int S,
+                        int n, const int32_t* offsets, const uint16_t* x, int64_t T, int64_t ldx,
+                        void* y, int y_type, int64_t ldy, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

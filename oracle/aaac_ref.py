@@ -376,3 +376,59 @@ def selector_bits_per_weight(g, S):
     """Extra bits per weight for the table choice: none when the sign bit of the scale holds it
     (S == g), one bit per selection group otherwise (§2 mechanism 3, §4)."""
     return 0.0 if S == g else 1.0 / S
+
+
+# ------------------------------------------------------------------------------------------------
+# MXFP4 (OCP Microscaling formats) and the products on 4-bit weights
+# ------------------------------------------------------------------------------------------------
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mxfp4_encode(x):
+    """(codes uint8 [M, Cp], scale bytes uint8 [M, Cp / 32]) of x [M, C], Cp = 32 ceil(C / 32): one
+    code per byte, blocks of 32 padded with zeros."""
+    x = np.asarray(x, dtype=np.float64)
+    M, C = x.shape
+    nb = -(-C // 32)
+    v = np.zeros((M, nb * 32))
+    v[:, :C] = x
+    v = v.reshape(M, nb, 32)
+    bad = ~np.isfinite(v).all(axis=-1)
+    v = np.where(bad[..., None], 0.0, v)
+    top = np.abs(v).max(axis=-1)
+    # top = m 2^k with m in [1/2, 1), so floor(log2 top) = k - 1
+    e = np.where(top > 0, np.frexp(top)[1] - 1 - 2, -127)
+    e = np.clip(e, -127, 127)
+    u = np.ldexp(v, -e[..., None])
+    d = np.abs(np.abs(u)[..., None] - E2M1)
+    near = d.min(axis=-1, keepdims=True)
+    # the nearest value; of two equally near ones (neighbours) the one with the even code
+    q = np.where(d == near, np.arange(8), 99)
+    first = q.min(axis=-1)
+    tie = (d == near).sum(axis=-1) == 2
+    code = np.where(tie & (first % 2 == 1), first + 1, first)
+    code = code | (np.signbit(u).astype(np.int64) << 3)
+    code = np.where(bad[..., None], 0, code)
+    byte = np.where(bad, 255, e + 127)
+    return code.reshape(M, nb * 32).astype(np.uint8), byte.astype(np.uint8)
+
+
+def mxfp4_decode(codes, scales, C):
+    """float64 [M, C] of one code per byte [M, Cp] and scale bytes [M, Cp / 32]."""
+    v = np.where(codes & 8, -1.0, 1.0) * E2M1[codes & 7]
+    s = np.ldexp(1.0, scales.astype(np.int64) - 127)
+    s = np.where(scales == 255, np.nan, s)
+    return (v * np.repeat(s, 32, axis=-1))[..., :C]
+
+
+def grouped_matmul(x, Ws, offsets):
+    """float64 [T, R] with NaN in the rows of no expert: rows offsets[e] .. offsets[e + 1] of x times
+    the transposed Ws[e]."""
+    x = np.asarray(x, dtype=np.float64)
+    y = np.full((x.shape[0], Ws[0].shape[0]), np.nan)
+    for e, W in enumerate(Ws):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if b > a:
+            y[a:b] = x[a:b] @ np.asarray(W, dtype=np.float64).T
+    return y

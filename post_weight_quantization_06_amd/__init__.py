@@ -16,10 +16,22 @@ from ._lib import (  # noqa: F401
     aaac_gemv_batch,
     aaac_importance,
     aaac_init_quantiles,
+    aaac_matmul,
+    aaac_mxfp4_dequant,
+    aaac_mxfp4_matmul,
+    aaac_mxfp4_quantize,
     aaac_pack,
     aaac_refine,
     aaac_refine_batch,
     load,
+)
+from .inference import (  # noqa: F401
+    MXFP4Matrix,
+    PackedExperts,
+    mxfp4_dequant,
+    mxfp4_matmul,
+    mxfp4_quantize,
+    packed_matmul,
 )
 from .quantize import (  # noqa: F401
     Layer,

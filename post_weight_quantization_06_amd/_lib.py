@@ -27,13 +27,17 @@ OP_IMPORTANCE, OP_INIT, OP_ASSIGN, OP_REFINE = 0, 1, 2, 3
 REFINE_ROUND_BF16 = 1
 REFINE_W2_KNOWN = 2
 MAX_BATCH = 8
+MXFP4 = 3
+# element types of the matmul and MXFP4 calls
+FLOAT_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 EXPORTED = (
     "aaac_status_string", "aaac_last_error", "aaac_workspace_bytes", "aaac_importance",
     "aaac_init_quantiles", "aaac_assign", "aaac_refine", "aaac_pack", "aaac_dequant",
     "aaac_batch_workspace_bytes", "aaac_assign_batch", "aaac_refine_batch", "aaac_awq_prescale",
     "aaac_gemv", "aaac_gemv_batch", "aaac_assign_refine_batch", "aaac_init_quantiles_batch",
-    "aaac_pack_batch", "aaac_dequant_batch", "aaac_refine_batch_noalloc",
+    "aaac_pack_batch", "aaac_dequant_batch", "aaac_refine_batch_noalloc", "aaac_mxfp4_quantize",
+    "aaac_mxfp4_dequant", "aaac_mxfp4_matmul", "aaac_matmul",
 )
 
 
@@ -103,6 +107,12 @@ def load(path: str = LIB_PATH):
         "aaac_gemv_batch": (c_int, [c_int, P(c_vp), P(c_vp), P(c_vp), P(c_vp), P(c_i64),
                                     P(c_i64), c_int, c_int, c_int, P(c_vp), c_int, P(c_vp),
                                     c_vp]),
+        "aaac_mxfp4_quantize": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
+        "aaac_mxfp4_dequant": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_i64, c_vp]),
+        "aaac_mxfp4_matmul": (c_int, [c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, c_vp,
+                                      c_i64, c_i64, c_vp, c_int, c_i64, c_vp]),
+        "aaac_matmul": (c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_int,
+                                c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_i64, c_vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -548,3 +558,178 @@ def aaac_refine_batch_noalloc(Ws: Sequence[torch.Tensor], g: int, S: int, n: int
         _arr(c_vp, [t.data_ptr() for t in sels]), _arr(c_vp, [t.data_ptr() for t in tables]),
         flags, _ptr(err), _ptr(w2), _stream(stream))
     _check(st, "aaac_refine_batch_noalloc")
+
+
+# ------------------------------------------------------------------------------------------------
+# MXFP4 and the products. These calls run on the tensors' own device: the launch happens there
+# whatever the current device is, on `stream` or on that device's current stream.
+# ------------------------------------------------------------------------------------------------
+
+def _on_gpu(what: str, *tensors):
+    """The index of the one GPU that every given tensor is on."""
+    first = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("%s: every tensor must be on the GPU (got %s)" % (what, t.device))
+        dev = t.get_device()
+        if first is None:
+            first = dev
+        elif dev != first:
+            raise ValueError("%s: tensors on cuda:%d and cuda:%d" % (what, first, dev))
+    return first
+
+
+def _no_grad(what: str, x: torch.Tensor):
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s has no gradient: call it under torch.no_grad() or detach x" % what)
+
+
+def _launch(name: str, dev: int, stream, *args):
+    """Call entry point `name` on device dev."""
+    fn = getattr(_lib or load(), name)
+    if stream is None:
+        raw = torch.cuda.current_stream(dev).cuda_stream
+    else:
+        if stream.device.index != dev:
+            raise ValueError("%s: stream on %s, tensors on cuda:%d" % (name, stream.device, dev))
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != AAAC_OK:
+        _check(st, name)
+
+
+def _rows(t: torch.Tensor, name: str):
+    """(rows, columns, row stride) of a 2-D tensor with unit column stride."""
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D (got %d-D)" % (name, t.dim()))
+    M, C = t.shape
+    s0, s1 = t.stride()
+    if s1 != 1 and C > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    if M <= 1:                 # the stride of a single row carries nothing: any that the call takes
+        return M, C, max(s0, C) if s0 % 8 == 0 and s0 >= C else (C + 7) // 8 * 8
+    return M, C, s0
+
+
+def _u8(t: torch.Tensor, name: str, numel: int):
+    if t.dtype is not torch.uint8 or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError("%s must be contiguous uint8 of %d elements (got %s %s)" % (
+            name, numel, t.dtype, tuple(t.shape)))
+
+
+def aaac_mxfp4_quantize(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
+    """codes u8 [M, Cp/2] and scales u8 [M, Cp/32] of X [M, C] (bf16, fp16 or fp32, any row
+    stride), Cp = 32 ceil(C / 32)."""
+    dev = _on_gpu("aaac_mxfp4_quantize", X, codes, scales)
+    _no_grad("aaac_mxfp4_quantize", X)
+    xt = FLOAT_TYPES.get(X.dtype)
+    if xt is None:
+        raise TypeError("X must be bf16, fp16 or fp32 (got %s)" % X.dtype)
+    M, C, ldx = _rows(X, "X")
+    blocks = (C + 31) // 32
+    _u8(codes, "codes", M * blocks * 16)
+    _u8(scales, "scales", M * blocks)
+    _launch("aaac_mxfp4_quantize", dev, stream, X.data_ptr(), xt, M, C, ldx, codes.data_ptr(),
+            scales.data_ptr())
+
+
+def aaac_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tensor, stream=None):
+    """Y [M, C] (bf16, fp16 or fp32, any row stride) = the values of the codes."""
+    dev = _on_gpu("aaac_mxfp4_dequant", codes, scales, Y)
+    yt = FLOAT_TYPES.get(Y.dtype)
+    if yt is None:
+        raise TypeError("Y must be bf16, fp16 or fp32 (got %s)" % Y.dtype)
+    M, C, ldy = _rows(Y, "Y")
+    blocks = (C + 31) // 32
+    _u8(codes, "codes", M * blocks * 16)
+    _u8(scales, "scales", M * blocks)
+    _launch("aaac_mxfp4_dequant", dev, stream, codes.data_ptr(), scales.data_ptr(), M, C,
+            Y.data_ptr(), yt, ldy)
+
+
+def _product_args(what: str, E: int, offsets, y: torch.Tensor, T: int, R: int):
+    """(offsets pointer, y type, row stride of y) after the checks that every product shares."""
+    yt = FLOAT_TYPES.get(y.dtype)
+    if yt is None:
+        raise TypeError("y must be bf16, fp16 or fp32 (got %s)" % y.dtype)
+    M, N, ldy = _rows(y, "y")
+    if M != T or N != R:
+        raise ValueError("%s: y must be [%d, %d] (got [%d, %d])" % (what, T, R, M, N))
+    if offsets is None:
+        return None, yt, ldy
+    if offsets.dtype is not torch.int32 or not offsets.is_contiguous() or \
+            offsets.numel() != E + 1:
+        raise ValueError("%s: offsets must be contiguous int32 [%d] (got %s %s)" % (
+            what, E + 1, offsets.dtype, tuple(offsets.shape)))
+    return offsets.data_ptr(), yt, ldy
+
+
+def aaac_mxfp4_matmul(codes: torch.Tensor, scales: torch.Tensor, C: int, x: torch.Tensor,
+                      y: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                      x_scales: Optional[torch.Tensor] = None, stream=None):
+    """y [T, R] = x times the transposed MXFP4 matrices: codes u8 [R, Cp/2] or [E, R, Cp/2] with
+    scales u8 [.., Cp/32]. x bf16 [T, C], or codes u8 [T, Cp/2] with x_scales u8 [T, Cp/32].
+    offsets: int32 [E + 1] (see aaac.h), or None for one matrix."""
+    what = "aaac_mxfp4_matmul"
+    dev = _on_gpu(what, codes, scales, x, y, offsets, x_scales)
+    blocks = (C + 31) // 32
+    shape = codes.shape
+    E, R = (1, shape[0]) if len(shape) == 2 else (shape[0], shape[1])
+    _u8(codes, "codes", E * R * blocks * 16)
+    _u8(scales, "scales", E * R * blocks)
+    if x_scales is None:
+        _no_grad(what, x)
+        if x.dtype is not torch.bfloat16:
+            raise TypeError("x must be bf16, or MXFP4 codes with x_scales (got %s)" % x.dtype)
+        T, K, ldx = _rows(x, "x")
+        if K != C:
+            raise ValueError("%s: x has %d columns, the weights %d" % (what, K, C))
+        xt, xs = 0, None
+    else:
+        T = x.shape[0]
+        _u8(x, "x", T * blocks * 16)
+        _u8(x_scales, "x_scales", T * blocks)
+        xt, xs, ldx = MXFP4, x_scales.data_ptr(), C
+    op, yt, ldy = _product_args(what, E, offsets, y, T, R)
+    _launch(what, dev, stream, codes.data_ptr(), scales.data_ptr(), E, R, C, op, x.data_ptr(), xt,
+            xs, T, ldx, y.data_ptr(), yt, ldy)
+
+
+def aaac_matmul(codes: torch.Tensor, scales: torch.Tensor, bitmap: Optional[torch.Tensor],
+                tables_bf16: torch.Tensor, g: int, S: int, n: int, x: torch.Tensor,
+                y: torch.Tensor, offsets: Optional[torch.Tensor] = None, stream=None):
+    """y [T, R] = x bf16 [T, C] times the transposed packed matrices: codes u8 [R, C/2] or
+    [E, R, C/2] with scales, bitmap and tables_bf16 stacked alike. offsets as in
+    aaac_mxfp4_matmul."""
+    what = "aaac_matmul"
+    dev = _on_gpu(what, codes, scales, bitmap, tables_bf16, x, y, offsets)
+    _no_grad(what, x)
+    shape = codes.shape
+    if len(shape) not in (2, 3):
+        raise ValueError("%s: codes must be [R, C/2] or [E, R, C/2]" % what)
+    E, R = (1, shape[0]) if len(shape) == 2 else (shape[0], shape[1])
+    C = 2 * shape[-1]
+    _u8(codes, "codes", E * R * C // 2)
+    if scales.dtype is not torch.int16 or not scales.is_contiguous() or \
+            scales.numel() * g != E * R * C:
+        raise ValueError("%s: scales must be contiguous int16 of E*R*C/g elements" % what)
+    if tables_bf16.dtype is not torch.int16 or not tables_bf16.is_contiguous() or \
+            tables_bf16.numel() != E * 2 * n:
+        raise ValueError("%s: tables_bf16 must be contiguous int16 of E*2*n elements" % what)
+    if bitmap is not None:
+        _u8(bitmap, "bitmap", E * ((R * (C // S) + 7) // 8))
+    if x.dtype is not torch.bfloat16:
+        raise TypeError("x must be bf16 (got %s)" % x.dtype)
+    T, K, ldx = _rows(x, "x")
+    if K != C:
+        raise ValueError("%s: x has %d columns, the weights %d" % (what, K, C))
+    op, yt, ldy = _product_args(what, E, offsets, y, T, R)
+    _launch(what, dev, stream, codes.data_ptr(), scales.data_ptr(),
+            None if bitmap is None else bitmap.data_ptr(), tables_bf16.data_ptr(), E, R, C, g, S,
+            n, op, x.data_ptr(), T, ldx, y.data_ptr(), yt, ldy)

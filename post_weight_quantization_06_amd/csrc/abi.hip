@@ -7,6 +7,7 @@
 
 #include "aaac.h"
 #include "common.h"
+#include "mxfp4.h"
 
 namespace aaac {
 
@@ -426,6 +427,54 @@ aaac_status do_dequant(int count, const uint8_t* const* codes, const uint16_t* c
                     who);
 }
 
+// Element size of a floating type, 0 for any other value.
+int type_bytes(int type) {
+  return type == AAAC_BF16 || type == AAAC_F16 ? 2 : type == AAAC_F32 ? 4 : 0;
+}
+
+constexpr int64_t kMaxMatmulCols = (int64_t)1 << 22;
+
+aaac_status check_mx_shape(int64_t M, int64_t C, int64_t ld, const char* who) {
+  if (M < 0 || C < 1 || C >= kMaxMatmulCols || ld < C)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
+                "%s: M=%lld C=%lld row stride %lld (need M >= 0, 1 <= C < 2^22, stride >= C)", who,
+                (long long)M, (long long)C, (long long)ld);
+  if (M > ((((int64_t)1 << 40) - 1) / (mx_blocks(C) * kMxBlock)) ||
+      (M > 1 && ld > (((int64_t)1 << 60) / M)))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: M*C must stay below 2^40", who);
+  return AAAC_OK;
+}
+
+// The checks shared by the products; x_bf16: x is given as bf16 rows.
+aaac_status check_matmul(const MatmulArgs& a, int64_t E, bool x_bf16, const char* who) {
+  if (E < 1 || E > 65535 || a.R < 1 || a.R >= ((int64_t)1 << 31) || a.C < 1 ||
+      a.C >= kMaxMatmulCols || a.R > ((((int64_t)1 << 40) - 1) / a.Cp) / E)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
+                "%s: E=%lld R=%lld C=%lld (need 1 <= E <= 65535, R >= 1, 1 <= C < 2^22, E*R*C < 2^40)",
+                who, (long long)E, (long long)a.R, (long long)a.C);
+  if (!a.offsets && E != 1)
+    return fail(AAAC_ERR_INVALID_ARG, "%s: E=%lld matrices need offsets", who, (long long)E);
+  if (a.offsets && !aligned(a.offsets, 4))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: offsets misaligned", who);
+  const int yb = type_bytes(a.y_type);
+  if (!yb) return fail(AAAC_ERR_INVALID_ARG, "%s: y_type %d", who, a.y_type);
+  if (a.T < 0 || a.T >= ((int64_t)1 << 31) || a.ldy < a.R || a.ldy >= ((int64_t)1 << 31))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld ldy=%lld (need 0 <= T < 2^31, R <= ldy < 2^31)",
+                who, (long long)a.T, (long long)a.ldy);
+  if (x_bf16 && (a.C % 8 != 0 || a.ldx < a.C || a.ldx % 8 != 0 || a.ldx >= ((int64_t)1 << 31)))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
+                "%s: C=%lld ldx=%lld (bf16 rows need C %% 8 == 0, ldx %% 8 == 0, C <= ldx < 2^31)", who,
+                (long long)a.C, (long long)a.ldx);
+  if (a.T > 0 && (!a.x || !aligned(a.x, 16) || !a.y || !aligned(a.y, yb)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: x or y null or misaligned (x needs 16 bytes)", who);
+  // 16-row tiles are the smallest any kernel uses
+  const int64_t rb = (a.R + 15) / 16, tt = a.T / 16 + (a.offsets ? E : 1);
+  if (rb > (((int64_t)1 << 31) - 1) / tt)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld times R=%lld is over 2^31 tiles", who,
+                (long long)a.T, (long long)a.R);
+  return AAAC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -693,6 +742,104 @@ aaac_status aaac_gemv_batch(int count, const uint8_t* const* codes, const uint16
                             const uint16_t* const* x, int B, float* const* y, void* stream) {
   return do_gemv(count, codes, scales, bitmap, tables_bf16, R, C, g, S, n, x, B, y, stream,
                  "aaac_gemv_batch");
+}
+
+aaac_status aaac_mxfp4_quantize(const void* X, int x_type, int64_t M, int64_t C, int64_t ldx,
+                                uint8_t* codes, uint8_t* scales, void* stream) {
+  const char* who = "aaac_mxfp4_quantize";
+  aaac_status st = check_mx_shape(M, C, ldx, who);
+  if (st != AAAC_OK) return st;
+  const int b = type_bytes(x_type);
+  if (!b) return fail(AAAC_ERR_INVALID_ARG, "%s: x_type %d", who, x_type);
+  if (M > 0 && (!X || !aligned(X, b) || !codes || !aligned(codes, 16) || !scales))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: null or misaligned pointer (codes need 16 bytes)", who);
+  return hip_status(launch_mxfp4_quantize(X, x_type, M, C, ldx, codes, scales,
+                                          static_cast<hipStream_t>(stream)),
+                    who);
+}
+
+aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t C,
+                               void* Y, int y_type, int64_t ldy, void* stream) {
+  const char* who = "aaac_mxfp4_dequant";
+  aaac_status st = check_mx_shape(M, C, ldy, who);
+  if (st != AAAC_OK) return st;
+  const int b = type_bytes(y_type);
+  if (!b) return fail(AAAC_ERR_INVALID_ARG, "%s: y_type %d", who, y_type);
+  if (M > 0 && (!Y || !aligned(Y, b) || !codes || !aligned(codes, 4) || !scales))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: null or misaligned pointer", who);
+  return hip_status(launch_mxfp4_dequant(codes, scales, M, C, Y, y_type, ldy,
+                                         static_cast<hipStream_t>(stream)),
+                    who);
+}
+
+aaac_status aaac_mxfp4_matmul(const uint8_t* w_codes, const uint8_t* w_scales, int64_t E, int64_t R,
+                              int64_t C, const int32_t* offsets, const void* x, int x_type,
+                              const uint8_t* x_scales, int64_t T, int64_t ldx, void* y, int y_type,
+                              int64_t ldy, void* stream) {
+  const char* who = "aaac_mxfp4_matmul";
+  if (x_type != AAAC_BF16 && x_type != AAAC_MXFP4)
+    return fail(AAAC_ERR_INVALID_ARG, "%s: x_type %d", who, x_type);
+  const bool mx = x_type == AAAC_MXFP4;
+  MatmulArgs a = {};
+  a.codes = w_codes;
+  a.scales = w_scales;
+  a.E = (int)E;
+  a.R = R;
+  a.C = C;
+  a.Cp = C > 0 && C < kMaxMatmulCols ? mx_blocks(C) * kMxBlock : 32;
+  a.offsets = offsets;
+  a.x = x;
+  a.x_scales = x_scales;
+  a.T = T;
+  a.ldx = ldx;
+  a.y = y;
+  a.y_type = y_type;
+  a.ldy = ldy;
+  aaac_status st = check_matmul(a, E, !mx, who);
+  if (st != AAAC_OK) return st;
+  if (!w_codes || !aligned(w_codes, 16) || !w_scales)
+    return fail(AAAC_ERR_INVALID_ARG, "%s: weights null or misaligned (codes need 16 bytes)", who);
+  if (mx ? (T > 0 && !x_scales) : x_scales != nullptr)
+    return fail(AAAC_ERR_INVALID_ARG, "%s: x_scales must be given exactly with MXFP4 x", who);
+  return hip_status(launch_mxfp4_matmul(a, mx, static_cast<hipStream_t>(stream)), who);
+}
+
+aaac_status aaac_matmul(const uint8_t* codes, const uint16_t* scales, const uint8_t* bitmap,
+                        const uint16_t* tables_bf16, int64_t E, int64_t R, int64_t C, int g, int S,
+                        int n, const int32_t* offsets, const uint16_t* x, int64_t T, int64_t ldx,
+                        void* y, int y_type, int64_t ldy, void* stream) {
+  const char* who = "aaac_matmul";
+  aaac_status st = check_shape(R, C, g, S, n, true, who);
+  if (st != AAAC_OK) return st;
+  if (C % 32 != 0)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: C=%lld (need C %% 32 == 0)", who, (long long)C);
+  MatmulArgs a = {};
+  a.codes = codes;
+  a.scales = scales;
+  a.bitmap = bitmap;
+  a.tables = tables_bf16;
+  a.bitmap_stride = (R * (C / S) + 7) / 8;
+  a.E = (int)E;
+  a.R = R;
+  a.C = a.Cp = C;
+  a.log2g = 31 - __builtin_clz((unsigned)g);
+  a.log2S = 31 - __builtin_clz((unsigned)S);
+  a.n = n;
+  a.offsets = offsets;
+  a.x = x;
+  a.T = T;
+  a.ldx = ldx;
+  a.y = y;
+  a.y_type = y_type;
+  a.ldy = ldy;
+  st = check_matmul(a, E, true, who);
+  if (st != AAAC_OK) return st;
+  if (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 2) || !tables_bf16 ||
+      !aligned(tables_bf16, 2))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: weights null or misaligned (codes need 16 bytes)", who);
+  if ((S < g) != (bitmap != nullptr))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: bitmap must be given exactly when S < g", who);
+  return hip_status(launch_packed_matmul(a, static_cast<hipStream_t>(stream)), who);
 }
 
 }  // extern "C"

@@ -1,0 +1,51 @@
+// Microscaled 4-bit floating point (OCP MX, format MXFP4) and the matrix products on 4-bit weights:
+// the host-side launchers that the C ABI calls after validating its arguments.
+//
+// MXFP4: a row is cut into blocks of 32 columns, the last one padded with zeros, Cp = 32 ceil(C/32).
+// A block holds one scale byte b (the value 2^(b - 127); 255 reads as NaN) and 32 e2m1 codes:
+// bit 3 the sign, magnitudes {0, 1/2, 1, 3/2, 2, 3, 4, 6}. Codes lie two to a byte, the even column
+// in the low nibble; codes [rows, Cp / 2] and scale bytes [rows, Cp / 32] are contiguous.
+#pragma once
+
+#include "common.h"
+
+namespace aaac {
+
+constexpr int kMxBlock = 32;
+
+__host__ __device__ __forceinline__ int64_t mx_blocks(int64_t C) {
+  return (C + kMxBlock - 1) / kMxBlock;
+}
+
+hipError_t launch_mxfp4_quantize(const void* X, int x_type, int64_t M, int64_t C, int64_t ldx,
+                                 uint8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t C,
+                                void* Y, int y_type, int64_t ldy, hipStream_t stream);
+
+// One product call: y[t, r] = sum_c x[t, c] W[e(t)][r, c] for the rows t of expert e,
+// offsets[e] <= t < offsets[e + 1] (offsets NULL: every row, one matrix). The offsets are clamped
+// to [0, T] and to ascending order where they are read, so no value of theirs leads outside x or y.
+struct MatmulArgs {
+  const uint8_t* codes;        // [E, R, Cp / 2]
+  const void* scales;          // MXFP4: bytes [E, R, Cp / 32]; packed: bf16 words [E, R, C / g]
+  const uint8_t* bitmap;       // packed, S < g: [E, bitmap_stride]
+  const uint16_t* tables;      // packed: [E, 2, n]
+  int64_t bitmap_stride;
+  int64_t R, C, Cp;
+  int E;
+  int log2g, log2S, n;
+  const int32_t* offsets;      // [E + 1] on the device, or NULL
+  const void* x;               // bf16 rows of ldx elements, or codes [T, Cp / 2]
+  const uint8_t* x_scales;     // with codes: [T, Cp / 32]
+  int64_t T, ldx;
+  void* y;                     // [T, R] of y_type, rows of ldy elements
+  int y_type;
+  int64_t ldy;
+  int64_t row_blocks;          // set by the launcher: row blocks of one expert
+  int y_vec;                   // set by the launcher: four neighbours of a row go out in one store
+};
+
+hipError_t launch_mxfp4_matmul(const MatmulArgs& a, bool x_mxfp4, hipStream_t stream);
+hipError_t launch_packed_matmul(const MatmulArgs& a, hipStream_t stream);
+
+}  // namespace aaac

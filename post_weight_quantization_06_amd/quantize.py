@@ -24,6 +24,7 @@ from typing import Callable, Dict, Iterable, List, Optional, Sequence, Tuple
 import torch
 
 from . import _lib as L
+from .inference import packed_matmul
 
 # relative slack of the monotonicity check: the error totals are fp64 sums of fp32-rounded terms
 # (relative error below 2.4e-7), and decisions inside the 1e-6 tie band may go either way
@@ -63,6 +64,14 @@ class QuantizedMatrix:
         L.aaac_gemv(self.codes, self.scales, self.bitmap, self.tables_bf16, self.R, self.C,
                     self.g, self.S, self.n, x2, out)
         return out
+
+    def matmul(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
+               dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+        """[..., R] = x (bf16 [..., C], any number of rows) times the transposed dequantized
+        weights, decoded on the fly; each weight is dequant's, rounded to bf16 (gemv multiplies by
+        the unrounded product of scale and table entry)."""
+        return packed_matmul(self.codes, self.scales, self.bitmap, self.tables_bf16, x, self.g,
+                             self.S, self.n, out=out, dtype=dtype)
 
 
 class Workspaces:
