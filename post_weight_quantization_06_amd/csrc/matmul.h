@@ -101,10 +101,13 @@ inline int can_store4(const MatmulArgs& a) {
   return (uintptr_t)a.y % (4 * b) == 0 && a.ldy % 4 == 0;
 }
 
+// B: which byte of the scale words counts.
+template <int B>
 __device__ __forceinline__ f32x4 mfma_fp4(u32x4 w, u32x4 x, f32x4 c, uint32_t sw, uint32_t sx) {
   const i32x8 aw = {(int)w.x, (int)w.y, (int)w.z, (int)w.w, 0, 0, 0, 0};
   const i32x8 ax = {(int)x.x, (int)x.y, (int)x.z, (int)x.w, 0, 0, 0, 0};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(aw, ax, c, 4, 4, 0, (int)sw, 0, (int)sx);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(aw, ax, c, 4, 4, B, (int)sw, B,
+                                                          (int)sx);
 }
 
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 w, u32x4 x, f32x4 c) {

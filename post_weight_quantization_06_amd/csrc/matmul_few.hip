@@ -187,7 +187,7 @@ __global__ __launch_bounds__(W * kWave) void few_mxfp4_kernel(MatmulArgs a) {
         const uint32_t sw = ws[i][p] >> (8 * q);
 #pragma unroll
         for (int j = 0; j < NT; ++j)
-          acc[i][j] = mfma_fp4(wc[i][p], xc[j][p], acc[i][j], sw, sx[j]);
+          acc[i][j] = mfma_fp4<0>(wc[i][p], xc[j][p], acc[i][j], sw, sx[j]);
       }
     }
   }
@@ -237,6 +237,7 @@ hipError_t launch_few_packed(const MatmulArgs& a, hipStream_t stream) {
 
 hipError_t launch_mxfp4_matmul(const MatmulArgs& a, bool x_mxfp4, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
+  if (x_mxfp4 && a.T > 64 * a.E) return launch_tile_mxfp4(a, stream);
   return x_mxfp4 ? launch_few_mxfp4(a, stream) : launch_few_mx_bf16(a, stream);
 }
 
