@@ -171,7 +171,7 @@ template <int GPL, int SPL>
 struct PackedRun {
   u32x4 codes;
   uint32_t scale[GPL];
-  uint32_t sel;                                  // bit i: selector of the i-th selection group
+  uint32_t bits, shift;                          // bitmap byte and the run's first bit in it
 };
 template <int GPL, int SPL, bool SIGN>
 struct PackedDecoder {
@@ -211,22 +211,21 @@ struct PackedDecoder {
     const uint16_t* sp = w.scales + (k >> a.log2g);
 #pragma unroll
     for (int i = 0; i < GPL; ++i) u.scale[i] = sp[i];
-    if (SIGN) {
-      u.sel = 0;
-#pragma unroll
-      for (int i = 0; i < GPL; ++i) u.sel |= (u.scale[i] >> 15) << i;
-    } else {
+    if (!SIGN) {
       const int64_t h = w.first + (k >> a.log2S);
-      u.sel = ((uint32_t)w.bitmap[h >> 3] >> (h & 7)) & ((1u << SPL) - 1u);
+      u.bits = w.bitmap[h >> 3];
+      u.shift = (uint32_t)h & 7u;
     }
-    return u;
+    return u;                                    // as loaded: nothing here waits for the words
   }
   __device__ __forceinline__ void decode(const MatmulArgs&, const Run& u, u32x4 (&out)[4]) const {
     uint32_t L[4], H[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (j % (4 / SPL) == 0) {
-        const bool one = (u.sel >> (j / (4 / SPL))) & 1u;
+        const int i = j / (4 / SPL);             // SIGN: SPL == GPL
+        const bool one = SIGN ? (u.scale[i < GPL ? i : 0] & 0x8000u) != 0
+                              : ((u.bits >> (u.shift + i)) & 1u) != 0;
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           L[v] = one ? lo[1][v] : lo[0][v];

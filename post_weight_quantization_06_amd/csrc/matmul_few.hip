@@ -235,15 +235,24 @@ hipError_t launch_few_packed(const MatmulArgs& a, hipStream_t stream) {
   return few_bf16<PackedDecoder<2, 4, false>>(a, stream);
 }
 
+namespace {
+
+// The 32-bit offsets of the tiles' loads reach every row of a tile.
+bool tiles_fit(const MatmulArgs& a) { return a.ldx < ((int64_t)1 << 21); }
+
+}  // namespace
+
 hipError_t launch_mxfp4_matmul(const MatmulArgs& a, bool x_mxfp4, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  if (x_mxfp4 && a.T > 64 * a.E) return launch_tile_mxfp4(a, stream);
-  return x_mxfp4 ? launch_few_mxfp4(a, stream) : launch_few_mx_bf16(a, stream);
+  const bool many = a.T > 64 * (int64_t)a.E;
+  if (x_mxfp4) return many ? launch_tile_mxfp4(a, stream) : launch_few_mxfp4(a, stream);
+  return many && tiles_fit(a) ? launch_tile_mx_bf16(a, stream) : launch_few_mx_bf16(a, stream);
 }
 
 hipError_t launch_packed_matmul(const MatmulArgs& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  return launch_few_packed(a, stream);
+  const bool many = a.T > 64 * (int64_t)a.E && tiles_fit(a);
+  return many ? launch_tile_packed(a, stream) : launch_few_packed(a, stream);
 }
 
 }  // namespace aaac

@@ -35,7 +35,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
 }
 // This wave's loads have landed; after the barrier every wave's have.
 __device__ __forceinline__ void stage_ready() {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0)
   __syncthreads();
 }
 
@@ -185,7 +185,155 @@ hipError_t tile_mxfp4(MatmulArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// ------------------------------------------------------------------------------------------------
+// bf16 x times decoded weights. A step takes 64 columns (128 bytes of bf16 a row). Two threads share
+// a weight row of the tile: each reads a run of 32 columns (16 bytes of codes) straight into
+// registers, decodes it and writes it to LDS as bf16, one step ahead of its use, so a weight is
+// decoded once per tile. Rows of x go to LDS unchanged. Both lie permuted as above. Instruction
+// h of a step takes pieces 4 h + q (columns 32 h + 8 q ..) of a row.
+// One half of the waves decodes before its matrix instructions, the other half after them, so that
+// the two waves of a SIMD keep both its units busy.
+// ------------------------------------------------------------------------------------------------
+template <class D, int WR, int WT, int FR, int FT>
+__global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArgs a) {
+  constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma;
+  static_assert(NW * kWave == 2 * BM, "two threads a weight row");
+  static_assert(BN % (8 * NW) == 0, "whole loads of x a wave");
+  constexpr int kW = BM * 128, kX = BN * 128;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kW + kX];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
+  const int64_t id = by_die(blockIdx.x, gridDim.x);
+  const int64_t tile = id / a.row_blocks, rb = id % a.row_blocks;
+  int e;
+  int64_t t0, t1;
+  if (!find_tile(a.offsets, a.E, a.T, BN, tile, e, t0, t1)) return;
+  const int64_t r0 = rb * BM;
+  const int64_t x_bytes = a.ldx * 2;
+  const int64_t nt = t1 - t0 < BN ? t1 - t0 : BN;
+  const u32x4 xr = rows_buffer(static_cast<const uint8_t*>(a.x) + t0 * x_bytes,
+                               (nt - 1) * x_bytes + a.C * 2);
+  const uint32_t lds0 = lds_address(&lds[0][0]);
+  const int piece = (lane & 7) ^ (lane >> 3);
+  auto load_x = [&](int buf, int64_t kt) {
+    const uint32_t dst = lds0 + buf * (kW + kX) + kW;
+    const uint32_t off0 =
+        (uint32_t)(lane >> 3) * (uint32_t)x_bytes + (uint32_t)(kt * 128) + piece * 16;
+    const bool in = kt * 64 + piece * 8 < a.C;
+#pragma unroll
+    for (int i = 0; i < BN / 8 / NW; ++i) {
+      const int row = (wave * (BN / 8 / NW) + i) * 8;
+      load_lds16(xr, in ? off0 + row * (uint32_t)x_bytes : kOutside, dst + row * 128);
+    }
+  };
+  D dec;
+  dec.init(a, e);
+  const int wrow = tid >> 1, half = tid & 1;
+  const typename D::Row wp = dec.row(a, e, r0 + wrow < a.R ? r0 + wrow : a.R - 1);
+  auto load_w = [&](int64_t kt) {
+    const int64_t k = kt * 64 + half * 32;
+    return dec.load(a, wp, k < a.Cp ? k : 0);
+  };
+  auto put_w = [&](int buf, int64_t kt, const typename D::Run& u) {
+    u32x4 v[4];
+    dec.decode(a, u, v);
+    const bool in = kt * 64 + half * 32 < a.Cp;  // columns past the row's end: zero times zero
+    uint8_t* p = lds[buf] + wrow * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<u32x4*>(p + (((4 * half + j) ^ (wrow & 7)) * 16)) =
+          in ? v[j] : u32x4{0u, 0u, 0u, 0u};
+  };
+
+  f32x4 acc[FR][FT];
+#pragma unroll
+  for (int i = 0; i < FR; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int wm = (wave / WT) * FR * kMfma, wn = (wave % WT) * FT * kMfma;
+  const int l = lane & 15, q = lane >> 4;
+  const int64_t steps = (a.Cp + 63) / 64;
+  auto multiply = [&](int buf) {
+    const uint8_t* base = lds[buf];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      u32x4 wf[FR], xf[FT];
+      const int p = ((4 * h + q) ^ (l & 7)) * 16;
+#pragma unroll
+      for (int i = 0; i < FR; ++i)
+        wf[i] = *reinterpret_cast<const u32x4*>(base + (wm + i * kMfma + l) * 128 + p);
+#pragma unroll
+      for (int j = 0; j < FT; ++j)
+        xf[j] = *reinterpret_cast<const u32x4*>(base + kW + (wn + j * kMfma + l) * 128 + p);
+#pragma unroll
+      for (int i = 0; i < FR; ++i)
+#pragma unroll
+        for (int j = 0; j < FT; ++j) acc[i][j] = mfma_bf16(wf[i], xf[j], acc[i][j]);
+    }
+  };
+
+  typename D::Run now = load_w(0);
+  load_x(0, 0);
+  put_w(0, 0, now);
+  if (steps > 1) now = load_w(1);
+  const bool decode_first = wave < NW / 2;
+  for (int64_t kt = 0; kt < steps; ++kt) {
+    const int buf = (int)(kt & 1);
+    stage_ready();
+    const bool more = kt + 1 < steps;
+    typename D::Run next = now;
+    if (more) load_x(buf ^ 1, kt + 1);
+    if (kt + 2 < steps) next = load_w(kt + 2);
+    if (more && decode_first) put_w(buf ^ 1, kt + 1, now);
+    multiply(buf);
+    if (more && !decode_first) put_w(buf ^ 1, kt + 1, now);
+    now = next;
+  }
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    const int64_t t = t0 + wn + j * kMfma + l;
+    if (t >= t1) continue;
+#pragma unroll
+    for (int i = 0; i < FR; ++i) {
+      const int64_t r = r0 + wm + i * kMfma + 4 * q;
+      if (r < a.R) store4(a, t, r, acc[i][j]);
+    }
+  }
+}
+
+template <class D, int WR, int WT, int FR, int FT>
+hipError_t tile_bf16(MatmulArgs a, hipStream_t stream) {
+  constexpr int BM = WR * FR * kMfma, BN = WT * FT * kMfma;
+  a.row_blocks = (a.R + BM - 1) / BM;
+  a.y_vec = can_store4(a);
+  const int64_t grid = a.row_blocks * token_tiles(a, BN);
+  hipLaunchKernelGGL((tile_bf16_kernel<D, WR, WT, FR, FT>), dim3((unsigned)grid),
+                     dim3(WR * WT * kWave), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <class D>
+hipError_t tile_bf16_any(const MatmulArgs& a, hipStream_t stream) {
+  return tile_bf16<D, 2, 4, 8, 4>(a, stream);
+}
+
 }  // namespace
+
+hipError_t launch_tile_mx_bf16(const MatmulArgs& a, hipStream_t stream) {
+  return tile_bf16_any<MxDecoder>(a, stream);
+}
+
+hipError_t launch_tile_packed(const MatmulArgs& a, hipStream_t stream) {
+  const int gpl = a.log2g >= 5 ? 1 : 32 >> a.log2g, spl = a.log2S >= 5 ? 1 : 32 >> a.log2S;
+  if (!a.bitmap) {
+    if (gpl == 1) return tile_bf16_any<PackedDecoder<1, 1, true>>(a, stream);
+    if (gpl == 2) return tile_bf16_any<PackedDecoder<2, 2, true>>(a, stream);
+    return tile_bf16_any<PackedDecoder<4, 4, true>>(a, stream);
+  }
+  if (gpl == 1 && spl == 1) return tile_bf16_any<PackedDecoder<1, 1, false>>(a, stream);
+  if (gpl == 1 && spl == 2) return tile_bf16_any<PackedDecoder<1, 2, false>>(a, stream);
+  if (gpl == 1) return tile_bf16_any<PackedDecoder<1, 4, false>>(a, stream);
+  return tile_bf16_any<PackedDecoder<2, 4, false>>(a, stream);
+}
 
 hipError_t launch_tile_mxfp4(const MatmulArgs& a, hipStream_t stream) {
   return tile_mxfp4<2, 4, 8, 4>(a, stream);

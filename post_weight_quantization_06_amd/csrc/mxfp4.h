@@ -45,6 +45,8 @@ struct MatmulArgs {
   int y_vec;                   // set by the launcher: four neighbours of a row go out in one store
 };
 
+hipError_t launch_tile_mx_bf16(const MatmulArgs& a, hipStream_t stream);
+hipError_t launch_tile_packed(const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_tile_mxfp4(const MatmulArgs& a, hipStream_t stream);
 hipError_t launch_mxfp4_matmul(const MatmulArgs& a, bool x_mxfp4, hipStream_t stream);
 hipError_t launch_packed_matmul(const MatmulArgs& a, hipStream_t stream);
