@@ -347,7 +347,7 @@ aaac_status aaac_assign_refine_batch(int count, const uint16_t* const* W, const 
  *         to its element; rows of 16-byte multiples on a 16-byte boundary are read fastest.
  * codes   u8 [M, Cp / 2], two codes per byte, the low nibble holds the even column; 16-byte aligned.
  * scales  u8 [M, Cp / 32].
- * Shapes: M >= 0 (0: nothing is written), 1 <= C < 2^22, M * Cp < 2^40. One kernel.
+ * Shapes: M >= 0 (0: nothing is written), 1 <= C < 2^21, M * Cp < 2^40. One kernel.
  */
 aaac_status aaac_mxfp4_quantize(const void* X, int x_type, int64_t M, int64_t C, int64_t ldx,
                                 uint8_t* codes, uint8_t* scales, void* stream);
@@ -373,14 +373,14 @@ aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int6
  * T        rows of x and y, 0 <= T < 2^31; T = 0 launches nothing.
  * y        [T, R] of y_type AAAC_BF16, AAAC_F16 or AAAC_F32, row stride ldy >= R, aligned to its
  *          element. y must not overlap an input.
- * Shapes: 1 <= E <= 65535, 1 <= R < 2^31, 1 <= C < 2^22, E * R * C < 2^40, and at most 2^31 output
+ * Shapes: 1 <= E <= 65535, 1 <= R < 2^31, 1 <= C < 2^21, E * R * C < 2^40, and at most 2^31 output
  * tiles. No workspace; one kernel.
  *
  * aaac_mxfp4_matmul: weights in MXFP4, w_codes [E, R, Cp / 2] (16-byte aligned) and w_scales
  * [E, R, Cp / 32] as aaac_mxfp4_quantize writes them for the stacked rows. x_type:
  *   AAAC_MXFP4  x = codes [T, Cp / 2] (16-byte aligned), x_scales [T, Cp / 32], ldx ignored; products
  *               of codes and scales are exact.
- *   AAAC_BF16   x bf16 [T, C], row stride ldx >= C; x 16-byte aligned, C % 8 == 0, ldx % 8 == 0;
+ *   AAAC_BF16   x bf16 [T, C], row stride C <= ldx < 2^21; x 16-byte aligned, C % 8 == 0, ldx % 8 == 0;
  *               x_scales NULL.
  *
  * aaac_matmul: weights in the packed dual-codebook format, stacked: codes [E, R, C / 2] (16-byte

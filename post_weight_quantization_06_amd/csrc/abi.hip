@@ -432,12 +432,13 @@ int type_bytes(int type) {
   return type == AAAC_BF16 || type == AAAC_F16 ? 2 : type == AAAC_F32 ? 4 : 0;
 }
 
-constexpr int64_t kMaxMatmulCols = (int64_t)1 << 22;
+// 256 rows of the widest x stay below 2^31 bytes: the kernels' offsets within a tile have 32 bits.
+constexpr int64_t kMaxMatmulCols = (int64_t)1 << 21;
 
 aaac_status check_mx_shape(int64_t M, int64_t C, int64_t ld, const char* who) {
   if (M < 0 || C < 1 || C >= kMaxMatmulCols || ld < C)
     return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
-                "%s: M=%lld C=%lld row stride %lld (need M >= 0, 1 <= C < 2^22, stride >= C)", who,
+                "%s: M=%lld C=%lld row stride %lld (need M >= 0, 1 <= C < 2^21, stride >= C)", who,
                 (long long)M, (long long)C, (long long)ld);
   if (M > ((((int64_t)1 << 40) - 1) / (mx_blocks(C) * kMxBlock)) ||
       (M > 1 && ld > (((int64_t)1 << 60) / M)))
@@ -450,7 +451,7 @@ aaac_status check_matmul(const MatmulArgs& a, int64_t E, bool x_bf16, const char
   if (E < 1 || E > 65535 || a.R < 1 || a.R >= ((int64_t)1 << 31) || a.C < 1 ||
       a.C >= kMaxMatmulCols || a.R > ((((int64_t)1 << 40) - 1) / a.Cp) / E)
     return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
-                "%s: E=%lld R=%lld C=%lld (need 1 <= E <= 65535, R >= 1, 1 <= C < 2^22, E*R*C < 2^40)",
+                "%s: E=%lld R=%lld C=%lld (need 1 <= E <= 65535, R >= 1, 1 <= C < 2^21, E*R*C < 2^40)",
                 who, (long long)E, (long long)a.R, (long long)a.C);
   if (!a.offsets && E != 1)
     return fail(AAAC_ERR_INVALID_ARG, "%s: E=%lld matrices need offsets", who, (long long)E);
@@ -461,9 +462,9 @@ aaac_status check_matmul(const MatmulArgs& a, int64_t E, bool x_bf16, const char
   if (a.T < 0 || a.T >= ((int64_t)1 << 31) || a.ldy < a.R || a.ldy >= ((int64_t)1 << 31))
     return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld ldy=%lld (need 0 <= T < 2^31, R <= ldy < 2^31)",
                 who, (long long)a.T, (long long)a.ldy);
-  if (x_bf16 && (a.C % 8 != 0 || a.ldx < a.C || a.ldx % 8 != 0 || a.ldx >= ((int64_t)1 << 31)))
+  if (x_bf16 && (a.C % 8 != 0 || a.ldx < a.C || a.ldx % 8 != 0 || a.ldx >= kMaxMatmulCols))
     return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
-                "%s: C=%lld ldx=%lld (bf16 rows need C %% 8 == 0, ldx %% 8 == 0, C <= ldx < 2^31)", who,
+                "%s: C=%lld ldx=%lld (bf16 rows need C %% 8 == 0, ldx %% 8 == 0, C <= ldx < 2^21)", who,
                 (long long)a.C, (long long)a.ldx);
   if (a.T > 0 && (!a.x || !aligned(a.x, 16) || !a.y || !aligned(a.y, yb)))
     return fail(AAAC_ERR_INVALID_ARG, "%s: x or y null or misaligned (x needs 16 bytes)", who);

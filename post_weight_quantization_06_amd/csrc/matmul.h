@@ -14,6 +14,19 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
+template <int N> struct Int { static constexpr int value = N; };
+
+// Rows as a buffer: loads past its `bytes` give zeros, so rows past a tile's last and columns past a
+// row's end need no branch. The ABI keeps a tile of 256 rows below 2^31 bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+__device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+}
+// An offset past every such buffer, also with a row's columns added to it.
+constexpr uint32_t kOutside = 0x80000000u;
+
 constexpr int kMfma = 16;                        // rows and columns of one matrix instruction
 
 // Token tiles of BN rows that a call can need at most: every expert's last tile may be partial.
@@ -116,47 +129,69 @@ __device__ __forceinline__ f32x4 mfma_bf16(u32x4 w, u32x4 x, f32x4 c) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Weights of a lane's run of 32 consecutive columns (16 bytes of codes) as bf16, eight at a time.
+// Decoders: 4-bit weights to bf16, eight at a time. A kernel reads a weight row either by runs (32
+// consecutive columns a thread: the tiles, which pass the result on through LDS) or by chunks (128
+// consecutive columns a wave row of four lane groups: the few-row kernels, which feed it to the
+// matrix instructions directly). In a chunk lane group q = lane >> 4 reads the 16 code bytes of run
+// q; a transposition over the four groups then leaves it with the codes of columns 32 p + 8 q ..
+// 32 p + 8 q + 7 in word p, the columns that instruction p of the chunk wants from it. Eight
+// neighbouring columns never cross a scale or selection group.
 // ------------------------------------------------------------------------------------------------
+__device__ __forceinline__ u32x4 over_groups(u32x4 v) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
+  const u32x2 b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
+  const u32x2 c = __builtin_amdgcn_permlane16_swap(a.x, b.x, false, false);
+  const u32x2 d = __builtin_amdgcn_permlane16_swap(a.y, b.y, false, false);
+  return u32x4{c.x, c.y, d.x, d.y};
+}
 
-// MXFP4: the run is one block; code times power of two is exact in bf16.
-struct MxRun {
-  u32x4 codes;
-  uint32_t byte;
-};
+// MXFP4: a run is one block; code times power of two is exact in bf16 (and in fp32 before it).
 struct MxDecoder {
-  typedef MxRun Run;
   struct Row { const uint8_t* codes; const uint8_t* scales; };
+  struct Run { u32x4 codes; uint32_t byte; };
+  struct Chunk { u32x4 codes; uint32_t bytes; };
   __device__ __forceinline__ void init(const MatmulArgs&, int) {}
   __device__ __forceinline__ Row row(const MatmulArgs& a, int e, int64_t r) const {
     const int64_t i = (int64_t)e * a.R + r;
     return {a.codes + i * (a.Cp >> 1), static_cast<const uint8_t*>(a.scales) + i * (a.Cp >> 5)};
   }
-  __device__ __forceinline__ Run load(const MatmulArgs&, const Row& w, int64_t k) const {
-    Run u;
-    u.codes = *reinterpret_cast<const u32x4*>(w.codes + (k >> 1));
-    u.byte = w.scales[k >> 5];
+  static __device__ __forceinline__ u32x4 eight(uint32_t w, uint32_t b) {
+    // 2^(b - 127): byte 0 is the subnormal 2^-127, byte 255 a NaN
+    const float s = __uint_as_float(b == 0 ? 0x00400000u : (b == 255u ? 0x7fc00000u : b << 23));
+    const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+    const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+    const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+    const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+    return u32x4{pack_bf16(v0.x * s, v0.y * s), pack_bf16(v1.x * s, v1.y * s),
+                 pack_bf16(v2.x * s, v2.y * s), pack_bf16(v3.x * s, v3.y * s)};
+  }
+  __device__ __forceinline__ Run load_run(const MatmulArgs&, const Row& w, int64_t k) const {
+    return {*reinterpret_cast<const u32x4*>(w.codes + (k >> 1)), w.scales[k >> 5]};
+  }
+  __device__ __forceinline__ void decode_run(const Run& u, u32x4 (&out)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = eight(u.codes[j], u.byte);
+  }
+  __device__ __forceinline__ Chunk load_chunk(const MatmulArgs&, const Row& w, int c, int q) const {
+    Chunk u;
+    u.codes = *reinterpret_cast<const u32x4*>(w.codes + (int64_t)c * 64 + 16 * q);
+    __builtin_memcpy(&u.bytes, w.scales + c * 4, 4);
     return u;
   }
-  static __device__ __forceinline__ float value(uint32_t b) {
-    return __uint_as_float(b == 0 ? 0x00400000u : (b == 255u ? 0x7fc00000u : b << 23));
+  // The row's last chunk: runs at or past its end are zeros.
+  __device__ __forceinline__ Chunk load_last(const MatmulArgs& a, const Row& w, int c, int q) const {
+    Chunk u = {u32x4{0u, 0u, 0u, 0u}, 0u};
+    const int left = (int)(a.Cp >> 5) - 4 * c;
+    if (q < left) u.codes = *reinterpret_cast<const u32x4*>(w.codes + (int64_t)c * 64 + 16 * q);
+    for (int i = 0; i < 4; ++i)
+      if (i < left) u.bytes |= (uint32_t)w.scales[c * 4 + i] << (8 * i);
+    return u;
   }
-  __device__ __forceinline__ void decode(const MatmulArgs&, const Run& u, u32x4 (&out)[4]) const {
-    const float s = value(u.byte);
+  __device__ __forceinline__ void decode_chunk(const Chunk& u, int, u32x4 (&out)[4]) const {
+    const u32x4 w = over_groups(u.codes);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t o[4];
-      // code values are exact in fp32 and so is their product with the power of two
-      const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u.codes[j], 1.0f, 0);
-      const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u.codes[j], 1.0f, 1);
-      const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u.codes[j], 1.0f, 2);
-      const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(u.codes[j], 1.0f, 3);
-      o[0] = pack_bf16(v0.x * s, v0.y * s);
-      o[1] = pack_bf16(v1.x * s, v1.y * s);
-      o[2] = pack_bf16(v2.x * s, v2.y * s);
-      o[3] = pack_bf16(v3.x * s, v3.y * s);
-      out[j] = u32x4{o[0], o[1], o[2], o[3]};
-    }
+    for (int p = 0; p < 4; ++p) out[p] = eight(w[p], (u.bytes >> (8 * p)) & 0xffu);
   }
 };
 
@@ -165,19 +200,20 @@ struct MxDecoder {
 // entries, a second permute picks between the lower and the upper eight by bit 3 of the code, and a
 // third puts the two bytes of an entry where fp32 keeps them. One product and one rounding follow,
 // as in dequant.
-// GPL, SPL: scale and selection groups in a run (1 for groups of 32 and more). SIGN: the selector
-// is the scale's sign bit (S == g), else a bit of the bitmap.
-template <int GPL, int SPL>
-struct PackedRun {
-  u32x4 codes;
-  uint32_t scale[GPL];
-  uint32_t bits, shift;                          // bitmap byte and the run's first bit in it
-};
-template <int GPL, int SPL, bool SIGN>
+// LG: log2 of the scale group, 7 for 128 and more. LS: the same of the selection group when its
+// selectors are in the bitmap, 0 when they are the scales' sign bits (S == g).
+template <int LG, int LS>
 struct PackedDecoder {
-  typedef PackedRun<GPL, SPL> Run;
-  struct Row { const uint8_t* codes; const uint16_t* scales; const uint8_t* bitmap; int64_t first; };
+  static constexpr bool kSign = LS == 0;
+  static constexpr int kGpl = LG >= 5 ? 1 : 32 >> LG;               // scale groups in a run
+  static constexpr int kScaleBytes = LG >= 7 ? 2 : 256 >> LG;       // of a chunk
+  static constexpr int kScaleWords = (kScaleBytes + 3) / 4;
+  struct Row { const uint8_t* codes; const uint16_t* scales; int64_t first; };
+  struct Run { u32x4 codes; uint32_t scale[kGpl]; uint32_t bits, shift; };
+  struct Chunk { u32x4 codes; uint32_t scale[kScaleWords]; uint32_t bits, shift; };
   uint32_t lo[2][4], hi[2][4];
+  const uint8_t* bitmap;
+  int64_t bitmap_bytes;
 
   __device__ __forceinline__ void init(const MatmulArgs& a, int e) {
 #pragma unroll
@@ -198,64 +234,163 @@ struct PackedDecoder {
         hi[c][v] = h;
       }
     }
+    bitmap = kSign ? nullptr : a.bitmap + (int64_t)e * a.bitmap_stride;
+    bitmap_bytes = a.bitmap_stride;
   }
   __device__ __forceinline__ Row row(const MatmulArgs& a, int e, int64_t r) const {
     const int64_t i = (int64_t)e * a.R + r;
-    return {a.codes + i * (a.C >> 1),
-            static_cast<const uint16_t*>(a.scales) + i * (a.C >> a.log2g),
-            SIGN ? nullptr : a.bitmap + (int64_t)e * a.bitmap_stride, r * (a.C >> a.log2S)};
+    return {a.codes + i * (a.C >> 1), static_cast<const uint16_t*>(a.scales) + i * (a.C >> a.log2g),
+            kSign ? 0 : r * (a.C >> a.log2S)};
   }
-  __device__ __forceinline__ Run load(const MatmulArgs& a, const Row& w, int64_t k) const {
+  struct Planes { uint32_t L[4], H[4]; };
+  __device__ __forceinline__ Planes planes(bool one) const {
+    Planes p;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      p.L[v] = one ? lo[1][v] : lo[0][v];
+      p.H[v] = one ? hi[1][v] : hi[0][v];
+    }
+    return p;
+  }
+  static __device__ __forceinline__ u32x4 eight(uint32_t w, const Planes& t, uint32_t scale) {
+    const float s = __uint_as_float((scale & 0x7fffu) << 16);
+    uint32_t pl[2], ph[2];                       // entry bytes of the even and the odd columns
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) {
+      const uint32_t idx = (odd ? w >> 4 : w) & 0x07070707u;
+      const uint32_t pick = ((odd ? w >> 5 : w >> 1) & 0x04040404u) | 0x03020100u;
+      pl[odd] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t.L[3], t.L[2], idx),
+                                      __builtin_amdgcn_perm(t.L[1], t.L[0], idx), pick);
+      ph[odd] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t.H[3], t.H[2], idx),
+                                      __builtin_amdgcn_perm(t.H[1], t.H[0], idx), pick);
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      // bytes: 0, 0, low, high (selector 12 is a zero byte; 0..3 index the low plane's word)
+      const uint32_t sel = 0x00000c0cu | ((uint32_t)p << 16) | ((uint32_t)(4 + p) << 24);
+      const float ve = __uint_as_float(__builtin_amdgcn_perm(ph[0], pl[0], sel));
+      const float vo = __uint_as_float(__builtin_amdgcn_perm(ph[1], pl[1], sel));
+      o[p] = pack_bf16(ve * s, vo * s);
+    }
+    return u32x4{o[0], o[1], o[2], o[3]};
+  }
+
+  // The words as loaded: nothing here waits for them.
+  __device__ __forceinline__ Run load_run(const MatmulArgs& a, const Row& w, int64_t k) const {
     Run u;
     u.codes = *reinterpret_cast<const u32x4*>(w.codes + (k >> 1));
     const uint16_t* sp = w.scales + (k >> a.log2g);
 #pragma unroll
-    for (int i = 0; i < GPL; ++i) u.scale[i] = sp[i];
-    if (!SIGN) {
+    for (int i = 0; i < kGpl; ++i) u.scale[i] = sp[i];
+    if (!kSign) {
       const int64_t h = w.first + (k >> a.log2S);
-      u.bits = w.bitmap[h >> 3];
+      u.bits = bitmap[h >> 3];                   // the run's selectors lie in one byte
       u.shift = (uint32_t)h & 7u;
     }
-    return u;                                    // as loaded: nothing here waits for the words
+    return u;
   }
-  __device__ __forceinline__ void decode(const MatmulArgs&, const Run& u, u32x4 (&out)[4]) const {
-    uint32_t L[4], H[4];
+  __device__ __forceinline__ void decode_run(const Run& u, u32x4 (&out)[4]) const {
+    Planes t;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (j % (4 / SPL) == 0) {
-        const int i = j / (4 / SPL);             // SIGN: SPL == GPL
-        const bool one = SIGN ? (u.scale[i < GPL ? i : 0] & 0x8000u) != 0
-                              : ((u.bits >> (u.shift + i)) & 1u) != 0;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          L[v] = one ? lo[1][v] : lo[0][v];
-          H[v] = one ? hi[1][v] : hi[0][v];
-        }
+      const int gi = LG >= 5 ? 0 : (8 * j) >> LG, si = LS >= 5 ? 0 : (8 * j) >> LS;
+      if (kSign) {
+        if (j == 0 || (LG < 5 && (8 * j) % (1 << LG) == 0)) t = planes((u.scale[gi] & 0x8000u) != 0);
+      } else if (j == 0 || (LS < 5 && (8 * j) % (1 << LS) == 0)) {
+        t = planes(((u.bits >> (u.shift + si)) & 1u) != 0);
       }
-      const float s = __uint_as_float((u.scale[j / (4 / GPL)] & 0x7fffu) << 16);
-      const uint32_t w = u.codes[j];
-      uint32_t pl[2], ph[2];                     // entry bytes of the even and the odd columns
+      out[j] = eight(u.codes[j], t, u.scale[gi]);
+    }
+  }
+
+  __device__ __forceinline__ Chunk load_chunk(const MatmulArgs& a, const Row& w, int c, int q) const {
+    Chunk u;
+    u.codes = *reinterpret_cast<const u32x4*>(w.codes + (int64_t)c * 64 + 16 * q);
+    const uint16_t* sp = w.scales + (((int64_t)c * 128) >> a.log2g);
+    if (LG >= 7) u.scale[0] = sp[0];
+    else __builtin_memcpy(u.scale, sp, kScaleBytes);
+    if (!kSign) load_bits(a, w, c, u);
+    return u;
+  }
+  // The selectors of a chunk as the low bits of bits >> shift: four bytes from the first one's, or
+  // the four last bytes of this matrix's map where those would end past it.
+  __device__ __forceinline__ void load_bits(const MatmulArgs& a, const Row& w, int c, Chunk& u) const {
+    const int64_t h = w.first + (((int64_t)c * 128) >> a.log2S);
+    if (bitmap_bytes >= 4) {
+      const int64_t last = bitmap_bytes - 4, at = (h >> 3) < last ? (h >> 3) : last;
+      __builtin_memcpy(&u.bits, bitmap + at, 4);
+      u.shift = (uint32_t)(h - 8 * at);
+    } else {
+      u.bits = 0;
+      for (int i = 0; i < (int)bitmap_bytes; ++i) u.bits |= (uint32_t)bitmap[i] << (8 * i);
+      u.shift = (uint32_t)h;
+    }
+  }
+  // The row's last chunk: runs at or past its end are zeros (and their codes entry 0: the caller
+  // clears what it decodes to).
+  __device__ __forceinline__ Chunk load_last(const MatmulArgs& a, const Row& w, int c, int q) const {
+    Chunk u;
+    u.codes = u32x4{0u, 0u, 0u, 0u};
+    const int64_t k = (int64_t)c * 128 + 32 * q;
+    if (k < a.C) u.codes = *reinterpret_cast<const u32x4*>(w.codes + (k >> 1));
+    const int64_t g0 = ((int64_t)c * 128) >> a.log2g, gn = a.C >> a.log2g;
 #pragma unroll
-      for (int odd = 0; odd < 2; ++odd) {
-        const uint32_t idx = (odd ? w >> 4 : w) & 0x07070707u;
-        const uint32_t pick = ((odd ? w >> 5 : w >> 1) & 0x04040404u) | 0x03020100u;
-        pl[odd] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(L[3], L[2], idx),
-                                        __builtin_amdgcn_perm(L[1], L[0], idx), pick);
-        ph[odd] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(H[3], H[2], idx),
-                                        __builtin_amdgcn_perm(H[1], H[0], idx), pick);
-      }
-      uint32_t o[4];
+    for (int i = 0; i < kScaleWords; ++i) u.scale[i] = 0;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        // bytes: 0, 0, low, high (selector 12 is a zero byte; 0..3 index the low plane's word)
-        const uint32_t sel = 0x00000c0cu | ((uint32_t)p << 16) | ((uint32_t)(4 + p) << 24);
-        const float ve = __uint_as_float(__builtin_amdgcn_perm(ph[0], pl[0], sel));
-        const float vo = __uint_as_float(__builtin_amdgcn_perm(ph[1], pl[1], sel));
-        o[p] = pack_bf16(ve * s, vo * s);
+    for (int i = 0; i < kScaleBytes / 2; ++i)
+      if (g0 + i < gn) u.scale[i >> 1] |= (uint32_t)w.scales[g0 + i] << (16 * (i & 1));
+    if (!kSign) load_bits(a, w, c, u);
+    return u;
+  }
+  __device__ __forceinline__ void decode_chunk(const Chunk& u, int q, u32x4 (&out)[4]) const {
+    const u32x4 w = over_groups(u.codes);
+    Planes t;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      uint32_t s;
+      if (LG >= 7) s = u.scale[0];
+      else if (LG == 6) s = u.scale[0] >> (16 * (p >> 1));
+      else if (LG == 5) s = u.scale[p >> 1] >> (16 * (p & 1));
+      else if (LG == 4) s = u.scale[p] >> (16 * (q >> 1));
+      else s = (q >> 1 ? u.scale[2 * p + 1] : u.scale[2 * p]) >> (16 * (q & 1));
+      if (kSign) {
+        if (p == 0 || LG < 6 || (LG == 6 && p == 2)) t = planes((s & 0x8000u) != 0);
+      } else if (p == 0 || LS < 6 || (LS == 6 && p == 2)) {
+        const int i = LS >= 7 ? 0 : LS >= 5 ? (32 * p) >> LS : ((32 * p) >> LS) + ((8 * q) >> LS);
+        t = planes(((u.bits >> (u.shift + i)) & 1u) != 0);
       }
-      out[j] = u32x4{o[0], o[1], o[2], o[3]};
+      out[p] = eight(w[p], t, s);
     }
   }
 };
+
+// Calls f with the decoder type of a packed call.
+template <class F>
+hipError_t with_packed_decoder(const MatmulArgs& a, F f) {
+  const int lg = a.log2g < 7 ? a.log2g : 7, ls = a.log2S < 7 ? a.log2S : 7;
+  if (!a.bitmap) {
+    switch (lg) {
+      case 3: return f(PackedDecoder<3, 0>());
+      case 4: return f(PackedDecoder<4, 0>());
+      case 5: return f(PackedDecoder<5, 0>());
+      case 6: return f(PackedDecoder<6, 0>());
+      default: return f(PackedDecoder<7, 0>());
+    }
+  }
+  switch (8 * lg + ls) {
+    case 8 * 4 + 3: return f(PackedDecoder<4, 3>());
+    case 8 * 5 + 3: return f(PackedDecoder<5, 3>());
+    case 8 * 5 + 4: return f(PackedDecoder<5, 4>());
+    case 8 * 6 + 3: return f(PackedDecoder<6, 3>());
+    case 8 * 6 + 4: return f(PackedDecoder<6, 4>());
+    case 8 * 6 + 5: return f(PackedDecoder<6, 5>());
+    case 8 * 7 + 3: return f(PackedDecoder<7, 3>());
+    case 8 * 7 + 4: return f(PackedDecoder<7, 4>());
+    case 8 * 7 + 5: return f(PackedDecoder<7, 5>());
+    case 8 * 7 + 6: return f(PackedDecoder<7, 6>());
+    default: return f(PackedDecoder<7, 7>());
+  }
+}
 
 }  // namespace aaac

@@ -36,12 +36,13 @@ __device__ __forceinline__ void join_and_store(const MatmulArgs& a, const f32x4 
 }
 
 // ------------------------------------------------------------------------------------------------
-// bf16 rows of x times decoded weights. A chunk is 128 columns: run q of a lane is the 32 columns
-// 32 q .. 32 q + 31 of the chunk, and instruction j of a chunk takes columns 8 j .. 8 j + 7 of every
-// run (weights and x in the same order, so the order does not matter to the sum).
+// bf16 rows of x times decoded weights. Instruction p of a chunk of 128 columns takes columns
+// 32 p + 8 q .. 32 p + 8 q + 7 from lane group q, so a load of x reads 64 neighbouring bytes of each
+// row. The chunks go to the waves in turn, U at a time, so that U loads of each weight row are in
+// flight. Rows past the tile's last lie outside the x buffer and load as zeros.
 // ------------------------------------------------------------------------------------------------
-template <class D, int RT, int NT, int W>
-__global__ __launch_bounds__(W * kWave) void few_bf16_kernel(MatmulArgs a) {
+template <class D, int RT, int NT, int W, int U>
+__global__ __launch_bounds__(W * kWave, 1) void few_bf16_kernel(MatmulArgs a) {
   const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
   const int64_t tile = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
   int e;
@@ -56,48 +57,69 @@ __global__ __launch_bounds__(W * kWave) void few_bf16_kernel(MatmulArgs a) {
     const int64_t r = r0 + i * kMfma + (lane & 15);
     w[i] = dec.row(a, e, r < a.R ? r : a.R - 1);
   }
-  const uint16_t* xp[NT];
+  const int64_t nt = t1 - t0 < NT * kMfma ? t1 - t0 : NT * kMfma;
+  const __amdgpu_buffer_rsrc_t xr = rows_rsrc(
+      static_cast<const uint16_t*>(a.x) + t0 * a.ldx, (nt - 1) * a.ldx * 2 + a.C * 2);
+  const int q = lane >> 4;
+  uint32_t xoff[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t t = t0 + j * kMfma + (lane & 15);
-    xp[j] = static_cast<const uint16_t*>(a.x) + (t < t1 ? t : t1 - 1) * a.ldx;
-  }
+  for (int j = 0; j < NT; ++j)
+    xoff[j] = j * kMfma + (lane & 15) < nt
+                  ? (uint32_t)(((j * kMfma + (lane & 15)) * a.ldx + 8 * q) * 2) : kOutside;
   f32x4 acc[RT][NT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int run = 32 * (lane >> 4);
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  for (int64_t c = (int64_t)wave * 128; c < a.Cp; c += W * 128) {
-    const int64_t k = c + run;
-    const bool whole = c + 128 <= a.C;           // uniform: every run of the chunk lies in the row
-    const bool in = k < a.Cp;
-    const int64_t kl = in ? k : 0;
-    typename D::Run u[RT];
+
+  const int whole = (int)(a.C >> 7);             // chunks whose every run lies in the row
+  auto chunks = [&](int c, auto n) {
+    constexpr int N = decltype(n)::value;
+    typename D::Chunk u[N][RT];
+    u32x4 x[N][NT][4];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) u[i] = dec.load(a, w[i], kl);
-    u32x4 x[NT][4];
+    for (int s = 0; s < N; ++s)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+      for (int i = 0; i < RT; ++i) u[s][i] = dec.load_chunk(a, w[i], c + s * W, q);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        if (whole) {
-          x[j][p] = *reinterpret_cast<const u32x4*>(xp[j] + k + 8 * p);
-        } else {
-          x[j][p] = zero;                        // columns past the row's end: zero times zero
-          if (k + 8 * p < a.C) x[j][p] = *reinterpret_cast<const u32x4*>(xp[j] + k + 8 * p);
-        }
+    for (int s = 0; s < N; ++s)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+          x[s][j][p] = buffer_load16(xr, xoff[j] + (uint32_t)((c + s * W) * 256 + 64 * p));
+#pragma unroll
+    for (int s = 0; s < N; ++s)
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        u32x4 wv[4];
+        dec.decode_chunk(u[s][i], q, wv);
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[i][j] = mfma_bf16(wv[p], x[s][j][p], acc[i][j]);
       }
+  };
+  int c = wave;
+  for (; c + (U - 1) * W < whole; c += U * W) chunks(c, Int<U>());
+  if (U > 1)
+    for (; c < whole; c += W) chunks(c, Int<1>());
+  if (c == whole && (int64_t)whole * 128 < a.Cp) {
+    // the row's last columns: zero times zero past its end
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       u32x4 wv[4];
-      dec.decode(a, u[i], wv);
+      dec.decode_chunk(dec.load_last(a, w[i], whole, q), q, wv);
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        if (!whole && k + 8 * p >= a.C) wv[p] = zero;
+        const bool in = (int64_t)whole * 128 + 32 * p + 8 * q < a.C;
+        if (!in) wv[p] = zero;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = mfma_bf16(wv[p], x[j][p], acc[i][j]);
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = mfma_bf16(
+              wv[p], buffer_load16(xr, in ? xoff[j] + (uint32_t)(whole * 256 + 64 * p) : kOutside),
+              acc[i][j]);
       }
     }
   }
@@ -109,7 +131,7 @@ __global__ __launch_bounds__(W * kWave) void few_bf16_kernel(MatmulArgs a) {
 // are stored. Run q of a lane is one block of 32 columns; a chunk is 512 columns, so that a lane
 // reads the 16 scale bytes of its row in one load and takes byte 4 j + q for instruction j.
 // ------------------------------------------------------------------------------------------------
-__device__ __forceinline__ u32x4 load_scales(const uint8_t* p, int64_t left) {
+__device__ __forceinline__ u32x4 load_scales(const uint8_t* p, int left) {
   u32x4 v;
   if (left >= 16) {
     __builtin_memcpy(&v, p, 16);
@@ -124,15 +146,16 @@ __device__ __forceinline__ u32x4 load_scales(const uint8_t* p, int64_t left) {
 }
 
 template <int RT, int NT, int W>
-__global__ __launch_bounds__(W * kWave) void few_mxfp4_kernel(MatmulArgs a) {
+__global__ __launch_bounds__(W * kWave, 1) void few_mxfp4_kernel(MatmulArgs a) {
   const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
   const int64_t tile = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
   int e;
   int64_t t0, t1;
   if (!find_tile(a.offsets, a.E, a.T, NT * kMfma, tile, e, t0, t1)) return;
   const int64_t r0 = rb * (RT * kMfma);
-  const int64_t kb = a.Cp >> 5;                  // blocks in a row
-  const uint8_t *wp[RT], *wsp[RT], *xp[NT], *xsp[NT];
+  const int kb = (int)(a.Cp >> 5);               // blocks in a row
+  const uint8_t *wp[RT], *wsp[RT], *xsp[NT];
+  const int q = lane >> 4;
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
     const int64_t r = r0 + i * kMfma + (lane & 15);
@@ -140,22 +163,26 @@ __global__ __launch_bounds__(W * kWave) void few_mxfp4_kernel(MatmulArgs a) {
     wp[i] = a.codes + row * (a.Cp >> 1);
     wsp[i] = static_cast<const uint8_t*>(a.scales) + row * kb;
   }
+  const int64_t nt = t1 - t0 < NT * kMfma ? t1 - t0 : NT * kMfma;
+  const __amdgpu_buffer_rsrc_t xr =
+      rows_rsrc(static_cast<const uint8_t*>(a.x) + t0 * (a.Cp >> 1), nt * (a.Cp >> 1));
+  uint32_t xoff[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    int64_t t = t0 + j * kMfma + (lane & 15);
-    t = t < t1 ? t : t1 - 1;
-    xp[j] = static_cast<const uint8_t*>(a.x) + t * (a.Cp >> 1);
-    xsp[j] = a.x_scales + t * kb;
+    const int t = j * kMfma + (lane & 15);
+    const bool in = t < nt;
+    xoff[j] = in ? (uint32_t)(t * (a.Cp >> 1)) : kOutside;
+    xsp[j] = a.x_scales + (t0 + (in ? t : 0)) * kb;
   }
   f32x4 acc[RT][NT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int q = lane >> 4;
   const u32x4 zero = {0u, 0u, 0u, 0u};
-  for (int64_t b0 = (int64_t)wave * 16; b0 < kb; b0 += W * 16) {
-    const int64_t left = kb - b0;
+  auto chunk = [&](int b0, auto all) {
+    constexpr bool ALL = decltype(all)::value;   // every block of the chunk lies in the row
+    const int left = ALL ? 16 : kb - b0;
     u32x4 ws[RT], xs[NT], wc[RT][4], xc[NT][4];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -163,7 +190,7 @@ __global__ __launch_bounds__(W * kWave) void few_mxfp4_kernel(MatmulArgs a) {
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         wc[i][p] = zero;                         // past the row's end: zero codes, scale byte 0
-        if (4 * p + q < left)
+        if (ALL || 4 * p + q < left)
           wc[i][p] = *reinterpret_cast<const u32x4*>(wp[i] + (b0 + 4 * p + q) * 16);
       }
     }
@@ -171,11 +198,9 @@ __global__ __launch_bounds__(W * kWave) void few_mxfp4_kernel(MatmulArgs a) {
     for (int j = 0; j < NT; ++j) {
       xs[j] = load_scales(xsp[j] + b0, left);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        xc[j][p] = zero;
-        if (4 * p + q < left)
-          xc[j][p] = *reinterpret_cast<const u32x4*>(xp[j] + (b0 + 4 * p + q) * 16);
-      }
+      for (int p = 0; p < 4; ++p)
+        xc[j][p] = buffer_load16(xr, ALL || 4 * p + q < left
+                                         ? xoff[j] + (uint32_t)((b0 + 4 * p + q) * 16) : kOutside);
     }
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
@@ -190,7 +215,10 @@ __global__ __launch_bounds__(W * kWave) void few_mxfp4_kernel(MatmulArgs a) {
           acc[i][j] = mfma_fp4<0>(wc[i][p], xc[j][p], acc[i][j], sw, sx[j]);
       }
     }
-  }
+  };
+  int b0 = wave * 16;
+  for (; b0 + 16 <= kb; b0 += W * 16) chunk(b0, Int<1>());
+  if (b0 < kb) chunk(b0, Int<0>());
   join_and_store<RT, NT, W>(a, acc, r0, t0, t1);
 }
 
@@ -201,21 +229,47 @@ int64_t few_grid(MatmulArgs& a) {
   return a.row_blocks * token_tiles(a, NT * kMfma);
 }
 
+#ifndef RT_
+#define RT_ 1
+#endif
+#ifndef W_
+#define W_ 8
+#endif
+#ifndef U_
+#define U_ 2
+#endif
+template <class D, int NT>
+hipError_t few_bf16_nt(MatmulArgs a, hipStream_t stream) {
+  const int64_t grid = few_grid<RT_, NT>(a);
+  hipLaunchKernelGGL((few_bf16_kernel<D, RT_, NT, W_, (NT > 2 ? 1 : U_)>), dim3((unsigned)grid), dim3(W_ * kWave), 0,
+                     stream, a);
+  return hipGetLastError();
+}
 template <class D>
-hipError_t few_bf16(MatmulArgs a, hipStream_t stream) {
-  const int64_t grid = few_grid<1, 1>(a);
-  hipLaunchKernelGGL((few_bf16_kernel<D, 1, 1, 4>), dim3((unsigned)grid), dim3(4 * kWave), 0,
+hipError_t few_bf16(const MatmulArgs& a, hipStream_t stream) {
+  const int64_t rows = (a.T + a.E - 1) / a.E;
+  if (rows <= kMfma) return few_bf16_nt<D, 1>(a, stream);
+  if (rows <= 2 * kMfma) return few_bf16_nt<D, 2>(a, stream);
+  if (rows <= 3 * kMfma) return few_bf16_nt<D, 3>(a, stream);
+  return few_bf16_nt<D, 4>(a, stream);
+}
+
+template <int NT>
+hipError_t few_mxfp4_nt(MatmulArgs a, hipStream_t stream) {
+  const int64_t grid = few_grid<RT_, NT>(a);
+  hipLaunchKernelGGL((few_mxfp4_kernel<RT_, NT, W_>), dim3((unsigned)grid), dim3(W_ * kWave), 0,
                      stream, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_few_mxfp4(MatmulArgs a, hipStream_t stream) {
-  const int64_t grid = few_grid<1, 1>(a);
-  hipLaunchKernelGGL((few_mxfp4_kernel<1, 1, 4>), dim3((unsigned)grid), dim3(4 * kWave), 0, stream,
-                     a);
-  return hipGetLastError();
+hipError_t launch_few_mxfp4(const MatmulArgs& a, hipStream_t stream) {
+  const int64_t rows = (a.T + a.E - 1) / a.E;
+  if (rows <= kMfma) return few_mxfp4_nt<1>(a, stream);
+  if (rows <= 2 * kMfma) return few_mxfp4_nt<2>(a, stream);
+  if (rows <= 3 * kMfma) return few_mxfp4_nt<3>(a, stream);
+  return few_mxfp4_nt<4>(a, stream);
 }
 
 hipError_t launch_few_mx_bf16(const MatmulArgs& a, hipStream_t stream) {
@@ -223,35 +277,19 @@ hipError_t launch_few_mx_bf16(const MatmulArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_few_packed(const MatmulArgs& a, hipStream_t stream) {
-  const int gpl = a.log2g >= 5 ? 1 : 32 >> a.log2g, spl = a.log2S >= 5 ? 1 : 32 >> a.log2S;
-  if (!a.bitmap) {
-    if (gpl == 1) return few_bf16<PackedDecoder<1, 1, true>>(a, stream);
-    if (gpl == 2) return few_bf16<PackedDecoder<2, 2, true>>(a, stream);
-    return few_bf16<PackedDecoder<4, 4, true>>(a, stream);
-  }
-  if (gpl == 1 && spl == 1) return few_bf16<PackedDecoder<1, 1, false>>(a, stream);
-  if (gpl == 1 && spl == 2) return few_bf16<PackedDecoder<1, 2, false>>(a, stream);
-  if (gpl == 1) return few_bf16<PackedDecoder<1, 4, false>>(a, stream);
-  return few_bf16<PackedDecoder<2, 4, false>>(a, stream);
+  return with_packed_decoder(a, [&](auto d) { return few_bf16<decltype(d)>(a, stream); });
 }
-
-namespace {
-
-// The 32-bit offsets of the tiles' loads reach every row of a tile.
-bool tiles_fit(const MatmulArgs& a) { return a.ldx < ((int64_t)1 << 21); }
-
-}  // namespace
 
 hipError_t launch_mxfp4_matmul(const MatmulArgs& a, bool x_mxfp4, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
   const bool many = a.T > 64 * (int64_t)a.E;
   if (x_mxfp4) return many ? launch_tile_mxfp4(a, stream) : launch_few_mxfp4(a, stream);
-  return many && tiles_fit(a) ? launch_tile_mx_bf16(a, stream) : launch_few_mx_bf16(a, stream);
+  return many ? launch_tile_mx_bf16(a, stream) : launch_few_mx_bf16(a, stream);
 }
 
 hipError_t launch_packed_matmul(const MatmulArgs& a, hipStream_t stream) {
   if (a.T == 0) return hipSuccess;
-  const bool many = a.T > 64 * (int64_t)a.E && tiles_fit(a);
+  const bool many = a.T > 64 * (int64_t)a.E;
   return many ? launch_tile_packed(a, stream) : launch_few_packed(a, stream);
 }
 

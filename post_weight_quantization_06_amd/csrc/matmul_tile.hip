@@ -8,15 +8,11 @@ namespace {
 
 typedef __attribute__((address_space(3))) void* LdsPtr;
 
-// Rows as a buffer: loads past its `bytes` give zeros, so rows past a tile's last and columns past a
-// row's end need no branch.
+// rows_rsrc as the four words that an assembly operand takes.
 __device__ __forceinline__ u32x4 rows_buffer(const void* p, int64_t bytes) {
   const uint64_t b = (uint64_t)p;
   return u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)bytes, 0x00027000u};
 }
-
-// An offset past every buffer used here.
-constexpr uint32_t kOutside = 0x80000000u;
 
 // Asynchronous loads from a buffer into LDS: lane l's bytes land at dst + l * size (dst uniform).
 // In assembly because the compiler would wait for them before any LDS read, of the other stage too;
@@ -191,8 +187,6 @@ hipError_t tile_mxfp4(MatmulArgs a, hipStream_t stream) {
 // registers, decodes it and writes it to LDS as bf16, one step ahead of its use, so a weight is
 // decoded once per tile. Rows of x go to LDS unchanged. Both lie permuted as above. Instruction
 // h of a step takes pieces 4 h + q (columns 32 h + 8 q ..) of a row.
-// One half of the waves decodes before its matrix instructions, the other half after them, so that
-// the two waves of a SIMD keep both its units busy.
 // ------------------------------------------------------------------------------------------------
 template <class D, int WR, int WT, int FR, int FT>
 __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArgs a) {
@@ -231,11 +225,11 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
   const typename D::Row wp = dec.row(a, e, r0 + wrow < a.R ? r0 + wrow : a.R - 1);
   auto load_w = [&](int64_t kt) {
     const int64_t k = kt * 64 + half * 32;
-    return dec.load(a, wp, k < a.Cp ? k : 0);
+    return dec.load_run(a, wp, k < a.Cp ? k : 0);
   };
   auto put_w = [&](int buf, int64_t kt, const typename D::Run& u) {
     u32x4 v[4];
-    dec.decode(a, u, v);
+    dec.decode_run(u, v);
     const bool in = kt * 64 + half * 32 < a.Cp;  // columns past the row's end: zero times zero
     uint8_t* p = lds[buf] + wrow * 128;
 #pragma unroll
@@ -275,7 +269,6 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
   load_x(0, 0);
   put_w(0, 0, now);
   if (steps > 1) now = load_w(1);
-  const bool decode_first = wave < NW / 2;
   for (int64_t kt = 0; kt < steps; ++kt) {
     const int buf = (int)(kt & 1);
     stage_ready();
@@ -283,9 +276,8 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
     typename D::Run next = now;
     if (more) load_x(buf ^ 1, kt + 1);
     if (kt + 2 < steps) next = load_w(kt + 2);
-    if (more && decode_first) put_w(buf ^ 1, kt + 1, now);
     multiply(buf);
-    if (more && !decode_first) put_w(buf ^ 1, kt + 1, now);
+    if (more) put_w(buf ^ 1, kt + 1, now);
     now = next;
   }
 #pragma unroll
@@ -323,16 +315,7 @@ hipError_t launch_tile_mx_bf16(const MatmulArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_tile_packed(const MatmulArgs& a, hipStream_t stream) {
-  const int gpl = a.log2g >= 5 ? 1 : 32 >> a.log2g, spl = a.log2S >= 5 ? 1 : 32 >> a.log2S;
-  if (!a.bitmap) {
-    if (gpl == 1) return tile_bf16_any<PackedDecoder<1, 1, true>>(a, stream);
-    if (gpl == 2) return tile_bf16_any<PackedDecoder<2, 2, true>>(a, stream);
-    return tile_bf16_any<PackedDecoder<4, 4, true>>(a, stream);
-  }
-  if (gpl == 1 && spl == 1) return tile_bf16_any<PackedDecoder<1, 1, false>>(a, stream);
-  if (gpl == 1 && spl == 2) return tile_bf16_any<PackedDecoder<1, 2, false>>(a, stream);
-  if (gpl == 1) return tile_bf16_any<PackedDecoder<1, 4, false>>(a, stream);
-  return tile_bf16_any<PackedDecoder<2, 4, false>>(a, stream);
+  return with_packed_decoder(a, [&](auto d) { return tile_bf16_any<decltype(d)>(a, stream); });
 }
 
 hipError_t launch_tile_mxfp4(const MatmulArgs& a, hipStream_t stream) {

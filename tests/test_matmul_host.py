@@ -112,7 +112,7 @@ def test_mxfp4_quantize_and_dequant_refusals(lib):
         assert f(lib, t=MXFP4) == INVALID and f(lib, t=-1) == INVALID
         assert f(lib, M=-1) == SHAPE and f(lib, C=0, **{ld: 0}) == SHAPE
         assert f(lib, **{ld: 63}) == SHAPE                        # rows would overlap
-        assert f(lib, C=1 << 22, **{ld: 1 << 22}) == SHAPE
+        assert f(lib, C=1 << 21, **{ld: 1 << 21}) == SHAPE
         assert f(lib, M=1 << 35) == SHAPE                         # M * Cp >= 2^40
         assert f(lib, codes=None) == INVALID and f(lib, scales=None) == INVALID
         assert f(lib, codes=OFF2) == INVALID
@@ -128,13 +128,14 @@ def test_mxfp4_matmul_refusals(lib):
     assert _mx(lib, E=0) == SHAPE and _mx(lib, E=65536, off=FAKE) == SHAPE
     assert _mx(lib, E=2) == INVALID                               # experts without offsets
     assert _mx(lib, off=OFF2) == INVALID
-    assert _mx(lib, R=0) == SHAPE and _mx(lib, C=0) == SHAPE and _mx(lib, C=1 << 22) == SHAPE
+    assert _mx(lib, R=0) == SHAPE and _mx(lib, C=0) == SHAPE and _mx(lib, C=1 << 21) == SHAPE
     assert _mx(lib, C=-5) == SHAPE and _mx(lib, R=-1) == SHAPE
     assert _mx(lib, T=-1) == SHAPE and _mx(lib, T=1 << 31) == SHAPE
     assert _mx(lib, ldy=15) == SHAPE and _mx(lib, ldx=56) == SHAPE
     assert _mx(lib, C=60, ldx=64) == SHAPE                        # bf16 rows: C % 8
     assert _mx(lib, ldx=68) == SHAPE                              # bf16 rows: ldx % 8
     assert _mx(lib, C=60, t=MXFP4) == INVALID                     # any width, but x_scales missing
+    assert _mx(lib, ldx=1 << 21) == SHAPE
     assert _mx(lib, xs=FAKE) == INVALID                           # bf16 x has no scales
     assert _mx(lib, x=OFF8) == INVALID and _mx(lib, x=None) == INVALID
     assert _mx(lib, y=None) == INVALID and _mx(lib, y=OFF2, yt=F32) == INVALID
