@@ -360,11 +360,24 @@ aaac_status aaac_mxfp4_quantize(const void* X, int x_type, int64_t M, int64_t C,
 aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t C,
                                void* Y, int y_type, int64_t ldy, void* stream);
 
+/* The products below, as aaac_matmul_workspace_bytes names them. */
+#define AAAC_MATMUL_PACKED 0            /* aaac_matmul */
+#define AAAC_MATMUL_MXFP4 1             /* aaac_mxfp4_matmul, x bf16 */
+#define AAAC_MATMUL_MXFP4_X 2           /* aaac_mxfp4_matmul, x in MXFP4 */
+#define AAAC_MATMUL_QUANTIZE_X 3        /* aaac_mxfp4_matmul with AAAC_QUANTIZE_X */
+
+/* Flags of aaac_mxfp4_matmul. */
+#define AAAC_QUANTIZE_X 1               /* x is quantized to MXFP4 first, in the workspace */
+
+/* Workspace bytes of one product call of the given kind, 0 for an unsupported shape or where the
+ * call uses none. The workspace needs no particular contents and keeps none that matter. */
+size_t aaac_matmul_workspace_bytes(int kind, int64_t E, int64_t R, int64_t C, int64_t T);
+
 /*
  * Matrix products on 4-bit weights for any number of rows of x, grouped by expert:
  *   y[t, r] = sum_c x[t, c] W_e[r, c]   for offsets[e] <= t < offsets[e + 1],
  * W_e the values of the e-th of E stacked [R, C] matrices; sums in fp32 in an order fixed by the
- * call's shapes (bitwise reproducible), rounded once to y_type.
+ * call's shapes and by whether it has a workspace (bitwise reproducible), rounded once to y_type.
  * offsets  int32 [E + 1] on the device, ascending: the rows of x sorted by expert; an expert may
  *          have none. Rows of y outside [offsets[0], offsets[E]) are left as they were. Values are
  *          not checked on the host: the kernels clamp them to [0, T] and to ascending order, so a
@@ -373,15 +386,22 @@ aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int6
  * T        rows of x and y, 0 <= T < 2^31; T = 0 launches nothing.
  * y        [T, R] of y_type AAAC_BF16, AAAC_F16 or AAAC_F32, row stride ldy >= R, aligned to its
  *          element. y must not overlap an input.
+ * ws       NULL with ws_bytes 0, or aaac_matmul_workspace_bytes(...) bytes, 256-byte aligned. With
+ *          it a product of few output tiles splits its columns over workgroups and adds their fp32
+ *          sums in order with a second kernel.
  * Shapes: 1 <= E <= 65535, 1 <= R < 2^31, 1 <= C < 2^21, E * R * C < 2^40, and at most 2^31 output
- * tiles. No workspace; one kernel.
+ * tiles of 16 x 16.
  *
  * aaac_mxfp4_matmul: weights in MXFP4, w_codes [E, R, Cp / 2] (16-byte aligned) and w_scales
  * [E, R, Cp / 32] as aaac_mxfp4_quantize writes them for the stacked rows. x_type:
  *   AAAC_MXFP4  x = codes [T, Cp / 2] (16-byte aligned), x_scales [T, Cp / 32], ldx ignored; products
  *               of codes and scales are exact.
- *   AAAC_BF16   x bf16 [T, C], row stride C <= ldx < 2^21; x 16-byte aligned, C % 8 == 0, ldx % 8 == 0;
- *               x_scales NULL.
+ *   AAAC_BF16   x bf16 [T, C], row stride C <= ldx < 2^21; x 16-byte aligned, C % 8 == 0,
+ *               ldx % 8 == 0; x_scales NULL.
+ *   with the flag AAAC_QUANTIZE_X: AAAC_BF16, AAAC_F16 or AAAC_F32, x [T, C] of any row stride
+ *               ldx >= C, aligned to its element; x_scales NULL. The call runs aaac_mxfp4_quantize
+ *               into ws (which it then needs) and multiplies the result: the same bits as the two
+ *               calls with a workspace give.
  *
  * aaac_matmul: weights in the packed dual-codebook format, stacked: codes [E, R, C / 2] (16-byte
  * aligned), scales [E, R, C / g], tables_bf16 [E, 2, n], bitmap [E, ceil(R * C / S / 8)] exactly
@@ -391,12 +411,12 @@ aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int6
  */
 aaac_status aaac_mxfp4_matmul(const uint8_t* w_codes, const uint8_t* w_scales, int64_t E, int64_t R,
                               int64_t C, const int32_t* offsets, const void* x, int x_type,
-                              const uint8_t* x_scales, int64_t T, int64_t ldx, void* y, int y_type,
-                              int64_t ldy, void* stream);
+                              const uint8_t* x_scales, int64_t T, int64_t ldx, int flags, void* y,
+                              int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 aaac_status aaac_matmul(const uint8_t* codes, const uint16_t* scales, const uint8_t* bitmap,
                         const uint16_t* tables_bf16, int64_t E, int64_t R, int64_t C, int g, int S,
                         int n, const int32_t* offsets, const uint16_t* x, int64_t T, int64_t ldx,
-                        void* y, int y_type, int64_t ldy, void* stream);
+                        void* y, int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -9,6 +9,7 @@ fallback: if the library is missing or no GPU is visible, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -28,6 +29,8 @@ REFINE_ROUND_BF16 = 1
 REFINE_W2_KNOWN = 2
 MAX_BATCH = 8
 MXFP4 = 3
+MATMUL_PACKED, MATMUL_MXFP4, MATMUL_MXFP4_X, MATMUL_QUANTIZE_X = 0, 1, 2, 3
+QUANTIZE_X = 1
 # element types of the matmul and MXFP4 calls
 FLOAT_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
@@ -37,7 +40,7 @@ EXPORTED = (
     "aaac_batch_workspace_bytes", "aaac_assign_batch", "aaac_refine_batch", "aaac_awq_prescale",
     "aaac_gemv", "aaac_gemv_batch", "aaac_assign_refine_batch", "aaac_init_quantiles_batch",
     "aaac_pack_batch", "aaac_dequant_batch", "aaac_refine_batch_noalloc", "aaac_mxfp4_quantize",
-    "aaac_mxfp4_dequant", "aaac_mxfp4_matmul", "aaac_matmul",
+    "aaac_mxfp4_dequant", "aaac_mxfp4_matmul", "aaac_matmul", "aaac_matmul_workspace_bytes",
 )
 
 
@@ -109,10 +112,13 @@ def load(path: str = LIB_PATH):
                                     c_vp]),
         "aaac_mxfp4_quantize": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
         "aaac_mxfp4_dequant": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_i64, c_vp]),
+        "aaac_matmul_workspace_bytes": (c_size, [c_int, c_i64, c_i64, c_i64, c_i64]),
         "aaac_mxfp4_matmul": (c_int, [c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, c_vp,
-                                      c_i64, c_i64, c_vp, c_int, c_i64, c_vp]),
+                                      c_i64, c_i64, c_int, c_vp, c_int, c_i64, c_vp, c_size,
+                                      c_vp]),
         "aaac_matmul": (c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_int, c_int, c_int,
-                                c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_i64, c_vp]),
+                                c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_i64, c_vp, c_size,
+                                c_vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -613,7 +619,7 @@ def _rows(t: torch.Tensor, name: str):
     if s1 != 1 and C > 1:
         raise ValueError("%s must have unit column stride" % name)
     if M <= 1:                 # the stride of a single row carries nothing: any that the call takes
-        return M, C, max(s0, C) if s0 % 8 == 0 and s0 >= C else (C + 7) // 8 * 8
+        s0 = (C + 7) // 8 * 8
     return M, C, s0
 
 
@@ -623,14 +629,19 @@ def _u8(t: torch.Tensor, name: str, numel: int):
             name, numel, t.dtype, tuple(t.shape)))
 
 
+def _float_type(t: torch.Tensor, name: str) -> int:
+    ft = FLOAT_TYPES.get(t.dtype)
+    if ft is None:
+        raise TypeError("%s must be bf16, fp16 or fp32 (got %s)" % (name, t.dtype))
+    return ft
+
+
 def aaac_mxfp4_quantize(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None):
     """codes u8 [M, Cp/2] and scales u8 [M, Cp/32] of X [M, C] (bf16, fp16 or fp32, any row
     stride), Cp = 32 ceil(C / 32)."""
     dev = _on_gpu("aaac_mxfp4_quantize", X, codes, scales)
     _no_grad("aaac_mxfp4_quantize", X)
-    xt = FLOAT_TYPES.get(X.dtype)
-    if xt is None:
-        raise TypeError("X must be bf16, fp16 or fp32 (got %s)" % X.dtype)
+    xt = _float_type(X, "X")
     M, C, ldx = _rows(X, "X")
     blocks = (C + 31) // 32
     _u8(codes, "codes", M * blocks * 16)
@@ -642,9 +653,7 @@ def aaac_mxfp4_quantize(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tens
 def aaac_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tensor, stream=None):
     """Y [M, C] (bf16, fp16 or fp32, any row stride) = the values of the codes."""
     dev = _on_gpu("aaac_mxfp4_dequant", codes, scales, Y)
-    yt = FLOAT_TYPES.get(Y.dtype)
-    if yt is None:
-        raise TypeError("Y must be bf16, fp16 or fp32 (got %s)" % Y.dtype)
+    yt = _float_type(Y, "Y")
     M, C, ldy = _rows(Y, "Y")
     blocks = (C + 31) // 32
     _u8(codes, "codes", M * blocks * 16)
@@ -653,62 +662,85 @@ def aaac_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tenso
             Y.data_ptr(), yt, ldy)
 
 
-def _product_args(what: str, E: int, offsets, y: torch.Tensor, T: int, R: int):
-    """(offsets pointer, y type, row stride of y) after the checks that every product shares."""
-    yt = FLOAT_TYPES.get(y.dtype)
-    if yt is None:
-        raise TypeError("y must be bf16, fp16 or fp32 (got %s)" % y.dtype)
+@functools.lru_cache(maxsize=4096)
+def matmul_workspace_bytes(kind: int, E: int, R: int, C: int, T: int) -> int:
+    return int((_lib or load()).aaac_matmul_workspace_bytes(kind, E, R, C, T))
+
+
+def _product_args(what: str, kind: int, E: int, C: int, offsets, y: torch.Tensor, T: int, R: int,
+                  ws):
+    """(offsets pointer, y type, row stride of y, workspace, its pointer and bytes) after the checks
+    that every product shares. Without a workspace one is taken from torch where the call uses one;
+    it belongs to the stream the caller allocates on, so a call on another stream needs its own."""
+    yt = _float_type(y, "y")
     M, N, ldy = _rows(y, "y")
     if M != T or N != R:
         raise ValueError("%s: y must be [%d, %d] (got [%d, %d])" % (what, T, R, M, N))
-    if offsets is None:
-        return None, yt, ldy
-    if offsets.dtype is not torch.int32 or not offsets.is_contiguous() or \
-            offsets.numel() != E + 1:
-        raise ValueError("%s: offsets must be contiguous int32 [%d] (got %s %s)" % (
-            what, E + 1, offsets.dtype, tuple(offsets.shape)))
-    return offsets.data_ptr(), yt, ldy
+    op = None
+    if offsets is not None:
+        if offsets.dtype is not torch.int32 or not offsets.is_contiguous() or \
+                offsets.numel() != E + 1:
+            raise ValueError("%s: offsets must be contiguous int32 [%d] (got %s %s)" % (
+                what, E + 1, offsets.dtype, tuple(offsets.shape)))
+        op = offsets.data_ptr()
+    need = matmul_workspace_bytes(kind, E, R, C, T)
+    if need == 0:
+        return op, yt, ldy, None, None, 0
+    if ws is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=y.device)
+    elif ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError("%s: ws must be contiguous uint8" % what)
+    return op, yt, ldy, ws, ws.data_ptr(), ws.numel()
 
 
 def aaac_mxfp4_matmul(codes: torch.Tensor, scales: torch.Tensor, C: int, x: torch.Tensor,
                       y: torch.Tensor, offsets: Optional[torch.Tensor] = None,
-                      x_scales: Optional[torch.Tensor] = None, stream=None):
+                      x_scales: Optional[torch.Tensor] = None, flags: int = 0,
+                      ws: Optional[torch.Tensor] = None, stream=None):
     """y [T, R] = x times the transposed MXFP4 matrices: codes u8 [R, Cp/2] or [E, R, Cp/2] with
-    scales u8 [.., Cp/32]. x bf16 [T, C], or codes u8 [T, Cp/2] with x_scales u8 [T, Cp/32].
-    offsets: int32 [E + 1] (see aaac.h), or None for one matrix."""
+    scales u8 [.., Cp/32]. x bf16 [T, C]; or with the flag QUANTIZE_X bf16, fp16 or fp32 [T, C],
+    quantized first; or codes u8 [T, Cp/2] with x_scales u8 [T, Cp/32]. offsets: int32 [E + 1] (see
+    aaac.h), or None for one matrix."""
     what = "aaac_mxfp4_matmul"
-    dev = _on_gpu(what, codes, scales, x, y, offsets, x_scales)
+    dev = _on_gpu(what, codes, scales, x, y, offsets, x_scales, ws)
     blocks = (C + 31) // 32
     shape = codes.shape
+    if len(shape) not in (2, 3):
+        raise ValueError("%s: codes must be [R, Cp/2] or [E, R, Cp/2]" % what)
     E, R = (1, shape[0]) if len(shape) == 2 else (shape[0], shape[1])
     _u8(codes, "codes", E * R * blocks * 16)
     _u8(scales, "scales", E * R * blocks)
     if x_scales is None:
         _no_grad(what, x)
-        if x.dtype is not torch.bfloat16:
-            raise TypeError("x must be bf16, or MXFP4 codes with x_scales (got %s)" % x.dtype)
         T, K, ldx = _rows(x, "x")
         if K != C:
             raise ValueError("%s: x has %d columns, the weights %d" % (what, K, C))
-        xt, xs = 0, None
+        if flags & QUANTIZE_X:
+            xt, kind = _float_type(x, "x"), MATMUL_QUANTIZE_X
+        elif x.dtype is torch.bfloat16:
+            xt, kind = 0, MATMUL_MXFP4
+        else:
+            raise TypeError("x must be bf16, or MXFP4 codes with x_scales (got %s)" % x.dtype)
+        xs = None
     else:
         T = x.shape[0]
         _u8(x, "x", T * blocks * 16)
         _u8(x_scales, "x_scales", T * blocks)
-        xt, xs, ldx = MXFP4, x_scales.data_ptr(), C
-    op, yt, ldy = _product_args(what, E, offsets, y, T, R)
+        xt, kind, xs, ldx = MXFP4, MATMUL_MXFP4_X, x_scales.data_ptr(), C
+    op, yt, ldy, ws, wp, wn = _product_args(what, kind, E, C, offsets, y, T, R, ws)
     _launch(what, dev, stream, codes.data_ptr(), scales.data_ptr(), E, R, C, op, x.data_ptr(), xt,
-            xs, T, ldx, y.data_ptr(), yt, ldy)
+            xs, T, ldx, flags, y.data_ptr(), yt, ldy, wp, wn)
 
 
 def aaac_matmul(codes: torch.Tensor, scales: torch.Tensor, bitmap: Optional[torch.Tensor],
                 tables_bf16: torch.Tensor, g: int, S: int, n: int, x: torch.Tensor,
-                y: torch.Tensor, offsets: Optional[torch.Tensor] = None, stream=None):
+                y: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+                ws: Optional[torch.Tensor] = None, stream=None):
     """y [T, R] = x bf16 [T, C] times the transposed packed matrices: codes u8 [R, C/2] or
     [E, R, C/2] with scales, bitmap and tables_bf16 stacked alike. offsets as in
     aaac_mxfp4_matmul."""
     what = "aaac_matmul"
-    dev = _on_gpu(what, codes, scales, bitmap, tables_bf16, x, y, offsets)
+    dev = _on_gpu(what, codes, scales, bitmap, tables_bf16, x, y, offsets, ws)
     _no_grad(what, x)
     shape = codes.shape
     if len(shape) not in (2, 3):
@@ -729,7 +761,7 @@ def aaac_matmul(codes: torch.Tensor, scales: torch.Tensor, bitmap: Optional[torc
     T, K, ldx = _rows(x, "x")
     if K != C:
         raise ValueError("%s: x has %d columns, the weights %d" % (what, K, C))
-    op, yt, ldy = _product_args(what, E, offsets, y, T, R)
+    op, yt, ldy, ws, wp, wn = _product_args(what, MATMUL_PACKED, E, C, offsets, y, T, R, ws)
     _launch(what, dev, stream, codes.data_ptr(), scales.data_ptr(),
             None if bitmap is None else bitmap.data_ptr(), tables_bf16.data_ptr(), E, R, C, g, S,
-            n, op, x.data_ptr(), T, ldx, y.data_ptr(), yt, ldy)
+            n, op, x.data_ptr(), T, ldx, y.data_ptr(), yt, ldy, wp, wn)

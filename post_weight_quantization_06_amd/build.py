@@ -17,8 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libaaac.so")
 SOURCES = ["abi.hip", "assign.hip", "refine.hip", "importance.hip", "init.hip", "pack.hip",
-           "awq.hip", "gemv.hip", "mxfp4.hip", "matmul_few.hip",
-           "matmul_tile.hip"]
+           "awq.hip", "gemv.hip", "mxfp4.hip", "matmul.hip",
+           "matmul_few.hip", "matmul_tile.hip"]
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "--offload-arch=gfx950", "-fPIC",

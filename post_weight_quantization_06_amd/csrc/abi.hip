@@ -447,7 +447,8 @@ aaac_status check_mx_shape(int64_t M, int64_t C, int64_t ld, const char* who) {
 }
 
 // The checks shared by the products; x_bf16: x is given as bf16 rows.
-aaac_status check_matmul(const MatmulArgs& a, int64_t E, bool x_bf16, const char* who) {
+aaac_status check_matmul(const MatmulArgs& a, int64_t E, bool x_bf16, int x_align,
+                         const char* who) {
   if (E < 1 || E > 65535 || a.R < 1 || a.R >= ((int64_t)1 << 31) || a.C < 1 ||
       a.C >= kMaxMatmulCols || a.R > ((((int64_t)1 << 40) - 1) / a.Cp) / E)
     return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
@@ -466,14 +467,57 @@ aaac_status check_matmul(const MatmulArgs& a, int64_t E, bool x_bf16, const char
     return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
                 "%s: C=%lld ldx=%lld (bf16 rows need C %% 8 == 0, ldx %% 8 == 0, C <= ldx < 2^21)", who,
                 (long long)a.C, (long long)a.ldx);
-  if (a.T > 0 && (!a.x || !aligned(a.x, 16) || !a.y || !aligned(a.y, yb)))
-    return fail(AAAC_ERR_INVALID_ARG, "%s: x or y null or misaligned (x needs 16 bytes)", who);
+  if (a.T > 0 && (!a.x || !aligned(a.x, x_align) || !a.y || !aligned(a.y, yb)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: x or y null or misaligned (x needs %d bytes)", who, x_align);
   // 16-row tiles are the smallest any kernel uses
   const int64_t rb = (a.R + 15) / 16, tt = a.T / 16 + (a.offsets ? E : 1);
   if (rb > (((int64_t)1 << 31) - 1) / tt)
     return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld times R=%lld is over 2^31 tiles", who,
                 (long long)a.T, (long long)a.R);
   return AAAC_OK;
+}
+
+MatmulKind kernel_kind(int kind) {
+  return kind == AAAC_MATMUL_PACKED ? kPacked : kind == AAAC_MATMUL_MXFP4 ? kMxBf16 : kMxMxfp4;
+}
+
+// Where a product's workspace holds what: the parts of split sums, then quantized rows of x.
+struct MatmulWs {
+  size_t codes, scales, bytes;
+};
+
+MatmulWs matmul_ws(const MatmulArgs& a, int kind) {
+  MatmulWs w;
+  const size_t parts = parts_bytes(a, plan_matmul(a, kernel_kind(kind), true));
+  w.codes = (parts + 255) / 256 * 256;
+  w.scales = w.codes + (size_t)a.T * (size_t)(a.Cp / 2);
+  w.bytes = kind == AAAC_MATMUL_QUANTIZE_X ? w.scales + (size_t)a.T * (size_t)(a.Cp / 32) : parts;
+  return w;
+}
+
+aaac_status run_matmul(MatmulArgs& a, int kind, int x_type, void* ws, size_t ws_bytes,
+                       hipStream_t stream, const char* who) {
+  if (a.T == 0) return ok();
+  const bool quantize = kind == AAAC_MATMUL_QUANTIZE_X;
+  if (ws || quantize) {
+    const MatmulWs w = matmul_ws(a, kind);
+    if (!ws || !aligned(ws, 256))
+      return fail(AAAC_ERR_INVALID_ARG, "%s: ws null or not 256-byte aligned", who);
+    if (ws_bytes < w.bytes)
+      return fail(AAAC_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", who, ws_bytes,
+                  w.bytes);
+    a.parts = static_cast<float*>(ws);
+    if (quantize) {
+      uint8_t* codes = static_cast<uint8_t*>(ws) + w.codes;
+      uint8_t* scales = static_cast<uint8_t*>(ws) + w.scales;
+      const hipError_t e = launch_mxfp4_quantize(a.x, x_type, a.T, a.C, a.ldx, codes, scales, stream);
+      if (e != hipSuccess) return hip_status(e, who);
+      a.x = codes;
+      a.x_scales = scales;
+    }
+  }
+  const MatmulKind k = kernel_kind(kind);
+  return hip_status(launch_matmul(a, k, plan_matmul(a, k, ws != nullptr), stream), who);
 }
 
 }  // namespace
@@ -773,14 +817,31 @@ aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int6
                     who);
 }
 
+size_t aaac_matmul_workspace_bytes(int kind, int64_t E, int64_t R, int64_t C, int64_t T) {
+  if (kind < AAAC_MATMUL_PACKED || kind > AAAC_MATMUL_QUANTIZE_X || E < 1 || E > 65535 || R < 1 ||
+      R >= ((int64_t)1 << 31) || C < 1 || C >= kMaxMatmulCols || T < 1 || T >= ((int64_t)1 << 31))
+    return 0;
+  MatmulArgs a = {};
+  a.E = (int)E;
+  a.R = R;
+  a.C = C;
+  a.Cp = mx_blocks(C) * kMxBlock;
+  a.T = T;
+  return matmul_ws(a, kind).bytes;
+}
+
 aaac_status aaac_mxfp4_matmul(const uint8_t* w_codes, const uint8_t* w_scales, int64_t E, int64_t R,
                               int64_t C, const int32_t* offsets, const void* x, int x_type,
-                              const uint8_t* x_scales, int64_t T, int64_t ldx, void* y, int y_type,
-                              int64_t ldy, void* stream) {
+                              const uint8_t* x_scales, int64_t T, int64_t ldx, int flags, void* y,
+                              int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
   const char* who = "aaac_mxfp4_matmul";
-  if (x_type != AAAC_BF16 && x_type != AAAC_MXFP4)
+  if (flags & ~AAAC_QUANTIZE_X) return fail(AAAC_ERR_INVALID_ARG, "%s: unknown flags %d", who, flags);
+  const bool quantize = (flags & AAAC_QUANTIZE_X) != 0;
+  const int xb = type_bytes(x_type);
+  if (quantize ? xb == 0 : x_type != AAAC_BF16 && x_type != AAAC_MXFP4)
     return fail(AAAC_ERR_INVALID_ARG, "%s: x_type %d", who, x_type);
-  const bool mx = x_type == AAAC_MXFP4;
+  const int kind = quantize ? AAAC_MATMUL_QUANTIZE_X
+                   : x_type == AAAC_MXFP4 ? AAAC_MATMUL_MXFP4_X : AAAC_MATMUL_MXFP4;
   MatmulArgs a = {};
   a.codes = w_codes;
   a.scales = w_scales;
@@ -796,19 +857,23 @@ aaac_status aaac_mxfp4_matmul(const uint8_t* w_codes, const uint8_t* w_scales, i
   a.y = y;
   a.y_type = y_type;
   a.ldy = ldy;
-  aaac_status st = check_matmul(a, E, !mx, who);
+  aaac_status st = check_matmul(a, E, kind == AAAC_MATMUL_MXFP4, quantize ? xb : 16, who);
   if (st != AAAC_OK) return st;
+  if (quantize) {
+    st = check_mx_shape(T, C, ldx, who);
+    if (st != AAAC_OK) return st;
+  }
   if (!w_codes || !aligned(w_codes, 16) || !w_scales)
     return fail(AAAC_ERR_INVALID_ARG, "%s: weights null or misaligned (codes need 16 bytes)", who);
-  if (mx ? (T > 0 && !x_scales) : x_scales != nullptr)
+  if (kind == AAAC_MATMUL_MXFP4_X ? (T > 0 && !x_scales) : x_scales != nullptr)
     return fail(AAAC_ERR_INVALID_ARG, "%s: x_scales must be given exactly with MXFP4 x", who);
-  return hip_status(launch_mxfp4_matmul(a, mx, static_cast<hipStream_t>(stream)), who);
+  return run_matmul(a, kind, x_type, ws, ws_bytes, static_cast<hipStream_t>(stream), who);
 }
 
 aaac_status aaac_matmul(const uint8_t* codes, const uint16_t* scales, const uint8_t* bitmap,
                         const uint16_t* tables_bf16, int64_t E, int64_t R, int64_t C, int g, int S,
                         int n, const int32_t* offsets, const uint16_t* x, int64_t T, int64_t ldx,
-                        void* y, int y_type, int64_t ldy, void* stream) {
+                        void* y, int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
   const char* who = "aaac_matmul";
   aaac_status st = check_shape(R, C, g, S, n, true, who);
   if (st != AAAC_OK) return st;
@@ -833,14 +898,15 @@ aaac_status aaac_matmul(const uint8_t* codes, const uint16_t* scales, const uint
   a.y = y;
   a.y_type = y_type;
   a.ldy = ldy;
-  st = check_matmul(a, E, true, who);
+  st = check_matmul(a, E, true, 16, who);
   if (st != AAAC_OK) return st;
   if (!codes || !aligned(codes, 16) || !scales || !aligned(scales, 2) || !tables_bf16 ||
       !aligned(tables_bf16, 2))
     return fail(AAAC_ERR_INVALID_ARG, "%s: weights null or misaligned (codes need 16 bytes)", who);
   if ((S < g) != (bitmap != nullptr))
     return fail(AAAC_ERR_INVALID_ARG, "%s: bitmap must be given exactly when S < g", who);
-  return hip_status(launch_packed_matmul(a, static_cast<hipStream_t>(stream)), who);
+  return run_matmul(a, AAAC_MATMUL_PACKED, AAAC_BF16, ws, ws_bytes, static_cast<hipStream_t>(stream),
+                    who);
 }
 
 }  // extern "C"

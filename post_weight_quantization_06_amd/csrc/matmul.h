@@ -29,13 +29,6 @@ constexpr uint32_t kOutside = 0x80000000u;
 
 constexpr int kMfma = 16;                        // rows and columns of one matrix instruction
 
-// Token tiles of BN rows that a call can need at most: every expert's last tile may be partial.
-inline int64_t token_tiles(const MatmulArgs& a, int BN) {
-  if (!a.offsets) return (a.T + BN - 1) / BN;
-  const int64_t e = a.E < a.T ? a.E : a.T;
-  return a.T / BN + e;
-}
-
 // The expert and the rows [t0, t1) of token tile `tile` (uniform over the wave), or false past the
 // last one. Every wave counts the experts' tiles by itself, 64 experts at a time.
 __device__ __forceinline__ bool find_tile(const int32_t* offsets, int E, int64_t T, int BN,
@@ -107,6 +100,14 @@ __device__ __forceinline__ void store4(const MatmulArgs& a, int64_t t, int64_t r
       static_cast<uint16_t*>(a.y)[i + k] = (uint16_t)pack_bf16(v[k], 0.0f);
     else static_cast<uint16_t*>(a.y)[i + k] = (uint16_t)pack_f16(v[k], 0.0f);
   }
+}
+
+// A tile's result: y itself, or part `part` of a sum split over workgroups, kept in fp32 in rows of
+// whole 16-byte words.
+__device__ __forceinline__ void store_part(const MatmulArgs& a, int part, int64_t t, int64_t r,
+                                           f32x4 v) {
+  if (a.split == 1) store4(a, t, r, v);
+  else *reinterpret_cast<f32x4*>(a.parts + ((int64_t)part * a.T + t) * part_row(a.R) + r) = v;
 }
 
 inline int can_store4(const MatmulArgs& a) {

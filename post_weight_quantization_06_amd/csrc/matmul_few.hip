@@ -225,72 +225,58 @@ __global__ __launch_bounds__(W * kWave, 1) void few_mxfp4_kernel(MatmulArgs a) {
 template <int RT, int NT>
 int64_t few_grid(MatmulArgs& a) {
   a.row_blocks = (a.R + RT * kMfma - 1) / (RT * kMfma);
-  a.y_vec = can_store4(a);
   return a.row_blocks * token_tiles(a, NT * kMfma);
 }
 
-#ifndef RT_
-#define RT_ 1
-#endif
-#ifndef W_
-#define W_ 8
-#endif
-#ifndef U_
-#define U_ 2
-#endif
-template <class D, int NT>
-hipError_t few_bf16_nt(MatmulArgs a, hipStream_t stream) {
-  const int64_t grid = few_grid<RT_, NT>(a);
-  hipLaunchKernelGGL((few_bf16_kernel<D, RT_, NT, W_, (NT > 2 ? 1 : U_)>), dim3((unsigned)grid), dim3(W_ * kWave), 0,
+template <class D, int RT, int NT, int W, int U>
+hipError_t few_bf16(MatmulArgs a, hipStream_t stream) {
+  const int64_t grid = few_grid<RT, NT>(a);
+  hipLaunchKernelGGL((few_bf16_kernel<D, RT, NT, W, U>), dim3((unsigned)grid), dim3(W * kWave), 0,
                      stream, a);
   return hipGetLastError();
 }
+
 template <class D>
-hipError_t few_bf16(const MatmulArgs& a, hipStream_t stream) {
-  const int64_t rows = (a.T + a.E - 1) / a.E;
-  if (rows <= kMfma) return few_bf16_nt<D, 1>(a, stream);
-  if (rows <= 2 * kMfma) return few_bf16_nt<D, 2>(a, stream);
-  if (rows <= 3 * kMfma) return few_bf16_nt<D, 3>(a, stream);
-  return few_bf16_nt<D, 4>(a, stream);
+hipError_t few_bf16_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  if (p.nt == 1) {
+    if (p.rt == 2) return few_bf16<D, 2, 1, 8, 2>(a, stream);
+    return p.waves == 16 ? few_bf16<D, 1, 1, 16, 1>(a, stream) : few_bf16<D, 1, 1, 8, 1>(a, stream);
+  }
+  if (p.rt == 2) return few_bf16<D, 2, 2, 8, 1>(a, stream);
+  return p.waves == 16 ? few_bf16<D, 1, 2, 16, 1>(a, stream) : few_bf16<D, 1, 2, 8, 1>(a, stream);
+}
+
+template <int RT, int NT, int W>
+hipError_t few_mxfp4(MatmulArgs a, hipStream_t stream) {
+  const int64_t grid = few_grid<RT, NT>(a);
+  hipLaunchKernelGGL((few_mxfp4_kernel<RT, NT, W>), dim3((unsigned)grid), dim3(W * kWave), 0, stream,
+                     a);
+  return hipGetLastError();
 }
 
 template <int NT>
-hipError_t few_mxfp4_nt(MatmulArgs a, hipStream_t stream) {
-  const int64_t grid = few_grid<RT_, NT>(a);
-  hipLaunchKernelGGL((few_mxfp4_kernel<RT_, NT, W_>), dim3((unsigned)grid), dim3(W_ * kWave), 0,
-                     stream, a);
-  return hipGetLastError();
+hipError_t few_mxfp4_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  if (p.rt == 2) return few_mxfp4<2, NT, 8>(a, stream);
+  return p.waves == 16 ? few_mxfp4<1, NT, 16>(a, stream) : few_mxfp4<1, NT, 8>(a, stream);
 }
 
 }  // namespace
 
-hipError_t launch_few_mxfp4(const MatmulArgs& a, hipStream_t stream) {
-  const int64_t rows = (a.T + a.E - 1) / a.E;
-  if (rows <= kMfma) return few_mxfp4_nt<1>(a, stream);
-  if (rows <= 2 * kMfma) return few_mxfp4_nt<2>(a, stream);
-  if (rows <= 3 * kMfma) return few_mxfp4_nt<3>(a, stream);
-  return few_mxfp4_nt<4>(a, stream);
+hipError_t launch_few_mxfp4(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  switch (p.nt) {
+    case 1: return few_mxfp4_any<1>(a, p, stream);
+    case 2: return few_mxfp4_any<2>(a, p, stream);
+    case 3: return few_mxfp4_any<3>(a, p, stream);
+    default: return few_mxfp4_any<4>(a, p, stream);
+  }
 }
 
-hipError_t launch_few_mx_bf16(const MatmulArgs& a, hipStream_t stream) {
-  return few_bf16<MxDecoder>(a, stream);
+hipError_t launch_few_mx_bf16(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  return few_bf16_any<MxDecoder>(a, p, stream);
 }
 
-hipError_t launch_few_packed(const MatmulArgs& a, hipStream_t stream) {
-  return with_packed_decoder(a, [&](auto d) { return few_bf16<decltype(d)>(a, stream); });
-}
-
-hipError_t launch_mxfp4_matmul(const MatmulArgs& a, bool x_mxfp4, hipStream_t stream) {
-  if (a.T == 0) return hipSuccess;
-  const bool many = a.T > 64 * (int64_t)a.E;
-  if (x_mxfp4) return many ? launch_tile_mxfp4(a, stream) : launch_few_mxfp4(a, stream);
-  return many ? launch_tile_mx_bf16(a, stream) : launch_few_mx_bf16(a, stream);
-}
-
-hipError_t launch_packed_matmul(const MatmulArgs& a, hipStream_t stream) {
-  if (a.T == 0) return hipSuccess;
-  const bool many = a.T > 64 * (int64_t)a.E;
-  return many ? launch_tile_packed(a, stream) : launch_few_packed(a, stream);
+hipError_t launch_few_packed(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  return with_packed_decoder(a, [&](auto d) { return few_bf16_any<decltype(d)>(a, p, stream); });
 }
 
 }  // namespace aaac

@@ -56,8 +56,9 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_mxfp4_kernel(MatmulAr
   constexpr int kW = BM * 128, kX = BN * 128, kWs = BM * 8, kXs = BN * 8;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kW + kX + kWs + kXs];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
-  const int64_t id = by_die(blockIdx.x, gridDim.x);
-  const int64_t tile = id / a.row_blocks, rb = id % a.row_blocks;
+  const int64_t id = by_die(blockIdx.x, gridDim.x), tiles = gridDim.x / a.split;
+  const int part = (int)(id / tiles);
+  const int64_t tile = id % tiles / a.row_blocks, rb = id % a.row_blocks;
   int e;
   int64_t t0, t1;
   if (!find_tile(a.offsets, a.E, a.T, BN, tile, e, t0, t1)) return;
@@ -120,10 +121,11 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_mxfp4_kernel(MatmulAr
     for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int wm = (wave / WT) * FR * kMfma, wn = (wave % WT) * FT * kMfma;
   const int l = lane & 15, q = lane >> 4;
-  const int64_t steps = (kb + 7) / 8;
-  load(0, 0);
-  for (int64_t kt = 0; kt < steps; ++kt) {
-    const int buf = (int)(kt & 1);
+  const int64_t all = (kb + 7) / 8, first = all * part / a.split;
+  const int64_t steps = all * (part + 1) / a.split;
+  load(0, first);
+  for (int64_t kt = first; kt < steps; ++kt) {
+    const int buf = (int)((kt - first) & 1);
     stage_ready();
     if (kt + 1 < steps) load(buf ^ 1, kt + 1);
     const uint8_t* base = lds[buf];
@@ -160,7 +162,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_mxfp4_kernel(MatmulAr
 #pragma unroll
     for (int i = 0; i < FR; ++i) {
       const int64_t r = r0 + wm + i * kMfma + 4 * q;
-      if (r < a.R) store4(a, t, r, acc[i][j]);
+      if (r < a.R) store_part(a, part, t, r, acc[i][j]);
     }
   }
 }
@@ -169,8 +171,7 @@ template <int WR, int WT, int FR, int FT>
 hipError_t tile_mxfp4(MatmulArgs a, hipStream_t stream) {
   constexpr int BM = WR * FR * kMfma, BN = WT * FT * kMfma;
   a.row_blocks = (a.R + BM - 1) / BM;
-  a.y_vec = can_store4(a);
-  const int64_t grid = a.row_blocks * token_tiles(a, BN);
+  const int64_t grid = a.row_blocks * token_tiles(a, BN) * a.split;
   const bool whole = a.Cp % 256 == 0 && (uintptr_t)a.scales % 4 == 0 && (uintptr_t)a.x_scales % 4 == 0;
   if (whole)
     hipLaunchKernelGGL((tile_mxfp4_kernel<WR, WT, FR, FT, true>), dim3((unsigned)grid),
@@ -196,8 +197,9 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
   constexpr int kW = BM * 128, kX = BN * 128;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kW + kX];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
-  const int64_t id = by_die(blockIdx.x, gridDim.x);
-  const int64_t tile = id / a.row_blocks, rb = id % a.row_blocks;
+  const int64_t id = by_die(blockIdx.x, gridDim.x), tiles = gridDim.x / a.split;
+  const int part = (int)(id / tiles);
+  const int64_t tile = id % tiles / a.row_blocks, rb = id % a.row_blocks;
   int e;
   int64_t t0, t1;
   if (!find_tile(a.offsets, a.E, a.T, BN, tile, e, t0, t1)) return;
@@ -245,7 +247,8 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
     for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int wm = (wave / WT) * FR * kMfma, wn = (wave % WT) * FT * kMfma;
   const int l = lane & 15, q = lane >> 4;
-  const int64_t steps = (a.Cp + 63) / 64;
+  const int64_t all = (a.Cp + 63) / 64, first = all * part / a.split;
+  const int64_t steps = all * (part + 1) / a.split;
   auto multiply = [&](int buf) {
     const uint8_t* base = lds[buf];
 #pragma unroll
@@ -265,12 +268,12 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
     }
   };
 
-  typename D::Run now = load_w(0);
-  load_x(0, 0);
-  put_w(0, 0, now);
-  if (steps > 1) now = load_w(1);
-  for (int64_t kt = 0; kt < steps; ++kt) {
-    const int buf = (int)(kt & 1);
+  typename D::Run now = load_w(first);
+  load_x(0, first);
+  put_w(0, first, now);
+  if (first + 1 < steps) now = load_w(first + 1);
+  for (int64_t kt = first; kt < steps; ++kt) {
+    const int buf = (int)((kt - first) & 1);
     stage_ready();
     const bool more = kt + 1 < steps;
     typename D::Run next = now;
@@ -287,7 +290,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
 #pragma unroll
     for (int i = 0; i < FR; ++i) {
       const int64_t r = r0 + wm + i * kMfma + 4 * q;
-      if (r < a.R) store4(a, t, r, acc[i][j]);
+      if (r < a.R) store_part(a, part, t, r, acc[i][j]);
     }
   }
 }
@@ -296,30 +299,38 @@ template <class D, int WR, int WT, int FR, int FT>
 hipError_t tile_bf16(MatmulArgs a, hipStream_t stream) {
   constexpr int BM = WR * FR * kMfma, BN = WT * FT * kMfma;
   a.row_blocks = (a.R + BM - 1) / BM;
-  a.y_vec = can_store4(a);
-  const int64_t grid = a.row_blocks * token_tiles(a, BN);
+  const int64_t grid = a.row_blocks * token_tiles(a, BN) * a.split;
   hipLaunchKernelGGL((tile_bf16_kernel<D, WR, WT, FR, FT>), dim3((unsigned)grid),
                      dim3(WR * WT * kWave), 0, stream, a);
   return hipGetLastError();
 }
 
 template <class D>
-hipError_t tile_bf16_any(const MatmulArgs& a, hipStream_t stream) {
-  return tile_bf16<D, 2, 4, 8, 4>(a, stream);
+hipError_t tile_bf16_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  switch (p.bn) {
+    case 32: return tile_bf16<D, 4, 1, 2, 2>(a, stream);
+    case 64: return tile_bf16<D, 2, 2, 4, 2>(a, stream);
+    case 128: return tile_bf16<D, 2, 2, 4, 4>(a, stream);
+    default: return tile_bf16<D, 2, 4, 8, 4>(a, stream);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_tile_mx_bf16(const MatmulArgs& a, hipStream_t stream) {
-  return tile_bf16_any<MxDecoder>(a, stream);
+hipError_t launch_tile_mx_bf16(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  return tile_bf16_any<MxDecoder>(a, p, stream);
 }
 
-hipError_t launch_tile_packed(const MatmulArgs& a, hipStream_t stream) {
-  return with_packed_decoder(a, [&](auto d) { return tile_bf16_any<decltype(d)>(a, stream); });
+hipError_t launch_tile_packed(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  return with_packed_decoder(a, [&](auto d) { return tile_bf16_any<decltype(d)>(a, p, stream); });
 }
 
-hipError_t launch_tile_mxfp4(const MatmulArgs& a, hipStream_t stream) {
-  return tile_mxfp4<2, 4, 8, 4>(a, stream);
+hipError_t launch_tile_mxfp4(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  switch (p.bn) {
+    case 64: return tile_mxfp4<2, 2, 4, 2>(a, stream);
+    case 128: return tile_mxfp4<2, 2, 4, 4>(a, stream);
+    default: return tile_mxfp4<2, 4, 8, 4>(a, stream);
+  }
 }
 
 }  // namespace aaac

@@ -41,14 +41,41 @@ struct MatmulArgs {
   void* y;                     // [T, R] of y_type, rows of ldy elements
   int y_type;
   int64_t ldy;
+  int y_vec;                   // four neighbours of a row go out in one store
+  int split;                   // workgroups that share a tile's columns; their sums lie in parts
+  float* parts;                // [split, T, part_row(R)], with split > 1
   int64_t row_blocks;          // set by the launcher: row blocks of one expert
-  int y_vec;                   // set by the launcher: four neighbours of a row go out in one store
 };
 
-hipError_t launch_tile_mx_bf16(const MatmulArgs& a, hipStream_t stream);
-hipError_t launch_tile_packed(const MatmulArgs& a, hipStream_t stream);
-hipError_t launch_tile_mxfp4(const MatmulArgs& a, hipStream_t stream);
-hipError_t launch_mxfp4_matmul(const MatmulArgs& a, bool x_mxfp4, hipStream_t stream);
-hipError_t launch_packed_matmul(const MatmulArgs& a, hipStream_t stream);
+__host__ __device__ __forceinline__ int64_t part_row(int64_t R) { return (R + 3) & ~(int64_t)3; }
+
+// Token tiles of BN rows that a call can need at most: every expert's last tile may be partial.
+inline int64_t token_tiles(const MatmulArgs& a, int BN) {
+  if (!a.offsets) return (a.T + BN - 1) / BN;
+  const int64_t e = a.E < a.T ? a.E : a.T;
+  return a.T / BN + e;
+}
+
+// How a call is run. bn == 0: the few-row kernels with rt x 16 weight rows by nt x 16 rows of x a
+// workgroup of `waves` waves. Else tiles of bm weight rows by bn rows of x, their columns split over
+// `split` workgroups.
+struct MatmulPlan {
+  int bm, bn, split;
+  int rt, nt, waves;
+};
+
+enum MatmulKind { kMxBf16, kMxMxfp4, kPacked };
+
+// can_split: a workspace for parts may be used.
+MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split);
+size_t parts_bytes(const MatmulArgs& a, const MatmulPlan& p);
+hipError_t launch_matmul(MatmulArgs a, MatmulKind kind, const MatmulPlan& p, hipStream_t stream);
+
+hipError_t launch_few_mxfp4(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
+hipError_t launch_few_mx_bf16(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
+hipError_t launch_few_packed(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
+hipError_t launch_tile_mxfp4(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
+hipError_t launch_tile_mx_bf16(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
+hipError_t launch_tile_packed(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
 
 }  // namespace aaac

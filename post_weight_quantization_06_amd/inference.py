@@ -62,8 +62,7 @@ def mxfp4_matmul(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
     if act == "bf16":
         L.aaac_mxfp4_matmul(codes, scales, C, x2, y2, offsets)
     elif act == "mxfp4":
-        xc, xs = mxfp4_quantize(x2)
-        L.aaac_mxfp4_matmul(codes, scales, C, xc, y2, offsets, xs)
+        L.aaac_mxfp4_matmul(codes, scales, C, x2, y2, offsets, None, L.QUANTIZE_X)
     else:
         raise ValueError("act must be 'bf16' or 'mxfp4' (got %r)" % (act,))
     return out
