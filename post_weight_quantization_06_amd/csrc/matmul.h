@@ -27,6 +27,38 @@ __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_
 // An offset past every such buffer, also with a row's columns added to it.
 constexpr uint32_t kOutside = 0x80000000u;
 
+typedef __attribute__((address_space(3))) void* LdsPtr;
+
+// rows_rsrc as the four words that an assembly operand takes.
+__device__ __forceinline__ u32x4 rows_buffer(const void* p, int64_t bytes) {
+  const uint64_t b = (uint64_t)p;
+  return u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)bytes, 0x00027000u};
+}
+
+// Any bytes as a buffer of whole words: the word that holds the first byte is word 0 and that byte
+// lies `lead` bytes into it. The last word may reach past the last byte, never past its own address.
+__device__ __forceinline__ u32x4 words_buffer(const void* p, int64_t bytes, uint32_t& lead) {
+  lead = (uint32_t)(uintptr_t)p & 3u;
+  return rows_buffer(static_cast<const uint8_t*>(p) - lead, (bytes + lead + 3) & ~(int64_t)3);
+}
+
+// Asynchronous loads from a buffer into LDS: lane l's bytes land at dst + l * size (dst uniform).
+// `more` is a uniform offset, kept out of what the hardware may or may not count when it checks the
+// range: rows are clamped by the caller, and kOutside is outside with or without it.
+// In assembly because the compiler would wait for them before any LDS read, of the other stage too;
+// the caller waits (stage_ready) before the barrier after which they are read. The move to m0 needs
+// one wait state before the load.
+__device__ __forceinline__ void load_lds16(u32x4 buf, uint32_t off, uint32_t more, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(dst), "v"(off), "s"(buf), "s"(more) : "memory");
+}
+__device__ __forceinline__ void load_lds4(u32x4 buf, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+               :: "s"(dst), "v"(off), "s"(buf) : "memory");
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(LdsPtr)(void*)p;
+}
 constexpr int kMfma = 16;                        // rows and columns of one matrix instruction
 
 // The expert and the rows [t0, t1) of token tile `tile` (uniform over the wave), or false past the
@@ -131,7 +163,8 @@ __device__ __forceinline__ f32x4 mfma_bf16(u32x4 w, u32x4 x, f32x4 c) {
 
 // ------------------------------------------------------------------------------------------------
 // Decoders: 4-bit weights to bf16, eight at a time. A kernel reads a weight row either by runs (32
-// consecutive columns a thread: the tiles, which pass the result on through LDS) or by chunks (128
+// consecutive columns a thread: the tiles, which stage codes, scale and selector words of a run in
+// LDS, `issue` and `fetch`, and pass the result on through LDS, `piece`) or by chunks (128
 // consecutive columns a wave row of four lane groups: the few-row kernels, which feed it to the
 // matrix instructions directly). In a chunk lane group q = lane >> 4 reads the 16 code bytes of run
 // q; a transposition over the four groups then leaves it with the codes of columns 32 p + 8 q ..
@@ -157,9 +190,12 @@ struct MxDecoder {
     const int64_t i = (int64_t)e * a.R + r;
     return {a.codes + i * (a.Cp >> 1), static_cast<const uint8_t*>(a.scales) + i * (a.Cp >> 5)};
   }
+  // 2^(b - 127): byte 0 is the subnormal 2^-127, byte 255 a NaN.
+  static __device__ __forceinline__ float value(uint32_t b) {
+    return __uint_as_float(b == 0 ? 0x00400000u : (b == 255u ? 0x7fc00000u : b << 23));
+  }
   static __device__ __forceinline__ u32x4 eight(uint32_t w, uint32_t b) {
-    // 2^(b - 127): byte 0 is the subnormal 2^-127, byte 255 a NaN
-    const float s = __uint_as_float(b == 0 ? 0x00400000u : (b == 255u ? 0x7fc00000u : b << 23));
+    const float s = value(b);
     const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
     const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
     const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
@@ -167,12 +203,31 @@ struct MxDecoder {
     return u32x4{pack_bf16(v0.x * s, v0.y * s), pack_bf16(v1.x * s, v1.y * s),
                  pack_bf16(v2.x * s, v2.y * s), pack_bf16(v3.x * s, v3.y * s)};
   }
-  __device__ __forceinline__ Run load_run(const MatmulArgs&, const Row& w, int64_t k) const {
-    return {*reinterpret_cast<const u32x4*>(w.codes + (k >> 1)), w.scales[k >> 5]};
+
+  static constexpr int kWords = 1;
+  u32x4 codes_buf, scales_buf;
+  uint32_t lead;                                 // bytes from the word that holds the first scale
+  __device__ __forceinline__ void init_tile(const MatmulArgs& a, int e, int64_t r0, int64_t nr) {
+    const int64_t i = (int64_t)e * a.R + r0, kb = a.Cp >> 5;
+    codes_buf = rows_buffer(a.codes + i * (a.Cp >> 1), nr * (a.Cp >> 1));
+    scales_buf = words_buffer(static_cast<const uint8_t*>(a.scales) + i * kb, nr * kb, lead);
   }
-  __device__ __forceinline__ void decode_run(const Run& u, u32x4 (&out)[4]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = eight(u.codes[j], u.byte);
+  // Loads of a run: columns 64 step + half .. + 31 of tile row `row`.
+  __device__ __forceinline__ void issue(const MatmulArgs& a, int row, int step, int half, bool in,
+                                        uint32_t dst, uint32_t words, int) const {
+    const uint32_t kb = (uint32_t)(a.Cp >> 5);
+    load_lds16(codes_buf, in ? row * (kb * 16) + half / 2 : kOutside, step * 32, dst);
+    load_lds4(scales_buf, in ? (lead + row * kb + 2 * step + half / 32) & ~3u : kOutside, words);
+  }
+  __device__ __forceinline__ Run fetch(const MatmulArgs& a, int row, int step, int half, bool,
+                                       const void* codes, const uint32_t* words, int) const {
+    const uint32_t at = lead + row * (uint32_t)(a.Cp >> 5) + 2 * step + half / 32;
+    return {*static_cast<const u32x4*>(codes), (*words >> (8 * (at & 3u))) & 0xffu};
+  }
+  struct Planes {};
+  struct Eight { u32x4 out; };
+  __device__ __forceinline__ void piece(const Run& u, int j, int n, Planes&, Eight& v) const {
+    if (n == 0) v.out = eight(u.codes[j], u.byte);
   }
   __device__ __forceinline__ Chunk load_chunk(const MatmulArgs&, const Row& w, int c, int q) const {
     Chunk u;
@@ -197,7 +252,7 @@ struct MxDecoder {
 };
 
 // Packed dual-codebook weights: bf16(|s| T_sel[q]). The two tables of 16 bf16 entries lie in
-// registers as planes of low and high bytes; a byte permute looks four codes up at once in eight
+// scalar registers as planes of low and high bytes, the second as its difference to the first; a byte permute looks four codes up at once in eight
 // entries, a second permute picks between the lower and the upper eight by bit 3 of the code, and a
 // third puts the two bytes of an entry where fp32 keeps them. One product and one rounding follow,
 // as in dequant.
@@ -210,9 +265,9 @@ struct PackedDecoder {
   static constexpr int kScaleBytes = LG >= 7 ? 2 : 256 >> LG;       // of a chunk
   static constexpr int kScaleWords = (kScaleBytes + 3) / 4;
   struct Row { const uint8_t* codes; const uint16_t* scales; int64_t first; };
-  struct Run { u32x4 codes; uint32_t scale[kGpl]; uint32_t bits, shift; };
+  struct Run { u32x4 codes; uint32_t scale[kGpl]; uint32_t bits, pick; };
   struct Chunk { u32x4 codes; uint32_t scale[kScaleWords]; uint32_t bits, shift; };
-  uint32_t lo[2][4], hi[2][4];
+  uint32_t lo[2][4], hi[2][4];                   // T0, and T0 ^ T1; uniform, in scalar registers
   const uint8_t* bitmap;
   int64_t bitmap_bytes;
 
@@ -230,9 +285,10 @@ struct PackedDecoder {
           l |= (b & 0xffu) << (8 * k);
           h |= (b >> 8) << (8 * k);
         }
-        asm volatile("" : "+v"(l), "+v"(h));     // vector registers: a permute reads two of them
-        lo[c][v] = l;
-        hi[c][v] = h;
+        l = __builtin_amdgcn_readfirstlane(l);
+        h = __builtin_amdgcn_readfirstlane(h);
+        lo[c][v] = c == 0 ? l : l ^ lo[0][v];
+        hi[c][v] = c == 0 ? h : h ^ hi[0][v];
       }
     }
     bitmap = kSign ? nullptr : a.bitmap + (int64_t)e * a.bitmap_stride;
@@ -244,65 +300,117 @@ struct PackedDecoder {
             kSign ? 0 : r * (a.C >> a.log2S)};
   }
   struct Planes { uint32_t L[4], H[4]; };
-  __device__ __forceinline__ Planes planes(bool one) const {
+  // The table of a selector in bit `bit` of word w, by a mask of that bit.
+  __device__ __forceinline__ Planes planes(uint32_t w, int bit) const {
+    const uint32_t one = (uint32_t)__builtin_amdgcn_sbfe((int)w, (uint32_t)bit, 1u);
     Planes p;
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      p.L[v] = one ? lo[1][v] : lo[0][v];
-      p.H[v] = one ? hi[1][v] : hi[0][v];
+      p.L[v] = lo[0][v] ^ (lo[1][v] & one);
+      p.H[v] = hi[0][v] ^ (hi[1][v] & one);
     }
     return p;
   }
-  static __device__ __forceinline__ u32x4 eight(uint32_t w, const Planes& t, uint32_t scale) {
-    const float s = __uint_as_float((scale & 0x7fffu) << 16);
-    uint32_t pl[2], ph[2];                       // entry bytes of the even and the odd columns
-#pragma unroll
-    for (int odd = 0; odd < 2; ++odd) {
-      const uint32_t idx = (odd ? w >> 4 : w) & 0x07070707u;
-      const uint32_t pick = ((odd ? w >> 5 : w >> 1) & 0x04040404u) | 0x03020100u;
-      pl[odd] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t.L[3], t.L[2], idx),
-                                      __builtin_amdgcn_perm(t.L[1], t.L[0], idx), pick);
-      ph[odd] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t.H[3], t.H[2], idx),
-                                      __builtin_amdgcn_perm(t.H[1], t.H[0], idx), pick);
+  // Eight weights in four parts of equal work, which a kernel can place between matrix instructions:
+  // the entry bytes of the even and of the odd columns, then two words of bf16 pairs twice.
+  // from: kPick, or 0x0c0c0c0c (zero bytes) with codes of zero for columns past the row's end.
+  static constexpr uint32_t kPick = 0x03020100u;
+  struct Eight { uint32_t l[2], h[2]; u32x4 out; };
+  static __device__ __forceinline__ void part(Eight& v, int n, uint32_t w, const Planes& t,
+                                              uint32_t scale, uint32_t from) {
+    if (n < 2) {
+      const uint32_t idx = (n ? w >> 4 : w) & 0x07070707u;
+      const uint32_t pick = ((n ? w >> 5 : w >> 1) & 0x04040404u) | from;
+      v.l[n] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t.L[3], t.L[2], idx),
+                                     __builtin_amdgcn_perm(t.L[1], t.L[0], idx), pick);
+      v.h[n] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t.H[3], t.H[2], idx),
+                                     __builtin_amdgcn_perm(t.H[1], t.H[0], idx), pick);
+      return;
     }
-    uint32_t o[4];
+    const float s = __uint_as_float((scale & 0x7fffu) << 16);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 2 * n - 4; p < 2 * n - 2; ++p) {
       // bytes: 0, 0, low, high (selector 12 is a zero byte; 0..3 index the low plane's word)
       const uint32_t sel = 0x00000c0cu | ((uint32_t)p << 16) | ((uint32_t)(4 + p) << 24);
-      const float ve = __uint_as_float(__builtin_amdgcn_perm(ph[0], pl[0], sel));
-      const float vo = __uint_as_float(__builtin_amdgcn_perm(ph[1], pl[1], sel));
-      o[p] = pack_bf16(ve * s, vo * s);
+      const float ve = __uint_as_float(__builtin_amdgcn_perm(v.h[0], v.l[0], sel));
+      const float vo = __uint_as_float(__builtin_amdgcn_perm(v.h[1], v.l[1], sel));
+      v.out[p] = pack_bf16(ve * s, vo * s);
     }
-    return u32x4{o[0], o[1], o[2], o[3]};
+  }
+  static __device__ __forceinline__ u32x4 eight(uint32_t w, const Planes& t, uint32_t scale,
+                                                uint32_t from) {
+    Eight v;
+#pragma unroll
+    for (int n = 0; n < 4; ++n) part(v, n, w, t, scale, from);
+    return v.out;
   }
 
-  // The words as loaded: nothing here waits for them.
-  __device__ __forceinline__ Run load_run(const MatmulArgs& a, const Row& w, int64_t k) const {
-    Run u;
-    u.codes = *reinterpret_cast<const u32x4*>(w.codes + (k >> 1));
-    const uint16_t* sp = w.scales + (k >> a.log2g);
-#pragma unroll
-    for (int i = 0; i < kGpl; ++i) u.scale[i] = sp[i];
+  static constexpr int kScaleLoads = (kGpl + 1) / 2;                // words with a run's scales
+  static constexpr int kWords = kScaleLoads + (kSign ? 0 : 1);
+  u32x4 codes_buf, scales_buf, bits_buf;
+  uint32_t lead, bits_lead;                      // see words_buffer; bits_lead in bits
+  __device__ __forceinline__ void init_tile(const MatmulArgs& a, int e, int64_t r0, int64_t nr) {
+    const int64_t i = (int64_t)e * a.R + r0, per = a.C >> a.log2g;
+    codes_buf = rows_buffer(a.codes + i * (a.C >> 1), nr * (a.C >> 1));
+    scales_buf = words_buffer(static_cast<const uint16_t*>(a.scales) + i * per, nr * per * 2, lead);
     if (!kSign) {
-      const int64_t h = w.first + (k >> a.log2S);
-      u.bits = bitmap[h >> 3];                   // the run's selectors lie in one byte
-      u.shift = (uint32_t)h & 7u;
+      const int64_t h = r0 * (a.C >> a.log2S), bits = nr * (a.C >> a.log2S) + (h & 7);
+      bits_buf = words_buffer(bitmap + (h >> 3), (bits + 7) >> 3, bits_lead);
+      bits_lead = 8 * bits_lead + (uint32_t)(h & 7);
     }
+  }
+  __device__ __forceinline__ uint32_t scale_at(const MatmulArgs& a, int row, int step,
+                                               int half) const {
+    const uint32_t g = LG >= 6 ? (step * 64) >> a.log2g : (step * 64 + half) >> a.log2g;
+    return lead + 2 * (row * (uint32_t)(a.C >> a.log2g) + g);
+  }
+  __device__ __forceinline__ uint32_t bit_at(const MatmulArgs& a, int row, int step, int half) const {
+    const uint32_t h = LS >= 6 ? (step * 64) >> a.log2S : (step * 64 + half) >> a.log2S;
+    return bits_lead + row * (uint32_t)(a.C >> a.log2S) + h;
+  }
+  __device__ __forceinline__ void issue(const MatmulArgs& a, int row, int step, int half, bool in,
+                                        uint32_t dst, uint32_t words, int threads) const {
+    load_lds16(codes_buf, in ? row * (uint32_t)(a.C >> 1) + half / 2 : kOutside, step * 32, dst);
+    const uint32_t at = scale_at(a, row, step, half) & ~3u;
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i)
+      load_lds4(scales_buf, in ? at + 4 * i : kOutside, words + i * threads * 4);
+    if (!kSign)
+      load_lds4(bits_buf, in ? (bit_at(a, row, step, half) >> 5) * 4 : kOutside,
+                words + kScaleLoads * threads * 4);
+  }
+  __device__ __forceinline__ Run fetch(const MatmulArgs& a, int row, int step, int half, bool in,
+                                       const void* codes, const uint32_t* words,
+                                       int threads) const {
+    Run u;
+    u.codes = *static_cast<const u32x4*>(codes);
+    u.pick = in ? kPick : 0x0c0c0c0cu;
+    const uint32_t at = scale_at(a, row, step, half);
+#pragma unroll
+    for (int i = 0; i < kScaleLoads; ++i) {
+      const uint32_t w = words[i * threads];
+      if (kGpl == 1) {
+        u.scale[0] = w >> (8 * (at & 2u));
+      } else {
+        u.scale[2 * i] = w;
+        u.scale[2 * i + 1] = w >> 16;
+      }
+    }
+    if (!kSign) u.bits = words[kScaleLoads * threads] >> (bit_at(a, row, step, half) & 31u);
     return u;
   }
-  __device__ __forceinline__ void decode_run(const Run& u, u32x4 (&out)[4]) const {
-    Planes t;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int gi = LG >= 5 ? 0 : (8 * j) >> LG, si = LS >= 5 ? 0 : (8 * j) >> LS;
+  // Part n of columns 8 j .. 8 j + 7 of a run, in ascending order; t carries the tables from one j
+  // to the next of the same selection group.
+  __device__ __forceinline__ void piece(const Run& u, int j, int n, Planes& t, Eight& v) const {
+    const int gi = LG >= 5 ? 0 : (8 * j) >> LG, si = LS >= 5 ? 0 : (8 * j) >> LS;
+    if (n == 0) {
       if (kSign) {
-        if (j == 0 || (LG < 5 && (8 * j) % (1 << LG) == 0)) t = planes((u.scale[gi] & 0x8000u) != 0);
+        if (j == 0 || (LG < 5 && (8 * j) % (1 << LG) == 0)) t = planes(u.scale[gi], 15);
       } else if (j == 0 || (LS < 5 && (8 * j) % (1 << LS) == 0)) {
-        t = planes(((u.bits >> (u.shift + si)) & 1u) != 0);
+        t = planes(u.bits, si);
       }
-      out[j] = eight(u.codes[j], t, u.scale[gi]);
     }
+    part(v, n, u.codes[j], t, u.scale[gi], u.pick);
   }
 
   __device__ __forceinline__ Chunk load_chunk(const MatmulArgs& a, const Row& w, int c, int q) const {
@@ -356,12 +464,12 @@ struct PackedDecoder {
       else if (LG == 4) s = u.scale[p] >> (16 * (q >> 1));
       else s = (q >> 1 ? u.scale[2 * p + 1] : u.scale[2 * p]) >> (16 * (q & 1));
       if (kSign) {
-        if (p == 0 || LG < 6 || (LG == 6 && p == 2)) t = planes((s & 0x8000u) != 0);
+        if (p == 0 || LG < 6 || (LG == 6 && p == 2)) t = planes(s, 15);
       } else if (p == 0 || LS < 6 || (LS == 6 && p == 2)) {
         const int i = LS >= 7 ? 0 : LS >= 5 ? (32 * p) >> LS : ((32 * p) >> LS) + ((8 * q) >> LS);
-        t = planes(((u.bits >> (u.shift + i)) & 1u) != 0);
+        t = planes(u.bits, (int)u.shift + i);
       }
-      out[p] = eight(w[p], t, s);
+      out[p] = eight(w[p], t, s, kPick);
     }
   }
 };

@@ -6,33 +6,19 @@ namespace aaac {
 
 namespace {
 
-typedef __attribute__((address_space(3))) void* LdsPtr;
-
-// rows_rsrc as the four words that an assembly operand takes.
-__device__ __forceinline__ u32x4 rows_buffer(const void* p, int64_t bytes) {
-  const uint64_t b = (uint64_t)p;
-  return u32x4{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)bytes, 0x00027000u};
+// At most N of this wave's loads are still under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
 }
-
-// Asynchronous loads from a buffer into LDS: lane l's bytes land at dst + l * size (dst uniform).
-// In assembly because the compiler would wait for them before any LDS read, of the other stage too;
-// the caller waits (stage_ready) before the barrier after which they are read. The move to m0 needs
-// one wait state before the load.
-__device__ __forceinline__ void load_lds16(u32x4 buf, uint32_t off, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(dst), "v"(off), "s"(buf) : "memory");
-}
-__device__ __forceinline__ void load_lds4(u32x4 buf, uint32_t off, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :: "s"(dst), "v"(off), "s"(buf) : "memory");
-}
-__device__ __forceinline__ uint32_t lds_address(const void* p) {
-  return (uint32_t)(uintptr_t)(LdsPtr)(void*)p;
-}
-// This wave's loads have landed; after the barrier every wave's have.
-__device__ __forceinline__ void stage_ready() {
-  __builtin_amdgcn_s_waitcnt(0x0f70);           // vmcnt(0)
-  __syncthreads();
+// After it, every wave's LDS writes, and the loads it waited for, can be read.
+__device__ __forceinline__ void step_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);            // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // Workgroups go to the eight dies in turn; numbering them so that a die gets consecutive tiles lets
@@ -51,7 +37,7 @@ __device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
 // column of pieces over all banks.
 // ------------------------------------------------------------------------------------------------
 template <int WR, int WT, int FR, int FT, bool WHOLE>
-__global__ __launch_bounds__(WR * WT * kWave, 1) void tile_mxfp4_kernel(MatmulArgs a) {
+__global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulArgs a) {
   constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma;
   constexpr int kW = BM * 128, kX = BN * 128, kWs = BM * 8, kXs = BN * 8;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kW + kX + kWs + kXs];
@@ -83,12 +69,12 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_mxfp4_kernel(MatmulAr
 #pragma unroll
     for (int i = 0; i < BM / 8 / NW; ++i) {
       const int row = (wave * (BM / 8 / NW) + i) * 8;
-      load_lds16(wr, in ? off0 + row * (uint32_t)row_bytes : kOutside, dst + row * 128);
+      load_lds16(wr, in ? off0 + row * (uint32_t)row_bytes : kOutside, 0, dst + row * 128);
     }
 #pragma unroll
     for (int i = 0; i < BN / 8 / NW; ++i) {
       const int row = (wave * (BN / 8 / NW) + i) * 8;
-      load_lds16(xr, in ? off0 + row * (uint32_t)row_bytes : kOutside, dst + kW + row * 128);
+      load_lds16(xr, in ? off0 + row * (uint32_t)row_bytes : kOutside, 0, dst + kW + row * 128);
     }
     if (WHOLE) {
       const uint32_t soff = (uint32_t)(lane >> 1) * (uint32_t)kb + (uint32_t)(kt * 8) + 4 * (lane & 1);
@@ -123,38 +109,67 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_mxfp4_kernel(MatmulAr
   const int l = lane & 15, q = lane >> 4;
   const int64_t all = (kb + 7) / 8, first = all * part / a.split;
   const int64_t steps = all * (part + 1) / a.split;
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  u32x4 wf[FR], xf[2][FT];
+  uint32_t sw[FR], sx[2][FT];                    // scale words
+#pragma unroll
+  for (int i = 0; i < FR; ++i) {
+    wf[i] = zero;
+    sw[i] = 0;
+  }
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    xf[1][j] = zero;
+    sx[1][j] = 0;
+  }
   load(0, first);
   for (int64_t kt = first; kt < steps; ++kt) {
     const int buf = (int)((kt - first) & 1);
-    stage_ready();
+    wait_loads<0>();
+    step_barrier();
     if (kt + 1 < steps) load(buf ^ 1, kt + 1);
     const uint8_t* base = lds[buf];
-    uint32_t sw[FR], sx[FT];
+    const uint8_t* wb = base + (wm + l) * 128;
+    const uint8_t* wsb = base + kW + kX + (wm + l) * 8 + 2 * q;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int i = 0; i < FR; ++i)
-      sw[i] = *reinterpret_cast<const uint16_t*>(base + kW + kX + (wm + i * kMfma + l) * 8 + 2 * q);
-#pragma unroll
-    for (int j = 0; j < FT; ++j)
-      sx[j] = *reinterpret_cast<const uint16_t*>(base + kW + kX + kWs + (wn + j * kMfma + l) * 8 +
-                                                 2 * q);
+    for (int j = 0; j < FT; ++j) {
+      sx[0][j] = sx[1][j];
+      sx[1][j] = *reinterpret_cast<const uint16_t*>(base + kW + kX + kWs + (wn + j * kMfma + l) * 8 +
+                                                    2 * q);
+    }
+    // half 0 of the pass: instructions of the step before, on its second half's fragments, while
+    // this step's first half is read; half 1: this step's first half, while its second is read
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      u32x4 wf[FR], xf[FT];
       const int p = ((2 * q + h) ^ (l & 7)) * 16;
 #pragma unroll
-      for (int i = 0; i < FR; ++i)
-        wf[i] = *reinterpret_cast<const u32x4*>(base + (wm + i * kMfma + l) * 128 + p);
-#pragma unroll
       for (int j = 0; j < FT; ++j)
-        xf[j] = *reinterpret_cast<const u32x4*>(base + kW + (wn + j * kMfma + l) * 128 + p);
+        xf[h][j] = *reinterpret_cast<const u32x4*>(base + kW + (wn + j * kMfma + l) * 128 + p);
 #pragma unroll
-      for (int i = 0; i < FR; ++i)
+      for (int i = 0; i < FR; ++i) {
+        // the registers of the group before
+        if (i > 0) {
+          wf[i - 1] = *reinterpret_cast<const u32x4*>(wb + (i - 1) * kMfma * 128 + p);
+          if (h == 0) sw[i - 1] = *reinterpret_cast<const uint16_t*>(wsb + (i - 1) * kMfma * 8);
+        } else if (h == 1) {
+          wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (p ^ 16));
+          sw[FR - 1] = *reinterpret_cast<const uint16_t*>(wsb + (FR - 1) * kMfma * 8);
+        }
 #pragma unroll
         for (int j = 0; j < FT; ++j)
-          acc[i][j] = h == 0 ? mfma_fp4<0>(wf[i], xf[j], acc[i][j], sw[i], sx[j])
-                             : mfma_fp4<1>(wf[i], xf[j], acc[i][j], sw[i], sx[j]);
+          acc[i][j] = h == 0 ? mfma_fp4<1>(wf[i], xf[1][j], acc[i][j], sw[i], sx[0][j])
+                             : mfma_fp4<0>(wf[i], xf[0][j], acc[i][j], sw[i], sx[1][j]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+    wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (((2 * q + 1) ^ (l & 7)) * 16));
   }
+#pragma unroll
+  for (int i = 0; i < FR; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j)
+      acc[i][j] = mfma_fp4<1>(wf[i], xf[1][j], acc[i][j], sw[i], sx[1][j]);
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int64_t t = t0 + wn + j * kMfma + l;
@@ -184,18 +199,25 @@ hipError_t tile_mxfp4(MatmulArgs a, hipStream_t stream) {
 
 // ------------------------------------------------------------------------------------------------
 // bf16 x times decoded weights. A step takes 64 columns (128 bytes of bf16 a row). Two threads share
-// a weight row of the tile: each reads a run of 32 columns (16 bytes of codes) straight into
-// registers, decodes it and writes it to LDS as bf16, one step ahead of its use, so a weight is
-// decoded once per tile. Rows of x go to LDS unchanged. Both lie permuted as above. Instruction
-// h of a step takes pieces 4 h + q (columns 32 h + 8 q ..) of a row.
+// a weight row of the tile, a run of 32 columns each: a thread decodes its run and writes it to LDS
+// as bf16 one step ahead of its use, so a weight is decoded once per tile. Rows of x go to LDS
+// unchanged. Both lie permuted as above. Instruction h of a step takes pieces 4 h + q (columns
+// 32 h + 8 q ..) of a row.
+// Memory is NS - 1 steps ahead: group j of asynchronous loads holds x of step j and the codes and
+// scales of step j + 1, and at most NS - 2 younger groups are in flight when a step begins. Loads
+// past the last step lie outside their buffers, so every group has the same count.
+// Fragments are one half step ahead of the matrix instructions: a barrier falls between the two
+// halves of a step's instructions, and each register is read again as soon as it has been used.
 // ------------------------------------------------------------------------------------------------
-template <class D, int WR, int WT, int FR, int FT>
-__global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArgs a) {
-  constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma;
-  static_assert(NW * kWave == 2 * BM, "two threads a weight row");
+template <class D, int WR, int WT, int FR, int FT, int NS>
+__global__ __launch_bounds__(WR * WT * kWave, 2) void tile_bf16_kernel(MatmulArgs a) {
+  constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma, kThreads = NW * kWave;
+  static_assert(kThreads == 2 * BM, "two threads a weight row");
   static_assert(BN % (8 * NW) == 0, "whole loads of x a wave");
-  constexpr int kW = BM * 128, kX = BN * 128;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kW + kX];
+  constexpr int kW = BM * 128, kX = BN * 128, kC = kThreads * 16, kS = D::kWords * kThreads * 4;
+  constexpr int kSlot = kX + kC + kS;
+  constexpr int kLoads = BN / 8 / NW + 1 + D::kWords;        // a wave's loads in a group
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kW + NS * kSlot];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
   const int64_t id = by_die(blockIdx.x, gridDim.x), tiles = gridDim.x / a.split;
   const int part = (int)(id / tiles);
@@ -205,39 +227,54 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
   if (!find_tile(a.offsets, a.E, a.T, BN, tile, e, t0, t1)) return;
   const int64_t r0 = rb * BM;
   const int64_t x_bytes = a.ldx * 2;
-  const int64_t nt = t1 - t0 < BN ? t1 - t0 : BN;
+  const int64_t nt = t1 - t0 < BN ? t1 - t0 : BN, nr = a.R - r0 < BM ? a.R - r0 : BM;
   const u32x4 xr = rows_buffer(static_cast<const uint8_t*>(a.x) + t0 * x_bytes,
                                (nt - 1) * x_bytes + a.C * 2);
-  const uint32_t lds0 = lds_address(&lds[0][0]);
-  const int piece = (lane & 7) ^ (lane >> 3);
-  auto load_x = [&](int buf, int64_t kt) {
-    const uint32_t dst = lds0 + buf * (kW + kX) + kW;
-    const uint32_t off0 =
-        (uint32_t)(lane >> 3) * (uint32_t)x_bytes + (uint32_t)(kt * 128) + piece * 16;
-    const bool in = kt * 64 + piece * 8 < a.C;
-#pragma unroll
-    for (int i = 0; i < BN / 8 / NW; ++i) {
-      const int row = (wave * (BN / 8 / NW) + i) * 8;
-      load_lds16(xr, in ? off0 + row * (uint32_t)x_bytes : kOutside, dst + row * 128);
-    }
-  };
   D dec;
   dec.init(a, e);
-  const int wrow = tid >> 1, half = tid & 1;
-  const typename D::Row wp = dec.row(a, e, r0 + wrow < a.R ? r0 + wrow : a.R - 1);
-  auto load_w = [&](int64_t kt) {
-    const int64_t k = kt * 64 + half * 32;
-    return dec.load_run(a, wp, k < a.Cp ? k : 0);
-  };
-  auto put_w = [&](int buf, int64_t kt, const typename D::Run& u) {
-    u32x4 v[4];
-    dec.decode_run(u, v);
-    const bool in = kt * 64 + half * 32 < a.Cp;  // columns past the row's end: zero times zero
-    uint8_t* p = lds[buf] + wrow * 128;
+  dec.init_tile(a, e, r0, nr);
+  const uint32_t slots = lds_address(&lds[2 * kW]);
+  const int piece = (lane & 7) ^ (lane >> 3);
+  // the weight row that this thread decodes; rows past the matrix repeat its last one
+  const int wrow = tid >> 1, half = 32 * (tid & 1);
+  const int mrow = wrow < nr ? wrow : (int)nr - 1;
+  const int all = (int)((a.Cp + 63) / 64);
+  const int first = (int)((int64_t)all * part / a.split);
+  const int steps = (int)((int64_t)all * (part + 1) / a.split);
+  const int cols = (int)a.C, wcols = (int)a.Cp;
+  constexpr int kXl = BN / 8 / NW;
+  uint32_t xoff[kXl];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<u32x4*>(p + (((4 * half + j) ^ (wrow & 7)) * 16)) =
-          in ? v[j] : u32x4{0u, 0u, 0u, 0u};
+  for (int i = 0; i < kXl; ++i) {
+    const int row = (wave * kXl + i) * 8 + (lane >> 3);
+    xoff[i] = (uint32_t)(row < nt ? row : (int)nt - 1) * (uint32_t)x_bytes + piece * 16;
+  }
+  auto load_w = [&](int slot, int kt) {
+    const uint32_t dst = slots + slot * kSlot + kX;
+    dec.issue(a, mrow, kt, half, kt < steps && kt * 64 + half < wcols, dst + wave * (kWave * 16),
+              dst + kC + wave * (kWave * 4), kThreads);
+  };
+  auto load_group = [&](int slot, int kt) {
+    const uint32_t dst = slots + slot * kSlot + wave * kXl * 1024;
+    if (kt < steps && kt * 64 + 64 <= cols) {
+#pragma unroll
+      for (int i = 0; i < kXl; ++i) load_lds16(xr, xoff[i], kt * 128, dst + i * 1024);
+    } else {
+      const bool in = kt < steps && kt * 64 + piece * 8 < cols;
+#pragma unroll
+      for (int i = 0; i < kXl; ++i)
+        load_lds16(xr, in ? xoff[i] : kOutside, kt * 128, dst + i * 1024);
+    }
+    load_w(slot, kt + 1);
+  };
+  auto fetch = [&](int slot, int kt) {
+    const uint8_t* p = lds + 2 * kW + slot * kSlot + kX;
+    return dec.fetch(a, mrow, kt, half, kt < steps && kt * 64 + half < wcols, p + tid * 16,
+                     reinterpret_cast<const uint32_t*>(p + kC) + tid, kThreads);
+  };
+  auto put = [&](int buf, int j, u32x4 v) {
+    uint8_t* p = lds + buf * kW + wrow * 128;
+    *reinterpret_cast<u32x4*>(p + (((half / 8 + j) ^ (wrow & 7)) * 16)) = v;
   };
 
   f32x4 acc[FR][FT];
@@ -247,42 +284,74 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
     for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int wm = (wave / WT) * FR * kMfma, wn = (wave % WT) * FT * kMfma;
   const int l = lane & 15, q = lane >> 4;
-  const int64_t all = (a.Cp + 63) / 64, first = all * part / a.split;
-  const int64_t steps = all * (part + 1) / a.split;
-  auto multiply = [&](int buf) {
-    const uint8_t* base = lds[buf];
+
+  load_w(NS - 1, first);
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) load_group(s, first + s);
+  wait_loads<(NS - 1) * kLoads>();
+  {
+    typename D::Planes t;
+    const typename D::Run u = fetch(NS - 1, first);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      typename D::Eight v;
+#pragma unroll
+      for (int n = 0; n < 4; ++n) dec.piece(u, j, n, t, v);
+      put(0, j, v.out);
+    }
+  }
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  u32x4 wf[FR], xf[2][FT];
+#pragma unroll
+  for (int i = 0; i < FR; ++i) wf[i] = zero;
+#pragma unroll
+  for (int j = 0; j < FT; ++j) xf[1][j] = zero;
+  int slot = 0;
+  for (int kt = first; kt < steps; ++kt) {
+    const int buf = (kt - first) & 1;
+    wait_loads<(NS - 2) * kLoads>();
+    step_barrier();
+    load_group(slot == 0 ? NS - 1 : slot - 1, kt + NS - 1);
+    typename D::Planes t;
+    typename D::Eight v;
+    const typename D::Run u = fetch(slot, kt + 1);
+    const uint8_t* wb = lds + buf * kW + (wm + l) * 128;
+    const uint8_t* xb = lds + 2 * kW + slot * kSlot + (wn + l) * 128;
+    __builtin_amdgcn_sched_barrier(0);
+    // half 0 of the pass: instructions of the step before, on its second half's fragments, while
+    // this step's first half is read; half 1: this step's first half, while its second is read
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      u32x4 wf[FR], xf[FT];
       const int p = ((4 * h + q) ^ (l & 7)) * 16;
 #pragma unroll
-      for (int i = 0; i < FR; ++i)
-        wf[i] = *reinterpret_cast<const u32x4*>(base + (wm + i * kMfma + l) * 128 + p);
-#pragma unroll
       for (int j = 0; j < FT; ++j)
-        xf[j] = *reinterpret_cast<const u32x4*>(base + kW + (wn + j * kMfma + l) * 128 + p);
+        xf[h][j] = *reinterpret_cast<const u32x4*>(xb + j * kMfma * 128 + p);
 #pragma unroll
-      for (int i = 0; i < FR; ++i)
+      for (int i = 0; i < FR; ++i) {
+        // the registers of the group before
+        if (i > 0) wf[i - 1] = *reinterpret_cast<const u32x4*>(wb + (i - 1) * kMfma * 128 + p);
+        else if (h == 1) wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (p ^ 64));
 #pragma unroll
-        for (int j = 0; j < FT; ++j) acc[i][j] = mfma_bf16(wf[i], xf[j], acc[i][j]);
+        for (int j = 0; j < FT; ++j) acc[i][j] = mfma_bf16(wf[i], xf[h ^ 1][j], acc[i][j]);
+        // the decoding in sixteen parts beside the instructions; the barriers keep the compiler
+        // from gathering the reads, or the vector work, of several parts
+        constexpr int kParts = 8 / FR;
+#pragma unroll
+        for (int n = 0; n < kParts; ++n) {
+          const int w = (h * FR + i) * kParts + n;
+          dec.piece(u, w / 4, w % 4, t, v);
+          if (w % 4 == 3) put(buf ^ 1, w / 4, v.out);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-  };
-
-  typename D::Run now = load_w(first);
-  load_x(0, first);
-  put_w(0, first, now);
-  if (first + 1 < steps) now = load_w(first + 1);
-  for (int64_t kt = first; kt < steps; ++kt) {
-    const int buf = (int)((kt - first) & 1);
-    stage_ready();
-    const bool more = kt + 1 < steps;
-    typename D::Run next = now;
-    if (more) load_x(buf ^ 1, kt + 1);
-    if (kt + 2 < steps) next = load_w(kt + 2);
-    multiply(buf);
-    if (more) put_w(buf ^ 1, kt + 1, now);
-    now = next;
+    wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (((4 + q) ^ (l & 7)) * 16));
+    slot = slot + 1 == NS ? 0 : slot + 1;
   }
+#pragma unroll
+  for (int i = 0; i < FR; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[i][j] = mfma_bf16(wf[i], xf[1][j], acc[i][j]);
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int64_t t = t0 + wn + j * kMfma + l;
@@ -295,12 +364,12 @@ __global__ __launch_bounds__(WR * WT * kWave, 1) void tile_bf16_kernel(MatmulArg
   }
 }
 
-template <class D, int WR, int WT, int FR, int FT>
+template <class D, int WR, int WT, int FR, int FT, int NS>
 hipError_t tile_bf16(MatmulArgs a, hipStream_t stream) {
   constexpr int BM = WR * FR * kMfma, BN = WT * FT * kMfma;
   a.row_blocks = (a.R + BM - 1) / BM;
   const int64_t grid = a.row_blocks * token_tiles(a, BN) * a.split;
-  hipLaunchKernelGGL((tile_bf16_kernel<D, WR, WT, FR, FT>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((tile_bf16_kernel<D, WR, WT, FR, FT, NS>), dim3((unsigned)grid),
                      dim3(WR * WT * kWave), 0, stream, a);
   return hipGetLastError();
 }
@@ -308,10 +377,10 @@ hipError_t tile_bf16(MatmulArgs a, hipStream_t stream) {
 template <class D>
 hipError_t tile_bf16_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
   switch (p.bn) {
-    case 32: return tile_bf16<D, 4, 1, 2, 2>(a, stream);
-    case 64: return tile_bf16<D, 2, 2, 4, 2>(a, stream);
-    case 128: return tile_bf16<D, 2, 2, 4, 4>(a, stream);
-    default: return tile_bf16<D, 2, 4, 8, 4>(a, stream);
+    case 32: return tile_bf16<D, 4, 1, 2, 2, 4>(a, stream);
+    case 64: return tile_bf16<D, 2, 2, 4, 2, 3>(a, stream);
+    case 128: return tile_bf16<D, 2, 2, 4, 4, 2>(a, stream);
+    default: return tile_bf16<D, 2, 4, 8, 4, 2>(a, stream);
   }
 }
 
