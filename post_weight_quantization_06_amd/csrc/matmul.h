@@ -59,6 +59,21 @@ __device__ __forceinline__ void load_lds4(u32x4 buf, uint32_t off, uint32_t dst)
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(LdsPtr)(void*)p;
 }
+// At most N of this wave's loads are still under way.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N < 64, "six bits");
+  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
+  asm volatile("" ::: "memory");
+}
+// After it, every wave's LDS writes, and the loads it waited for, can be read.
+__device__ __forceinline__ void step_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xc07f);            // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 constexpr int kMfma = 16;                        // rows and columns of one matrix instruction
 
 // The expert and the rows [t0, t1) of token tile `tile` (uniform over the wave), or false past the
@@ -180,8 +195,18 @@ __device__ __forceinline__ u32x4 over_groups(u32x4 v) {
   return u32x4{c.x, c.y, d.x, d.y};
 }
 
+// Word p of the result: v of lane group p.
+__device__ __forceinline__ u32x4 from_groups(uint32_t v) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  const u32x2 a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  const u32x2 c = __builtin_amdgcn_permlane16_swap(a.x, a.x, false, false);
+  const u32x2 d = __builtin_amdgcn_permlane16_swap(a.y, a.y, false, false);
+  return u32x4{c.x, c.y, d.x, d.y};
+}
+
 // MXFP4: a run is one block; code times power of two is exact in bf16 (and in fp32 before it).
 struct MxDecoder {
+  static constexpr bool kFour = true;            // see load_four
   struct Row { const uint8_t* codes; const uint8_t* scales; };
   struct Run { u32x4 codes; uint32_t byte; };
   struct Chunk { u32x4 codes; uint32_t bytes; };
@@ -235,6 +260,21 @@ struct MxDecoder {
     __builtin_memcpy(&u.bytes, w.scales + c * 4, 4);
     return u;
   }
+  // Four chunks at once, the scales of chunk q read by lane group q: `Four` as loaded, `chunk` one of
+  // them.
+  struct Four { u32x4 codes[4]; uint32_t bytes; };
+  __device__ __forceinline__ Four load_four(const MatmulArgs&, const Row& w, int c, int q) const {
+    Four u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u.codes[i] = *reinterpret_cast<const u32x4*>(w.codes + (int64_t)(c + i) * 64 + 16 * q);
+    __builtin_memcpy(&u.bytes, w.scales + (c + q) * 4, 4);
+    return u;
+  }
+  static __device__ __forceinline__ Chunk chunk(const Four& u, const u32x4& bytes, int i) {
+    return {u.codes[i], bytes[i]};
+  }
+  static __device__ __forceinline__ u32x4 spread(const Four& u) { return from_groups(u.bytes); }
   // The row's last chunk: runs at or past its end are zeros.
   __device__ __forceinline__ Chunk load_last(const MatmulArgs& a, const Row& w, int c, int q) const {
     Chunk u = {u32x4{0u, 0u, 0u, 0u}, 0u};
@@ -261,6 +301,7 @@ struct MxDecoder {
 template <int LG, int LS>
 struct PackedDecoder {
   static constexpr bool kSign = LS == 0;
+  static constexpr bool kFour = kSign && LG >= 6;                   // see load_four
   static constexpr int kGpl = LG >= 5 ? 1 : 32 >> LG;               // scale groups in a run
   static constexpr int kScaleBytes = LG >= 7 ? 2 : 256 >> LG;       // of a chunk
   static constexpr int kScaleWords = (kScaleBytes + 3) / 4;
@@ -421,6 +462,26 @@ struct PackedDecoder {
     else __builtin_memcpy(u.scale, sp, kScaleBytes);
     if (!kSign) load_bits(a, w, c, u);
     return u;
+  }
+  // Four chunks at once (scale groups of 64 and more, selectors in the sign): lane group q reads the
+  // scales of chunk q.
+  struct Four { u32x4 codes[4]; uint32_t scale; };
+  __device__ __forceinline__ Four load_four(const MatmulArgs& a, const Row& w, int c, int q) const {
+    Four u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u.codes[i] = *reinterpret_cast<const u32x4*>(w.codes + (int64_t)(c + i) * 64 + 16 * q);
+    const uint16_t* sp = w.scales + (((int64_t)(c + q) * 128) >> a.log2g);
+    if (LG >= 7) u.scale = sp[0];
+    else __builtin_memcpy(&u.scale, sp, 4);
+    return u;
+  }
+  static __device__ __forceinline__ u32x4 spread(const Four& u) { return from_groups(u.scale); }
+  static __device__ __forceinline__ Chunk chunk(const Four& u, const u32x4& scales, int i) {
+    Chunk v;
+    v.codes = u.codes[i];
+    v.scale[0] = scales[i];
+    return v;
   }
   // The selectors of a chunk as the low bits of bits >> shift: four bytes from the first one's, or
   // the four last bytes of this matrix's map where those would end past it.

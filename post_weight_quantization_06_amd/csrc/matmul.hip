@@ -34,16 +34,17 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
   {
     auto v = [](const char* n, int d) { const char* s = getenv(n); return s ? atoi(s) : d; };
     p.bn = v("BN", 0); p.bm = p.bn == 256 ? 256 : 128; p.split = can_split ? v("SPLIT", 1) : 1;
-    p.rt = v("RT", 1); p.nt = v("NT", 1); p.waves = v("WAVES", 8);
+    p.rt = v("RT", 1); p.nt = v("NT", 1); p.waves = v("WAVES", 8); p.chunks = v("U", 4);
     return p;
   }
 #endif
   const bool fp4 = kind == kMxMxfp4;
-  if (rows <= (fp4 ? 64 : 32)) {
+  if (rows <= (fp4 ? 64 : kMfma)) {
     p.nt = (int)((rows + kMfma - 1) / kMfma);
     const int64_t blocks = (a.R + kMfma - 1) / kMfma * (a.E < a.T ? a.E : a.T);
     p.rt = blocks > 512 ? 2 : 1;
     p.waves = blocks > 256 ? 8 : 16;
+    p.chunks = a.C >= 512 * p.waves ? 4 : 1;
     return p;
   }
   p.bn = rows <= 64 ? 64 : rows <= 512 ? 128 : 256;

@@ -12,43 +12,75 @@ namespace aaac {
 
 namespace {
 
-// Adds the waves' sums acc[RT][NT] in wave order and stores them.
+template <bool B, class X, class Y> struct Pick { typedef X type; };
+template <class X, class Y> struct Pick<false, X, Y> { typedef Y type; };
+
+constexpr int64_t kXLds = 64 << 10;              // LDS bytes for rows of x
+
+// Adds the waves' sums acc[RT][NT] in wave order and stores them. red: join_bytes of LDS.
+template <int RT, int NT, int W>
+constexpr int join_bytes() { return W * NT * kMfma * (RT * kMfma + 4) * 4; }
 template <int RT, int NT, int W>
 __device__ __forceinline__ void join_and_store(const MatmulArgs& a, const f32x4 (&acc)[RT][NT],
-                                               int64_t r0, int64_t t0, int64_t t1) {
-  constexpr int kRowsPad = RT * kMfma + 4;       // floats between x rows
-  __shared__ float red[W][NT * kMfma][kRowsPad];
+                                               int64_t r0, int64_t t0, int64_t t1, float* red) {
+  constexpr int kRow = RT * kMfma + 4;           // floats between x rows
+  constexpr int kPart = NT * kMfma * kRow;       // and between waves
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      *reinterpret_cast<f32x4*>(&red[wave][j * kMfma + (lane & 15)][i * kMfma + 4 * (lane >> 4)]) =
-          acc[i][j];
+      *reinterpret_cast<f32x4*>(red + wave * kPart + (j * kMfma + (lane & 15)) * kRow + i * kMfma +
+                                4 * (lane >> 4)) = acc[i][j];
   __syncthreads();
   for (int u = tid; u < NT * kMfma * RT * 4; u += W * kWave) {
     const int t = u / (RT * 4), r = 4 * (u % (RT * 4));
-    f32x4 v = *reinterpret_cast<const f32x4*>(&red[0][t][r]);
+    const float* p = red + t * kRow + r;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p);
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += *reinterpret_cast<const f32x4*>(&red[w][t][r]);
+    for (int w = 1; w < W; ++w) v += *reinterpret_cast<const f32x4*>(p + w * kPart);
     if (t0 + t < t1 && r0 + r < a.R) store4(a, t0 + t, r0 + r, v);
   }
 }
 
+// Bytes between the rows of x in LDS: whole 1 KB pieces, and 16 more to spread a column over banks.
+__host__ __device__ __forceinline__ int64_t x_row_bytes(int64_t C) {
+  return (2 * C + 1023) / 1024 * 1024 + 16;
+}
+
 // ------------------------------------------------------------------------------------------------
 // bf16 rows of x times decoded weights. Instruction p of a chunk of 128 columns takes columns
-// 32 p + 8 q .. 32 p + 8 q + 7 from lane group q, so a load of x reads 64 neighbouring bytes of each
-// row. The chunks go to the waves in turn, U at a time, so that U loads of each weight row are in
-// flight. Rows past the tile's last lie outside the x buffer and load as zeros.
+// 32 p + 8 q .. 32 p + 8 q + 7 from lane group q. U chunks in a row go to one wave, the groups of U
+// to the waves in turn, the loads of a wave's next group under way while it uses one. The count of
+// load instructions bounds this kernel before their bytes do, hence one scale load for four chunks
+// (U = 4), and x in LDS where the tile's rows fit into a.x_rows of them; otherwise x is read
+// directly, 64 neighbouring bytes a row, and rows past the tile's last load as zeros.
 // ------------------------------------------------------------------------------------------------
 template <class D, int RT, int NT, int W, int U>
 __global__ __launch_bounds__(W * kWave, 1) void few_bf16_kernel(MatmulArgs a) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
   const int64_t tile = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
   int e;
   int64_t t0, t1;
   if (!find_tile(a.offsets, a.E, a.T, NT * kMfma, tile, e, t0, t1)) return;
   const int64_t r0 = rb * (RT * kMfma);
+  const int nt = (int)(t1 - t0 < NT * kMfma ? t1 - t0 : NT * kMfma);
+  const int64_t x_bytes = (nt - 1) * a.ldx * 2 + a.C * 2;
+  const void* x0 = static_cast<const uint16_t*>(a.x) + t0 * a.ldx;
+  const int xstride = (int)x_row_bytes(a.C);
+  const bool in_lds = nt <= a.x_rows;
+  if (in_lds) {
+    const u32x4 xb = rows_buffer(x0, x_bytes);
+    const uint32_t base = lds_address(smem);
+    const int pieces = xstride / 1024;
+    for (int i = wave; i < nt * pieces; i += W) {
+      const int row = i / pieces, col = (i % pieces) * 512 + lane * 8;
+      load_lds16(xb, col < a.C ? (uint32_t)(row * a.ldx + col) * 2 : kOutside, 0,
+                 base + row * xstride + (i % pieces) * 1024);
+    }
+  }
+  const __amdgpu_buffer_rsrc_t xr = rows_rsrc(x0, x_bytes);
   D dec;
   dec.init(a, e);
   typename D::Row w[RT];
@@ -57,15 +89,16 @@ __global__ __launch_bounds__(W * kWave, 1) void few_bf16_kernel(MatmulArgs a) {
     const int64_t r = r0 + i * kMfma + (lane & 15);
     w[i] = dec.row(a, e, r < a.R ? r : a.R - 1);
   }
-  const int64_t nt = t1 - t0 < NT * kMfma ? t1 - t0 : NT * kMfma;
-  const __amdgpu_buffer_rsrc_t xr = rows_rsrc(
-      static_cast<const uint16_t*>(a.x) + t0 * a.ldx, (nt - 1) * a.ldx * 2 + a.C * 2);
   const int q = lane >> 4;
+  // where this lane's 16 bytes of x rows start: in LDS rows past the last repeat it
   uint32_t xoff[NT];
+  const uint8_t* xlds[NT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j)
-    xoff[j] = j * kMfma + (lane & 15) < nt
-                  ? (uint32_t)(((j * kMfma + (lane & 15)) * a.ldx + 8 * q) * 2) : kOutside;
+  for (int j = 0; j < NT; ++j) {
+    const int t = j * kMfma + (lane & 15);
+    xoff[j] = t < nt ? (uint32_t)((t * a.ldx + 8 * q) * 2) : kOutside;
+    xlds[j] = smem + (t < nt ? t : nt - 1) * xstride + 16 * q;
+  }
   f32x4 acc[RT][NT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -73,57 +106,89 @@ __global__ __launch_bounds__(W * kWave, 1) void few_bf16_kernel(MatmulArgs a) {
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const u32x4 zero = {0u, 0u, 0u, 0u};
 
-  const int whole = (int)(a.C >> 7);             // chunks whose every run lies in the row
-  auto chunks = [&](int c, auto n) {
-    constexpr int N = decltype(n)::value;
-    typename D::Chunk u[N][RT];
-    u32x4 x[N][NT][4];
+  // one chunk's products; `cut`: columns at or past the row's end are zero times zero
+  auto multiply = [&](int c, const typename D::Chunk (&u)[RT], auto from_lds, bool cut)
+      __attribute__((always_inline)) {
+    u32x4 x[NT][4];
 #pragma unroll
-    for (int s = 0; s < N; ++s)
+    for (int p = 0; p < 4; ++p) {
+      const bool in = !cut || c * 128 + 32 * p + 8 * q < a.C;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) u[s][i] = dec.load_chunk(a, w[i], c + s * W, q);
-#pragma unroll
-    for (int s = 0; s < N; ++s)
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-          x[s][j][p] = buffer_load16(xr, xoff[j] + (uint32_t)((c + s * W) * 256 + 64 * p));
-#pragma unroll
-    for (int s = 0; s < N; ++s)
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        u32x4 wv[4];
-        dec.decode_chunk(u[s][i], q, wv);
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-          for (int j = 0; j < NT; ++j) acc[i][j] = mfma_bf16(wv[p], x[s][j][p], acc[i][j]);
+      for (int j = 0; j < NT; ++j) {
+        if (decltype(from_lds)::value)           // LDS rows are padded with zeros
+          x[j][p] = in ? *reinterpret_cast<const u32x4*>(xlds[j] + c * 256 + 64 * p) : zero;
+        else
+          x[j][p] = buffer_load16(xr, in ? xoff[j] + (uint32_t)(c * 256 + 64 * p) : kOutside);
       }
-  };
-  int c = wave;
-  for (; c + (U - 1) * W < whole; c += U * W) chunks(c, Int<U>());
-  if (U > 1)
-    for (; c < whole; c += W) chunks(c, Int<1>());
-  if (c == whole && (int64_t)whole * 128 < a.Cp) {
-    // the row's last columns: zero times zero past its end
+    }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       u32x4 wv[4];
-      dec.decode_chunk(dec.load_last(a, w[i], whole, q), q, wv);
+      dec.decode_chunk(u[i], q, wv);
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const bool in = (int64_t)whole * 128 + 32 * p + 8 * q < a.C;
-        if (!in) wv[p] = zero;
+        if (cut && c * 128 + 32 * p + 8 * q >= a.C) wv[p] = zero;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] = mfma_bf16(
-              wv[p], buffer_load16(xr, in ? xoff[j] + (uint32_t)(whole * 256 + 64 * p) : kOutside),
-              acc[i][j]);
+        for (int j = 0; j < NT; ++j) acc[i][j] = mfma_bf16(wv[p], x[j][p], acc[i][j]);
       }
     }
+  };
+  const int whole = (int)(a.C >> 7), groups = whole / U;
+  typedef typename Pick<U == 4, typename D::Four, typename D::Chunk>::type Group;
+  auto load = [&](int g, Group (&u)[RT]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      if constexpr (U == 4) u[i] = dec.load_four(a, w[i], 4 * g, q);
+      else u[i] = dec.load_chunk(a, w[i], g, q);
+    }
+  };
+  auto use = [&](int g, const Group (&u)[RT], auto from_lds) __attribute__((always_inline)) {
+    if constexpr (U == 4) {
+      u32x4 s[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i) s[i] = D::spread(u[i]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        typename D::Chunk v[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) v[i] = D::chunk(u[i], s[i], k);
+        multiply(4 * g + k, v, from_lds, false);
+      }
+    } else {
+      multiply(g, u, from_lds, false);
+    }
+  };
+  Group even[RT], odd[RT];
+  int g = wave;
+  if (g < groups) load(g, even);
+  auto run = [&](auto from_lds) __attribute__((always_inline)) {
+    while (g < groups) {
+      if (g + W < groups) load(g + W, odd);
+      use(g, even, from_lds);
+      g += W;
+      if (g >= groups) break;
+      if (g + W < groups) load(g + W, even);
+      use(g, odd, from_lds);
+      g += W;
+    }
+    // what is left of the row, a chunk a wave
+    for (int c = groups * U + (wave + W - groups % W) % W; c * 128 < a.Cp; c += W) {
+      typename D::Chunk v[RT];
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        v[i] = c < whole ? dec.load_chunk(a, w[i], c, q) : dec.load_last(a, w[i], c, q);
+      multiply(c, v, from_lds, c >= whole);
+    }
+  };
+  if (in_lds) {
+    wait_loads<0>();
+    step_barrier();
+    run(Int<1>());
+  } else {
+    run(Int<0>());
   }
-  join_and_store<RT, NT, W>(a, acc, r0, t0, t1);
+  __syncthreads();                               // the rows of x give way to the waves' sums
+  join_and_store<RT, NT, W>(a, acc, r0, t0, t1, reinterpret_cast<float*>(smem));
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -219,7 +284,8 @@ __global__ __launch_bounds__(W * kWave, 1) void few_mxfp4_kernel(MatmulArgs a) {
   int b0 = wave * 16;
   for (; b0 + 16 <= kb; b0 += W * 16) chunk(b0, Int<1>());
   if (b0 < kb) chunk(b0, Int<0>());
-  join_and_store<RT, NT, W>(a, acc, r0, t0, t1);
+  __shared__ float red[join_bytes<RT, NT, W>() / 4];
+  join_and_store<RT, NT, W>(a, acc, r0, t0, t1, red);
 }
 
 template <int RT, int NT>
@@ -231,19 +297,27 @@ int64_t few_grid(MatmulArgs& a) {
 template <class D, int RT, int NT, int W, int U>
 hipError_t few_bf16(MatmulArgs a, hipStream_t stream) {
   const int64_t grid = few_grid<RT, NT>(a);
-  hipLaunchKernelGGL((few_bf16_kernel<D, RT, NT, W, U>), dim3((unsigned)grid), dim3(W * kWave), 0,
+  // x rows in LDS, as many as leave two workgroups room on a CU
+  const int64_t most = kXLds / x_row_bytes(a.C), want = a.T < NT * kMfma ? a.T : NT * kMfma;
+  a.x_rows = (int)(most < want ? most : want);
+  const int64_t x_lds = a.x_rows * x_row_bytes(a.C);
+  const int lds = (int)(x_lds > join_bytes<RT, NT, W>() ? x_lds : join_bytes<RT, NT, W>());
+  hipLaunchKernelGGL((few_bf16_kernel<D, RT, NT, W, U>), dim3((unsigned)grid), dim3(W * kWave), lds,
                      stream, a);
   return hipGetLastError();
 }
 
+// Groups of four chunks need the registers of four chunks: only decoders that read their scales for
+// four at a time have that form.
 template <class D>
 hipError_t few_bf16_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
-  if (p.nt == 1) {
-    if (p.rt == 2) return few_bf16<D, 2, 1, 8, 2>(a, stream);
-    return p.waves == 16 ? few_bf16<D, 1, 1, 16, 1>(a, stream) : few_bf16<D, 1, 1, 8, 1>(a, stream);
+  if constexpr (D::kFour) {
+    if (p.chunks == 4) {
+      if (p.rt == 2) return few_bf16<D, 2, 1, 8, 4>(a, stream);
+      return p.waves == 16 ? few_bf16<D, 1, 1, 16, 4>(a, stream) : few_bf16<D, 1, 1, 8, 4>(a, stream);
+    }
   }
-  if (p.rt == 2) return few_bf16<D, 2, 2, 8, 1>(a, stream);
-  return p.waves == 16 ? few_bf16<D, 1, 2, 16, 1>(a, stream) : few_bf16<D, 1, 2, 8, 1>(a, stream);
+  return p.rt == 2 ? few_bf16<D, 2, 1, 8, 1>(a, stream) : few_bf16<D, 1, 1, 8, 1>(a, stream);
 }
 
 template <int RT, int NT, int W>

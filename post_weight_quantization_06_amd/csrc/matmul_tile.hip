@@ -6,21 +6,6 @@ namespace aaac {
 
 namespace {
 
-// At most N of this wave's loads are still under way.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(N < 64, "six bits");
-  __builtin_amdgcn_s_waitcnt(0x0f70 | (N & 15) | ((N >> 4) << 14));
-  asm volatile("" ::: "memory");
-}
-// After it, every wave's LDS writes, and the loads it waited for, can be read.
-__device__ __forceinline__ void step_barrier() {
-  __builtin_amdgcn_s_waitcnt(0xc07f);            // lgkmcnt(0)
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Workgroups go to the eight dies in turn; numbering them so that a die gets consecutive tiles lets
 // its L2 serve the rows that neighbouring tiles share.
 constexpr int kDies = 8;

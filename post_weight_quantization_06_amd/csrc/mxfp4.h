@@ -45,6 +45,7 @@ struct MatmulArgs {
   int split;                   // workgroups that share a tile's columns; their sums lie in parts
   float* parts;                // [split, T, part_row(R)], with split > 1
   int64_t row_blocks;          // set by the launcher: row blocks of one expert
+  int x_rows;                  // set by the launcher: rows of x that the workgroup's LDS holds
 };
 
 __host__ __device__ __forceinline__ int64_t part_row(int64_t R) { return (R + 3) & ~(int64_t)3; }
@@ -57,11 +58,11 @@ inline int64_t token_tiles(const MatmulArgs& a, int BN) {
 }
 
 // How a call is run. bn == 0: the few-row kernels with rt x 16 weight rows by nt x 16 rows of x a
-// workgroup of `waves` waves. Else tiles of bm weight rows by bn rows of x, their columns split over
+// workgroup of `waves` waves, `chunks` (4 or 1) chunks of columns a wave at a time. Else tiles of bm weight rows by bn rows of x, their columns split over
 // `split` workgroups.
 struct MatmulPlan {
   int bm, bn, split;
-  int rt, nt, waves;
+  int rt, nt, waves, chunks;
 };
 
 enum MatmulKind { kMxBf16, kMxMxfp4, kPacked };
