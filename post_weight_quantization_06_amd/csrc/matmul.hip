@@ -63,6 +63,7 @@ size_t parts_bytes(const MatmulArgs& a, const MatmulPlan& p) {
 
 hipError_t launch_matmul(MatmulArgs a, MatmulKind kind, const MatmulPlan& p, hipStream_t stream) {
   a.y_vec = can_store4(a);
+  a.y_row = a.y_type != AAAC_F32 && (uintptr_t)a.y % 16 == 0 && a.ldy % 8 == 0;
   a.split = p.split;
   hipError_t e;
   if (p.bn == 0)

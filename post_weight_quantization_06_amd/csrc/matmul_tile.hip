@@ -6,6 +6,55 @@ namespace aaac {
 
 namespace {
 
+// A wave's result, FR * 16 weight rows by FT * 16 rows of x, into y. A lane holds four neighbours of
+// 16 rows of x at a time, 32 bytes of a row together in 16 bits; through `lds` (tile_bytes, this
+// wave's own) a row's FR * 32 bytes go out together, 16 a lane (256 x 256 tiles of bf16, 4096 x 14336
+// x 4096 in MXFP4: XX us, YY without).
+template <int FR, int FT>
+constexpr int tile_bytes() { return FT * kMfma * (FR * 32 + 16); }
+template <int FR, int FT>
+__device__ __forceinline__ void store_tile(const MatmulArgs& a, int part, const f32x4 (&acc)[FR][FT],
+                                           uint8_t* lds, int64_t t0, int64_t t1, int64_t r0) {
+  const int lane = threadIdx.x & (kWave - 1), l = lane & 15, q = lane >> 4;
+  if (!a.y_row || a.split > 1) {
+#pragma unroll
+    for (int j = 0; j < FT; ++j) {
+      const int64_t t = t0 + j * kMfma + l;
+      if (t >= t1) continue;
+#pragma unroll
+      for (int i = 0; i < FR; ++i) {
+        const int64_t r = r0 + i * kMfma + 4 * q;
+        if (r < a.R) store_part(a, part, t, r, acc[i][j]);
+      }
+    }
+    return;
+  }
+  constexpr int kRow = FR * 32 + 16, kLanes = FR * 2;        // bytes and 16-byte pieces of a row
+#pragma unroll
+  for (int j = 0; j < FT; ++j)
+#pragma unroll
+    for (int i = 0; i < FR; ++i) {
+      const f32x4 v = acc[i][j];
+      const uint2 w = a.y_type == AAAC_BF16 ? make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w))
+                                            : make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
+      *reinterpret_cast<uint2*>(lds + (j * kMfma + l) * kRow + i * 32 + q * 8) = w;
+    }
+  const int64_t r = r0 + 8 * (lane % kLanes);
+  uint16_t* y = static_cast<uint16_t*>(a.y) + r;
+  for (int k = lane / kLanes; k < FT * kMfma; k += kWave / kLanes) {
+    if (t0 + k >= t1) break;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + k * kRow + 16 * (lane % kLanes));
+    uint16_t* p = y + (t0 + k) * a.ldy;
+    if (r + 8 <= a.R) {
+      *reinterpret_cast<u32x4*>(p) = v;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (r + c < a.R) p[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
+    }
+  }
+}
+
 // Workgroups go to the eight dies in turn; numbering them so that a die gets consecutive tiles lets
 // its L2 serve the rows that neighbouring tiles share.
 constexpr int kDies = 8;
@@ -155,16 +204,10 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
 #pragma unroll
     for (int j = 0; j < FT; ++j)
       acc[i][j] = mfma_fp4<1>(wf[i], xf[1][j], acc[i][j], sw[i], sx[1][j]);
-#pragma unroll
-  for (int j = 0; j < FT; ++j) {
-    const int64_t t = t0 + wn + j * kMfma + l;
-    if (t >= t1) continue;
-#pragma unroll
-    for (int i = 0; i < FR; ++i) {
-      const int64_t r = r0 + wm + i * kMfma + 4 * q;
-      if (r < a.R) store_part(a, part, t, r, acc[i][j]);
-    }
-  }
+  static_assert(sizeof(lds) >= NW * tile_bytes<FR, FT>(), "the waves' results fit");
+  wait_loads<0>();
+  step_barrier();                                // the stages give way to the results
+  store_tile<FR, FT>(a, part, acc, &lds[0][0] + wave * tile_bytes<FR, FT>(), t0 + wn, t1, r0 + wm);
 }
 
 template <int WR, int WT, int FR, int FT>
@@ -337,16 +380,10 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_bf16_kernel(MatmulArg
   for (int i = 0; i < FR; ++i)
 #pragma unroll
     for (int j = 0; j < FT; ++j) acc[i][j] = mfma_bf16(wf[i], xf[1][j], acc[i][j]);
-#pragma unroll
-  for (int j = 0; j < FT; ++j) {
-    const int64_t t = t0 + wn + j * kMfma + l;
-    if (t >= t1) continue;
-#pragma unroll
-    for (int i = 0; i < FR; ++i) {
-      const int64_t r = r0 + wm + i * kMfma + 4 * q;
-      if (r < a.R) store_part(a, part, t, r, acc[i][j]);
-    }
-  }
+  static_assert(sizeof(lds) >= NW * tile_bytes<FR, FT>(), "the waves' results fit");
+  wait_loads<0>();
+  step_barrier();                                // the stages give way to the results
+  store_tile<FR, FT>(a, part, acc, &lds[0] + wave * tile_bytes<FR, FT>(), t0 + wn, t1, r0 + wm);
 }
 
 template <class D, int WR, int WT, int FR, int FT, int NS>
