@@ -9,6 +9,8 @@ namespace aaac {
 
 namespace {
 
+constexpr int64_t kL2Bytes = (int64_t)32 << 20;   // the L2s of the eight dies together
+
 // y = the sum of the parts in order, four columns a thread. Rows that no expert has were not written
 // by the tiles and are left alone here.
 __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
@@ -64,6 +66,7 @@ size_t parts_bytes(const MatmulArgs& a, const MatmulPlan& p) {
 hipError_t launch_matmul(MatmulArgs a, MatmulKind kind, const MatmulPlan& p, hipStream_t stream) {
   a.y_vec = can_store4(a);
   a.y_row = a.y_type != AAAC_F32 && (uintptr_t)a.y % 16 == 0 && a.ldy % 8 == 0;
+  if (a.y_row && a.T * a.R * 2 > kL2Bytes) a.y_row = 2;
   a.split = p.split;
   hipError_t e;
   if (p.bn == 0)

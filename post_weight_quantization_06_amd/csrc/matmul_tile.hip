@@ -46,7 +46,9 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, int part, const 
     const u32x4 v = *reinterpret_cast<const u32x4*>(lds + k * kRow + 16 * (lane % kLanes));
     uint16_t* p = y + (t0 + k) * a.ldy;
     if (r + 8 <= a.R) {
-      *reinterpret_cast<u32x4*>(p) = v;
+      // results larger than the L2s together are not kept there
+      if (a.y_row == 2) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+      else *reinterpret_cast<u32x4*>(p) = v;
     } else {
 #pragma unroll
       for (int c = 0; c < 8; ++c)
@@ -73,8 +75,10 @@ __device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
 template <int WR, int WT, int FR, int FT, bool WHOLE>
 __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulArgs a) {
   constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma;
-  constexpr int kW = BM * 128, kX = BN * 128, kWs = BM * 8, kXs = BN * 8;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2][kW + kX + kWs + kXs];
+  // LDS: two stages of codes, then the scale bytes of two times four steps, 32 a row; the halves of
+  // these 32 are swapped in rows with bit 3 set, so that 16 rows' bytes of a step lie in 16 banks
+  constexpr int kW = BM * 128, kX = BN * 128, kStage = kW + kX, kWs = BM * 32, kScales = kWs + BN * 32;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (kStage + kScales)];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
   const int64_t id = by_die(blockIdx.x, gridDim.x), tiles = gridDim.x / a.split;
   const int part = (int)(id / tiles);
@@ -93,10 +97,13 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
   const uint8_t* xs = a.x_scales + t0 * kb;
   const u32x4 wsr = rows_buffer(ws, nr * kb), xsr = rows_buffer(xs, nt * kb);
 
+  const int64_t all = (kb + 7) / 8, first = all * part / a.split;
+  const int64_t steps = all * (part + 1) / a.split;
   const int piece = (lane & 7) ^ (lane >> 3);    // the 16-byte piece of the row that a lane loads
-  const uint32_t lds0 = lds_address(&lds[0][0]);
+  const uint32_t lds0 = lds_address(&lds[0]);
   auto load = [&](int buf, int64_t kt) {
-    const uint32_t dst = lds0 + buf * (kW + kX + kWs + kXs);
+    const uint32_t dst = lds0 + buf * kStage;
+    const int at4 = 2 * kStage + (int)(kt >> 2 & 1) * kScales;
     const bool in = WHOLE || kt * 8 + piece < kb;
     const uint32_t col = (uint32_t)(kt * 128) + piece * 16;
     const uint32_t off0 = (uint32_t)(lane >> 3) * (uint32_t)row_bytes + col;
@@ -111,16 +118,19 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
       load_lds16(xr, in ? off0 + row * (uint32_t)row_bytes : kOutside, 0, dst + kW + row * 128);
     }
     if (WHOLE) {
-      const uint32_t soff = (uint32_t)(lane >> 1) * (uint32_t)kb + (uint32_t)(kt * 8) + 4 * (lane & 1);
+      // scale rows are read for four steps at a time: a load costs by its rows, not their bytes
+      if (kt != first && (kt & 3) != 0) return;
+      const uint32_t sdst = lds0 + at4;
+      const uint32_t soff = (uint32_t)(lane >> 1) * (uint32_t)kb + (uint32_t)(kt >> 2) * 32 +
+                            16 * ((lane ^ (lane >> 4)) & 1);
 #pragma unroll
       for (int i = 0; i < BM / 32; i += NW)
         if (BM / 32 % NW == 0 || i + wave < BM / 32)
-          load_lds4(wsr, soff + (i + wave) * 32 * (uint32_t)kb, dst + kW + kX + (i + wave) * 256);
+          load_lds16(wsr, soff + (i + wave) * 32 * (uint32_t)kb, 0, sdst + (i + wave) * 1024);
 #pragma unroll
       for (int i = 0; i < BN / 32; i += NW)
         if (BN / 32 % NW == 0 || i + wave < BN / 32)
-          load_lds4(xsr, soff + (i + wave) * 32 * (uint32_t)kb,
-                    dst + kW + kX + kWs + (i + wave) * 256);
+          load_lds16(xsr, soff + (i + wave) * 32 * (uint32_t)kb, 0, sdst + kWs + (i + wave) * 1024);
     } else {
       // scale rows of any length: byte by byte, zero past the row's end
       for (int i = tid; i < (BM + BN) * 8; i += NW * kWave) {
@@ -129,7 +139,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
         uint8_t v = 0;
         if (kt * 8 + b < kb && row < (isw ? nr : nt))
           v = (isw ? ws : xs)[(int64_t)row * kb + kt * 8 + b];
-        lds[buf][kW + kX + i] = v;
+        lds[at4 + (isw ? 0 : kWs) + row * 32 + (((int)(kt & 3) * 8) ^ (row & 8) * 2) + b] = v;
       }
     }
   };
@@ -141,8 +151,6 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
     for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int wm = (wave / WT) * FR * kMfma, wn = (wave % WT) * FT * kMfma;
   const int l = lane & 15, q = lane >> 4;
-  const int64_t all = (kb + 7) / 8, first = all * part / a.split;
-  const int64_t steps = all * (part + 1) / a.split;
   const u32x4 zero = {0u, 0u, 0u, 0u};
   u32x4 wf[FR], xf[2][FT];
   uint32_t sw[FR], sx[2][FT];                    // scale words
@@ -162,15 +170,16 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
     wait_loads<0>();
     step_barrier();
     if (kt + 1 < steps) load(buf ^ 1, kt + 1);
-    const uint8_t* base = lds[buf];
+    const uint8_t* base = lds + buf * kStage;
     const uint8_t* wb = base + (wm + l) * 128;
-    const uint8_t* wsb = base + kW + kX + (wm + l) * 8 + 2 * q;
+    const uint8_t* sb = lds + 2 * kStage + (int)(kt >> 2 & 1) * kScales +
+                        (((int)(kt & 3) * 8) ^ (l & 8) * 2) + 2 * q;
+    const uint8_t *wsb = sb + (wm + l) * 32, *xsb = sb + kWs + (wn + l) * 32;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 0; j < FT; ++j) {
       sx[0][j] = sx[1][j];
-      sx[1][j] = *reinterpret_cast<const uint16_t*>(base + kW + kX + kWs + (wn + j * kMfma + l) * 8 +
-                                                    2 * q);
+      sx[1][j] = *reinterpret_cast<const uint16_t*>(xsb + j * kMfma * 32);
     }
     // half 0 of the pass: instructions of the step before, on its second half's fragments, while
     // this step's first half is read; half 1: this step's first half, while its second is read
@@ -185,10 +194,10 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
         // the registers of the group before
         if (i > 0) {
           wf[i - 1] = *reinterpret_cast<const u32x4*>(wb + (i - 1) * kMfma * 128 + p);
-          if (h == 0) sw[i - 1] = *reinterpret_cast<const uint16_t*>(wsb + (i - 1) * kMfma * 8);
+          if (h == 0) sw[i - 1] = *reinterpret_cast<const uint16_t*>(wsb + (i - 1) * kMfma * 32);
         } else if (h == 1) {
           wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (p ^ 16));
-          sw[FR - 1] = *reinterpret_cast<const uint16_t*>(wsb + (FR - 1) * kMfma * 8);
+          sw[FR - 1] = *reinterpret_cast<const uint16_t*>(wsb + (FR - 1) * kMfma * 32);
         }
 #pragma unroll
         for (int j = 0; j < FT; ++j)
@@ -207,7 +216,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
   static_assert(sizeof(lds) >= NW * tile_bytes<FR, FT>(), "the waves' results fit");
   wait_loads<0>();
   step_barrier();                                // the stages give way to the results
-  store_tile<FR, FT>(a, part, acc, &lds[0][0] + wave * tile_bytes<FR, FT>(), t0 + wn, t1, r0 + wm);
+  store_tile<FR, FT>(a, part, acc, &lds[0] + wave * tile_bytes<FR, FT>(), t0 + wn, t1, r0 + wm);
 }
 
 template <int WR, int WT, int FR, int FT>

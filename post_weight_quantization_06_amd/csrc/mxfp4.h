@@ -42,7 +42,7 @@ struct MatmulArgs {
   int y_type;
   int64_t ldy;
   int y_vec;                   // four neighbours of a row go out in one store
-  int y_row;                   // 16-bit y whose rows start on 16 bytes
+  int y_row;                   // 16-bit y whose rows start on 16 bytes; 2: past the caches
   int split;                   // workgroups that share a tile's columns; their sums lie in parts
   float* parts;                // [split, T, part_row(R)], with split > 1
   int64_t row_blocks;          // set by the launcher: row blocks of one expert
