@@ -26,36 +26,70 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
   store4(a, t, r, v);
 }
 
+// The choice. Up to 16 rows of x a matrix (32 for one matrix in MXFP4) go to the few-row kernels,
+// which read each weight once: one row against 14336 x 4096 packed weights takes 18 us there and 26 in
+// the best tiles, 17 rows 27 us in tiles. Two blocks of 16 weight rows a workgroup halve the reads of
+// x, one block makes more workgroups: 32 experts of 2048 x 4096 (some 3500 blocks) take 33 us with
+// two and 41 with one, 4096 x 14336 (256 blocks) 19 and 12. Four chunks at a time pay on long rows:
+// 12.6 us down to 11.9 at 14336 columns, 7.3 up to 7.8 at 4096.
+//
+// Tiles: the least estimated time over tile widths and splits. A tile takes its steps times kStep
+// (measured with every CU at work) and kTile to start and end; the busiest CU runs
+// ceil(workgroups / CUs) of them, two at a time where LDS holds two, which takes kTwo of one after the
+// other. A split adds a launch and the traffic of the parts. It picks, in microseconds and packed
+// weights of 14336 x 4096: 64 rows: 64 wide, split 4 (32; unsplit 53); 512 rows: 256 wide, split 2
+// (85; 128 wide unsplit 96); 2048 rows: 256 wide unsplit (250; 128 wide 334).
+struct TileCost { int bm, bn; double step; bool two; };
+constexpr TileCost kBf16Tiles[] = {{128, 32, 0.70, true}, {128, 64, 0.77, true}, {128, 128, 0.96, true},
+                                   {256, 256, 1.85, false}};
+constexpr TileCost kMxTiles[] = {{128, 64, 0.60, true}, {128, 128, 0.75, true}, {256, 256, 1.90, false}};
+constexpr double kTile = 2.3, kTwoBf16 = 0.80, kTwoMx = 0.95, kLaunch = 3.0, kPartBytes = 6e6;
+
+template <int N>
+void plan_tiles(const MatmulArgs& a, const TileCost (&tiles)[N], double two, int cols, bool can_split,
+                MatmulPlan& p) {
+  const int cus = device_cu_count();
+  const int64_t steps = (a.Cp + cols - 1) / cols;
+  // experts' last tiles: some are empty, and the split of the rows over the experts is not known here
+  const double extra = a.E > 1 ? 0.75 * (double)(a.E < a.T ? a.E : a.T) : 0.0;
+  double best = 1e30;
+  for (const TileCost& t : tiles) {
+    const double across = a.E > 1 ? (double)a.T / t.bn + extra : (double)((a.T + t.bn - 1) / t.bn);
+    const double n = (double)((a.R + t.bm - 1) / t.bm) * across;
+    for (int split = 1; split <= (can_split ? 16 : 1); ++split) {
+      if (split > 1 && (steps < 4 * split || n * split > 4.0 * cus)) break;
+      const double each = (double)((steps + split - 1) / split) * t.step + kTile;
+      const double on_cu = n * split / cus;
+      double time = on_cu <= 1 ? each : (double)(int64_t)(on_cu + 0.999) * each * (t.two ? two : 1.0);
+      if (split > 1) time += kLaunch + 8.0 * split * (double)a.T * (double)a.R / kPartBytes;
+      if (time < best) {
+        best = time;
+        p.bm = t.bm;
+        p.bn = t.bn;
+        p.split = split;
+      }
+    }
+  }
+}
+
 }  // namespace
 
 MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
   MatmulPlan p = {};
   p.split = 1;
   const int64_t rows = (a.T + a.E - 1) / a.E;    // rows of x an expert, on average
-#ifdef TUNE
-  {
-    auto v = [](const char* n, int d) { const char* s = getenv(n); return s ? atoi(s) : d; };
-    p.bn = v("BN", 0); p.bm = p.bn == 256 ? 256 : 128; p.split = can_split ? v("SPLIT", 1) : 1;
-    p.rt = v("RT", 1); p.nt = v("NT", 1); p.waves = v("WAVES", 8); p.chunks = v("U", 4);
-    return p;
-  }
-#endif
-  const bool fp4 = kind == kMxMxfp4;
-  if (rows <= (fp4 ? 64 : kMfma)) {
-    p.nt = (int)((rows + kMfma - 1) / kMfma);
+  if (rows <= kMfma || (kind == kMxMxfp4 && a.E == 1 && rows <= 2 * kMfma)) {
     const int64_t blocks = (a.R + kMfma - 1) / kMfma * (a.E < a.T ? a.E : a.T);
-    p.rt = blocks > 512 ? 2 : 1;
-    p.waves = blocks > 256 ? 8 : 16;
-    p.chunks = a.C >= 512 * p.waves ? 4 : 1;
+    p.nt = rows <= kMfma ? 1 : 2;
+    p.rt = blocks > 2 * device_cu_count() ? 2 : 1;
+    p.chunks = a.C >= 8192 ? 4 : 1;
     return p;
   }
-  p.bn = rows <= 64 ? 64 : rows <= 512 ? 128 : 256;
-  p.bm = p.bn == 256 ? 256 : 128;
-  if (can_split) {
-    const int64_t tiles = (a.R + p.bm - 1) / p.bm * ((a.T + p.bn - 1) / p.bn);
-    const int64_t steps = (a.Cp + (fp4 ? 255 : 63)) / (fp4 ? 256 : 64);
-    while (tiles * p.split < 256 && p.split * 8 <= steps) ++p.split;
-  }
+  if (kind == kMxMxfp4) plan_tiles(a, kMxTiles, kTwoMx, 256, can_split, p);
+  else plan_tiles(a, kBf16Tiles, kTwoBf16, 64, can_split, p);
+#ifdef TUNE
+  if (getenv("BN")) { p.bn = atoi(getenv("BN")); p.bm = p.bn == 256 ? 256 : 128; p.split = can_split && getenv("SPLIT") ? atoi(getenv("SPLIT")) : 1; }
+#endif
   return p;
 }
 

@@ -307,15 +307,11 @@ hipError_t few_bf16(MatmulArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Groups of four chunks need the registers of four chunks: only decoders that read their scales for
-// four at a time have that form.
+// Only decoders that read their scales for four chunks at a time have the form with groups of four.
 template <class D>
 hipError_t few_bf16_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
   if constexpr (D::kFour) {
-    if (p.chunks == 4) {
-      if (p.rt == 2) return few_bf16<D, 2, 1, 8, 4>(a, stream);
-      return p.waves == 16 ? few_bf16<D, 1, 1, 16, 4>(a, stream) : few_bf16<D, 1, 1, 8, 4>(a, stream);
-    }
+    if (p.rt == 1 && p.chunks == 4) return few_bf16<D, 1, 1, 8, 4>(a, stream);
   }
   return p.rt == 2 ? few_bf16<D, 2, 1, 8, 1>(a, stream) : few_bf16<D, 1, 1, 8, 1>(a, stream);
 }
@@ -328,21 +324,12 @@ hipError_t few_mxfp4(MatmulArgs a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int NT>
-hipError_t few_mxfp4_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
-  if (p.rt == 2) return few_mxfp4<2, NT, 8>(a, stream);
-  return p.waves == 16 ? few_mxfp4<1, NT, 16>(a, stream) : few_mxfp4<1, NT, 8>(a, stream);
-}
-
 }  // namespace
 
 hipError_t launch_few_mxfp4(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
-  switch (p.nt) {
-    case 1: return few_mxfp4_any<1>(a, p, stream);
-    case 2: return few_mxfp4_any<2>(a, p, stream);
-    case 3: return few_mxfp4_any<3>(a, p, stream);
-    default: return few_mxfp4_any<4>(a, p, stream);
-  }
+  if (p.nt == 1)
+    return p.rt == 2 ? few_mxfp4<2, 1, 8>(a, stream) : few_mxfp4<1, 1, 8>(a, stream);
+  return p.rt == 2 ? few_mxfp4<2, 2, 8>(a, stream) : few_mxfp4<1, 2, 8>(a, stream);
 }
 
 hipError_t launch_few_mx_bf16(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {

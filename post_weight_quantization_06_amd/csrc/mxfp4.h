@@ -59,11 +59,11 @@ inline int64_t token_tiles(const MatmulArgs& a, int BN) {
 }
 
 // How a call is run. bn == 0: the few-row kernels with rt x 16 weight rows by nt x 16 rows of x a
-// workgroup of `waves` waves, `chunks` (4 or 1) chunks of columns a wave at a time. Else tiles of bm weight rows by bn rows of x, their columns split over
-// `split` workgroups.
+// workgroup, `chunks` (4 or 1) chunks of columns a wave at a time. Else tiles of bm weight rows by bn
+// rows of x, their columns split over `split` workgroups.
 struct MatmulPlan {
   int bm, bn, split;
-  int rt, nt, waves, chunks;
+  int rt, nt, chunks;
 };
 
 enum MatmulKind { kMxBf16, kMxMxfp4, kPacked };

@@ -34,14 +34,16 @@ __device__ __forceinline__ float to_f32(typename Elem<TYPE>::T v) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
 }
 
-// Eight consecutive elements as fp32. VEC: the 16-byte loads are aligned and inside the row;
-// otherwise elements at or past `valid` read as zero.
+// Eight consecutive elements as fp32; those at or past `valid` read as zero. Eight inside the row are
+// read in 16-byte words, aligned (VEC) or not (1003 x 5003 in fp32: XX us, YY element by element).
 template <int TYPE, bool VEC>
 __device__ __forceinline__ void load8(const typename Elem<TYPE>::T* p, int valid, float (&v)[8]) {
   typedef typename Elem<TYPE>::T T;
-  if (VEC) {
+  if (VEC || valid == 8) {
     if (sizeof(T) == 2) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
+      uint4 u;
+      if (VEC) u = *reinterpret_cast<const uint4*>(p);
+      else __builtin_memcpy(&u, p, 16);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -49,8 +51,14 @@ __device__ __forceinline__ void load8(const typename Elem<TYPE>::T* p, int valid
         v[2 * k + 1] = to_f32<TYPE>((T)(w[k] >> 16));
       }
     } else {
-      const uint4 a = reinterpret_cast<const uint4*>(p)[0];
-      const uint4 b = reinterpret_cast<const uint4*>(p)[1];
+      uint4 a, b;
+      if (VEC) {
+        a = reinterpret_cast<const uint4*>(p)[0];
+        b = reinterpret_cast<const uint4*>(p)[1];
+      } else {
+        __builtin_memcpy(&a, p, 16);
+        __builtin_memcpy(&b, p + 4, 16);
+      }
       const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
@@ -124,6 +132,8 @@ __device__ __forceinline__ void store8(typename Elem<TYPE>::T* p, bool vec, int 
     if (vec) {
       reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else if (valid == 8) {
+      __builtin_memcpy(p, v, 32);
     } else {
       for (int k = 0; k < 8; ++k)
         if (k < valid) p[k] = (T)__float_as_uint(v[k]);
@@ -139,6 +149,8 @@ __device__ __forceinline__ void store8(typename Elem<TYPE>::T* p, bool vec, int 
   }
   if (vec) {
     *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (valid == 8) {
+    __builtin_memcpy(p, w, 16);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
