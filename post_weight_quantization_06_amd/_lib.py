@@ -671,15 +671,20 @@ def aaac_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tenso
 
 
 @functools.lru_cache(maxsize=4096)
-def matmul_workspace_bytes(kind: int, E: int, R: int, C: int, T: int) -> int:
-    return int((_lib or load()).aaac_matmul_workspace_bytes(kind, E, R, C, T))
+def matmul_workspace_bytes(kind: int, E: int, R: int, C: int, T: int, dev: int = 0) -> int:
+    """Workspace bytes of a product (MATMUL_*) on GPU dev."""
+    fn = (_lib or load()).aaac_matmul_workspace_bytes
+    if torch.cuda.is_available():
+        with torch.cuda.device(dev):
+            return int(fn(kind, E, R, C, T))
+    return int(fn(kind, E, R, C, T))
 
 
 def _product_args(what: str, kind: int, E: int, C: int, offsets, y: torch.Tensor, T: int, R: int,
-                  ws):
+                  ws, dev: int, stream):
     """(offsets pointer, y type, row stride of y, workspace, its pointer and bytes) after the checks
-    that every product shares. Without a workspace one is taken from torch where the call uses one;
-    it belongs to the stream the caller allocates on, so a call on another stream needs its own."""
+    that every product shares. Without a workspace one is taken from torch where the call uses one,
+    on the call's stream, where it is free again once the call's work is done."""
     yt = _float_type(y, "y")
     M, N, ldy = _rows(y, "y")
     if M != T or N != R:
@@ -691,11 +696,15 @@ def _product_args(what: str, kind: int, E: int, C: int, offsets, y: torch.Tensor
             raise ValueError("%s: offsets must be contiguous int32 [%d] (got %s %s)" % (
                 what, E + 1, offsets.dtype, tuple(offsets.shape)))
         op = offsets.data_ptr()
-    need = matmul_workspace_bytes(kind, E, R, C, T)
+    need = matmul_workspace_bytes(kind, E, R, C, T, dev)
     if need == 0:
         return op, yt, ldy, None, None, 0
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=y.device)
+        if stream is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=y.device)
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=y.device)
     elif ws.dtype is not torch.uint8 or not ws.is_contiguous():
         raise ValueError("%s: ws must be contiguous uint8" % what)
     return op, yt, ldy, ws, ws.data_ptr(), ws.numel()
@@ -735,7 +744,8 @@ def aaac_mxfp4_matmul(codes: torch.Tensor, scales: torch.Tensor, C: int, x: torc
         _u8(x, "x", T * blocks * 16)
         _u8(x_scales, "x_scales", T * blocks)
         xt, kind, xs, ldx = MXFP4, MATMUL_MXFP4_X, x_scales.data_ptr(), C
-    op, yt, ldy, ws, wp, wn = _product_args(what, kind, E, C, offsets, y, T, R, ws)
+    op, yt, ldy, ws, wp, wn = _product_args(what, kind, E, C, offsets, y, T, R, ws, dev,
+                                             stream)
     _launch(what, dev, stream, codes.data_ptr(), scales.data_ptr(), E, R, C, op, x.data_ptr(), xt,
             xs, T, ldx, flags, y.data_ptr(), yt, ldy, wp, wn)
 
@@ -769,7 +779,8 @@ def aaac_matmul(codes: torch.Tensor, scales: torch.Tensor, bitmap: Optional[torc
     T, K, ldx = _rows(x, "x")
     if K != C:
         raise ValueError("%s: x has %d columns, the weights %d" % (what, K, C))
-    op, yt, ldy, ws, wp, wn = _product_args(what, MATMUL_PACKED, E, C, offsets, y, T, R, ws)
+    op, yt, ldy, ws, wp, wn = _product_args(what, MATMUL_PACKED, E, C, offsets, y, T, R, ws,
+                                             dev, stream)
     _launch(what, dev, stream, codes.data_ptr(), scales.data_ptr(),
             None if bitmap is None else bitmap.data_ptr(), tables_bf16.data_ptr(), E, R, C, g, S,
             n, op, x.data_ptr(), T, ldx, y.data_ptr(), yt, ldy, wp, wn)

@@ -50,11 +50,11 @@ __device__ __forceinline__ u32x4 words_buffer(const void* p, int64_t bytes, uint
 // one wait state before the load.
 __device__ __forceinline__ void load_lds16(u32x4 buf, uint32_t off, uint32_t more, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"(dst), "v"(off), "s"(buf), "s"(more) : "memory");
+               :: "s"(dst), "v"(off), "s"(buf), "s"(more) : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds4(u32x4 buf, uint32_t off, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
-               :: "s"(dst), "v"(off), "s"(buf) : "memory");
+               :: "s"(dst), "v"(off), "s"(buf) : "memory", "m0");
 }
 __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(LdsPtr)(void*)p;

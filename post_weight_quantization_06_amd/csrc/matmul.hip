@@ -1,9 +1,6 @@
 // How a product call is run: the choice of kernel and tile, and the kernel that adds the parts of a
 // sum that was split over workgroups.
 #include "matmul.h"
-#ifdef TUNE
-#include <stdlib.h>
-#endif
 
 namespace aaac {
 
@@ -87,9 +84,6 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
   }
   if (kind == kMxMxfp4) plan_tiles(a, kMxTiles, kTwoMx, 256, can_split, p);
   else plan_tiles(a, kBf16Tiles, kTwoBf16, 64, can_split, p);
-#ifdef TUNE
-  if (getenv("BN")) { p.bn = atoi(getenv("BN")); p.bm = p.bn == 256 ? 256 : 128; p.split = can_split && getenv("SPLIT") ? atoi(getenv("SPLIT")) : 1; }
-#endif
   return p;
 }
 

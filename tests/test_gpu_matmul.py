@@ -226,6 +226,69 @@ def test_widths_that_are_no_multiple_of_a_block():
                 P.mxfp4_matmul(codes[0], scales[0], xd)
 
 
+@pytest.mark.parametrize("g,S,n", [(128, 128, 13), (16, 16, 15), (32, 8, 3), (8, 8, 2)])
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_codes_past_the_table_read_entry_0_as_dequant_does(g, S, n, T):
+    _say("codes past the table", g, S, n, T)
+    rng = np.random.default_rng(n)
+    R, C = 72, 256
+    codes, scales, bitmap, tables, _ = _packed(rng, 1, R, C, g, S, n, True)
+    codes = torch.from_numpy(rng.integers(0, 256, size=(R, C // 2)).astype(np.uint8)).to(DEV)
+    W = torch.empty(R, C, dtype=torch.bfloat16, device=DEV)
+    L.aaac_dequant(codes.view(-1), scales.view(-1), None if bitmap is None else bitmap.view(-1),
+                   tables.view(-1), R, C, g, S, n, W)
+    x, xd = _x(rng, T, C, True)
+    y = P.packed_matmul(codes, scales[0], None if bitmap is None else bitmap[0], tables[0], xd, g, S,
+                        n, dtype=torch.float32)
+    assert np.array_equal(y.double().cpu().numpy(), x @ W.double().cpu().numpy().T)
+
+
+@pytest.mark.parametrize("R,T", [(296, 300), (300, 300), (8, 600), (1000, 70), (4104, 4200)])
+def test_16_bit_results_in_whole_rows(R, T):
+    # rows of y that start on 16 bytes or not, tiles cut by R and T, and a y larger than the caches
+    _say("16-bit rows", R, T)
+    rng = np.random.default_rng(R + T)
+    C = 64
+    codes, scales, W = _mx(rng, 1, R, C, True)
+    x, xd = _x(rng, T, C, True)
+    for dtype in (torch.bfloat16, torch.float16):
+        for act in ("bf16", "mxfp4"):
+            xv = x if act == "bf16" else ref.mxfp4_decode(*ref.mxfp4_encode(x), C)
+            frame = torch.full((T + 2, R), 9.0, dtype=dtype, device=DEV)
+            P.mxfp4_matmul(codes[0], scales[0], xd, act=act, out=frame[1:T + 1])
+            assert torch.equal(frame[1:T + 1].cpu(), _rounded(xv @ W[0].T, dtype))
+            assert (frame[0] == 9.0).all() and (frame[T + 1] == 9.0).all()
+
+
+def test_workspaces_given_or_not_and_a_stream_of_its_own():
+    # a shape whose columns are split: the library's workspace, the caller's, none, another stream
+    rng = np.random.default_rng(21)
+    R, C, T = 256, 4096, 64
+    codes, scales, W = _mx(rng, 1, R, C, True)
+    x, xd = _x(rng, T, C, True)
+    need = L.matmul_workspace_bytes(L.MATMUL_MXFP4, 1, R, C, T)
+    assert need > 0
+    want = (x @ W[0].T).astype(np.float32)
+    ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for kw in ({}, {"ws": ws}, {"stream": side}, {"ws": ws, "stream": side}):
+        _say("workspace", sorted(kw))
+        y = torch.zeros(T, R, dtype=torch.float32, device=DEV)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            L.aaac_mxfp4_matmul(codes[0], scales[0], C, xd, y, **kw)
+        torch.cuda.synchronize()
+        assert np.array_equal(y.cpu().numpy(), want)
+    assert (ws[need:] == 0xFF).all()                 # nothing past what was asked for
+    lib, p = L.load(), (lambda t: t.data_ptr())
+    y = torch.zeros(T, R, dtype=torch.float32, device=DEV)
+    st = lib.aaac_mxfp4_matmul(p(codes), p(scales), 1, R, C, None, p(xd), 0, None, T, C, 0, p(y), 2,
+                               R, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert np.array_equal(y.cpu().numpy(), want)
+
+
 # ------------------------------------------------------------------ rows, strides, extremes
 
 def _calls(rng, E, R, C, T, g=32, S=16, n=16):
