@@ -55,6 +55,10 @@ __host__ __device__ __forceinline__ int64_t x_row_bytes(int64_t C) {
 // load instructions bounds this kernel before their bytes do, hence one scale load for four chunks
 // (U = 4), and x in LDS where the tile's rows fit into a.x_rows of them; otherwise x is read
 // directly, 64 neighbouring bytes a row, and rows past the tile's last load as zeros.
+// 14336 columns by 4096 rows in MXFP4, one row of x: 11.1 us, 2.8 TB/s (the reads of x and of the scales
+// took 3 us each of 14 before they were gathered); 32 experts of 2048 x 4096, 61 rows: 28 us, 5.1 TB/s.
+// In the packed format the decoding bounds it: some seven vector instructions a weight with scale
+// groups of 16, five with 128.
 // ------------------------------------------------------------------------------------------------
 template <class D, int RT, int NT, int W, int U>
 __global__ __launch_bounds__(W * kWave, 1) void few_bf16_kernel(MatmulArgs a) {
@@ -194,7 +198,8 @@ __global__ __launch_bounds__(W * kWave, 1) void few_bf16_kernel(MatmulArgs a) {
 // ------------------------------------------------------------------------------------------------
 // MXFP4 x times MXFP4 weights: the scaled matrix instruction takes codes and scale bytes as they
 // are stored. Run q of a lane is one block of 32 columns; a chunk is 512 columns, so that a lane
-// reads the 16 scale bytes of its row in one load and takes byte 4 j + q for instruction j.
+// reads the 16 scale bytes of its row in one load and takes byte 4 j + q for instruction j. One row
+// against 14336 x 4096: 8 us, 3.9 TB/s.
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ u32x4 load_scales(const uint8_t* p, int left) {
   u32x4 v;
