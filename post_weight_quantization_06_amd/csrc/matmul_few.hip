@@ -199,7 +199,7 @@ __global__ __launch_bounds__(W * kWave, 1) void few_bf16_kernel(MatmulArgs a) {
 // MXFP4 x times MXFP4 weights: the scaled matrix instruction takes codes and scale bytes as they
 // are stored. Run q of a lane is one block of 32 columns; a chunk is 512 columns, so that a lane
 // reads the 16 scale bytes of its row in one load and takes byte 4 j + q for instruction j. One row
-// against 14336 x 4096: 8 us, 3.9 TB/s.
+// against 14336 x 4096, quantised in the call: 12 us.
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ u32x4 load_scales(const uint8_t* p, int left) {
   u32x4 v;

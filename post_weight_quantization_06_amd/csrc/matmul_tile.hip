@@ -57,12 +57,16 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, int part, const 
   }
 }
 
-// Workgroups go to the eight dies in turn; numbering them so that a die gets consecutive tiles lets
-// its L2 serve the rows that neighbouring tiles share.
-constexpr int kDies = 8;
+// Workgroups go to the eight dies in turn. Renumbered so that a die gets runs of kRun consecutive
+// tiles, as many as it works on at once, its L2 serves the rows that neighbouring tiles share. Runs
+// and not an eighth of the tiles each: a grouped call's last tiles are empty, and the dies share them
+// (8 experts of 14336 x 4096, 4093 rows: 637 us, 767 in eighths).
+constexpr int kDies = 8, kRun = 32;
 __device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
-  const int64_t per = n / kDies, rest = n % kDies, d = b % kDies, i = b / kDies;
-  return d * per + (d < rest ? d : rest) + i;
+  const int64_t whole = n / (kDies * kRun) * (kDies * kRun);
+  if (b >= whole) return b;
+  const int64_t d = b % kDies, i = b / kDies;
+  return (i / kRun * kDies + d) * kRun + i % kRun;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -75,8 +79,8 @@ __device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
 // of a step's instructions, and each register is read again as soon as it has been used.
 //
 // 4096 x 14336 x 4096: 148 us, 3.2 PFLOP/s, of the 8.8 that the instruction alone reaches here. What
-// bounds it is the supply of the stages: without its matrix instructions it takes 90 % of the time,
-// without its loads 70 %. Eight waves of 128 x 64 rather than four of 128 x 128: four need 512
+// bounds it is the supply of the stages: without its matrix instructions it takes 87 % of the time,
+// without its loads 79 %. Eight waves of 128 x 64 rather than four of 128 x 128: four need 512
 // registers each and spill. Rows of x tiles advancing together (1 to 16 of them) and touching lines
 // two to four steps ahead measured equal or slower.
 // ------------------------------------------------------------------------------------------------
@@ -157,7 +161,10 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
   for (int i = 0; i < FR; ++i)
 #pragma unroll
     for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int wm = (wave / WT) * FR * kMfma, wn = (wave % WT) * FT * kMfma;
+  // neighbouring waves, on different SIMDs, share their rows of x; those past a partial tile's last
+  // row only help to load (and decode)
+  const int wm = (wave % WR) * FR * kMfma, wn = (wave / WR) * FT * kMfma;
+  const bool busy = wn < nt;
   const int l = lane & 15, q = lane >> 4;
   const u32x4 zero = {0u, 0u, 0u, 0u};
   u32x4 wf[FR], xf[2][FT];
@@ -173,49 +180,54 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
     sx[1][j] = 0;
   }
   load(0, first);
-  for (int64_t kt = first; kt < steps; ++kt) {
-    const int buf = (int)((kt - first) & 1);
-    wait_loads<0>();
-    step_barrier();
-    if (kt + 1 < steps) load(buf ^ 1, kt + 1);
-    const uint8_t* base = lds + buf * kStage;
-    const uint8_t* wb = base + (wm + l) * 128;
-    const uint8_t* sb = lds + 2 * kStage + (int)(kt >> 2 & 1) * kScales +
-                        (((int)(kt & 3) * 8) ^ (l & 8) * 2) + 2 * q;
-    const uint8_t *wsb = sb + (wm + l) * 32, *xsb = sb + kWs + (wn + l) * 32;
-    __builtin_amdgcn_sched_barrier(0);
+  auto walk = [&](auto with_products) __attribute__((always_inline)) {
+    for (int64_t kt = first; kt < steps; ++kt) {
+      const int buf = (int)((kt - first) & 1);
+      wait_loads<0>();
+      step_barrier();
+      if (kt + 1 < steps) load(buf ^ 1, kt + 1);
+      if (decltype(with_products)::value == 0) continue;
+      const uint8_t* base = lds + buf * kStage;
+      const uint8_t* wb = base + (wm + l) * 128;
+      const uint8_t* sb = lds + 2 * kStage + (int)(kt >> 2 & 1) * kScales +
+                          (((int)(kt & 3) * 8) ^ (l & 8) * 2) + 2 * q;
+      const uint8_t *wsb = sb + (wm + l) * 32, *xsb = sb + kWs + (wn + l) * 32;
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int j = 0; j < FT; ++j) {
-      sx[0][j] = sx[1][j];
-      sx[1][j] = *reinterpret_cast<const uint16_t*>(xsb + j * kMfma * 32);
-    }
-    // half 0 of the pass: instructions of the step before, on its second half's fragments, while
-    // this step's first half is read; half 1: this step's first half, while its second is read
+      for (int j = 0; j < FT; ++j) {
+        sx[0][j] = sx[1][j];
+        sx[1][j] = *reinterpret_cast<const uint16_t*>(xsb + j * kMfma * 32);
+      }
+      // half 0 of the pass: instructions of the step before, on its second half's fragments, while
+      // this step's first half is read; half 1: this step's first half, while its second is read
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int p = ((2 * q + h) ^ (l & 7)) * 16;
-#pragma unroll
-      for (int j = 0; j < FT; ++j)
-        xf[h][j] = *reinterpret_cast<const u32x4*>(base + kW + (wn + j * kMfma + l) * 128 + p);
-#pragma unroll
-      for (int i = 0; i < FR; ++i) {
-        // the registers of the group before
-        if (i > 0) {
-          wf[i - 1] = *reinterpret_cast<const u32x4*>(wb + (i - 1) * kMfma * 128 + p);
-          if (h == 0) sw[i - 1] = *reinterpret_cast<const uint16_t*>(wsb + (i - 1) * kMfma * 32);
-        } else if (h == 1) {
-          wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (p ^ 16));
-          sw[FR - 1] = *reinterpret_cast<const uint16_t*>(wsb + (FR - 1) * kMfma * 32);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const int p = ((2 * q + h) ^ (l & 7)) * 16;
 #pragma unroll
         for (int j = 0; j < FT; ++j)
-          acc[i][j] = h == 0 ? mfma_fp4<1>(wf[i], xf[1][j], acc[i][j], sw[i], sx[0][j])
-                             : mfma_fp4<0>(wf[i], xf[0][j], acc[i][j], sw[i], sx[1][j]);
-        __builtin_amdgcn_sched_barrier(0);
+          xf[h][j] = *reinterpret_cast<const u32x4*>(base + kW + (wn + j * kMfma + l) * 128 + p);
+#pragma unroll
+        for (int i = 0; i < FR; ++i) {
+          // the registers of the group before
+          if (i > 0) {
+            wf[i - 1] = *reinterpret_cast<const u32x4*>(wb + (i - 1) * kMfma * 128 + p);
+            if (h == 0) sw[i - 1] = *reinterpret_cast<const uint16_t*>(wsb + (i - 1) * kMfma * 32);
+          } else if (h == 1) {
+            wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (p ^ 16));
+            sw[FR - 1] = *reinterpret_cast<const uint16_t*>(wsb + (FR - 1) * kMfma * 32);
+          }
+#pragma unroll
+          for (int j = 0; j < FT; ++j)
+            acc[i][j] = h == 0 ? mfma_fp4<1>(wf[i], xf[1][j], acc[i][j], sw[i], sx[0][j])
+                               : mfma_fp4<0>(wf[i], xf[0][j], acc[i][j], sw[i], sx[1][j]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
+      wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (((2 * q + 1) ^ (l & 7)) * 16));
     }
-    wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (((2 * q + 1) ^ (l & 7)) * 16));
-  }
+  };
+  if (busy) walk(Int<1>());
+  else walk(Int<0>());
 #pragma unroll
   for (int i = 0; i < FR; ++i)
 #pragma unroll
@@ -332,7 +344,10 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_bf16_kernel(MatmulArg
   for (int i = 0; i < FR; ++i)
 #pragma unroll
     for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int wm = (wave / WT) * FR * kMfma, wn = (wave % WT) * FT * kMfma;
+  // neighbouring waves, on different SIMDs, share their rows of x; those past a partial tile's last
+  // row only help to load (and decode)
+  const int wm = (wave % WR) * FR * kMfma, wn = (wave / WR) * FT * kMfma;
+  const bool busy = wn < nt;
   const int l = lane & 15, q = lane >> 4;
 
   load_w(NS - 1, first);
@@ -356,48 +371,60 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_bf16_kernel(MatmulArg
   for (int i = 0; i < FR; ++i) wf[i] = zero;
 #pragma unroll
   for (int j = 0; j < FT; ++j) xf[1][j] = zero;
-  int slot = 0;
-  for (int kt = first; kt < steps; ++kt) {
-    const int buf = (kt - first) & 1;
-    wait_loads<(NS - 2) * kLoads>();
-    step_barrier();
-    load_group(slot == 0 ? NS - 1 : slot - 1, kt + NS - 1);
-    typename D::Planes t;
-    typename D::Eight v;
-    const typename D::Run u = fetch(slot, kt + 1);
-    const uint8_t* wb = lds + buf * kW + (wm + l) * 128;
-    const uint8_t* xb = lds + 2 * kW + slot * kSlot + (wn + l) * 128;
-    __builtin_amdgcn_sched_barrier(0);
-    // half 0 of the pass: instructions of the step before, on its second half's fragments, while
-    // this step's first half is read; half 1: this step's first half, while its second is read
+  auto walk = [&](auto with_products) __attribute__((always_inline)) {
+    constexpr bool kMul = decltype(with_products)::value != 0;
+    int slot = 0;
+    for (int kt = first; kt < steps; ++kt) {
+      const int buf = (kt - first) & 1;
+      wait_loads<(NS - 2) * kLoads>();
+      step_barrier();
+      load_group(slot == 0 ? NS - 1 : slot - 1, kt + NS - 1);
+      typename D::Planes t;
+      typename D::Eight v;
+      const typename D::Run u = fetch(slot, kt + 1);
+      const uint8_t* wb = lds + buf * kW + (wm + l) * 128;
+      const uint8_t* xb = lds + 2 * kW + slot * kSlot + (wn + l) * 128;
+      __builtin_amdgcn_sched_barrier(0);
+      // half 0 of the pass: instructions of the step before, on its second half's fragments, while
+      // this step's first half is read; half 1: this step's first half, while its second is read
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int p = ((4 * h + q) ^ (l & 7)) * 16;
+      for (int h = 0; h < 2; ++h) {
+        const int p = ((4 * h + q) ^ (l & 7)) * 16;
 #pragma unroll
-      for (int j = 0; j < FT; ++j)
-        xf[h][j] = *reinterpret_cast<const u32x4*>(xb + j * kMfma * 128 + p);
+        for (int j = 0; j < FT; ++j)
+          if (kMul) xf[h][j] = *reinterpret_cast<const u32x4*>(xb + j * kMfma * 128 + p);
 #pragma unroll
-      for (int i = 0; i < FR; ++i) {
-        // the registers of the group before
-        if (i > 0) wf[i - 1] = *reinterpret_cast<const u32x4*>(wb + (i - 1) * kMfma * 128 + p);
-        else if (h == 1) wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (p ^ 64));
+        for (int i = 0; i < FR; ++i) {
+          // the registers of the group before
+          if (!kMul) {
+          } else if (i > 0) {
+            wf[i - 1] = *reinterpret_cast<const u32x4*>(wb + (i - 1) * kMfma * 128 + p);
+          } else if (h == 1) {
+            wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (p ^ 64));
+          }
 #pragma unroll
-        for (int j = 0; j < FT; ++j) acc[i][j] = mfma_bf16(wf[i], xf[h ^ 1][j], acc[i][j]);
-        // the decoding in sixteen parts beside the instructions; the barriers keep the compiler
-        // from gathering the reads, or the vector work, of several parts
-        constexpr int kParts = 8 / FR;
+          for (int j = 0; j < FT; ++j)
+            if (kMul) acc[i][j] = mfma_bf16(wf[i], xf[h ^ 1][j], acc[i][j]);
+          // the decoding in sixteen parts beside the instructions; the barriers keep the compiler
+          // from gathering the reads, or the vector work, of several parts
+          constexpr int kParts = 8 / FR;
 #pragma unroll
-        for (int n = 0; n < kParts; ++n) {
-          const int w = (h * FR + i) * kParts + n;
-          dec.piece(u, w / 4, w % 4, t, v);
-          if (w % 4 == 3) put(buf ^ 1, w / 4, v.out);
+          for (int n = 0; n < kParts; ++n) {
+            const int w = (h * FR + i) * kParts + n;
+            dec.piece(u, w / 4, w % 4, t, v);
+            if (w % 4 == 3) put(buf ^ 1, w / 4, v.out);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
+      if (kMul)
+        wf[FR - 1] =
+            *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (((4 + q) ^ (l & 7)) * 16));
+      slot = slot + 1 == NS ? 0 : slot + 1;
     }
-    wf[FR - 1] = *reinterpret_cast<const u32x4*>(wb + (FR - 1) * kMfma * 128 + (((4 + q) ^ (l & 7)) * 16));
-    slot = slot + 1 == NS ? 0 : slot + 1;
-  }
+  };
+  if (busy) walk(Int<1>());
+  else walk(Int<0>());
 #pragma unroll
   for (int i = 0; i < FR; ++i)
 #pragma unroll
