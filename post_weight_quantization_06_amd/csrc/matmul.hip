@@ -35,11 +35,12 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // ceil(workgroups / CUs) of them, two at a time where LDS holds two, which takes kTwo of one after the
 // other. A split adds a launch and the traffic of the parts. It picks, in microseconds and packed
 // weights of 14336 x 4096: 64 rows: 64 wide, split 4 (32; unsplit 53); 512 rows: 256 wide, split 2
-// (85; 128 wide unsplit 96); 2048 rows: 256 wide unsplit (250; 128 wide 334).
+// (85; 128 wide unsplit 96); 2048 rows: 256 wide unsplit (250; 128 wide 334). Tiles of 64 weight rows
+// double the workgroups of a short MXFP4 product: 48 rows against 14336 x 4096 in 16.2 us, 17.0 in 128.
 struct TileCost { int bm, bn; double step; bool two; };
 constexpr TileCost kBf16Tiles[] = {{128, 32, 0.70, true}, {128, 64, 0.77, true}, {128, 128, 0.96, true},
                                    {256, 256, 1.85, false}};
-constexpr TileCost kMxTiles[] = {{128, 64, 0.60, true}, {128, 128, 0.75, true}, {256, 256, 1.90, false}};
+constexpr TileCost kMxTiles[] = {{64, 64, 0.45, true}, {128, 64, 0.60, true}, {128, 128, 0.75, true}, {256, 256, 1.90, false}};
 constexpr double kTile = 2.3, kTwoBf16 = 0.80, kTwoMx = 0.95, kLaunch = 3.0, kPartBytes = 6e6;
 
 template <int N>

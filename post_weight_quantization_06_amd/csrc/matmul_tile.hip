@@ -467,7 +467,7 @@ hipError_t launch_tile_packed(const MatmulArgs& a, const MatmulPlan& p, hipStrea
 
 hipError_t launch_tile_mxfp4(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
   switch (p.bn) {
-    case 64: return tile_mxfp4<2, 2, 4, 2>(a, stream);
+    case 64: return p.bm == 64 ? tile_mxfp4<1, 4, 4, 1>(a, stream) : tile_mxfp4<2, 2, 4, 2>(a, stream);
     case 128: return tile_mxfp4<2, 2, 4, 4>(a, stream);
     default: return tile_mxfp4<2, 4, 8, 4>(a, stream);
   }
