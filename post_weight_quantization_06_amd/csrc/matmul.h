@@ -24,7 +24,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64
 __device__ __forceinline__ u32x4 buffer_load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
 }
-// An offset past every such buffer, also with a row's columns added to it.
+// An offset past every such buffer, also with a tile's rows and columns added to it (below 2^29).
 constexpr uint32_t kOutside = 0x80000000u;
 
 typedef __attribute__((address_space(3))) void* LdsPtr;
