@@ -100,6 +100,8 @@ class MXFP4Matrix:
                out: Optional[torch.Tensor] = None,
                dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """x times the transposed matrix (see mxfp4_matmul)."""
+        if x.shape[-1] != self.C:
+            raise ValueError("x has %d columns, the weights %d" % (x.shape[-1], self.C))
         return mxfp4_matmul(self.codes, self.scales, x, offsets, act, out, dtype)
 
 

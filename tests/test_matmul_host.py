@@ -218,3 +218,12 @@ def test_stacking_experts_of_different_shapes_is_refused():
     b = types.SimpleNamespace(R=4, C=64, g=32, S=16, n=16)
     with pytest.raises(ValueError, match="expert 1"):
         P.PackedExperts.stack([a, b])
+
+
+@pytest.mark.parametrize("K", [33, 39, 41, 64])
+def test_mxfp4_matrix_refuses_other_columns_with_as_many_blocks(K):
+    import post_weight_quantization_06_amd as P
+
+    m = P.MXFP4Matrix(40, torch.zeros(16, 32, dtype=torch.uint8), torch.zeros(16, 2, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="x has %d columns, the weights 40" % K):
+        m.matmul(torch.zeros(4, K, dtype=torch.bfloat16), act="mxfp4")
