@@ -75,11 +75,11 @@ __device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
 // 2 q + 1 (q = l >> 4) of its row for the step's two halves, so its two scale bytes are neighbours.
 // In LDS the eight 16-byte pieces of a row lie permuted by row bits 1 to 3 (piece_turn). Permuted by
 // bits 0 to 2, half of the LDS's cycles were bank conflicts (15.1 M of 30.3 M, now 4.1 M of 19.3 M; the
-// case below took 151 us instead of 148).
+// case below took 149 us instead of 144).
 // Fragments are half a step ahead of the matrix instructions: a barrier falls between the two halves
 // of a step's instructions, and each register is read again as soon as it has been used.
 //
-// 4096 x 14336 x 4096: 148 us, 3.2 PFLOP/s, of the 8.8 that the instruction alone reaches here. What
+// 4096 x 14336 x 4096: 144 us, 3.3 PFLOP/s, of the 8.8 that the instruction alone reaches here. What
 // bounds it is the supply of the stages: without its matrix instructions it takes 87 % of the time,
 // without its loads 79 %. Eight waves of 128 x 64 rather than four of 128 x 128: four need 512
 // registers each and spill. Rows of x tiles advancing together (1 to 16 of them) and touching lines
