@@ -297,8 +297,10 @@ struct MxDecoder {
 // third puts the two bytes of an entry where fp32 keeps them. One product and one rounding follow,
 // as in dequant.
 // LG: log2 of the scale group, 7 for 128 and more. LS: the same of the selection group when its
-// selectors are in the bitmap, 0 when they are the scales' sign bits (S == g).
-template <int LG, int LS>
+// selectors are in the bitmap, 0 when they are the scales' sign bits (S == g). OFF: the scales start
+// two bytes past a word, with LG < 5, where a run's scales are whole words otherwise (C / g is even
+// there, so every row starts as the first one does); the tiles then read a word more a run.
+template <int LG, int LS, bool OFF = false>
 struct PackedDecoder {
   static constexpr bool kSign = LS == 0;
   static constexpr bool kFour = kSign && LG >= 6;                   // see load_four
@@ -386,7 +388,7 @@ struct PackedDecoder {
     return v.out;
   }
 
-  static constexpr int kScaleLoads = (kGpl + 1) / 2;                // words with a run's scales
+  static constexpr int kScaleLoads = (kGpl + 1) / 2 + (OFF ? 1 : 0);  // words with a run's scales
   static constexpr int kWords = kScaleLoads + (kSign ? 0 : 1);
   u32x4 codes_buf, scales_buf, bits_buf;
   uint32_t lead, bits_lead;                      // see words_buffer; bits_lead in bits
@@ -432,6 +434,9 @@ struct PackedDecoder {
       const uint32_t w = words[i * threads];
       if (kGpl == 1) {
         u.scale[0] = w >> (8 * (at & 2u));
+      } else if (OFF) {
+        if (i > 0) u.scale[2 * i - 1] = w;
+        if (2 * i < kGpl) u.scale[2 * i] = w >> 16;
       } else {
         u.scale[2 * i] = w;
         u.scale[2 * i + 1] = w >> 16;
@@ -535,10 +540,15 @@ struct PackedDecoder {
   }
 };
 
-// Calls f with the decoder type of a packed call.
-template <class F>
+// Calls f with the decoder type of a packed call. TILES: f reads weights by runs.
+template <bool TILES, class F>
 hipError_t with_packed_decoder(const MatmulArgs& a, F f) {
   const int lg = a.log2g < 7 ? a.log2g : 7, ls = a.log2S < 7 ? a.log2S : 7;
+  if constexpr (TILES) {
+    if (lg < 5 && (uintptr_t)a.scales % 4 != 0)
+      return a.bitmap ? f(PackedDecoder<4, 3, true>())
+             : lg == 3 ? f(PackedDecoder<3, 0, true>()) : f(PackedDecoder<4, 0, true>());
+  }
   if (!a.bitmap) {
     switch (lg) {
       case 3: return f(PackedDecoder<3, 0>());

@@ -342,7 +342,8 @@ hipError_t launch_few_mx_bf16(const MatmulArgs& a, const MatmulPlan& p, hipStrea
 }
 
 hipError_t launch_few_packed(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
-  return with_packed_decoder(a, [&](auto d) { return few_bf16_any<decltype(d)>(a, p, stream); });
+  return with_packed_decoder<false>(
+      a, [&](auto d) { return few_bf16_any<decltype(d)>(a, p, stream); });
 }
 
 }  // namespace aaac

@@ -470,7 +470,8 @@ hipError_t launch_tile_mx_bf16(const MatmulArgs& a, const MatmulPlan& p, hipStre
 }
 
 hipError_t launch_tile_packed(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
-  return with_packed_decoder(a, [&](auto d) { return tile_bf16_any<decltype(d)>(a, p, stream); });
+  return with_packed_decoder<true>(
+      a, [&](auto d) { return tile_bf16_any<decltype(d)>(a, p, stream); });
 }
 
 hipError_t launch_tile_mxfp4(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
