@@ -64,7 +64,7 @@ template <class D, int RT, int NT, int W, int U>
 __global__ __launch_bounds__(W * kWave, 1) void few_bf16_kernel(MatmulArgs a) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
-  const int64_t tile = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
+  const int64_t id = block_id(), tile = id / a.row_blocks, rb = id % a.row_blocks;
   int e;
   int64_t t0, t1;
   if (!find_tile(a.offsets, a.E, a.T, NT * kMfma, tile, e, t0, t1)) return;
@@ -218,7 +218,7 @@ __device__ __forceinline__ u32x4 load_scales(const uint8_t* p, int left) {
 template <int RT, int NT, int W>
 __global__ __launch_bounds__(W * kWave, 1) void few_mxfp4_kernel(MatmulArgs a) {
   const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
-  const int64_t tile = blockIdx.x / a.row_blocks, rb = blockIdx.x % a.row_blocks;
+  const int64_t id = block_id(), tile = id / a.row_blocks, rb = id % a.row_blocks;
   int e;
   int64_t t0, t1;
   if (!find_tile(a.offsets, a.E, a.T, NT * kMfma, tile, e, t0, t1)) return;
@@ -307,7 +307,7 @@ hipError_t few_bf16(MatmulArgs a, hipStream_t stream) {
   a.x_rows = (int)(most < want ? most : want);
   const int64_t x_lds = a.x_rows * x_row_bytes(a.C);
   const int lds = (int)(x_lds > join_bytes<RT, NT, W>() ? x_lds : join_bytes<RT, NT, W>());
-  hipLaunchKernelGGL((few_bf16_kernel<D, RT, NT, W, U>), dim3((unsigned)grid), dim3(W * kWave), lds,
+  hipLaunchKernelGGL((few_bf16_kernel<D, RT, NT, W, U>), grid_of(grid), dim3(W * kWave), lds,
                      stream, a);
   return hipGetLastError();
 }
@@ -324,7 +324,7 @@ hipError_t few_bf16_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t st
 template <int RT, int NT, int W>
 hipError_t few_mxfp4(MatmulArgs a, hipStream_t stream) {
   const int64_t grid = few_grid<RT, NT>(a);
-  hipLaunchKernelGGL((few_mxfp4_kernel<RT, NT, W>), dim3((unsigned)grid), dim3(W * kWave), 0, stream,
+  hipLaunchKernelGGL((few_mxfp4_kernel<RT, NT, W>), grid_of(grid), dim3(W * kWave), 0, stream,
                      a);
   return hipGetLastError();
 }

@@ -96,7 +96,8 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulAr
   constexpr int kW = BM * 128, kX = BN * 128, kStage = kW + kX, kWs = BM * 32, kScales = kWs + BN * 32;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * (kStage + kScales)];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
-  const int64_t id = by_die(blockIdx.x, gridDim.x), tiles = gridDim.x / a.split;
+  if (block_id() >= a.blocks) return;
+  const int64_t id = by_die(block_id(), a.blocks), tiles = a.blocks / a.split;
   const int part = (int)(id / tiles);
   const int64_t tile = id % tiles / a.row_blocks, rb = id % a.row_blocks;
   int e;
@@ -251,13 +252,13 @@ template <int WR, int WT, int FR, int FT>
 hipError_t tile_mxfp4(MatmulArgs a, hipStream_t stream) {
   constexpr int BM = WR * FR * kMfma, BN = WT * FT * kMfma;
   a.row_blocks = (a.R + BM - 1) / BM;
-  const int64_t grid = a.row_blocks * token_tiles(a, BN) * a.split;
+  a.blocks = a.row_blocks * token_tiles(a, BN) * a.split;
   const bool whole = a.Cp % 256 == 0 && (uintptr_t)a.scales % 4 == 0 && (uintptr_t)a.x_scales % 4 == 0;
   if (whole)
-    hipLaunchKernelGGL((tile_mxfp4_kernel<WR, WT, FR, FT, true>), dim3((unsigned)grid),
+    hipLaunchKernelGGL((tile_mxfp4_kernel<WR, WT, FR, FT, true>), grid_of(a.blocks),
                        dim3(WR * WT * kWave), 0, stream, a);
   else
-    hipLaunchKernelGGL((tile_mxfp4_kernel<WR, WT, FR, FT, false>), dim3((unsigned)grid),
+    hipLaunchKernelGGL((tile_mxfp4_kernel<WR, WT, FR, FT, false>), grid_of(a.blocks),
                        dim3(WR * WT * kWave), 0, stream, a);
   return hipGetLastError();
 }
@@ -289,7 +290,8 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_bf16_kernel(MatmulArg
   constexpr int kLoads = BN / 8 / NW + 1 + D::kWords;        // a wave's loads in a group
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kW + NS * kSlot];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
-  const int64_t id = by_die(blockIdx.x, gridDim.x), tiles = gridDim.x / a.split;
+  if (block_id() >= a.blocks) return;
+  const int64_t id = by_die(block_id(), a.blocks), tiles = a.blocks / a.split;
   const int part = (int)(id / tiles);
   const int64_t tile = id % tiles / a.row_blocks, rb = id % a.row_blocks;
   int e;
@@ -447,8 +449,8 @@ template <class D, int WR, int WT, int FR, int FT, int NS>
 hipError_t tile_bf16(MatmulArgs a, hipStream_t stream) {
   constexpr int BM = WR * FR * kMfma, BN = WT * FT * kMfma;
   a.row_blocks = (a.R + BM - 1) / BM;
-  const int64_t grid = a.row_blocks * token_tiles(a, BN) * a.split;
-  hipLaunchKernelGGL((tile_bf16_kernel<D, WR, WT, FR, FT, NS>), dim3((unsigned)grid),
+  a.blocks = a.row_blocks * token_tiles(a, BN) * a.split;
+  hipLaunchKernelGGL((tile_bf16_kernel<D, WR, WT, FR, FT, NS>), grid_of(a.blocks),
                      dim3(WR * WT * kWave), 0, stream, a);
   return hipGetLastError();
 }

@@ -17,6 +17,18 @@ __host__ __device__ __forceinline__ int64_t mx_blocks(int64_t C) {
   return (C + kMxBlock - 1) / kMxBlock;
 }
 
+// A grid of `blocks` workgroups numbered by block_id(). A dimension of a grid holds fewer than 2^32
+// threads (a launch of more is cut without an error), so long grids go over two; the last workgroups
+// may then lie past `blocks`.
+inline dim3 grid_of(int64_t blocks) {
+  constexpr int64_t kRow = (int64_t)1 << 22;     // workgroups of at most 512 threads
+  if (blocks <= kRow) return dim3((unsigned)blocks);
+  return dim3((unsigned)kRow, (unsigned)((blocks + kRow - 1) / kRow));
+}
+__device__ __forceinline__ int64_t block_id() {
+  return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+}
+
 hipError_t launch_mxfp4_quantize(const void* X, int x_type, int64_t M, int64_t C, int64_t ldx,
                                  uint8_t* codes, uint8_t* scales, hipStream_t stream);
 hipError_t launch_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t C,
@@ -46,6 +58,7 @@ struct MatmulArgs {
   int split;                   // workgroups that share a tile's columns; their sums lie in parts
   float* parts;                // [split, T, part_row(R)], with split > 1
   int64_t row_blocks;          // set by the launcher: row blocks of one expert
+  int64_t blocks;              // set by the launcher of tiles: workgroups that have one
   int x_rows;                  // set by the launcher: rows of x that the workgroup's LDS holds
 };
 

@@ -95,7 +95,7 @@ template <int TYPE, bool VEC, bool FLAT>
 __global__ __launch_bounds__(kBlock) void mxfp4_quantize_kernel(
     const typename Elem<TYPE>::T* __restrict__ X, int64_t C, int64_t ldx, int64_t lanes_per_row,
     int64_t total, uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const int64_t i0 = (int64_t)blockIdx.x * (kBlock * kMxSteps) + threadIdx.x;
+  const int64_t i0 = block_id() * (kBlock * kMxSteps) + threadIdx.x;
   float v[kMxSteps][8];
 #pragma unroll
   for (int u = 0; u < kMxSteps; ++u) {
@@ -164,7 +164,7 @@ template <int TYPE, bool FLAT>
 __global__ __launch_bounds__(kBlock) void mxfp4_dequant_kernel(
     const uint32_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t C, int64_t ldy,
     int64_t lanes_per_row, int64_t total, bool vec, typename Elem<TYPE>::T* __restrict__ Y) {
-  const int64_t i0 = (int64_t)blockIdx.x * (kBlock * kMxSteps) + threadIdx.x;
+  const int64_t i0 = block_id() * (kBlock * kMxSteps) + threadIdx.x;
   uint32_t word[kMxSteps], byte[kMxSteps];
 #pragma unroll
   for (int u = 0; u < kMxSteps; ++u) {
@@ -210,7 +210,7 @@ hipError_t quantize_t(const void* X, int64_t M, int64_t C, int64_t ldx, uint8_t*
   const bool vec = ((uintptr_t)X % 16 == 0) && (ldx * sizeof(T)) % 16 == 0;
   const bool flat = vec && C % kMxBlock == 0 && (ldx == C || M == 1);
   const int64_t per = kBlock * kMxSteps;
-  const dim3 grid((unsigned)((total + per - 1) / per));
+  const dim3 grid = grid_of((total + per - 1) / per);
   uint32_t* cw = reinterpret_cast<uint32_t*>(codes);
   if (flat)
     hipLaunchKernelGGL((mxfp4_quantize_kernel<TYPE, true, true>), grid, dim3(kBlock), 0, stream, x,
@@ -233,7 +233,7 @@ hipError_t dequant_t(const uint8_t* codes, const uint8_t* scales, int64_t M, int
   const bool vec = ((uintptr_t)Y % 16 == 0) && (ldy * sizeof(T)) % 16 == 0;
   const bool flat = vec && C % kMxBlock == 0 && (ldy == C || M == 1);
   const int64_t per = kBlock * kMxSteps;
-  const dim3 grid((unsigned)((total + per - 1) / per));
+  const dim3 grid = grid_of((total + per - 1) / per);
   const uint32_t* cw = reinterpret_cast<const uint32_t*>(codes);
   if (flat)
     hipLaunchKernelGGL((mxfp4_dequant_kernel<TYPE, true>), grid, dim3(kBlock), 0, stream, cw,

@@ -84,3 +84,70 @@ def test_mxfp4_scales_at_any_address(act, T):
         _say("mx addresses", act, T, by)
         y = P.mxfp4_matmul(codes[0], _moved(scales[0], by), xd, act=act, dtype=torch.float32)
         assert np.array_equal(y.cpu().numpy(), (xv @ W[0].T).astype(np.float32))
+
+
+# ------------------------------------------------------------------ launches of more than 2^32 threads
+
+def _room(gib):
+    free = torch.cuda.mem_get_info()[0] / 2 ** 30
+    if free < gib:
+        pytest.skip("needs %d GiB of free GPU memory (%.0f are)" % (gib, free))
+
+
+def test_product_of_more_than_2_32_threads():
+    """512 experts of 494000 x 32 with one row each: 8.4 million workgroups of 512 threads."""
+    _room(16)
+    _say("product, over 2^32 threads")
+    E, R, C = 512, 494000, 32
+    gen = torch.Generator(device=DEV).manual_seed(6)
+    codes = torch.randint(0, 256, (E, R, C // 2), generator=gen, device=DEV, dtype=torch.uint8)
+    scales = torch.randint(126, 129, (E, R, 1), generator=gen, device=DEV, dtype=torch.uint8)
+    x = torch.randint(-4, 5, (E, C), generator=gen, device=DEV).to(torch.bfloat16)
+    off = torch.arange(E + 1, device=DEV, dtype=torch.int32)
+    for act in ("bf16", "mxfp4"):
+        y = torch.full((E, R), 99.0, dtype=torch.float32, device=DEV)
+        P.mxfp4_matmul(codes, scales, x, off, act=act, out=y)
+        xv = x.double() if act == "bf16" else P.mxfp4_dequant(*P.mxfp4_quantize(x), C).double()
+        for e in (0, 1, 100, 255, 256, 300, 400, 480, 509, 510, 511):
+            W = P.mxfp4_dequant(codes[e], scales[e], C, dtype=torch.float32).double()
+            assert torch.equal(y[e].double(), (W * xv[e]).sum(1)), e
+    torch.cuda.empty_cache()
+
+
+def test_tiles_of_more_than_2_32_threads():
+    """4096 experts of 494000 x 32 with 17 rows each: 8.4 million workgroups of 512 threads."""
+    _room(130)
+    _say("tiles, over 2^32 threads")
+    E, R, C, N = 4096, 494000, 32, 17
+    gen = torch.Generator(device=DEV).manual_seed(8)
+    codes = torch.randint(0, 256, (E, R, C // 2), generator=gen, device=DEV, dtype=torch.uint8)
+    scales = torch.randint(126, 129, (E, R, 1), generator=gen, device=DEV, dtype=torch.uint8)
+    x = torch.randint(-4, 5, (E * N, C), generator=gen, device=DEV).to(torch.bfloat16)
+    off = torch.arange(0, E * N + 1, N, device=DEV, dtype=torch.int32)
+    y = torch.full((E * N, R), 99.0, dtype=torch.bfloat16, device=DEV)
+    P.mxfp4_matmul(codes, scales, x, off, out=y)
+    for e in (0, 1, 1000, 2047, 2048, 3000, 4000, 4080, 4094, 4095):
+        W = P.mxfp4_dequant(codes[e], scales[e], C, dtype=torch.float32).double()
+        want = x[e * N:e * N + N].double() @ W.t().contiguous()
+        assert torch.equal(y[e * N:e * N + N], want.to(torch.bfloat16)), e
+    del codes, scales, y
+    torch.cuda.empty_cache()
+
+
+def test_mxfp4_of_2_32_threads_and_more():
+    """2^32 + 100 rows of one column: a thread a row, rows past 32 bits."""
+    _room(100)
+    _say("mxfp4, over 2^32 threads")
+    M = 2 ** 32 + 100
+    x = torch.empty(M, 1, dtype=torch.bfloat16, device=DEV)
+    x.normal_(generator=torch.Generator(device=DEV).manual_seed(7))
+    codes, scales = P.mxfp4_quantize(x)
+    back = torch.full((M, 1), 99.0, dtype=torch.bfloat16, device=DEV)
+    P.mxfp4_dequant(codes, scales, 1, out=back)
+    for r in (0, 2 ** 24, 2 ** 30 - 256, 2 ** 31 - 256, 2 ** 32 - 4096, 2 ** 32 - 256, M - 512):
+        wc, ws = ref.mxfp4_encode(x[r:r + 512].double().cpu().numpy())
+        assert np.array_equal(scales[r:r + 512].cpu().numpy(), ws), r
+        assert np.array_equal(codes[r:r + 512, 0].cpu().numpy(), wc[:, 0]), r
+        assert np.array_equal(back[r:r + 512].double().cpu().numpy(), ref.mxfp4_decode(wc, ws, 1)), r
+    del x, codes, scales, back
+    torch.cuda.empty_cache()
