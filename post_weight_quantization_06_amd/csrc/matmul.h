@@ -43,11 +43,12 @@ __device__ __forceinline__ u32x4 words_buffer(const void* p, int64_t bytes, uint
 }
 
 // Asynchronous loads from a buffer into LDS: lane l's bytes land at dst + l * size (dst uniform).
-// `more` is a uniform offset, kept out of what the hardware may or may not count when it checks the
-// range: rows are clamped by the caller, and kOutside is outside with or without it.
+// `more` is a uniform offset below the buffer's bytes. The range check takes it from the buffer's bytes
+// before it compares, so a larger one could wrap round to a range that kOutside lies in; a smaller one
+// leaves kOutside outside whether it is counted or not.
 // In assembly because the compiler would wait for them before any LDS read, of the other stage too;
-// the caller waits (stage_ready) before the barrier after which they are read. The move to m0 needs
-// one wait state before the load.
+// the caller waits (wait_loads, then step_barrier) before they are read. The move to m0 needs one
+// wait state before the load.
 __device__ __forceinline__ void load_lds16(u32x4 buf, uint32_t off, uint32_t more, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                :: "s"(dst), "v"(off), "s"(buf), "s"(more) : "memory", "m0");
@@ -72,6 +73,11 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+}
+
+// Step `step` of 64 columns lies past the row's end: its loads are outside their buffers.
+__device__ __forceinline__ bool past_row(const MatmulArgs& a, int step) {
+  return step * 64 >= (int)a.Cp;
 }
 
 constexpr int kMfma = 16;                        // rows and columns of one matrix instruction
@@ -241,7 +247,8 @@ struct MxDecoder {
   __device__ __forceinline__ void issue(const MatmulArgs& a, int row, int step, int half, bool in,
                                         uint32_t dst, uint32_t words, int) const {
     const uint32_t kb = (uint32_t)(a.Cp >> 5);
-    load_lds16(codes_buf, in ? row * (kb * 16) + half / 2 : kOutside, step * 32, dst);
+    load_lds16(codes_buf, in ? row * (kb * 16) + half / 2 : kOutside, past_row(a, step) ? 0 : step * 32,
+               dst);
     load_lds4(scales_buf, in ? (lead + row * kb + 2 * step + half / 32) & ~3u : kOutside, words);
   }
   __device__ __forceinline__ Run fetch(const MatmulArgs& a, int row, int step, int half, bool,
@@ -413,7 +420,8 @@ struct PackedDecoder {
   }
   __device__ __forceinline__ void issue(const MatmulArgs& a, int row, int step, int half, bool in,
                                         uint32_t dst, uint32_t words, int threads) const {
-    load_lds16(codes_buf, in ? row * (uint32_t)(a.C >> 1) + half / 2 : kOutside, step * 32, dst);
+    load_lds16(codes_buf, in ? row * (uint32_t)(a.C >> 1) + half / 2 : kOutside,
+               past_row(a, step) ? 0 : step * 32, dst);
     const uint32_t at = scale_at(a, row, step, half) & ~3u;
 #pragma unroll
     for (int i = 0; i < kScaleLoads; ++i)

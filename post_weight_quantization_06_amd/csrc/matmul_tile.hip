@@ -335,7 +335,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_bf16_kernel(MatmulArg
       const bool in = kt < steps && kt * 64 + piece * 8 < cols;
 #pragma unroll
       for (int i = 0; i < kXl; ++i)
-        load_lds16(xr, in ? xoff[i] : kOutside, kt * 128, dst + i * 1024);
+        load_lds16(xr, in ? xoff[i] : kOutside, kt * 64 < cols ? kt * 128 : 0, dst + i * 1024);
     }
     load_w(slot, kt + 1);
   };

@@ -151,3 +151,28 @@ def test_mxfp4_of_2_32_threads_and_more():
         assert np.array_equal(back[r:r + 512].double().cpu().numpy(), ref.mxfp4_decode(wc, ws, 1)), r
     del x, codes, scales, back
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ tiles of one row
+
+@pytest.mark.parametrize("R,T,C", [(129, 33, 64), (129, 65, 320), (257, 129, 96), (513, 97, 800),
+                                   (2753, 1281, 64), (4097, 4097, 64), (4097, 4097, 200), (1, 257, 1280)])
+def test_last_tiles_of_one_row(R, T, C):
+    """One row of x and one weight row in the last tiles: the loads that run ahead of the last step
+    then lie past the ends of the smallest buffers."""
+    rng = np.random.default_rng(R + T + C)
+    codes, scales, W = _mx(rng, 1, R, C, True)
+    x, xd = _x(rng, T, C, True)
+    xv = {"bf16": x, "mxfp4": ref.mxfp4_decode(*ref.mxfp4_encode(x), C)}
+    for act, v in xv.items():
+        _say("one row", act, R, T, C)
+        y = P.mxfp4_matmul(codes[0], scales[0], xd, act=act, dtype=torch.float32)
+        assert np.array_equal(y.cpu().numpy(), (v @ W[0].T).astype(np.float32))
+    if C % 32:
+        return
+    for g, S in ((32, 32), (16, 8)):
+        _say("one row", g, S, R, T, C)
+        pc, ps, pb, pt, pW = _packed(rng, 1, R, C, g, S, 16, True)
+        y = P.packed_matmul(pc[0], ps[0], None if pb is None else pb[0], pt[0], xd, g, S, 16,
+                            dtype=torch.float32)
+        assert np.array_equal(y.cpu().numpy(), (x @ pW[0].T).astype(np.float32))
