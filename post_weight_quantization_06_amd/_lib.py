@@ -14,6 +14,7 @@ import os
 from typing import Optional, Sequence
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libaaac.so")
@@ -598,6 +599,8 @@ def _on_gpu(what: str, *tensors):
 def _no_grad(what: str, x: torch.Tensor):
     if x.requires_grad and torch.is_grad_enabled():
         raise ValueError("%s has no gradient: call it under torch.no_grad() or detach x" % what)
+    if unpack_dual(x).tangent is not None:     # 0.3 us of a call
+        raise ValueError("%s has no forward-mode gradient: detach x, which carries a tangent" % what)
 
 
 def _launch(name: str, dev: int, stream, *args):

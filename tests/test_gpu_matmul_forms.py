@@ -176,3 +176,22 @@ def test_last_tiles_of_one_row(R, T, C):
         y = P.packed_matmul(pc[0], ps[0], None if pb is None else pb[0], pt[0], xd, g, S, 16,
                             dtype=torch.float32)
         assert np.array_equal(y.cpu().numpy(), (x @ pW[0].T).astype(np.float32))
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_forward_mode_tangents_are_refused_by_every_call():
+    import torch.autograd.forward_ad as fw
+
+    rng = np.random.default_rng(14)
+    mc, ms, _ = _mx(rng, 1, 16, 64, True)
+    pc, ps, pb, pt, _ = _packed(rng, 1, 16, 64, 32, 16, 16, True)
+    x = torch.ones(4, 64, dtype=torch.bfloat16, device=DEV)
+    with fw.dual_level():
+        d = fw.make_dual(x, torch.ones_like(x))
+        for call in (lambda v: P.mxfp4_quantize(v), lambda v: P.mxfp4_matmul(mc[0], ms[0], v),
+                     lambda v: P.mxfp4_matmul(mc[0], ms[0], v, act="mxfp4"),
+                     lambda v: P.packed_matmul(pc[0], ps[0], pb[0], pt[0], v, 32, 16, 16)):
+            with pytest.raises(ValueError, match="tangent"):
+                call(d)
+            call(d.detach())

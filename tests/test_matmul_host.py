@@ -227,3 +227,23 @@ def test_mxfp4_matrix_refuses_other_columns_with_as_many_blocks(K):
     m = P.MXFP4Matrix(40, torch.zeros(16, 32, dtype=torch.uint8), torch.zeros(16, 2, dtype=torch.uint8))
     with pytest.raises(ValueError, match="x has %d columns, the weights 40" % K):
         m.matmul(torch.zeros(4, K, dtype=torch.bfloat16), act="mxfp4")
+
+
+def test_forward_mode_tangents_are_refused():
+    """A dual tensor does not require a gradient, and its tangent would be lost without a word."""
+    import torch.autograd.forward_ad as fw
+
+    import post_weight_quantization_06_amd as P
+
+    x = torch.zeros(2, 32)
+    P._lib._no_grad("call", x)
+    with fw.dual_level():
+        d = fw.make_dual(x, torch.ones_like(x))
+        assert not d.requires_grad
+        for v in (d, d[:1], d.reshape(-1)):
+            with pytest.raises(ValueError, match="tangent"):
+                P._lib._no_grad("call", v)
+        with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+            P._lib._no_grad("call", d)
+        P._lib._no_grad("call", d.detach())
+        P._lib._no_grad("call", x)
