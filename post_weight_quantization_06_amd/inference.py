@@ -52,12 +52,20 @@ def _rows_of(x: torch.Tensor, R: int, out: Optional[torch.Tensor], dtype: torch.
 def mxfp4_matmul(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
                  offsets: Optional[torch.Tensor] = None, act: str = "bf16",
                  out: Optional[torch.Tensor] = None,
-                 dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+                 dtype: torch.dtype = torch.bfloat16, C: Optional[int] = None) -> torch.Tensor:
     """[..., R] = x [..., C] times the transposed MXFP4 matrix (codes [R, Cp/2]), or with offsets
     each row times its expert's (codes [E, R, Cp/2]). act "bf16": x bf16 as it is; "mxfp4": x (bf16,
     fp16 or fp32) is quantized to MXFP4 first and the product is one of 4-bit values. Without `out`,
-    rows outside the offsets hold nothing defined; with it they stay as they were."""
-    C = x.shape[-1]
+    rows outside the offsets hold nothing defined; with it they stay as they were.
+
+    C: the width that the weights were quantized at, to refuse an x of another one. Codes hold whole
+    blocks of 32 columns, so without C an x of any width with as many blocks is multiplied, its missing
+    columns as zeros and those past the weights' width by zeros (MXFP4Matrix knows its C)."""
+    K = x.shape[-1]
+    if C is None:
+        C = K
+    elif C != K:
+        raise ValueError("x has %d columns, the weights %d" % (K, C))
     x2, y2, out = _rows_of(x, codes.shape[-2], out, dtype)
     if act == "bf16":
         L.aaac_mxfp4_matmul(codes, scales, C, x2, y2, offsets)
@@ -100,9 +108,7 @@ class MXFP4Matrix:
                out: Optional[torch.Tensor] = None,
                dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """x times the transposed matrix (see mxfp4_matmul)."""
-        if x.shape[-1] != self.C:
-            raise ValueError("x has %d columns, the weights %d" % (x.shape[-1], self.C))
-        return mxfp4_matmul(self.codes, self.scales, x, offsets, act, out, dtype)
+        return mxfp4_matmul(self.codes, self.scales, x, offsets, act, out, dtype, self.C)
 
 
 @dataclasses.dataclass

@@ -195,3 +195,18 @@ def test_forward_mode_tangents_are_refused_by_every_call():
             with pytest.raises(ValueError, match="tangent"):
                 call(d)
             call(d.detach())
+
+
+def test_mxfp4_matmul_with_the_width_given():
+    rng = np.random.default_rng(15)
+    codes, scales, W = _mx(rng, 1, 16, 40, True)
+    x, xd = _x(rng, 6, 40, True)
+    want = (x @ W[0].T).astype(np.float32)
+    m = P.MXFP4Matrix(40, codes[0], scales[0])
+    for y in (P.mxfp4_matmul(codes[0], scales[0], xd, dtype=torch.float32, C=40),
+              P.mxfp4_matmul(codes[0], scales[0], xd, dtype=torch.float32),
+              m.matmul(xd, dtype=torch.float32)):
+        assert np.array_equal(y.cpu().numpy(), want)
+    wide = torch.zeros(6, 64, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="64 columns, the weights 40"):
+        P.mxfp4_matmul(codes[0], scales[0], wide, C=40)

@@ -247,3 +247,15 @@ def test_forward_mode_tangents_are_refused():
             P._lib._no_grad("call", d)
         P._lib._no_grad("call", d.detach())
         P._lib._no_grad("call", x)
+
+
+@pytest.mark.parametrize("K", [33, 39, 41, 64])
+def test_mxfp4_matmul_refuses_other_columns_than_its_c(K):
+    import post_weight_quantization_06_amd as P
+
+    codes, scales = torch.zeros(16, 32, dtype=torch.uint8), torch.zeros(16, 2, dtype=torch.uint8)
+    for act in ("bf16", "mxfp4"):
+        with pytest.raises(ValueError, match="x has %d columns, the weights 40" % K):
+            P.mxfp4_matmul(codes, scales, torch.zeros(4, K, dtype=torch.bfloat16), act=act, C=40)
+    with pytest.raises(ValueError, match="GPU"):             # the right width goes on to the next check
+        P.mxfp4_matmul(codes, scales, torch.zeros(4, 40, dtype=torch.bfloat16), C=40)
