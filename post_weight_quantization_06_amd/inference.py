@@ -30,12 +30,19 @@ def mxfp4_quantize(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     return codes, scales
 
 
+def _last_axis(out: torch.Tensor, n: int):
+    """A result's rows are those of its last axis; one of another length would be filled out of order."""
+    if out.dim() == 0 or out.shape[-1] != n:
+        raise ValueError("out must be [..., %d] (got %s)" % (n, list(out.shape)))
+
+
 def mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor, C: int,
                   dtype: torch.dtype = torch.bfloat16,
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """The values [..., C] of MXFP4 codes."""
+    """The values [..., C] of MXFP4 codes, in `out` (then of its type) or a new tensor of `dtype`."""
     if out is None:
         out = torch.empty(*codes.shape[:-1], C, dtype=dtype, device=codes.device)
+    _last_axis(out, C)
     L.aaac_mxfp4_dequant(codes, scales, out if out.dim() == 2 else out.view(-1, C))
     return out
 
@@ -45,7 +52,8 @@ def _rows_of(x: torch.Tensor, R: int, out: Optional[torch.Tensor], dtype: torch.
     if out is None:
         out = torch.empty(*x.shape[:-1], R, dtype=dtype, device=x.device)
     if x.dim() == 2:
-        return x, out, out
+        return x, out, out                       # the binding compares their shapes
+    _last_axis(out, R)
     return x.reshape(-1, x.shape[-1]), out.view(-1, R), out
 
 

@@ -210,3 +210,18 @@ def test_mxfp4_matmul_with_the_width_given():
     wide = torch.zeros(6, 64, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError, match="64 columns, the weights 40"):
         P.mxfp4_matmul(codes[0], scales[0], wide, C=40)
+
+
+def test_results_of_other_shapes_are_filled_row_by_row_or_refused():
+    rng = np.random.default_rng(16)
+    codes, scales, W = _mx(rng, 1, 24, 64, True)
+    x, xd = _x(rng, 6, 64, True)
+    want = torch.from_numpy((x @ W[0].T).astype(np.float32))
+    for shape in ((2, 3, 24), (6, 24), (3, 2, 24)):
+        y = torch.zeros(shape, device=DEV)
+        P.mxfp4_matmul(codes[0], scales[0], xd.view(2, 3, 64), out=y)
+        assert torch.equal(y.cpu().view(6, 24), want)
+    with pytest.raises(ValueError, match="out must be"):
+        P.mxfp4_matmul(codes[0], scales[0], xd.view(2, 3, 64), out=torch.zeros(24, 6, device=DEV))
+    with pytest.raises(ValueError, match="out must be"):
+        P.mxfp4_dequant(codes[0], scales[0], 64, out=torch.zeros(24, 60, device=DEV))

@@ -259,3 +259,25 @@ def test_mxfp4_matmul_refuses_other_columns_than_its_c(K):
             P.mxfp4_matmul(codes, scales, torch.zeros(4, K, dtype=torch.bfloat16), act=act, C=40)
     with pytest.raises(ValueError, match="GPU"):             # the right width goes on to the next check
         P.mxfp4_matmul(codes, scales, torch.zeros(4, 40, dtype=torch.bfloat16), C=40)
+
+
+def test_results_of_another_last_axis_are_refused():
+    """An out of as many elements whose rows are not the result's, or of another width than C."""
+    import post_weight_quantization_06_amd as P
+
+    codes, scales = torch.zeros(16, 32, dtype=torch.uint8), torch.zeros(16, 2, dtype=torch.uint8)
+    x = torch.zeros(2, 3, 64, dtype=torch.bfloat16)
+    ps, pt = torch.zeros(16, 1, dtype=torch.int16), torch.zeros(2, 16, dtype=torch.int16)
+    for out in (torch.zeros(16, 6), torch.zeros(2, 3, 8), torch.zeros(96), torch.zeros(())):
+        with pytest.raises(ValueError, match=r"out must be \[\.\.\., 16\]"):
+            P.mxfp4_matmul(codes, scales, x, out=out)
+        with pytest.raises(ValueError, match=r"out must be \[\.\.\., 16\]"):
+            P.packed_matmul(codes, ps, None, pt, x, 64, 64, 16, out=out)
+    for C in (33, 40, 64):                           # as many blocks, another width
+        with pytest.raises(ValueError, match=r"out must be \[\.\.\., %d\] \(got \[16, 50\]\)" % C):
+            P.mxfp4_dequant(codes, scales, C, out=torch.zeros(16, 50))
+    for out in (torch.zeros(2, 3, 16), torch.zeros(6, 16)):  # the result's rows: on to the next check
+        with pytest.raises(ValueError, match="GPU"):
+            P.mxfp4_matmul(codes, scales, x, out=out)
+    with pytest.raises(ValueError, match="GPU"):
+        P.mxfp4_dequant(codes, scales, 50, out=torch.zeros(16, 50))
