@@ -374,6 +374,17 @@ aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int6
 size_t aaac_matmul_workspace_bytes(int kind, int64_t E, int64_t R, int64_t C, int64_t T);
 
 /*
+ * How one product call of the given kind runs on the current device, for tests and profiles:
+ *   plan[0], plan[1]  weight rows and rows of x in a tile, both 0 for the few-row kernels;
+ *   plan[2]           workgroups that share a tile's columns (1 without a workspace);
+ *   plan[3] .. [5]    few-row kernels: blocks of 16 weight rows and of 16 rows of x a workgroup,
+ *                     chunks of columns a wave at a time; 0 for tiles.
+ * AAAC_ERR_UNSUPPORTED_SHAPE where aaac_matmul_workspace_bytes knows no such call.
+ */
+aaac_status aaac_matmul_plan(int kind, int64_t E, int64_t R, int64_t C, int64_t T, int has_ws,
+                             int32_t plan[6]);
+
+/*
  * Matrix products on 4-bit weights for any number of rows of x, grouped by expert:
  *   y[t, r] = sum_c x[t, c] W_e[r, c]   for offsets[e] <= t < offsets[e + 1],
  * W_e the values of the e-th of E stacked [R, C] matrices; sums in fp32 in an order fixed by the

@@ -42,6 +42,7 @@ EXPORTED = (
     "aaac_gemv", "aaac_gemv_batch", "aaac_assign_refine_batch", "aaac_init_quantiles_batch",
     "aaac_pack_batch", "aaac_dequant_batch", "aaac_refine_batch_noalloc", "aaac_mxfp4_quantize",
     "aaac_mxfp4_dequant", "aaac_mxfp4_matmul", "aaac_matmul", "aaac_matmul_workspace_bytes",
+    "aaac_matmul_plan",
 )
 
 
@@ -114,6 +115,7 @@ def load(path: str = LIB_PATH):
         "aaac_mxfp4_quantize": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
         "aaac_mxfp4_dequant": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_int, c_i64, c_vp]),
         "aaac_matmul_workspace_bytes": (c_size, [c_int, c_i64, c_i64, c_i64, c_i64]),
+        "aaac_matmul_plan": (c_int, [c_int, c_i64, c_i64, c_i64, c_i64, c_int, P(ctypes.c_int32)]),
         "aaac_mxfp4_matmul": (c_int, [c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_int, c_vp,
                                       c_i64, c_i64, c_int, c_vp, c_int, c_i64, c_vp, c_size,
                                       c_vp]),
@@ -681,6 +683,14 @@ def matmul_workspace_bytes(kind: int, E: int, R: int, C: int, T: int, dev: int =
         with torch.cuda.device(dev):
             return int(fn(kind, E, R, C, T))
     return int(fn(kind, E, R, C, T))
+
+
+def matmul_plan(kind: int, E: int, R: int, C: int, T: int, has_ws: bool = True):
+    """(tile rows of weights, tile rows of x, split, rt, nt, chunks) of a product (MATMUL_*) on the
+    current device, see aaac_matmul_plan in aaac.h."""
+    plan = (ctypes.c_int32 * 6)()
+    _check(load().aaac_matmul_plan(kind, E, R, C, T, int(has_ws), plan), "aaac_matmul_plan")
+    return tuple(plan)
 
 
 def _product_args(what: str, kind: int, E: int, C: int, offsets, y: torch.Tensor, T: int, R: int,

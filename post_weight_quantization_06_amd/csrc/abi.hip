@@ -481,6 +481,19 @@ MatmulKind kernel_kind(int kind) {
   return kind == AAAC_MATMUL_PACKED ? kPacked : kind == AAAC_MATMUL_MXFP4 ? kMxBf16 : kMxMxfp4;
 }
 
+// The sizes of a product call that the queries are asked about; false for an unsupported one.
+bool query_args(int kind, int64_t E, int64_t R, int64_t C, int64_t T, MatmulArgs& a) {
+  if (kind < AAAC_MATMUL_PACKED || kind > AAAC_MATMUL_QUANTIZE_X || E < 1 || E > 65535 || R < 1 ||
+      R >= ((int64_t)1 << 31) || C < 1 || C >= kMaxMatmulCols || T < 1 || T >= ((int64_t)1 << 31))
+    return false;
+  a.E = (int)E;
+  a.R = R;
+  a.C = C;
+  a.Cp = mx_blocks(C) * kMxBlock;
+  a.T = T;
+  return true;
+}
+
 // Where a product's workspace holds what: the parts of split sums, then quantized rows of x.
 struct MatmulWs {
   size_t codes, scales, bytes;
@@ -818,16 +831,22 @@ aaac_status aaac_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int6
 }
 
 size_t aaac_matmul_workspace_bytes(int kind, int64_t E, int64_t R, int64_t C, int64_t T) {
-  if (kind < AAAC_MATMUL_PACKED || kind > AAAC_MATMUL_QUANTIZE_X || E < 1 || E > 65535 || R < 1 ||
-      R >= ((int64_t)1 << 31) || C < 1 || C >= kMaxMatmulCols || T < 1 || T >= ((int64_t)1 << 31))
-    return 0;
   MatmulArgs a = {};
-  a.E = (int)E;
-  a.R = R;
-  a.C = C;
-  a.Cp = mx_blocks(C) * kMxBlock;
-  a.T = T;
-  return matmul_ws(a, kind).bytes;
+  return query_args(kind, E, R, C, T, a) ? matmul_ws(a, kind).bytes : 0;
+}
+
+aaac_status aaac_matmul_plan(int kind, int64_t E, int64_t R, int64_t C, int64_t T, int has_ws,
+                             int32_t plan[6]) {
+  const char* who = "aaac_matmul_plan";
+  MatmulArgs a = {};
+  if (!query_args(kind, E, R, C, T, a))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: kind %d, E=%lld R=%lld C=%lld T=%lld", who, kind,
+                (long long)E, (long long)R, (long long)C, (long long)T);
+  if (!plan) return fail(AAAC_ERR_INVALID_ARG, "%s: plan null", who);
+  const MatmulPlan p = plan_matmul(a, kernel_kind(kind), has_ws != 0);
+  const int32_t v[6] = {p.bm, p.bn, p.split, p.rt, p.nt, p.chunks};
+  for (int i = 0; i < 6; ++i) plan[i] = v[i];
+  return ok();
 }
 
 aaac_status aaac_mxfp4_matmul(const uint8_t* w_codes, const uint8_t* w_scales, int64_t E, int64_t R,

@@ -225,3 +225,136 @@ def test_results_of_other_shapes_are_filled_row_by_row_or_refused():
         P.mxfp4_matmul(codes[0], scales[0], xd.view(2, 3, 64), out=torch.zeros(24, 6, device=DEV))
     with pytest.raises(ValueError, match="out must be"):
         P.mxfp4_dequant(codes[0], scales[0], 64, out=torch.zeros(24, 60, device=DEV))
+
+
+# ------------------------------------------------------------------ every kernel form, many steps
+
+# (kind, (g, S, n) of packed weights, E, R, C, T, expected plan). Plans: ("few", rt, nt, chunks) or
+# ("tile", weight rows, rows of x, split or not) on 256 CUs, by aaac_matmul_plan. R and T are cut by
+# every tile; the columns make 6 steps and more, in MXFP4 x whole blocks of 256 or not.
+PK, MX, MXX = L.MATMUL_PACKED, L.MATMUL_MXFP4, L.MATMUL_QUANTIZE_X
+FORMS = [
+    (PK, (128, 128, 16), 1, 1031, 640, 13, ("few", 1, 1, 1)),
+    (PK, (128, 16, 16), 1, 1031, 1152, 13, ("few", 1, 1, 1)),
+    (PK, (128, 128, 16), 1, 219, 8320, 3, ("few", 1, 1, 4)),        # x in LDS
+    (PK, (64, 64, 15), 1, 219, 8320, 13, ("few", 1, 1, 4)),         # x read directly
+    (PK, (128, 128, 16), 1, 8211, 640, 13, ("few", 2, 1, 1)),
+    (PK, (16, 16, 15), 5, 1645, 608, 61, ("few", 2, 1, 1)),
+    (PK, (128, 128, 16), 1, 8247, 8320, 5, ("few", 2, 1, 4)),
+    (PK, (128, 128, 16), 1, 131, 640, 19, ("tile", 128, 32, True)),
+    (PK, (16, 8, 16), 3, 300, 448, 99, ("tile", 128, 32, False)),
+    (PK, (128, 16, 16), 1, 132, 640, 4110, ("tile", 128, 64, False)),
+    (PK, (128, 128, 16), 1, 130, 4096, 513, ("tile", 128, 64, True)),
+    (PK, (32, 32, 16), 1, 262, 544, 5501, ("tile", 128, 128, False)),
+    (PK, (16, 16, 15), 5, 6231, 512, 97, ("tile", 128, 128, False)),
+    (PK, (128, 128, 16), 1, 263, 2048, 2069, ("tile", 128, 128, True)),
+    (PK, (128, 128, 16), 1, 7400, 640, 1031, ("tile", 256, 256, False)),
+    (PK, (128, 16, 16), 1, 7400, 640, 1031, ("tile", 256, 256, False)),
+    (PK, (16, 16, 15), 1, 7400, 640, 1031, ("tile", 256, 256, False)),
+    (PK, (8, 8, 16), 10, 7615, 512, 1620, ("tile", 256, 256, False)),
+    (PK, (128, 64, 16), 1, 258, 2176, 5674, ("tile", 256, 256, True)),
+    (MX, None, 1, 1031, 648, 13, ("few", 1, 1, 1)),
+    (MX, None, 1, 219, 8328, 3, ("few", 1, 1, 4)),
+    (MX, None, 1, 219, 8320, 13, ("few", 1, 1, 4)),
+    (MX, None, 1, 8211, 648, 13, ("few", 2, 1, 1)),
+    (MX, None, 10, 1000, 512, 60, ("few", 2, 1, 1)),
+    (MX, None, 1, 131, 648, 18, ("tile", 128, 32, True)),
+    (MX, None, 3, 300, 456, 99, ("tile", 128, 32, False)),
+    (MX, None, 1, 131, 552, 4171, ("tile", 128, 64, False)),
+    (MX, None, 1, 130, 1032, 2059, ("tile", 128, 64, True)),
+    (MX, None, 1, 260, 520, 5671, ("tile", 128, 128, False)),
+    (MX, None, 1, 263, 2056, 2069, ("tile", 128, 128, True)),
+    (MX, None, 1, 7400, 648, 1031, ("tile", 256, 256, False)),
+    (MX, None, 10, 7366, 512, 1710, ("tile", 256, 256, False)),
+    (MX, None, 1, 258, 2176, 5408, ("tile", 256, 256, True)),
+    (MXX, None, 1, 1031, 2085, 13, ("few", 1, 1, 1)),
+    (MXX, None, 1, 1031, 2304, 29, ("few", 1, 2, 1)),
+    (MXX, None, 1, 8242, 2085, 13, ("few", 2, 1, 1)),
+    (MXX, None, 1, 8391, 2080, 18, ("few", 2, 2, 1)),
+    (MXX, None, 5, 1645, 2080, 61, ("few", 2, 1, 1)),
+    (MXX, None, 1, 131, 2304, 70, ("tile", 64, 64, False)),
+    (MXX, None, 1, 131, 4101, 70, ("tile", 64, 64, True)),
+    (MXX, None, 1, 8249, 2304, 68, ("tile", 128, 64, False)),
+    (MXX, None, 1, 8249, 2081, 68, ("tile", 128, 64, False)),
+    (MXX, None, 1, 70, 4096, 2140, ("tile", 128, 64, True)),
+    (MXX, None, 1, 260, 2304, 5775, ("tile", 128, 128, False)),
+    (MXX, None, 1, 260, 2081, 5775, ("tile", 128, 128, False)),
+    (MXX, None, 1, 300, 8192, 901, ("tile", 128, 128, True)),
+    (MXX, None, 1, 7400, 2304, 1031, ("tile", 256, 256, False)),
+    (MXX, None, 1, 7400, 2081, 1031, ("tile", 256, 256, False)),
+    (MXX, None, 10, 7487, 2304, 1760, ("tile", 256, 256, False)),
+    (MXX, None, 1, 8441, 8192, 403, ("tile", 256, 256, True)),
+    (MXX, None, 1, 8441, 8160, 403, ("tile", 256, 256, True)),
+]
+
+
+def form(kind, E, R, C, T):
+    bm, bn, split, rt, nt, chunks = L.matmul_plan(kind, E, R, C, T)
+    return ("tile", bm, bn, split > 1) if bn else ("few", rt, nt, chunks)
+
+
+def _mx_dev(gen, E, R, C):
+    """MXFP4 weights of whole numbers up to 12, made on the GPU."""
+    nb = -(-C // 32)
+    whole = torch.tensor([0, 2, 4, 5, 6, 10, 12, 13], dtype=torch.uint8, device=DEV)
+    q = whole[torch.randint(0, 8, (E, R, nb * 32), generator=gen, device=DEV)]
+    q[..., C:] = 0
+    s = torch.randint(127, 129, (E, R, nb), generator=gen, device=DEV, dtype=torch.uint8)
+    return q[..., 0::2] | (q[..., 1::2] << 4), s
+
+
+def _packed_dev(gen, E, R, C, g, S, n):
+    """Packed weights of whole numbers and halves, made on the GPU."""
+    q = torch.randint(0, n, (E, R, C), generator=gen, device=DEV, dtype=torch.uint8)
+    s = torch.tensor([0.5, 1.0, 2.0], device=DEV)[
+        torch.randint(0, 3, (E, R, C // g), generator=gen, device=DEV)]
+    words, bitmap = s.to(torch.bfloat16).view(torch.int16), None
+    if S == g:
+        words = words | (torch.randint(0, 2, words.shape, generator=gen, device=DEV) << 15).to(torch.int16)
+    else:
+        bitmap = torch.randint(0, 256, (E, (R * (C // S) + 7) // 8), generator=gen, device=DEV,
+                               dtype=torch.uint8)
+    T = torch.randint(-8, 8, (E, 2, n), generator=gen, device=DEV) * 2
+    return q[..., 0::2] | (q[..., 1::2] << 4), words, bitmap, T.to(torch.bfloat16).view(torch.int16)
+
+
+def _starts(gen, E, T):
+    """Ascending offsets, one expert empty, on the CPU."""
+    cuts = torch.randint(0, T + 1, (E - 1,), generator=gen).sort().values
+    if E > 2:
+        cuts[1] = cuts[0]
+    return torch.nn.functional.pad(cuts, (1, 1), value=0).index_fill_(0, torch.tensor([E]), T).to(torch.int32)
+
+
+@pytest.mark.parametrize("kind,fmt,E,R,C,T,plan", FORMS)
+def test_every_kernel_form(kind, fmt, E, R, C, T, plan):
+    """Each kernel and tile that a plan can pick, against the framework's own dequantized weights."""
+    _say("form", kind, fmt, E, R, C, T, plan)
+    assert form(kind, E, R, C, T) == plan
+    gen = torch.Generator(device=DEV).manual_seed(R * 13 + C + T)
+    x = torch.randint(-4, 5, (T, C), generator=gen, device=DEV).to(torch.bfloat16)
+    at = [0, T] if E == 1 else _starts(torch.Generator().manual_seed(E + T), E, T).tolist()
+    off = None if E == 1 else torch.tensor(at, dtype=torch.int32, device=DEV)
+    if kind == PK:
+        g, S, n = fmt
+        w = _packed_dev(gen, E, R, C, g, S, n)
+        one = [None if t is None else t[0] for t in w] if E == 1 else w
+        y = P.packed_matmul(*one, x, g, S, n, off, dtype=torch.float32)
+    else:
+        w = _mx_dev(gen, E, R, C)
+        one = [t[0] for t in w] if E == 1 else w
+        y = P.mxfp4_matmul(*one, x, off, act="bf16" if kind == MX else "mxfp4", dtype=torch.float32, C=C)
+        if kind == MXX:                              # whole numbers up to 4 are MXFP4 values
+            assert torch.equal(P.mxfp4_dequant(*P.mxfp4_quantize(x), C), x)
+    for e in range(E):
+        if at[e] == at[e + 1]:
+            continue
+        if kind == PK:
+            W = torch.empty(R, C, dtype=torch.bfloat16, device=DEV)
+            L.aaac_dequant(w[0][e].reshape(-1), w[1][e].reshape(-1),
+                           None if w[2] is None else w[2][e], w[3][e].reshape(-1), R, C, g, S, n, W)
+        else:
+            W = P.mxfp4_dequant(w[0][e], w[1][e], C, dtype=torch.float32)
+        want = x[at[e]:at[e + 1]].double() @ W.double().t()
+        assert float(want.abs().max()) < 2 ** 22
+        assert torch.equal(y[at[e]:at[e + 1]].double(), want), e

@@ -281,3 +281,33 @@ def test_results_of_another_last_axis_are_refused():
             P.mxfp4_matmul(codes, scales, x, out=out)
     with pytest.raises(ValueError, match="GPU"):
         P.mxfp4_dequant(codes, scales, 50, out=torch.zeros(16, 50))
+
+
+def test_plans_of_the_tested_forms(lib):
+    """Every kernel and tile that a plan can pick is among the forms that the GPU tests run. Without a GPU
+    the plan is that of 256 CUs."""
+    from tests.test_gpu_matmul_forms import FORMS, MX, MXX, PK, form
+
+    if torch.cuda.is_available() and torch.cuda.get_device_properties(0).multi_processor_count != 256:
+        pytest.skip("plans of another GPU")
+    for kind, _, E, R, C, T, plan in FORMS:
+        assert form(kind, E, R, C, T) == plan, (kind, E, R, C, T)
+    few = {("few", 1, 1, 1), ("few", 1, 1, 4), ("few", 2, 1, 1)}
+    for kind, tiles in ((PK, ((128, 32), (128, 64), (128, 128), (256, 256))),
+                        (MX, ((128, 32), (128, 64), (128, 128), (256, 256))),
+                        (MXX, ((64, 64), (128, 64), (128, 128), (256, 256)))):
+        got = {f[-1] for f in FORMS if f[0] == kind}
+        want = {("tile", bm, bn, split) for bm, bn in tiles for split in (False, True)}
+        want |= few if kind != MXX else {("few", rt, nt, 1) for rt in (1, 2) for nt in (1, 2)}
+        assert want <= got, want - got
+
+
+def test_plan_query(lib):
+    f = lib.aaac_matmul_plan
+    plan = (ctypes.c_int32 * 6)(*[7] * 6)
+    for bad in ((4, 1, 16, 64, 4), (0, 0, 16, 64, 4), (0, 1, 0, 64, 4), (0, 1, 16, 0, 4), (0, 1, 16, 64, 0)):
+        assert f(bad[0], *[i64(v) for v in bad[1:]], 1, plan) == SHAPE and list(plan) == [7] * 6
+    assert f(0, i64(1), i64(16), i64(64), i64(4), 1, None) == INVALID
+    assert f(0, i64(1), i64(16), i64(64), i64(4), 1, plan) == OK and list(plan) == [0, 0, 1, 1, 1, 1]
+    assert f(0, i64(1), i64(1024), i64(8192), i64(256), 1, plan) == OK and plan[2] > 1
+    assert f(0, i64(1), i64(1024), i64(8192), i64(256), 0, plan) == OK and plan[2] == 1
