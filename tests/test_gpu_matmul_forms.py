@@ -358,3 +358,44 @@ def test_every_kernel_form(kind, fmt, E, R, C, T, plan):
         want = x[at[e]:at[e + 1]].double() @ W.double().t()
         assert float(want.abs().max()) < 2 ** 22
         assert torch.equal(y[at[e]:at[e + 1]].double(), want), e
+
+
+# ------------------------------------------------------------------ x as codes, rows, split sums
+
+SPREAD = [  # E, R, C, T: few rows, tiles, tiles with split columns, widths of no whole block
+    (1, 200, 1000, 9), (1, 200, 1024, 29), (1, 131, 2304, 70), (1, 131, 4101, 70), (1, 700, 777, 900),
+    (4, 300, 512, 40), (4, 300, 545, 500),
+]
+
+
+@pytest.mark.parametrize("E,R,C,T", SPREAD)
+def test_x_given_as_codes_has_the_bits_of_x_quantized_in_the_call(E, R, C, T):
+    _say("x as codes", E, R, C, T)
+    rng = np.random.default_rng(R + C + T)
+    codes, scales, W = _mx(rng, E, R, C, False)
+    x, xd = _x(rng, T, C, False)
+    off = _dev(np.linspace(0, T, E + 1).astype(np.int32))
+    xc, xs = P.mxfp4_quantize(xd)
+    ws = torch.full((L.matmul_workspace_bytes(L.MATMUL_MXFP4_X, E, R, C, T) or 256,), 0xFF, dtype=torch.uint8,
+                    device=DEV)                      # NaN where a sum would read what it did not write
+    for dtype in (torch.float32, torch.bfloat16):
+        want = P.mxfp4_matmul(codes, scales, xd, off, act="mxfp4", dtype=dtype, C=C)
+        y = torch.full((T, R), 99.0, dtype=dtype, device=DEV)
+        P.aaac_mxfp4_matmul(codes, scales, C, xc, y, off, x_scales=xs)
+        assert torch.equal(y, want)
+        y.fill_(99.0)
+        P.aaac_mxfp4_matmul(codes, scales, C, xc, y, off, x_scales=xs, ws=ws)
+        assert torch.equal(y, want)
+        y.fill_(99.0)
+        P.aaac_mxfp4_matmul(codes, scales, C, xc, y, off, x_scales=_moved(xs, 1))
+        assert torch.equal(y, want)
+    # and near the exact product of the values: an fp32 sum of C terms
+    xv = ref.mxfp4_decode(*ref.mxfp4_encode(x), C)
+    full = ref.grouped_matmul(xv, W, off.cpu().numpy())
+    mass = ref.grouped_matmul(np.abs(xv), np.abs(W), off.cpu().numpy())
+    got = P.mxfp4_matmul(codes, scales, xd, off, act="mxfp4", dtype=torch.float32).double().cpu().numpy()
+    assert np.all(np.abs(got - full) <= (C / 32 + 144) * 2.0 ** -23 * mass + 1e-30)
+    y = torch.empty(0, R, device=DEV)
+    P.aaac_mxfp4_matmul(codes, scales, C, xc[:0], y, off, x_scales=xs[:0])
+    with pytest.raises(ValueError, match="x_scales"):
+        P.aaac_mxfp4_matmul(codes, scales, C, xc, torch.empty(T, R, device=DEV), off, x_scales=xs[:-1])
