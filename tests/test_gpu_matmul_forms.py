@@ -399,3 +399,39 @@ def test_x_given_as_codes_has_the_bits_of_x_quantized_in_the_call(E, R, C, T):
     P.aaac_mxfp4_matmul(codes, scales, C, xc[:0], y, off, x_scales=xs[:0])
     with pytest.raises(ValueError, match="x_scales"):
         P.aaac_mxfp4_matmul(codes, scales, C, xc, torch.empty(T, R, device=DEV), off, x_scales=xs[:-1])
+
+
+def _three(E, R, C, seed):
+    """(name, call(x, offsets, out)) of the three products on random weights."""
+    rng = np.random.default_rng(seed)
+    mc, ms, _ = _mx(rng, E, R, C, False)
+    pc, ps, pb, pt, _ = _packed(rng, E, R, C, 32, 16, 16, False)
+    return [("mx bf16", lambda x, o, y: P.mxfp4_matmul(mc, ms, x, o, out=y)),
+            ("mx mxfp4", lambda x, o, y: P.mxfp4_matmul(mc, ms, x, o, act="mxfp4", out=y)),
+            ("packed", lambda x, o, y: P.packed_matmul(pc, ps, pb, pt, x, 32, 16, 16, o, out=y))]
+
+
+@pytest.mark.parametrize("E,R,C,T", [(3, 100, 512, 30), (1, 300, 608, 30), (3, 100, 512, 90),
+                                     (2, 1000, 320, 700), (1, 131, 4096, 70), (3, 256, 4096, 200)])
+def test_a_rows_result_depends_on_no_other_row(E, R, C, T):
+    """Bitwise, in few-row kernels, tiles and split sums: other rows changed, made NaN or infinite, and
+    the rows of an expert in another order."""
+    at = np.linspace(0, T, E + 1).astype(np.int32)
+    off = _dev(at)
+    x, xd = _x(np.random.default_rng(T), T, C, False)
+    keep = torch.zeros(T, dtype=torch.bool, device=DEV)
+    keep[::3] = True
+    order = torch.cat([torch.arange(int(a), int(b)).flip(0) for a, b in zip(at, at[1:])]).to(DEV)
+    for name, call in _three(E, R, C, R + C):
+        _say("row by row", name, E, R, C, T)
+        want = torch.empty(T, R, dtype=torch.float32, device=DEV)
+        call(xd, off, want)
+        assert torch.isfinite(want).all()
+        for other in (xd.flip(0) * 3, torch.full_like(xd, float("nan")),
+                      torch.full_like(xd, float("inf")), torch.zeros_like(xd)):
+            y = torch.empty_like(want)
+            call(torch.where(keep[:, None], xd, other), off, y)
+            assert torch.equal(y[keep], want[keep])
+        y = torch.empty_like(want)
+        call(xd[order], off, y)
+        assert torch.equal(y, want[order])
