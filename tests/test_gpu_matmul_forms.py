@@ -435,3 +435,20 @@ def test_a_rows_result_depends_on_no_other_row(E, R, C, T):
         y = torch.empty_like(want)
         call(xd[order], off, y)
         assert torch.equal(y, want[order])
+
+
+def test_rows_of_no_expert_stay_as_they_were_with_split_columns():
+    rng = np.random.default_rng(17)
+    E, R, C, T = 2, 256, 4096, 64
+    codes, scales, W = _mx(rng, E, R, C, True)
+    x, xd = _x(rng, T, C, True)
+    xd[:5], xd[50:] = float("nan"), float("inf")
+    off = np.array([5, 20, 50], np.int32)
+    want = ref.grouped_matmul(x, W, off)
+    want[np.isnan(want)] = 55.0
+    for act, kind in (("bf16", L.MATMUL_MXFP4), ("mxfp4", L.MATMUL_QUANTIZE_X)):
+        _say("split, outside rows", act)
+        assert form(kind, E, R, C, T)[-1] is True
+        y = torch.full((T, R), 55.0, dtype=torch.float32, device=DEV)
+        P.mxfp4_matmul(codes, scales, xd, _dev(off), act=act, out=y)
+        assert np.array_equal(y.cpu().numpy(), want.astype(np.float32))
