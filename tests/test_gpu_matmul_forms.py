@@ -452,3 +452,73 @@ def test_rows_of_no_expert_stay_as_they_were_with_split_columns():
         y = torch.full((T, R), 55.0, dtype=torch.float32, device=DEV)
         P.mxfp4_matmul(codes, scales, xd, _dev(off), act=act, out=y)
         assert np.array_equal(y.cpu().numpy(), want.astype(np.float32))
+
+
+def test_x_of_more_than_2_32_elements():
+    _room(40)
+    E, R, C, T = 2, 40, 8192, 530000
+    gen = torch.Generator(device=DEV).manual_seed(9)
+    x = torch.randint(-4, 5, (T, C), generator=gen, device=DEV, dtype=torch.int8).to(torch.bfloat16)
+    assert x.numel() > 2 ** 32
+    at = [0, 400001, T]
+    off = torch.tensor(at, dtype=torch.int32, device=DEV)
+    mx, pk = _mx_dev(gen, E, R, C), _packed_dev(gen, E, R, C, 128, 16, 16)
+    for name, call in (("mx bf16", lambda: P.mxfp4_matmul(*mx, x, off, dtype=torch.float32)),
+                       ("mx mxfp4", lambda: P.mxfp4_matmul(*mx, x, off, act="mxfp4", dtype=torch.float32)),
+                       ("packed", lambda: P.packed_matmul(*pk, x, 128, 16, 16, off, dtype=torch.float32))):
+        _say("large x", name)
+        y = call()
+        for e in range(E):
+            if name == "packed":
+                W = torch.empty(R, C, dtype=torch.bfloat16, device=DEV)
+                L.aaac_dequant(*[t[e].reshape(-1) for t in pk], R, C, 128, 16, 16, W)
+            else:
+                W = P.mxfp4_dequant(mx[0][e], mx[1][e], C, dtype=torch.float32)
+            for r in (at[e], at[e] + 131071, 262143 if e == 0 else 524287, at[e + 1] - 300):
+                assert torch.equal(y[r:r + 300].double(), x[r:r + 300].double() @ W.double().t()), (e, r)
+    del x, y
+    torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ calls at once
+
+def test_calls_on_two_streams_at_once_and_two_graphs():
+    """Products that use a workspace, in flight on two streams together, then captured into two graphs
+    that replay in turn and together: each call has a workspace of its own."""
+    E, R, C, T = 1, 256, 4096, 64
+    for name, call in _three(E, R, C, 23):
+        _say("at once", name)
+        off = torch.tensor([0, T], dtype=torch.int32, device=DEV)
+        xs = [_x(np.random.default_rng(s), T, C, False)[1] for s in (1, 2)]
+        want = [torch.empty(T, R, dtype=torch.float32, device=DEV) for _ in xs]
+        for x, w in zip(xs, want):
+            call(x, off, w)
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in xs]
+        ys = [[torch.zeros_like(w) for _ in range(20)] for w in want]
+        torch.cuda.synchronize()
+        for k in range(20):
+            for i, st in enumerate(streams):
+                with torch.cuda.stream(st):
+                    call(xs[i], off, ys[i][k])
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, want[i]) for i in (0, 1) for y in ys[i])
+        graphs, outs = [], []
+        for x in xs:
+            y, g = torch.zeros_like(want[0]), torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                call(x, off, y)
+            graphs.append(g)
+            outs.append(y)
+        for k in range(4):
+            for y in outs:
+                y.zero_()
+            torch.mm(torch.ones(64, 64, device=DEV), torch.ones(64, 64, device=DEV))
+            torch.cuda.synchronize()
+            for i, st in enumerate(streams):
+                with torch.cuda.stream(st):
+                    graphs[i if k % 2 else 1 - i].replay()
+                if k < 2:
+                    torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            assert all(torch.equal(y, w) for y, w in zip(outs, want))
