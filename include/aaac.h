@@ -419,6 +419,9 @@ aaac_status aaac_matmul_plan(int kind, int64_t E, int64_t R, int64_t C, int64_t 
  * when S < g, each matrix's part as aaac_assign and aaac_pack write it. The weight is aaac_dequant's
  * W_hat = bf16(|s| T~_sel[q]) (a product below 2^-126 may differ from it by its rounding); a code
  * >= n reads entry 0. x bf16 [T, C] as above. g, S, n as for the other calls, and C % 32 == 0.
+ *
+ * Weights may start where a larger tensor's part starts: scales and tables_bf16 of aaac_matmul on any
+ * 2-byte address, its bitmap, and w_scales and x_scales of aaac_mxfp4_matmul, on any byte.
  */
 aaac_status aaac_mxfp4_matmul(const uint8_t* w_codes, const uint8_t* w_scales, int64_t E, int64_t R,
                               int64_t C, const int32_t* offsets, const void* x, int x_type,

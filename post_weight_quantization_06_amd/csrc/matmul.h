@@ -298,11 +298,11 @@ struct MxDecoder {
   }
 };
 
-// Packed dual-codebook weights: bf16(|s| T_sel[q]). The two tables of 16 bf16 entries lie in
-// scalar registers as planes of low and high bytes, the second as its difference to the first; a byte permute looks four codes up at once in eight
-// entries, a second permute picks between the lower and the upper eight by bit 3 of the code, and a
-// third puts the two bytes of an entry where fp32 keeps them. One product and one rounding follow,
-// as in dequant.
+// Packed dual-codebook weights: bf16(|s| T_sel[q]). The two tables of 16 bf16 entries lie in scalar
+// registers as planes of low and high bytes, the second as its difference to the first; a byte
+// permute looks four codes up at once in eight entries, a second permute picks between the lower and
+// the upper eight by bit 3 of the code, and a third puts the two bytes of an entry where fp32 keeps
+// them. One product and one rounding follow, as in dequant.
 // LG: log2 of the scale group, 7 for 128 and more. LS: the same of the selection group when its
 // selectors are in the bitmap, 0 when they are the scales' sign bits (S == g). OFF: the scales start
 // two bytes past a word, with LG < 5, where a run's scales are whole words otherwise (C / g is even

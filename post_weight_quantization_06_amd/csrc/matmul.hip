@@ -24,11 +24,14 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 }
 
 // The choice. Up to 16 rows of x a matrix (32 for one matrix in MXFP4) go to the few-row kernels,
-// which read each weight once: one row against 14336 x 4096 packed weights takes 18 us there and 26 in
-// the best tiles, 17 rows 27 us in tiles. Two blocks of 16 weight rows a workgroup halve the reads of
-// x, one block makes more workgroups: 32 experts of 2048 x 4096 (some 3500 blocks) take 33 us with
-// two and 41 with one, 4096 x 14336 (256 blocks) 19 and 12. Four chunks at a time pay on long rows:
-// 12.6 us down to 11.9 at 14336 columns, 7.3 up to 7.8 at 4096.
+// which read each weight once for every 16 (32) rows: one row against 14336 x 4096 packed weights takes
+// 18 us there and 26 in the best tiles, 16 rows 19 us there, 17 rows 26 us in tiles. The offsets lie on
+// the device, so an average decides: 64 experts of 2048 x 2048 in MXFP4 with 1000 rows take 85 us spread
+// unevenly, 109 with 938 of them at one expert (28 for 1000 rows at that one alone, in tiles). Two blocks
+// of 16 weight rows a workgroup halve the reads of x, one block makes more workgroups: 32 experts of
+// 2048 x 4096 (some 3500 blocks) take 33 us with two and 41 with one, 4096 x 14336 (256 blocks) 19
+// and 12. Four chunks at a time pay on long rows: 12.6 us down to 11.9 at 14336 columns, 7.3 up to 7.8
+// at 4096.
 //
 // Tiles: the least estimated time over tile widths and splits. A tile takes its steps times kStep
 // (measured with every CU at work) and kTile to start and end; the busiest CU runs
@@ -37,11 +40,15 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // weights of 14336 x 4096: 64 rows: 64 wide, split 4 (32; unsplit 53); 512 rows: 256 wide, split 2
 // (85; 128 wide unsplit 96); 2048 rows: 256 wide unsplit (250; 128 wide 334). Tiles of 64 weight rows
 // double the workgroups of a short MXFP4 product: 48 rows against 14336 x 4096 in 16.2 us, 17.0 in 128.
+// The MXFP4 step times are those of rows of whole steps; the other form's steps (tile_mxfp4_kernel) take
+// about twice as long in every tile and have no table of their own.
 struct TileCost { int bm, bn; double step; bool two; };
-constexpr TileCost kBf16Tiles[] = {{128, 32, 0.70, true}, {128, 64, 0.77, true}, {128, 128, 0.96, true},
-                                   {256, 256, 1.85, false}};
-constexpr TileCost kMxTiles[] = {{64, 64, 0.45, true}, {128, 64, 0.60, true}, {128, 128, 0.75, true}, {256, 256, 1.90, false}};
-constexpr double kTile = 2.3, kTwoBf16 = 0.80, kTwoMx = 0.95, kLaunch = 3.0, kPartBytes = 6e6;
+constexpr TileCost kBf16Tiles[] = {{128, 32, 0.70, true}, {128, 64, 0.77, true},
+                                   {128, 128, 0.96, true}, {256, 256, 1.85, false}};
+constexpr TileCost kMxTiles[] = {{64, 64, 0.45, true}, {128, 64, 0.60, true},
+                                 {128, 128, 0.75, true}, {256, 256, 1.90, false}};
+constexpr double kTile = 2.3, kTwoBf16 = 0.80, kTwoMx = 0.95, kLaunch = 3.0;
+constexpr double kPartBytes = 6e6;
 
 template <int N>
 void plan_tiles(const MatmulArgs& a, const TileCost (&tiles)[N], double two, int cols, bool can_split,

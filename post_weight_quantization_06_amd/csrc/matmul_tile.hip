@@ -84,6 +84,10 @@ __device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
 // without its loads 79 %. Eight waves of 128 x 64 rather than four of 128 x 128: four need 512
 // registers each and spill. Rows of x tiles advancing together (1 to 16 of them) and touching lines
 // two to four steps ahead measured equal or slower.
+//
+// WHOLE: rows of whole steps whose scale bytes lie on words. Otherwise the scale bytes are loaded one by
+// one through registers, and each waits for memory, the next stage's loads among it, in every step: half
+// the rate (2048 x 2880 with 2816 columns 23 us, with 2880 or 2944 46 us; 32 experts, 4096 rows, 60 and 119).
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ int piece_turn(int row) {
   return (row >> 1 & 1) ^ (row & 4) ^ (row >> 3 & 1) * 6;
@@ -267,8 +271,8 @@ hipError_t tile_mxfp4(MatmulArgs a, hipStream_t stream) {
 // bf16 x times decoded weights. A step takes 64 columns (128 bytes of bf16 a row). Two threads share
 // a weight row of the tile, a run of 32 columns each: a thread decodes its run and writes it to LDS
 // as bf16 one step ahead of its use, so a weight is decoded once per tile. Rows of x go to LDS
-// unchanged. Both lie permuted as above. Instruction h of a step takes pieces 4 h + q (columns
-// 32 h + 8 q ..) of a row.
+// unchanged. The 16-byte pieces of both lie permuted by row bits 0 to 2. Instruction h of a step takes
+// pieces 4 h + q (columns 32 h + 8 q ..) of a row.
 // Memory is NS - 1 steps ahead: group j of asynchronous loads holds x of step j and the codes and
 // scales of step j + 1, and at most NS - 2 younger groups are in flight when a step begins. Loads
 // past the last step lie outside their buffers, so every group has the same count.
