@@ -213,7 +213,8 @@ aaac_status aaac_dequant_batch(int count, const uint8_t* const* codes,
  *                                     codes 16-byte aligned, scales 8-byte aligned.
  * x   bf16 [B, C] bit patterns (row stride C), 16-byte aligned; 1 <= B <= 4.
  * y   fp32 [B, R] (output, row stride R).
- * Shapes as for the other calls, and C % 32 == 0.
+ * Shapes as for the other calls, C % 32 == 0, and fewer than 2^24 blocks of 32 rows (of 16 over
+ * 4096 columns, 8 over 8192), in aaac_gemv_batch over all matrices together.
  */
 aaac_status aaac_gemv(const uint8_t* codes, const uint16_t* scales, const uint8_t* bitmap,
                       const uint16_t* tables_bf16, int64_t R, int64_t C, int g, int S, int n,

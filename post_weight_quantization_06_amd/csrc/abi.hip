@@ -356,6 +356,10 @@ aaac_status do_gemv(int count, const uint8_t* const* codes, const uint16_t* cons
     jb.split = gemv_split(C[i]);
     t += gemv_tasks(R[i], C[i]);
   }
+  // one workgroup a task: a launch of 2^32 threads and more is cut without an error
+  if (t >= ((int64_t)1 << 32) / kBlock)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: %lld blocks of rows are too many for one launch", who,
+                (long long)t);
   b.total_tasks = t;
   return hip_status(launch_gemv(b, static_cast<hipStream_t>(stream)), who);
 }

@@ -285,3 +285,15 @@ def test_refine_noalloc_rejects_bad_arguments_before_touching_the_device(lib):
     assert f(1, P, R, C, 128, 128, 16, P, P, P, P, 2, None, None, None) == INVALID   # W2 known
     assert f(1, P, R, C, 128, 128, 16, P, P, P, None, 0, None, None, None) == INVALID
     assert b"noalloc" in lib.aaac_last_error()
+
+
+def test_gemv_refuses_more_row_blocks_than_one_launch_holds(lib):
+    """2^24 blocks of rows are 2^32 threads: such a launch is cut without an error, so it is refused."""
+    P2 = (ctypes.c_void_p * 2)(FAKE, FAKE)
+    for Rs in ((1 << 29,), (1 << 28, 1 << 28)):
+        k = len(Rs)
+        R, Cs = (i64 * k)(*Rs), (i64 * k)(*[32] * k)
+        assert lib.aaac_gemv_batch(k, P2, P2, None, P2, R, Cs, 32, 32, 16, P2, 1, P2, None) == SHAPE
+        assert b"one launch" in lib.aaac_last_error()
+    assert lib.aaac_gemv(FAKE, FAKE, None, FAKE, i64(1 << 29), i64(32), 32, 32, 16, FAKE, 1, FAKE,
+                         None) == SHAPE
