@@ -433,6 +433,125 @@ aaac_status aaac_matmul(const uint8_t* codes, const uint16_t* scales, const uint
                         int n, const int32_t* offsets, const uint16_t* x, int64_t T, int64_t ldx,
                         void* y, int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
+#define AAAC_FP8 4                      /* aaac_fp8_matmul input: codes and scales of aaac_fp8_quantize */
+
+/*
+ * 8-bit floating point (OCP FP8 e4m3: largest value 448, 0x7f and 0xff NaN, no infinities) with one
+ * fp32 scale for each block of 128: 128 columns of a row (tile 0, activations), or 128 rows by 128
+ * columns of a weight matrix (tile 1). Blocks at a row's or a matrix's end may be short.
+ *   scale = max(top / 448, 2^-126), top = max |x| over the block, in fp32;
+ *   code  = the e4m3 value nearest to the fp32 quotient x / scale, ties to even.
+ * A block holding an infinity or a NaN has a NaN scale and NaN codes (0x7f) and reads back as NaN.
+ * X       [E, M, C] of x_type AAAC_BF16, AAAC_F16 or AAAC_F32, row stride ldx >= C, matrices stride_x >=
+ *         (M - 1) ldx + C elements apart, aligned to its element. tile 0: E = 1.
+ * codes   u8 [E, M, ldq], 16-byte aligned, ldq % 16 == 0, ldq >= C; the columns of a row from C to the
+ *         next multiple of 16 are zeroed, those behind it left alone.
+ * scales  fp32 [M, ceil(C / 128)], or with tile 1 [E, ceil(M / 128), ceil(C / 128)].
+ * Shapes: E >= 1, M >= 0 (0: nothing is written), 1 <= C < 2^21, E * M * C < 2^40. One kernel.
+ */
+aaac_status aaac_fp8_quantize(const void* X, int x_type, int64_t E, int64_t M, int64_t C, int64_t ldx,
+                              int64_t stride_x, int tile, uint8_t* codes, int64_t ldq, float* scales,
+                              void* stream);
+
+/*
+ * The values of FP8 codes: y = code * scale in fp32, rounded to y_type. codes as above but on any
+ * address and with any ldq >= C (those on 16 bytes are read fastest); Y [E M, C] with row stride ldy.
+ */
+aaac_status aaac_fp8_dequant(const uint8_t* codes, int64_t ldq, const float* scales, int64_t E,
+                             int64_t M, int64_t C, int tile, void* Y, int y_type, int64_t ldy,
+                             void* stream);
+
+/* Workspace bytes of one aaac_fp8_matmul call, 0 for an unsupported shape or where it uses none. The
+ * workspace needs no particular contents and keeps none that matter. quantize: x is not FP8. */
+size_t aaac_fp8_matmul_workspace_bytes(int64_t E, int64_t R, int64_t C, int64_t T, int64_t Tx,
+                                       int quantize);
+
+/* How one such call runs on the current device, as aaac_matmul_plan. */
+aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int has_ws,
+                                 int32_t plan[6]);
+
+/*
+ * Matrix product on FP8 weights for any number of rows, grouped by expert as the products above:
+ *   y[t, r] = sum over blocks b of sx[i, b] sw_e[r / 128, b] sum_{c in b} qx[i, c] qw_e[r, c],
+ * i = t, or rows[t]; fp32 sums of exact products in a fixed order, rounded once to y_type.
+ * w_codes  [E, R, ldw] (16-byte aligned, ldw % 16 == 0, C <= ldw < 2^22), w_scales fp32
+ *          [E, ceil(R / 128), ceil(C / 128)], as aaac_fp8_quantize writes them with tile 1. Bytes of a row
+ *          past C are not used.
+ * offsets  int32 [E + 1] or NULL, as above.
+ * rows     int32 [T] on the device or NULL: the row of x that row t of y multiplies, such as the token of
+ *          a routed slot. Values outside [0, Tx) stand for a row of zeros. NULL: Tx = T.
+ * x        AAAC_FP8: codes [Tx, ldx bytes] (16-byte aligned, ldx % 16 == 0, C <= ldx < 2^22) with x_scales
+ *          fp32 [Tx, ceil(C / 128)]; else AAAC_BF16, AAAC_F16 or AAAC_F32 [Tx, C], any row stride ldx >= C,
+ *          x_scales NULL: the call runs aaac_fp8_quantize into ws (which it then needs) and multiplies the
+ *          result, the same bits as two calls with a workspace give.
+ * y, ws    as above. y must not overlap an input.
+ * Shapes: 1 <= E <= 65535, 1 <= R < 2^31, 1 <= C < 2^21, E * R * C < 2^40, 0 <= T, Tx < 2^31, at most
+ * 2^31 output tiles of 16 x 16; with rows, codes and scales of x below 2^31 bytes each.
+ */
+aaac_status aaac_fp8_matmul(const uint8_t* w_codes, int64_t ldw, const float* w_scales, int64_t E,
+                            int64_t R, int64_t C, const int32_t* offsets, const int32_t* rows,
+                            const void* x, int x_type, const float* x_scales, int64_t Tx, int64_t ldx,
+                            int64_t T, void* y, int y_type, int64_t ldy, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Scores of aaac_route. */
+#define AAAC_SOFTMAX 0
+#define AAAC_SIGMOID 1
+
+/* Workspace bytes of one aaac_route call, 0 where it uses none. */
+size_t aaac_route_workspace_bytes(int64_t T, int64_t E);
+
+/*
+ * Routing of T tokens to k of E experts, and the order of the chosen slots by expert that the grouped
+ * products take.
+ * Choice: scores s = softmax(logits) over a token's experts or sigmoid(logits); value v = s + bias. An
+ * expert whose logit or bias is -inf is left out. The experts form `groups` groups of E / groups
+ * neighbours; a group's value is its largest v (group_top 1) or the sum of its two largest (group_top 2;
+ * one, where a group has only one left), and only the top_groups largest groups take part. The k largest
+ * v are chosen, in descending order; the lower index first among equals, of groups too. Values are
+ * compared in 64 bits, and where neither a bias nor a sum over a group enters, by the logits themselves.
+ * A NaN ranks above every number.
+ * Weights: s of the chosen experts, without the bias, divided by their sum with `renormalize` (a sum of
+ * zero gives zeros), times `scale`.
+ * logits   [T, E] of type AAAC_BF16, AAAC_F16 or AAAC_F32, row stride ldl >= E elements.
+ * bias     fp32 [E] or NULL.
+ * experts  int32 [T, k]: a token's experts, -1 where none is left; weights fp32 [T, k], 0 there.
+ * offsets  int32 [E + 1]: the places of expert e are offsets[e] <= p < offsets[e + 1].
+ * places   int32 [T, k]: the place of each slot, places of one expert in the order of their slots
+ *          (token by token); -1 for slots without an expert.
+ * rows     int32 [T k]: the token of each place, -1 from offsets[E] on.
+ * ws       NULL with ws_bytes 0 where the call uses none, else aaac_route_workspace_bytes(...) bytes,
+ *          256-byte aligned, no particular contents.
+ * Shapes: T >= 0 with T k < 2^31 (T = 0: the offsets are zeroed), 1 <= E <= 512, 1 <= k <= min(64,
+ * top_groups E / groups), 1 <= top_groups <= groups <= 64, E % groups == 0. Results are bitwise
+ * reproducible. One kernel up to 8 tokens, two above.
+ */
+aaac_status aaac_route(const void* logits, int type, int64_t T, int64_t E, int64_t ldl,
+                       const float* bias, int score, int64_t k, int groups, int top_groups,
+                       int group_top, int renormalize, float scale, int32_t* experts, float* weights,
+                       int32_t* offsets, int32_t* rows, int32_t* places, void* ws, size_t ws_bytes,
+                       void* stream);
+
+/*
+ * Rows to their experts: out[places[t, j]] = x[t] for j < k. x [T, C] of any type of `element` bytes (1,
+ * 2 or 4), row stride ldx >= C; out [N, C], row stride ldo >= C (elements). places int32 [T, k] on the
+ * device; those outside [0, N) are skipped, and rows of out that no place names are left as they were.
+ * A place may be named once. out must not overlap x. Shapes: 0 <= T, N < 2^31, 1 <= k <= 64,
+ * 1 <= C < 2^31.
+ */
+aaac_status aaac_rows_to_experts(const void* x, int element, int64_t T, int64_t C, int64_t ldx,
+                                 const int32_t* places, int64_t k, void* out, int64_t N, int64_t ldo,
+                                 void* stream);
+
+/*
+ * And back: out[t] = sum over j of weights[t, j] y[places[t, j]], in fp32 in the order of j, rounded once
+ * to out_type; places outside [0, N) add nothing. y [N, C] of y_type, out [T, C] of out_type (AAAC_BF16,
+ * AAAC_F16, AAAC_F32); weights fp32 [T, k]. Shapes as above.
+ */
+aaac_status aaac_rows_from_experts(const void* y, int y_type, int64_t N, int64_t C, int64_t ldy,
+                                   const int32_t* places, const float* weights, int64_t T, int64_t k,
+                                   void* out, int out_type, int64_t ldo, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -432,3 +432,101 @@ def grouped_matmul(x, Ws, offsets):
         if b > a:
             y[a:b] = x[a:b] @ np.asarray(W, dtype=np.float64).T
     return y
+
+
+# ----------------------------------------------------------------------------------------------
+# FP8 (e4m3) in blocks of 128, and routing
+# ----------------------------------------------------------------------------------------------
+
+def _e4m3_table():
+    """The values of codes 0 .. 127 (sign bit clear), the last a NaN."""
+    c = np.arange(128)
+    e, f = c >> 3, c & 7
+    v = np.where(e == 0, f / 8.0 * 2.0 ** -6, (1 + f / 8.0) * 2.0 ** (e - 7.0))
+    v[127] = np.nan
+    return v
+
+
+def _fp8_spread(scales, R, C, tile):
+    s = np.repeat(scales, 128, axis=1)[:, :C]
+    return np.repeat(s, 128, axis=0)[:R] if tile else s
+
+
+def fp8_encode(x, tile=False):
+    """x [R, C] (values of any float type) -> (codes u8 [R, C], scales f32).
+
+    scale = max(top / 448, 2^-126) as a float32, top the block's largest magnitude; the code is the e4m3
+    value nearest to the float32 quotient, ties to the even code. A block with an infinity or a NaN has a
+    NaN scale and codes 0x7f."""
+    x = np.asarray(x, dtype=np.float64)
+    R, C = x.shape
+    h = 128 if tile else 1
+    nr, nc = -(-R // h), -(-C // 128)
+    pad = np.zeros((nr * h, nc * 128))
+    pad[:R, :C] = np.abs(x)
+    bad = ~np.isfinite(pad)
+    pad[bad] = 0.0
+    blocks = pad.reshape(nr, h, nc, 128)
+    top = blocks.max(axis=(1, 3)).astype(np.float32)
+    with np.errstate(under="ignore"):
+        scales = np.maximum(top / np.float32(448), np.float32(2.0 ** -126))
+    scales[bad.reshape(nr, h, nc, 128).any(axis=(1, 3))] = np.nan
+    with np.errstate(invalid="ignore", under="ignore", over="ignore"):
+        q = (x.astype(np.float32) / _fp8_spread(scales, R, C, tile)).astype(np.float64)
+    table = _e4m3_table()[:127]
+    a = np.abs(np.where(np.isfinite(q), q, 0.0))
+    hi = np.searchsorted(table, a).clip(0, 126)
+    lo = np.maximum(hi - 1, 0)
+    dl, dh = a - table[lo], table[hi] - a
+    code = np.where(table[hi] <= a, hi, np.where(dl < dh, lo, np.where(dh < dl, hi, hi - (hi & 1))))
+    code = code.astype(np.uint8) | (np.signbit(q).astype(np.uint8) << 7)
+    code[np.isnan(_fp8_spread(scales, R, C, tile))] = 0x7f
+    return code, scales
+
+
+def fp8_decode(codes, scales, tile=False):
+    """fp64 values of codes [R, C] with their scales."""
+    codes = np.asarray(codes)
+    R, C = codes.shape
+    v = _e4m3_table()[codes & 127] * np.where(codes >> 7, -1.0, 1.0)
+    return v * _fp8_spread(np.asarray(scales, dtype=np.float64), R, C, tile)
+
+
+def route(logits, k, score="softmax", bias=None, groups=1, top_groups=None, group_top=1,
+          renormalize=True, scale=1.0):
+    """One token after the other, by Python's sort: (experts [T, k], weights [T, k], offsets [E + 1],
+    rows [T k], places [T, k]). logits without NaN or +inf."""
+    logits = np.asarray(logits, dtype=np.float64)
+    T, E = logits.shape
+    top_groups = groups if top_groups is None else top_groups
+    per = E // groups
+    experts, weights = np.full((T, k), -1), np.zeros((T, k))
+    for t in range(T):
+        l = logits[t]
+        alive = [e for e in range(E) if l[e] != -np.inf and (bias is None or bias[e] != -np.inf)]
+        if score == "sigmoid":
+            s = [1.0 / (1.0 + np.exp(-v)) if v >= 0 else np.exp(v) / (1.0 + np.exp(v)) for v in l]
+        else:
+            top = max(l)
+            x = [np.exp(v - top) if top > -np.inf else 0.0 for v in l]
+            s = [v / sum(x) if top > -np.inf else 0.0 for v in x]
+        by_logit = bias is None and (groups == top_groups or group_top == 1)
+        v = l if by_logit else [s[e] + (0.0 if bias is None else float(bias[e])) for e in range(E)]
+        group = []
+        for g in range(groups):
+            best = sorted((v[e] for e in alive if e // per == g), reverse=True)
+            if best:
+                group.append((-sum(best[:group_top]), g))
+        kept = {g for _, g in sorted(group)[:top_groups]}
+        chosen = sorted((-v[e], e) for e in alive if e // per in kept)[:k]
+        w = [s[e] for _, e in chosen]
+        total = sum(w) if renormalize else 1.0
+        for j, (_, e) in enumerate(chosen):
+            experts[t, j] = e
+            weights[t, j] = (w[j] / total if total != 0 else 0.0) * scale
+    order = sorted((e, i) for i, e in enumerate(experts.reshape(-1)) if e >= 0)
+    offsets = np.array([sum(1 for e, _ in order if e < n) for n in range(E + 1)])
+    rows, places = np.full(T * k, -1), np.full(T * k, -1)
+    for p, (_, i) in enumerate(order):
+        rows[p], places[i] = i // k, p
+    return experts, weights, offsets, rows, places.reshape(T, k)

@@ -12,6 +12,9 @@ from ._lib import (  # noqa: F401
     aaac_assign_refine_batch,
     aaac_awq_prescale,
     aaac_dequant,
+    aaac_fp8_dequant,
+    aaac_fp8_matmul,
+    aaac_fp8_quantize,
     aaac_gemv,
     aaac_gemv_batch,
     aaac_importance,
@@ -23,15 +26,26 @@ from ._lib import (  # noqa: F401
     aaac_pack,
     aaac_refine,
     aaac_refine_batch,
+    aaac_route,
+    aaac_rows_from_experts,
+    aaac_rows_to_experts,
     load,
 )
 from .inference import (  # noqa: F401
+    FP8Matrix,
     MXFP4Matrix,
     PackedExperts,
+    Routing,
+    fp8_dequant,
+    fp8_matmul,
+    fp8_quantize,
     mxfp4_dequant,
     mxfp4_matmul,
     mxfp4_quantize,
     packed_matmul,
+    route,
+    rows_from_experts,
+    rows_to_experts,
 )
 from .quantize import (  # noqa: F401
     Layer,

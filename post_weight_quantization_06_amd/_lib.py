@@ -30,6 +30,8 @@ REFINE_ROUND_BF16 = 1
 REFINE_W2_KNOWN = 2
 MAX_BATCH = 8
 MXFP4 = 3
+FP8 = 4
+SCORES = {"softmax": 0, "sigmoid": 1}
 MATMUL_PACKED, MATMUL_MXFP4, MATMUL_MXFP4_X, MATMUL_QUANTIZE_X = 0, 1, 2, 3
 QUANTIZE_X = 1
 # element types of the matmul and MXFP4 calls
@@ -42,7 +44,9 @@ EXPORTED = (
     "aaac_gemv", "aaac_gemv_batch", "aaac_assign_refine_batch", "aaac_init_quantiles_batch",
     "aaac_pack_batch", "aaac_dequant_batch", "aaac_refine_batch_noalloc", "aaac_mxfp4_quantize",
     "aaac_mxfp4_dequant", "aaac_mxfp4_matmul", "aaac_matmul", "aaac_matmul_workspace_bytes",
-    "aaac_matmul_plan",
+    "aaac_matmul_plan", "aaac_fp8_quantize", "aaac_fp8_dequant", "aaac_fp8_matmul",
+    "aaac_fp8_matmul_workspace_bytes", "aaac_fp8_matmul_plan", "aaac_route",
+    "aaac_route_workspace_bytes", "aaac_rows_to_experts", "aaac_rows_from_experts",
 )
 
 
@@ -107,6 +111,23 @@ def load(path: str = LIB_PATH):
         "aaac_assign_refine_batch": (c_int, [c_int, P(c_vp), P(c_i64), P(c_i64), c_int, c_int,
                                              c_int, P(c_vp), P(c_vp), P(c_vp), P(c_vp), c_int,
                                              c_vp, c_vp, c_vp, c_size, c_vp]),
+        "aaac_fp8_quantize": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_int, c_vp,
+                                      c_i64, c_vp, c_vp]),
+        "aaac_fp8_dequant": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_int,
+                                     c_i64, c_vp]),
+        "aaac_fp8_matmul_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i64, c_int]),
+        "aaac_fp8_matmul_plan": (c_int, [c_i64, c_i64, c_i64, c_i64, c_int, P(ctypes.c_int32)]),
+        "aaac_fp8_matmul": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_int,
+                                    c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_i64, c_vp, c_size,
+                                    c_vp]),
+        "aaac_route_workspace_bytes": (c_size, [c_i64, c_i64]),
+        "aaac_route": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_int, c_i64, c_int, c_int,
+                               c_int, c_int, ctypes.c_float, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                               c_size, c_vp]),
+        "aaac_rows_to_experts": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64,
+                                         c_i64, c_vp]),
+        "aaac_rows_from_experts": (c_int, [c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64,
+                                           c_i64, c_vp, c_int, c_i64, c_vp]),
         "aaac_gemv": (c_int, [c_vp, c_vp, c_vp, c_vp, c_i64, c_i64, c_int, c_int, c_int, c_vp,
                               c_int, c_vp, c_vp]),
         "aaac_gemv_batch": (c_int, [c_int, P(c_vp), P(c_vp), P(c_vp), P(c_vp), P(c_i64),
@@ -797,3 +818,235 @@ def aaac_matmul(codes: torch.Tensor, scales: torch.Tensor, bitmap: Optional[torc
     _launch(what, dev, stream, codes.data_ptr(), scales.data_ptr(),
             None if bitmap is None else bitmap.data_ptr(), tables_bf16.data_ptr(), E, R, C, g, S,
             n, op, x.data_ptr(), T, ldx, y.data_ptr(), yt, ldy, wp, wn)
+
+
+# ------------------------------------------------------------------------------------------------
+# FP8 in blocks of 128, routing, and rows to experts and back. These too run on the tensors' own device.
+# ------------------------------------------------------------------------------------------------
+
+def _own_ws(need: int, ws, like: torch.Tensor, stream, what: str):
+    """(workspace, its pointer, its bytes) of a call that needs `need` bytes: the caller's, or one from
+    torch on the call's stream."""
+    if need == 0:
+        return None, None, 0
+    if ws is None:
+        if stream is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+        else:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+    elif ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError("%s: ws must be contiguous uint8" % what)
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _stacked(t: torch.Tensor, name: str):
+    """(E, rows, columns, row stride, matrix stride) of a 2-D or 3-D tensor with unit column stride."""
+    if t.dim() not in (2, 3):
+        raise ValueError("%s must be 2-D or 3-D (got %d-D)" % (name, t.dim()))
+    M, C = t.shape[-2:]
+    if t.stride(-1) != 1 and C > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    E = t.shape[0] if t.dim() == 3 else 1
+    ld = t.stride(-2) if M > 1 else (t.stride(0) if E > 1 else (C + 15) // 16 * 16)
+    return E, M, C, ld, t.stride(0) if E > 1 else 0
+
+
+def _fp8_codes(t: torch.Tensor, name: str):
+    """(E, rows, columns, row stride) of e4m3 codes whose matrices follow one another."""
+    if t.dtype is not torch.float8_e4m3fn:
+        raise TypeError("%s must be float8_e4m3fn (got %s)" % (name, t.dtype))
+    E, M, C, ld, step = _stacked(t, name)
+    if E > 1 and M > 0 and step != M * ld:
+        raise ValueError("%s must hold its matrices one after the other" % name)
+    return E, M, C, ld
+
+
+def _f32(t: torch.Tensor, name: str, numel: int):
+    if t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError("%s must be contiguous float32 of %d elements (got %s %s)" % (
+            name, numel, t.dtype, tuple(t.shape)))
+
+
+def _i32(t: torch.Tensor, name: str, numel: int):
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() != numel:
+        raise ValueError("%s must be contiguous int32 of %d elements (got %s %s)" % (
+            name, numel, t.dtype, tuple(t.shape)))
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def aaac_fp8_quantize(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tile: bool = False,
+                      stream=None):
+    """codes e4m3 like X [M, C] (or with tile [E, M, C]) in rows whose stride is a multiple of 16, and
+    scales fp32 [M, ceil(C/128)] (with tile [E, ceil(M/128), ceil(C/128)])."""
+    what = "aaac_fp8_quantize"
+    dev = _on_gpu(what, X, codes, scales)
+    _no_grad(what, X)
+    xt = _float_type(X, "X")
+    E, M, C, ldx, step = _stacked(X, "X")
+    Eq, Mq, Cq, ldq = _fp8_codes(codes, "codes")
+    if (Eq, Mq, Cq) != (E, M, C):
+        raise ValueError("%s: codes must be shaped as X (got %s and %s)" % (
+            what, tuple(codes.shape), tuple(X.shape)))
+    _f32(scales, "scales", (E * _blocks(M) if tile else E * M) * _blocks(C))
+    _launch(what, dev, stream, X.data_ptr(), xt, E, M, C, ldx, step, int(tile), codes.data_ptr(), ldq,
+            scales.data_ptr())
+
+
+def aaac_fp8_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tensor, tile: bool = False,
+                     stream=None):
+    """Y [M, C] (or [E, M, C], its matrices one after the other) = the values of the codes."""
+    what = "aaac_fp8_dequant"
+    dev = _on_gpu(what, codes, scales, Y)
+    yt = _float_type(Y, "Y")
+    E, M, C, ldq = _fp8_codes(codes, "codes")
+    Ey, My, Cy, ldy, step = _stacked(Y, "Y")
+    if (Ey, My, Cy) != (E, M, C) or (E > 1 and M > 0 and step != M * ldy):
+        raise ValueError("%s: Y must be shaped as the codes, its matrices one after the other (got %s)" %
+                         (what, tuple(Y.shape)))
+    _f32(scales, "scales", (E * _blocks(M) if tile else E * M) * _blocks(C))
+    if not tile:
+        E, M = 1, E * M
+    _launch(what, dev, stream, codes.data_ptr(), ldq, scales.data_ptr(), E, M, C, int(tile),
+            Y.data_ptr(), yt, ldy)
+
+
+@functools.lru_cache(maxsize=4096)
+def fp8_matmul_workspace_bytes(E: int, R: int, C: int, T: int, Tx: int, quantize: bool,
+                               dev: int = 0) -> int:
+    """Workspace bytes of an FP8 product on GPU dev."""
+    fn = (_lib or load()).aaac_fp8_matmul_workspace_bytes
+    if torch.cuda.is_available():
+        with torch.cuda.device(dev):
+            return int(fn(E, R, C, T, Tx, int(quantize)))
+    return int(fn(E, R, C, T, Tx, int(quantize)))
+
+
+def fp8_matmul_plan(E: int, R: int, C: int, T: int, has_ws: bool = True):
+    """matmul_plan of an FP8 product."""
+    plan = (ctypes.c_int32 * 6)()
+    _check(load().aaac_fp8_matmul_plan(E, R, C, T, int(has_ws), plan), "aaac_fp8_matmul_plan")
+    return tuple(plan)
+
+
+def aaac_fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                    offsets: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+                    x_scales: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                    stream=None):
+    """y [T, R] = x times the transposed FP8 matrices: codes e4m3 [R, C] or [E, R, C] with scales fp32
+    [.., ceil(R/128), ceil(C/128)]. x bf16, fp16 or fp32 [Tx, C], quantized first, or codes e4m3
+    [Tx, C] with x_scales fp32 [Tx, ceil(C/128)]. rows: int32 [T], the row of x of each row of y;
+    None: T = Tx. offsets: int32 [E + 1] (see aaac.h), or None for one matrix."""
+    what = "aaac_fp8_matmul"
+    dev = _on_gpu(what, codes, scales, x, y, offsets, rows, x_scales, ws)
+    E, R, C, ldw = _fp8_codes(codes, "codes")
+    _f32(scales, "scales", E * _blocks(R) * _blocks(C))
+    if x.dim() != 2:
+        raise ValueError("%s: x must be 2-D (got %d-D)" % (what, x.dim()))
+    if x_scales is None:
+        _no_grad(what, x)
+        xt, xs = _float_type(x, "x"), None
+        Tx, K, ldx = _rows(x, "x")
+    else:
+        _, Tx, K, ldx = _fp8_codes(x, "x")
+        xt, xs = FP8, x_scales.data_ptr()
+        _f32(x_scales, "x_scales", Tx * _blocks(K))
+    if K != C:
+        raise ValueError("%s: x has %d columns, the weights %d" % (what, K, C))
+    T = y.shape[0] if rows is not None and y.dim() == 2 else Tx
+    yt = _float_type(y, "y")
+    M, N, ldy = _rows(y, "y")
+    if M != T or N != R:
+        raise ValueError("%s: y must be [%d, %d] (got [%d, %d])" % (what, T, R, M, N))
+    if offsets is not None:
+        _i32(offsets, "offsets", E + 1)
+    if rows is not None:
+        _i32(rows, "rows", T)
+    need = fp8_matmul_workspace_bytes(E, R, C, T, Tx, xs is None, dev)
+    ws, wp, wn = _own_ws(need, ws, y, stream, what)
+    _launch(what, dev, stream, codes.data_ptr(), ldw, scales.data_ptr(), E, R, C,
+            None if offsets is None else offsets.data_ptr(), None if rows is None else rows.data_ptr(),
+            x.data_ptr(), xt, xs, Tx, ldx, T, y.data_ptr(), yt, ldy, wp, wn)
+
+
+def aaac_route(logits: torch.Tensor, k: int, experts: torch.Tensor, weights: torch.Tensor,
+               offsets: torch.Tensor, rows: torch.Tensor, places: torch.Tensor,
+               score: str = "softmax", bias: Optional[torch.Tensor] = None, groups: int = 1,
+               top_groups: Optional[int] = None, group_top: int = 1, renormalize: bool = True,
+               scale: float = 1.0, ws: Optional[torch.Tensor] = None, stream=None):
+    """Routing of logits [T, E] (bf16, fp16 or fp32, any row stride) into experts int32 [T, k], weights
+    fp32 [T, k], offsets int32 [E + 1], rows int32 [T k] and places int32 [T, k] (see aaac.h)."""
+    what = "aaac_route"
+    dev = _on_gpu(what, logits, experts, weights, offsets, rows, places, bias, ws)
+    _no_grad(what, logits)
+    if bias is not None:
+        _no_grad(what, bias)
+    lt = _float_type(logits, "logits")
+    T, E, ldl = _rows(logits, "logits")
+    if score not in SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
+    if bias is not None:
+        _f32(bias, "bias", E)
+    _i32(experts, "experts", T * k)
+    _f32(weights, "weights", T * k)
+    _i32(offsets, "offsets", E + 1)
+    _i32(rows, "rows", T * k)
+    _i32(places, "places", T * k)
+    need = int((_lib or load()).aaac_route_workspace_bytes(T, E))
+    ws, wp, wn = _own_ws(need, ws, logits, stream, what)
+    _launch(what, dev, stream, logits.data_ptr(), lt, T, E, ldl,
+            None if bias is None else bias.data_ptr(), SCORES[score], k, groups,
+            groups if top_groups is None else top_groups, group_top, int(renormalize), scale,
+            experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+            places.data_ptr(), wp, wn)
+
+
+def _any_rows(t: torch.Tensor, name: str):
+    """_rows, a single row's stride being its length."""
+    M, C, ld = _rows(t, name)
+    return M, C, max(C, 1) if M <= 1 else ld
+
+
+def aaac_rows_to_experts(x: torch.Tensor, places: torch.Tensor, out: torch.Tensor, stream=None):
+    """out[places[t, j]] = x[t]: x [T, C] and out [N, C] of one type of 1, 2 or 4 bytes, any row
+    strides; places int32 [T, k]."""
+    what = "aaac_rows_to_experts"
+    dev = _on_gpu(what, x, places, out)
+    _no_grad(what, x)
+    if x.dtype is not out.dtype:
+        raise TypeError("%s: x is %s, out %s" % (what, x.dtype, out.dtype))
+    if x.dtype.itemsize not in (1, 2, 4):
+        raise TypeError("%s: x must have elements of 1, 2 or 4 bytes (got %s)" % (what, x.dtype))
+    T, C, ldx = _any_rows(x, "x")
+    N, Co, ldo = _any_rows(out, "out")
+    if C != Co or places.dim() != 2 or places.shape[0] != T:
+        raise ValueError("%s: x [T, C], places [T, k], out [N, C] (got %s, %s, %s)" % (
+            what, tuple(x.shape), tuple(places.shape), tuple(out.shape)))
+    k = places.shape[1]
+    _i32(places, "places", T * k)
+    _launch(what, dev, stream, x.data_ptr(), x.dtype.itemsize, T, C, ldx, places.data_ptr(), k,
+            out.data_ptr(), N, ldo)
+
+
+def aaac_rows_from_experts(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor,
+                           out: torch.Tensor, stream=None):
+    """out[t] = sum_j weights[t, j] y[places[t, j]]: y [N, C] and out [T, C] (bf16, fp16 or fp32 each, any
+    row strides), places int32 and weights fp32 [T, k]."""
+    what = "aaac_rows_from_experts"
+    dev = _on_gpu(what, y, places, weights, out)
+    _no_grad(what, y)
+    _no_grad(what, weights)
+    yt, ot = _float_type(y, "y"), _float_type(out, "out")
+    N, C, ldy = _any_rows(y, "y")
+    T, Co, ldo = _any_rows(out, "out")
+    if C != Co or places.dim() != 2 or places.shape[0] != T or weights.shape != places.shape:
+        raise ValueError("%s: y [N, C], places and weights [T, k], out [T, C] (got %s, %s, %s, %s)" % (
+            what, tuple(y.shape), tuple(places.shape), tuple(weights.shape), tuple(out.shape)))
+    k = places.shape[1]
+    _i32(places, "places", T * k)
+    _f32(weights, "weights", T * k)
+    _launch(what, dev, stream, y.data_ptr(), yt, N, C, ldy, places.data_ptr(), weights.data_ptr(), T, k,
+            out.data_ptr(), ot, ldo)

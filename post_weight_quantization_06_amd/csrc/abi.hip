@@ -7,6 +7,7 @@
 
 #include "aaac.h"
 #include "common.h"
+#include "fp8.h"
 #include "mxfp4.h"
 
 namespace aaac {
@@ -537,6 +538,46 @@ aaac_status run_matmul(MatmulArgs& a, int kind, int x_type, void* ws, size_t ws_
   return hip_status(launch_matmul(a, k, plan_matmul(a, k, ws != nullptr), stream), who);
 }
 
+// Shape and strides of an FP8 quantize or dequant call.
+aaac_status check_fp8_shape(int64_t E, int64_t M, int64_t C, int64_t ld, int64_t ldq, int tile,
+                            const char* who) {
+  if (tile != 0 && tile != 1) return fail(AAAC_ERR_INVALID_ARG, "%s: tile %d", who, tile);
+  if (E < 1 || (E != 1 && !tile) || M < 0 || C < 1 || C >= kMaxMatmulCols || ld < C || ldq < C)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
+                "%s: E=%lld M=%lld C=%lld strides %lld, %lld (need E >= 1, 1 without tiles, M >= 0, "
+                "1 <= C < 2^21, strides >= C)",
+                who, (long long)E, (long long)M, (long long)C, (long long)ld, (long long)ldq);
+  const int64_t wide = (C + kFp8Block - 1) / kFp8Block * kFp8Block;
+  if (M > ((((int64_t)1 << 40) - 1) / wide) / E ||
+      (E * M > 1 && (ld > ((int64_t)1 << 60) / (E * M) || ldq > ((int64_t)1 << 60) / (E * M))))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: E*M*C must stay below 2^40", who);
+  return AAAC_OK;
+}
+
+// The sizes of an FP8 product that the queries are asked about; false for an unsupported one.
+bool fp8_query_args(int64_t E, int64_t R, int64_t C, int64_t T, MatmulArgs& a) {
+  if (E < 1 || E > 65535 || R < 1 || R >= ((int64_t)1 << 31) || C < 1 || C >= kMaxMatmulCols || T < 1 ||
+      T >= ((int64_t)1 << 31))
+    return false;
+  a.E = (int)E;
+  a.R = R;
+  a.C = C;
+  a.Cp = fp8_blocks(C) * kFp8Block;
+  a.T = T;
+  return true;
+}
+
+// Where an FP8 product's workspace holds what: the parts of split sums, then quantized rows of x (codes
+// [Tx, Cp], zeros past C, and scales a block at a time, [Cp / 128, Tx]).
+MatmulWs fp8_matmul_ws(const MatmulArgs& a, int64_t Tx, bool quantize) {
+  MatmulWs w;
+  const size_t parts = parts_bytes(a, plan_matmul(a, kFp8, true));
+  w.codes = (parts + 255) / 256 * 256;
+  w.scales = w.codes + (size_t)Tx * (size_t)a.Cp;
+  w.bytes = quantize ? w.scales + (size_t)Tx * (size_t)(a.Cp / kFp8Block) * sizeof(float) : parts;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
@@ -929,6 +970,251 @@ aaac_status aaac_matmul(const uint8_t* codes, const uint16_t* scales, const uint
   if ((S < g) != (bitmap != nullptr))
     return fail(AAAC_ERR_INVALID_ARG, "%s: bitmap must be given exactly when S < g", who);
   return run_matmul(a, AAAC_MATMUL_PACKED, AAAC_BF16, ws, ws_bytes, static_cast<hipStream_t>(stream),
+                    who);
+}
+
+aaac_status aaac_fp8_quantize(const void* X, int x_type, int64_t E, int64_t M, int64_t C, int64_t ldx,
+                              int64_t stride_x, int tile, uint8_t* codes, int64_t ldq, float* scales,
+                              void* stream) {
+  const char* who = "aaac_fp8_quantize";
+  aaac_status st = check_fp8_shape(E, M, C, ldx, ldq, tile, who);
+  if (st != AAAC_OK) return st;
+  const int b = type_bytes(x_type);
+  if (!b) return fail(AAAC_ERR_INVALID_ARG, "%s: x_type %d", who, x_type);
+  if (ldq % 16 != 0)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: ldq=%lld (need a multiple of 16)", who, (long long)ldq);
+  if (E > 1 && M > 0 && (stride_x < (M - 1) * ldx + C || stride_x > ((int64_t)1 << 60) / E))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: stride_x=%lld", who, (long long)stride_x);
+  if (M > 0 && (!X || !aligned(X, b) || !codes || !aligned(codes, 16) || !scales || !aligned(scales, 4)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: null or misaligned pointer (codes need 16 bytes)", who);
+  return hip_status(launch_fp8_quantize(X, x_type, E, M, C, ldx, E > 1 ? stride_x : 0, tile != 0, codes, ldq,
+                                        (C + 15) / 16 * 16, scales, fp8_blocks(C), 1,
+                                        static_cast<hipStream_t>(stream)),
+                    who);
+}
+
+aaac_status aaac_fp8_dequant(const uint8_t* codes, int64_t ldq, const float* scales, int64_t E,
+                             int64_t M, int64_t C, int tile, void* Y, int y_type, int64_t ldy,
+                             void* stream) {
+  const char* who = "aaac_fp8_dequant";
+  aaac_status st = check_fp8_shape(E, M, C, ldy, ldq, tile, who);
+  if (st != AAAC_OK) return st;
+  const int b = type_bytes(y_type);
+  if (!b) return fail(AAAC_ERR_INVALID_ARG, "%s: y_type %d", who, y_type);
+  if (M > 0 && (!Y || !aligned(Y, b) || !codes || !scales || !aligned(scales, 4)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: null or misaligned pointer", who);
+  return hip_status(launch_fp8_dequant(codes, ldq, scales, E, M, C, tile != 0, Y, y_type, ldy,
+                                       static_cast<hipStream_t>(stream)),
+                    who);
+}
+
+size_t aaac_fp8_matmul_workspace_bytes(int64_t E, int64_t R, int64_t C, int64_t T, int64_t Tx,
+                                       int quantize) {
+  MatmulArgs a = {};
+  if (!fp8_query_args(E, R, C, T, a) || Tx < 0 || Tx >= ((int64_t)1 << 31)) return 0;
+  return fp8_matmul_ws(a, Tx, quantize != 0).bytes;
+}
+
+aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int has_ws,
+                                 int32_t plan[6]) {
+  const char* who = "aaac_fp8_matmul_plan";
+  MatmulArgs a = {};
+  if (!fp8_query_args(E, R, C, T, a))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: E=%lld R=%lld C=%lld T=%lld", who, (long long)E,
+                (long long)R, (long long)C, (long long)T);
+  if (!plan) return fail(AAAC_ERR_INVALID_ARG, "%s: plan null", who);
+  const MatmulPlan p = plan_matmul(a, kFp8, has_ws != 0);
+  const int32_t v[6] = {p.bm, p.bn, p.split, p.rt, p.nt, p.chunks};
+  for (int i = 0; i < 6; ++i) plan[i] = v[i];
+  return ok();
+}
+
+aaac_status aaac_fp8_matmul(const uint8_t* w_codes, int64_t ldw, const float* w_scales, int64_t E,
+                            int64_t R, int64_t C, const int32_t* offsets, const int32_t* rows,
+                            const void* x, int x_type, const float* x_scales, int64_t Tx, int64_t ldx,
+                            int64_t T, void* y, int y_type, int64_t ldy, void* ws, size_t ws_bytes,
+                            void* stream) {
+  const char* who = "aaac_fp8_matmul";
+  const bool quantize = x_type != AAAC_FP8;
+  const int xb = quantize ? type_bytes(x_type) : 16;
+  if (!xb) return fail(AAAC_ERR_INVALID_ARG, "%s: x_type %d", who, x_type);
+  MatmulArgs a = {};
+  a.codes = w_codes;
+  a.scales = w_scales;
+  a.E = (int)E;
+  a.R = R;
+  a.C = C;
+  a.Cp = C > 0 && C < kMaxMatmulCols ? fp8_blocks(C) * kFp8Block : kFp8Block;
+  a.offsets = offsets;
+  a.T = T;
+  a.ldx = ldx;
+  a.pick = rows;
+  a.Tx = Tx;
+  a.ldw = ldw;
+  a.y = y;
+  a.y_type = y_type;
+  a.ldy = ldy;
+  a.x = Tx > 0 ? x : y;                          // of an x without rows nothing is read
+  aaac_status st = check_matmul(a, E, false, Tx > 0 ? xb : 1, who);
+  a.x = x;
+  if (st != AAAC_OK) return st;
+  if (Tx < 0 || Tx >= ((int64_t)1 << 31) || (!rows && Tx != T))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: Tx=%lld T=%lld (need Tx == T without rows)", who,
+                (long long)Tx, (long long)T);
+  constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;
+  if (ldw < C || ldw % 16 != 0 || ldw >= kMaxRowBytes ||
+      (!quantize && (ldx < C || ldx % 16 != 0 || ldx >= kMaxRowBytes)))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
+                "%s: ldw=%lld ldx=%lld (rows of codes need a stride of at least C, a multiple of 16 below "
+                "2^22)", who, (long long)ldw, (long long)ldx);
+  if (!w_codes || !aligned(w_codes, 16) || !w_scales || !aligned(w_scales, 4))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: weights null or misaligned (codes need 16 bytes)", who);
+  if (rows && !aligned(rows, 4)) return fail(AAAC_ERR_INVALID_ARG, "%s: rows misaligned", who);
+  if (quantize ? x_scales != nullptr : (Tx > 0 && (!x_scales || !aligned(x_scales, 4))))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: x_scales must be given exactly with FP8 x", who);
+  if (quantize) {
+    st = check_fp8_shape(1, Tx, C, ldx, C, 0, who);
+    if (st != AAAC_OK) return st;
+  }
+  const int64_t row_bytes = quantize ? a.Cp : ldx;
+  if (rows && Tx > 0 &&
+      (Tx > (((int64_t)1 << 31) - 16) / row_bytes || Tx > (((int64_t)1 << 31) - 16) / (a.Cp / 32)))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: with rows, x must stay below 2^31 bytes of codes", who);
+  if (T == 0) return ok();
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  a.x_blocks = x_scales;
+  a.xs_row = fp8_blocks(C);
+  a.xs_blk = 1;
+  if (ws || quantize) {
+    const MatmulWs w = fp8_matmul_ws(a, Tx, quantize);
+    if (!ws || !aligned(ws, 256))
+      return fail(AAAC_ERR_INVALID_ARG, "%s: ws null or not 256-byte aligned", who);
+    if (ws_bytes < w.bytes)
+      return fail(AAAC_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", who, ws_bytes,
+                  w.bytes);
+    a.parts = static_cast<float*>(ws);
+    if (quantize) {
+      uint8_t* codes = static_cast<uint8_t*>(ws) + w.codes;
+      float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.scales);
+      const hipError_t e = launch_fp8_quantize(x, x_type, 1, Tx, C, ldx, 0, false, codes, a.Cp, a.Cp,
+                                               scales, 1, Tx, s);
+      if (e != hipSuccess) return hip_status(e, who);
+      a.x = codes;
+      a.ldx = a.Cp;
+      a.x_blocks = scales;
+      a.xs_row = 1;
+      a.xs_blk = Tx;
+    }
+  }
+  return hip_status(launch_matmul(a, kFp8, plan_matmul(a, kFp8, ws != nullptr), s), who);
+}
+
+size_t aaac_route_workspace_bytes(int64_t T, int64_t E) {
+  if (T < 1 || T >= ((int64_t)1 << 31) || E < 1 || E > kMaxExperts) return 0;
+  return route_workspace_bytes(T, (int)E);
+}
+
+aaac_status aaac_route(const void* logits, int type, int64_t T, int64_t E, int64_t ldl,
+                       const float* bias, int score, int64_t k, int groups, int top_groups,
+                       int group_top, int renormalize, float scale, int32_t* experts, float* weights,
+                       int32_t* offsets, int32_t* rows, int32_t* places, void* ws, size_t ws_bytes,
+                       void* stream) {
+  const char* who = "aaac_route";
+  const int b = type_bytes(type);
+  if (!b) return fail(AAAC_ERR_INVALID_ARG, "%s: type %d", who, type);
+  if (score != AAAC_SOFTMAX && score != AAAC_SIGMOID)
+    return fail(AAAC_ERR_INVALID_ARG, "%s: score %d", who, score);
+  if (E < 1 || E > kMaxExperts || groups < 1 || groups > kMaxGroups || E % groups != 0)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
+                "%s: E=%lld in %d groups (need 1 <= E <= %d, 1 <= groups <= %d, E %% groups == 0)", who,
+                (long long)E, groups, kMaxExperts, kMaxGroups);
+  if (top_groups < 1 || top_groups > groups || (group_top != 1 && group_top != 2))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: top_groups=%d of %d, group_top=%d (need 1 or 2)", who,
+                top_groups, groups, group_top);
+  if (k < 1 || k > kMaxChoices || k > top_groups * (E / groups))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: k=%lld (need 1 <= k <= %d, at most %lld experts take part)",
+                who, (long long)k, kMaxChoices, (long long)(top_groups * (E / groups)));
+  if (T < 0 || T > (((int64_t)1 << 31) - 1) / k || ldl < E || ldl > ((int64_t)1 << 60) / (T > 0 ? T : 1))
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: T=%lld ldl=%lld (need T k < 2^31, ldl >= E)", who,
+                (long long)T, (long long)ldl);
+  if (!offsets || !aligned(offsets, 4) || (bias && !aligned(bias, 4)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: offsets null, or offsets or bias misaligned", who);
+  if (T > 0 && (!logits || !aligned(logits, b) || !experts || !aligned(experts, 4) || !weights ||
+                !aligned(weights, 4) || !rows || !aligned(rows, 4) || !places || !aligned(places, 4)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: null or misaligned pointer", who);
+  const size_t need = aaac_route_workspace_bytes(T, E);
+  if (need > 0 && (!ws || !aligned(ws, 256)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: ws null or not 256-byte aligned", who);
+  if (ws_bytes < need)
+    return fail(AAAC_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
+  RouteArgs a = {};
+  a.logits = logits;
+  a.type = type;
+  a.T = T;
+  a.ldl = ldl;
+  a.E = (int)E;
+  a.k = (int)k;
+  a.bias = bias;
+  a.sigmoid = score == AAAC_SIGMOID;
+  a.renormalize = renormalize != 0;
+  a.groups = groups;
+  a.top_groups = top_groups;
+  a.group_top = group_top;
+  a.scale = scale;
+  a.experts = experts;
+  a.weights = weights;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.places = places;
+  a.counts = static_cast<int32_t*>(ws);
+  return hip_status(launch_route(a, static_cast<hipStream_t>(stream)), who);
+}
+
+// The sizes shared by the rows' way to their experts and back.
+static aaac_status check_rows(int64_t T, int64_t N, int64_t C, int64_t k, int64_t ld1, int64_t ld2,
+                              const int32_t* places, const char* who) {
+  const int64_t most = (int64_t)1 << 31;
+  if (T < 0 || T >= most || N < 0 || N >= most || C < 1 || C >= most || k < 1 || k > kMaxChoices)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE,
+                "%s: T=%lld N=%lld C=%lld k=%lld (need 0 <= T, N < 2^31, 1 <= C < 2^31, 1 <= k <= %d)", who,
+                (long long)T, (long long)N, (long long)C, (long long)k, kMaxChoices);
+  if (ld1 < C || ld2 < C || ld1 >= most || ld2 >= most)
+    return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: row strides %lld, %lld (need C <= stride < 2^31)", who,
+                (long long)ld1, (long long)ld2);
+  if (T > 0 && (!places || !aligned(places, 4)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: places null or misaligned", who);
+  return AAAC_OK;
+}
+
+aaac_status aaac_rows_to_experts(const void* x, int element, int64_t T, int64_t C, int64_t ldx,
+                                 const int32_t* places, int64_t k, void* out, int64_t N, int64_t ldo,
+                                 void* stream) {
+  const char* who = "aaac_rows_to_experts";
+  if (element != 1 && element != 2 && element != 4)
+    return fail(AAAC_ERR_INVALID_ARG, "%s: element of %d bytes", who, element);
+  aaac_status st = check_rows(T, N, C, k, ldx, ldo, places, who);
+  if (st != AAAC_OK) return st;
+  if (T == 0 || N == 0) return ok();
+  if (!x || !aligned(x, element) || !out || !aligned(out, element))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: null or misaligned pointer", who);
+  return hip_status(launch_rows_to_experts(x, T, C * element, ldx * element, places, (int)k, out, N,
+                                           ldo * element, element, static_cast<hipStream_t>(stream)),
+                    who);
+}
+
+aaac_status aaac_rows_from_experts(const void* y, int y_type, int64_t N, int64_t C, int64_t ldy,
+                                   const int32_t* places, const float* weights, int64_t T, int64_t k,
+                                   void* out, int out_type, int64_t ldo, void* stream) {
+  const char* who = "aaac_rows_from_experts";
+  const int yb = type_bytes(y_type), ob = type_bytes(out_type);
+  if (!yb || !ob) return fail(AAAC_ERR_INVALID_ARG, "%s: y_type %d, out_type %d", who, y_type, out_type);
+  aaac_status st = check_rows(T, N, C, k, ldy, ldo, places, who);
+  if (st != AAAC_OK) return st;
+  if (T > 0 && ((N > 0 && (!y || !aligned(y, yb))) || !out || !aligned(out, ob) || !weights ||
+                !aligned(weights, 4)))
+    return fail(AAAC_ERR_INVALID_ARG, "%s: null or misaligned pointer", who);
+  return hip_status(launch_rows_from_experts(y, y_type, N, C, ldy, places, weights, T, (int)k, out, out_type,
+                                             ldo, static_cast<hipStream_t>(stream)),
                     who);
 }
 

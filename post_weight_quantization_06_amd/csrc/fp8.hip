@@ -1,0 +1,355 @@
+// Quantisation to 8-bit floating point (e4m3) in blocks of 128, and its inverse.
+//
+// quantise: scale = max(top / 448, 2^-126) in fp32 with top = max |x| over the block, code = the e4m3
+// value nearest to the fp32 quotient x / scale, ties to even. The smallest normal number as the least
+// scale keeps the quotient's divisor and its reciprocal normal and a block of zeros free of 0 / 0. The
+// quotient never passes 448 by as much as half a step, so nothing saturates. A block with an infinity or
+// a NaN has no finite scale: its scale and codes are NaN and all of it reads back as NaN.
+//
+// Both directions move each byte once and are bound by memory.
+#include "aaac.h"
+#include "fp8.h"
+
+namespace aaac {
+
+namespace {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kLane = 16;                        // columns a lane: eight lanes make a block
+constexpr int kSteps = 2;                        // lane pieces in flight per thread
+
+template <int TYPE> struct Elem;
+template <> struct Elem<AAAC_BF16> { typedef uint16_t T; };
+template <> struct Elem<AAAC_F16> { typedef uint16_t T; };
+template <> struct Elem<AAAC_F32> { typedef uint32_t T; };
+
+template <int TYPE>
+__device__ __forceinline__ float to_f32(typename Elem<TYPE>::T v) {
+  if (TYPE == AAAC_F32) return __uint_as_float((uint32_t)v);
+  if (TYPE == AAAC_BF16) return __uint_as_float((uint32_t)v << 16);
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
+}
+
+// Sixteen consecutive elements as fp32; those at or past `valid` read as zero. VEC: p is aligned to 16
+// bytes.
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void load16(const typename Elem<TYPE>::T* p, int valid, float (&v)[kLane]) {
+  typedef typename Elem<TYPE>::T T;
+  if (valid < kLane) {
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) v[i] = i < valid ? to_f32<TYPE>(p[i]) : 0.0f;
+    return;
+  }
+  constexpr int kWords = kLane * sizeof(T) / 16;
+  u32x4 w[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) {
+    if (VEC) w[i] = reinterpret_cast<const u32x4*>(p)[i];
+    else __builtin_memcpy(&w[i], reinterpret_cast<const uint8_t*>(p) + 16 * i, 16);
+  }
+#pragma unroll
+  for (int i = 0; i < kLane; ++i) {
+    if (sizeof(T) == 4) v[i] = __uint_as_float(w[i >> 2][i & 3]);
+    else v[i] = to_f32<TYPE>((T)(w[i >> 3][(i >> 1) & 3] >> (16 * (i & 1))));
+  }
+}
+
+__device__ __forceinline__ uint32_t top_bits(const float (&v)[kLane]) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kLane; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  return top;
+}
+
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  if (top >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  return fmaxf(__uint_as_float(top) / 448.0f, 0x1p-126f);
+}
+
+// The codes of sixteen elements. Their quotients are the correctly rounded ones: with r the rounded
+// reciprocal of the scale, x r is within two units of the quotient, one correction by its remainder
+// brings it within one and the second one rounds it correctly (Markstein). Scales so small that a
+// remainder may underflow are divided by.
+__device__ __forceinline__ u32x4 encode16(const float (&v)[kLane], float scale) {
+  float q[kLane];
+  if (scale >= 0x1p-80f) {
+    const float r = 1.0f / scale;
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) {
+      float u = v[i] * r;
+      u = __builtin_fmaf(__builtin_fmaf(-u, scale, v[i]), r, u);
+      q[i] = __builtin_fmaf(__builtin_fmaf(-u, scale, v[i]), r, u);
+      // a zero keeps its sign
+      q[i] = v[i] == 0.0f ? v[i] : q[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) q[i] = v[i] / scale;
+  }
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int p = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
+    p = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], p, true);
+    w[i] = (uint32_t)p;
+  }
+  // no number: the scale of a block with an infinity or a NaN
+  if (!(scale == scale)) w = u32x4{0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
+  return w;
+}
+
+__device__ __forceinline__ int64_t divide(int64_t i, int64_t n, int64_t total) {
+  return total <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)n) : i / n;
+}
+
+// Codes past a row's last column are zeros, of a NaN block too.
+__device__ __forceinline__ u32x4 keep_first(u32x4 w, int valid) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = valid - 4 * i;
+    if (n < 4) w[i] = n <= 0 ? 0u : w[i] & ((1u << (8 * n)) - 1u);
+  }
+  return w;
+}
+
+// Blocks of 1 x 128: eight neighbouring lanes hold a block.
+template <int TYPE, bool VEC>
+__global__ __launch_bounds__(kBlock) void fp8_quantize_rows_kernel(
+    const typename Elem<TYPE>::T* __restrict__ X, int64_t C, int64_t ldx, int64_t per_row,
+    int64_t total, uint8_t* __restrict__ codes, int64_t ldq, int64_t Cw, float* __restrict__ scales,
+    int64_t s_row, int64_t s_blk) {
+  const int64_t i0 = block_id() * (kBlock * kSteps) + threadIdx.x;
+  float v[kSteps][kLane];
+  int64_t row[kSteps], col[kSteps];
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    const int64_t i = i0 + u * kBlock;
+    if (i >= total) break;
+    row[u] = divide(i, per_row, total);
+    col[u] = (i - row[u] * per_row) * kLane;
+    const int64_t left = C - col[u];
+    load16<TYPE, VEC>(X + row[u] * ldx + col[u], left > kLane ? kLane : left < 0 ? 0 : (int)left, v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    if (i0 + u * kBlock >= total) break;         // total is a multiple of 8: whole blocks leave
+    const float s = scale_of(block_max_u32_t<8>(top_bits(v[u]), 8));
+    const int64_t left = C - col[u];
+    if (col[u] < Cw) {
+      u32x4 w = encode16(v[u], s);
+      if (left < kLane) w = keep_first(w, (int)left);
+      *reinterpret_cast<u32x4*>(codes + row[u] * ldq + col[u]) = w;
+    }
+    if ((threadIdx.x & 7) == 0) scales[row[u] * s_row + col[u] / kFp8Block * s_blk] = s;
+  }
+}
+
+// Blocks of 128 x 128: one a workgroup, four rows of a lane piece a thread.
+template <int TYPE, bool VEC>
+__global__ __launch_bounds__(kBlock) void fp8_quantize_tiles_kernel(
+    const typename Elem<TYPE>::T* __restrict__ X, int64_t M, int64_t C, int64_t ldx, int64_t stride_x,
+    int64_t tiles, uint8_t* __restrict__ codes, int64_t ldq, int64_t Cw, float* __restrict__ scales) {
+  constexpr int kRows = kBlock / 8, kEach = kFp8Block / kRows;
+  __shared__ uint32_t tops[kWavesPerBlock];
+  const int64_t id = block_id();
+  if (id >= tiles) return;
+  const int64_t cb = fp8_blocks(C), rb = fp8_blocks(M);
+  const int64_t e = id / (cb * rb), tr = id / cb % rb, tc = id % cb;
+  const int64_t col = tc * kFp8Block + (threadIdx.x & 7) * kLane, row0 = tr * kFp8Block + (threadIdx.x >> 3);
+  const int64_t left = C - col;
+  const int valid = left > kLane ? kLane : left < 0 ? 0 : (int)left;
+  float v[kEach][kLane];
+  uint32_t top = 0;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int64_t r = row0 + u * kRows;
+    load16<TYPE, VEC>(X + e * stride_x + r * ldx + col, r < M ? valid : 0, v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) top = max(top, top_bits(v[u]));
+  top = block_max_u32_t<kWave>(top, kWave);
+  if ((threadIdx.x & (kWave - 1)) == 0) tops[wave_index()] = top;
+  __syncthreads();
+  top = max(max(tops[0], tops[1]), max(tops[2], tops[3]));
+  const float s = scale_of(top);
+  if (threadIdx.x == 0) scales[id] = s;
+  if (col >= Cw) return;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int64_t r = row0 + u * kRows;
+    if (r >= M) break;
+    u32x4 w = encode16(v[u], s);
+    if (valid < kLane) w = keep_first(w, valid);
+    *reinterpret_cast<u32x4*>(codes + (e * M + r) * ldq + col) = w;
+  }
+}
+
+// fp32 product of code and scale, rounded once more to a 16-bit type.
+template <int TYPE, bool VEC>
+__device__ __forceinline__ void store16(typename Elem<TYPE>::T* p, int valid, const float (&v)[kLane]) {
+  typedef typename Elem<TYPE>::T T;
+  constexpr int kWords = kLane * sizeof(T) / 16;
+  u32x4 w[kWords];
+#pragma unroll
+  for (int i = 0; i < kLane * (int)sizeof(T) / 4; ++i) {
+    if (TYPE == AAAC_F32) {
+      w[i >> 2][i & 3] = __float_as_uint(v[i]);
+    } else {
+      const f32x2 f = {v[2 * i], v[2 * i + 1]};
+      w[i >> 2][i & 3] = TYPE == AAAC_BF16
+                             ? __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2))
+                             : __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+    }
+  }
+  if (valid == kLane) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if (VEC) reinterpret_cast<u32x4*>(p)[i] = w[i];
+      else __builtin_memcpy(reinterpret_cast<uint8_t*>(p) + 16 * i, &w[i], 16);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kLane; ++i)
+    if (i < valid) {
+      if (sizeof(T) == 4) p[i] = (T)w[i >> 2][i & 3];
+      else p[i] = (T)(w[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
+    }
+}
+
+// per: rows that share a row of scales (128 with tiles, else 1). VEC: rows of Y start on 16 bytes; CV:
+// rows of codes do.
+template <int TYPE, bool VEC, bool CV>
+__global__ __launch_bounds__(kBlock) void fp8_dequant_kernel(
+    const uint8_t* __restrict__ codes, int64_t ldq, const float* __restrict__ scales, int64_t M,
+    int64_t C, int per, int64_t per_row, int64_t total, typename Elem<TYPE>::T* __restrict__ Y,
+    int64_t ldy) {
+  const int64_t i0 = block_id() * (kBlock * kSteps) + threadIdx.x;
+  const int64_t cb = fp8_blocks(C), rb = (M + per - 1) / per;
+  u32x4 w[kSteps];
+  float s[kSteps];
+  int64_t row[kSteps], col[kSteps];
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    const int64_t i = i0 + u * kBlock;
+    if (i >= total) break;
+    row[u] = divide(i, per_row, total);
+    col[u] = (i - row[u] * per_row) * kLane;
+    const uint8_t* p = codes + row[u] * ldq + col[u];
+    const int64_t left = C - col[u];
+    if (left >= kLane) {
+      if (CV) w[u] = *reinterpret_cast<const u32x4*>(p);
+      else __builtin_memcpy(&w[u], p, 16);
+    } else {
+      w[u] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int k = 0; k < kLane; ++k)
+        if (k < left) w[u][k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));
+    }
+    int64_t at = row[u];
+    if (per > 1) {
+      const int64_t e = divide(row[u], M, total);
+      at = e * rb + (row[u] - e * M) / per;
+    }
+    s[u] = scales[at * cb + col[u] / kFp8Block];
+  }
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    if (i0 + u * kBlock >= total) break;
+    float v[kLane];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u][k], false);
+      const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u][k], true);
+      v[4 * k] = a.x * s[u];
+      v[4 * k + 1] = a.y * s[u];
+      v[4 * k + 2] = b.x * s[u];
+      v[4 * k + 3] = b.y * s[u];
+    }
+    const int64_t left = C - col[u];
+    store16<TYPE, VEC>(Y + row[u] * ldy + col[u], left > kLane ? kLane : (int)left, v);
+  }
+}
+
+template <int TYPE>
+hipError_t quantize_t(const void* X, int64_t E, int64_t M, int64_t C, int64_t ldx, int64_t stride_x,
+                      bool tile, uint8_t* codes, int64_t ldq, int64_t Cw, float* scales, int64_t s_row,
+                      int64_t s_blk, hipStream_t stream) {
+  typedef typename Elem<TYPE>::T T;
+  const T* x = static_cast<const T*>(X);
+  const bool vec = (uintptr_t)X % 16 == 0 && (ldx * sizeof(T)) % 16 == 0 && (stride_x * sizeof(T)) % 16 == 0;
+  if (tile) {
+    const int64_t tiles = E * fp8_blocks(M) * fp8_blocks(C);
+    if (vec)
+      hipLaunchKernelGGL((fp8_quantize_tiles_kernel<TYPE, true>), grid_of(tiles), dim3(kBlock), 0,
+                         stream, x, M, C, ldx, stride_x, tiles, codes, ldq, Cw, scales);
+    else
+      hipLaunchKernelGGL((fp8_quantize_tiles_kernel<TYPE, false>), grid_of(tiles), dim3(kBlock), 0,
+                         stream, x, M, C, ldx, stride_x, tiles, codes, ldq, Cw, scales);
+    return hipGetLastError();
+  }
+  const int64_t per_row = fp8_blocks(C) * (kFp8Block / kLane), total = M * per_row;
+  const dim3 grid = grid_of((total + kBlock * kSteps - 1) / (kBlock * kSteps));
+  if (vec)
+    hipLaunchKernelGGL((fp8_quantize_rows_kernel<TYPE, true>), grid, dim3(kBlock), 0, stream, x, C, ldx,
+                       per_row, total, codes, ldq, Cw, scales, s_row, s_blk);
+  else
+    hipLaunchKernelGGL((fp8_quantize_rows_kernel<TYPE, false>), grid, dim3(kBlock), 0, stream, x, C,
+                       ldx, per_row, total, codes, ldq, Cw, scales, s_row, s_blk);
+  return hipGetLastError();
+}
+
+template <int TYPE>
+hipError_t dequant_t(const uint8_t* codes, int64_t ldq, const float* scales, int64_t E, int64_t M,
+                     int64_t C, bool tile, void* Y, int64_t ldy, hipStream_t stream) {
+  typedef typename Elem<TYPE>::T T;
+  T* y = static_cast<T*>(Y);
+  const bool vec = (uintptr_t)Y % 16 == 0 && (ldy * sizeof(T)) % 16 == 0;
+  const bool cv = (uintptr_t)codes % 16 == 0 && ldq % 16 == 0;
+  const int64_t per_row = (C + kLane - 1) / kLane, total = E * M * per_row;
+  const dim3 grid = grid_of((total + kBlock * kSteps - 1) / (kBlock * kSteps));
+  const int per = tile ? kFp8Block : 1;
+  if (vec && cv)
+    hipLaunchKernelGGL((fp8_dequant_kernel<TYPE, true, true>), grid, dim3(kBlock), 0, stream, codes,
+                       ldq, scales, M, C, per, per_row, total, y, ldy);
+  else if (cv)
+    hipLaunchKernelGGL((fp8_dequant_kernel<TYPE, false, true>), grid, dim3(kBlock), 0, stream, codes,
+                       ldq, scales, M, C, per, per_row, total, y, ldy);
+  else
+    hipLaunchKernelGGL((fp8_dequant_kernel<TYPE, false, false>), grid, dim3(kBlock), 0, stream, codes,
+                       ldq, scales, M, C, per, per_row, total, y, ldy);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize(const void* X, int x_type, int64_t E, int64_t M, int64_t C, int64_t ldx,
+                               int64_t stride_x, bool tile, uint8_t* codes, int64_t ldq, int64_t Cw,
+                               float* scales, int64_t s_row, int64_t s_blk, hipStream_t stream) {
+  if (E * M == 0) return hipSuccess;
+  if (x_type == AAAC_BF16)
+    return quantize_t<AAAC_BF16>(X, E, M, C, ldx, stride_x, tile, codes, ldq, Cw, scales, s_row, s_blk,
+                                 stream);
+  if (x_type == AAAC_F16)
+    return quantize_t<AAAC_F16>(X, E, M, C, ldx, stride_x, tile, codes, ldq, Cw, scales, s_row, s_blk,
+                                stream);
+  return quantize_t<AAAC_F32>(X, E, M, C, ldx, stride_x, tile, codes, ldq, Cw, scales, s_row, s_blk,
+                              stream);
+}
+
+hipError_t launch_fp8_dequant(const uint8_t* codes, int64_t ldq, const float* scales, int64_t E,
+                              int64_t M, int64_t C, bool tile, void* Y, int y_type, int64_t ldy,
+                              hipStream_t stream) {
+  if (E * M == 0) return hipSuccess;
+  if (y_type == AAAC_BF16)
+    return dequant_t<AAAC_BF16>(codes, ldq, scales, E, M, C, tile, Y, ldy, stream);
+  if (y_type == AAAC_F16)
+    return dequant_t<AAAC_F16>(codes, ldq, scales, E, M, C, tile, Y, ldy, stream);
+  return dequant_t<AAAC_F32>(codes, ldq, scales, E, M, C, tile, Y, ldy, stream);
+}
+
+}  // namespace aaac

@@ -1,0 +1,397 @@
+// Products of rows of x and weights in 8-bit floating point with a scale for each block of 128: for
+// every block b of 128 columns the matrix instruction sums the codes' products, and the block's sum goes
+// into the result times sx[t, b] sw[r / 128, b], so fp32 sums are scaled, never codes.
+//   y[t, r] = sum_b sx[t, b] sw[r / 128, b] sum_{c in b} qx[t, c] qw[r, c]
+// Matrix instructions take 16 weight rows as the A operand and 16 rows of x as B, 128 columns at a time:
+// one instruction is one block. Lane l holds, for weight row (and x row) l & 15, the same 32 of the 128
+// columns, and in the result four neighbouring weight rows of x row l & 15; a sum does not depend on
+// which lane holds which columns.
+#include "fp8.h"
+#include "matmul.h"
+
+namespace aaac {
+
+namespace {
+
+// A fragment: a lane's 32 codes of a block, for the FP8 instruction as they are, for the bf16 one (WIDE)
+// as bf16 numbers, eight of them for each of its four instructions.
+//
+// The FP8 instruction adds eight products at a time, aligned to the largest and cut below 2^-13 of it
+// (measured: 2^16 + 2^2 gives 2^16, 2^16 + 2^3 does not), then in fp32: its sums are off by 2^-19.4 of the
+// sum of magnitudes on average over normal values, 2^-15.8 at most. That is a hundredth of half a step of
+// bf16 and a thirtieth of fp16's, so results of these types use it. fp32 results take the bf16 instruction, whose
+// sums of the same exact products are fp32 sums, at half the rate; so do the few-row kernels, which wait for
+// memory.
+template <bool WIDE> struct Frag;
+template <> struct Frag<false> { u32x4 v[2]; };
+template <> struct Frag<true> { u32x4 v[4]; };
+
+__device__ __forceinline__ uint32_t two_bf16(uint32_t w, bool hi) {
+  return hi ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true))
+            : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+}
+template <bool WIDE>
+__device__ __forceinline__ Frag<WIDE> frag(u32x4 a, u32x4 b) {
+  Frag<WIDE> f;
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t lo = i < 2 ? a[2 * i] : b[2 * i - 4], hi = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+      f.v[i] = u32x4{two_bf16(lo, false), two_bf16(lo, true), two_bf16(hi, false), two_bf16(hi, true)};
+    }
+  } else {
+    f.v[0] = a;
+    f.v[1] = b;
+  }
+  return f;
+}
+
+// The sum over a block.
+template <bool WIDE>
+__device__ __forceinline__ f32x4 block_sum(const Frag<WIDE>& w, const Frag<WIDE>& x) {
+  f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c = mfma_bf16(w.v[i], x.v[i], c);
+    return c;
+  } else {
+    const u32x4 *a = w.v, *b = x.v;
+    const i32x8 wa = {(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w,
+                      (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
+    const i32x8 xa = {(int)b[0].x, (int)b[0].y, (int)b[0].z, (int)b[0].w,
+                      (int)b[1].x, (int)b[1].y, (int)b[1].z, (int)b[1].w};
+    // e4m3 on both sides, no scales (zeros select the instruction without)
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, xa, c, 0, 0, 0, 0, 0, 0);
+  }
+}
+
+// A 16-byte piece without its bytes at or past `valid`.
+__device__ __forceinline__ u32x4 first_bytes(u32x4 v, int valid) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int n = valid - 4 * i;
+    if (n < 4) v[i] = n <= 0 ? 0u : v[i] & ((1u << (8 * n)) - 1u);
+  }
+  return v;
+}
+
+// The row of x that row t of y multiplies, -1 for none.
+__device__ __forceinline__ int64_t x_row(const MatmulArgs& a, int64_t t) {
+  if (!a.pick) return t;
+  const int64_t p = a.pick[t];
+  return p >= 0 && p < a.Tx ? p : -1;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Few rows of x per matrix: the weights are read once, straight into registers, and bound the time.
+// A workgroup owns RT * 16 rows of one expert's matrix and up to NT * 16 rows of x; its waves take the
+// blocks of columns in turn and add their sums in wave order through LDS.
+// ------------------------------------------------------------------------------------------------
+template <int RT, int NT, int W>
+__global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
+  constexpr int U = 4;                           // blocks in flight
+  const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
+  const int64_t id = block_id(), tile = id / a.row_blocks, rb = id % a.row_blocks;
+  int e;
+  int64_t t0, t1;
+  if (!find_tile(a.offsets, a.E, a.T, NT * kMfma, tile, e, t0, t1)) return;
+  const int64_t r0 = rb * (RT * kMfma);
+  const int l = lane & 15, q = lane >> 4;
+  const int64_t cb = fp8_blocks(a.C);
+  const uint8_t* wp[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    const int64_t r = r0 + i * kMfma + l;
+    wp[i] = a.codes + ((int64_t)e * a.R + (r < a.R ? r : a.R - 1)) * a.ldw + 16 * q;
+  }
+  const float* sw = static_cast<const float*>(a.scales) +
+                    ((int64_t)e * fp8_blocks(a.R) + r0 / kFp8Block) * cb;
+  const uint8_t* xp[NT];
+  const float* sx[NT];
+  bool in[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t t = t0 + j * kMfma + l, x = t < t1 ? x_row(a, t) : -1;
+    in[j] = x >= 0;
+    xp[j] = static_cast<const uint8_t*>(a.x) + (in[j] ? x : 0) * a.ldx + 16 * q;
+    sx[j] = a.x_blocks + (in[j] ? x : 0) * a.xs_row;
+  }
+  f32x4 acc[RT][NT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  auto multiply = [&](const u32x4 (&w)[RT][2], const u32x4 (&x)[NT][2], const float (&f)[NT])
+      __attribute__((always_inline)) {
+    Frag<true> xf[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xf[j] = frag<true>(x[j][0], x[j][1]);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const Frag<true> wf = frag<true>(w[i][0], w[i][1]);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] += block_sum<true>(wf, xf[j]) * f[j];
+    }
+  };
+  // lane group q takes the 16-byte pieces q and q + 4 of a block: 64 neighbouring bytes of a row a load
+  auto blocks = [&](int64_t b0, auto count, auto step) __attribute__((always_inline)) {
+    constexpr int N = decltype(count)::value;
+    u32x4 w[N][RT][2], x[N][NT][2];
+    float fw[N], fx[N][NT];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int64_t b = b0 + n * decltype(step)::value;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[n][i][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + b * kFp8Block + 64 * h));
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          x[n][j][h] = in[j] ? *reinterpret_cast<const u32x4*>(xp[j] + b * kFp8Block + 64 * h) : zero;
+        fx[n][j] = in[j] ? sx[j][b * a.xs_blk] : 0.0f;
+      }
+      fw[n] = sw[b];
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      float f[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) f[j] = fx[n][j] * fw[n];
+      multiply(w[n], x[n], f);
+    }
+  };
+  const int64_t whole = a.C / kFp8Block;
+  int64_t b = wave;
+  for (; b + (U - 1) * W < whole; b += U * W) blocks(b, Int<U>(), Int<W>());
+  for (; b < whole; b += W) blocks(b, Int<1>(), Int<W>());
+  if (b == whole && whole < cb) {                // the row's last, short block, by one wave
+    u32x4 w[RT][2], x[NT][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int64_t c = whole * kFp8Block + 64 * h;
+      const int64_t left = a.C - c - 16 * q;
+      const int valid = left > 16 ? 16 : left < 0 ? 0 : (int)left;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+        w[i][h] = valid > 0 ? first_bytes(*reinterpret_cast<const u32x4*>(wp[i] + c), valid) : zero;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        x[j][h] = valid > 0 && in[j] ? first_bytes(*reinterpret_cast<const u32x4*>(xp[j] + c), valid) : zero;
+    }
+    float f[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) f[j] = (in[j] ? sx[j][whole * a.xs_blk] : 0.0f) * sw[whole];
+    multiply(w, x, f);
+  }
+  __shared__ float red[join_bytes<RT, NT, W>() / 4];
+  join_and_store<RT, NT, W>(a, acc, r0, t0, t1, red);
+}
+
+template <int RT, int NT, int W>
+hipError_t few_fp8(MatmulArgs a, hipStream_t stream) {
+  a.row_blocks = (a.R + RT * kMfma - 1) / (RT * kMfma);
+  const int64_t grid = a.row_blocks * token_tiles(a, NT * kMfma);
+  hipLaunchKernelGGL((few_fp8_kernel<RT, NT, W>), grid_of(grid), dim3(W * kWave), 0, stream, a);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------------
+// More rows: tiles of BM weight rows by BN rows of x, both staged through LDS, a block of 128 columns a
+// step. Loads run NS - 1 steps ahead and go to LDS asynchronously. The 16-byte pieces of a row lie
+// permuted by row bits 1 to 3 (piece_turn). A stage ends with the step's scales: those of the tile's rows
+// of x, then of its blocks of weight rows.
+// ------------------------------------------------------------------------------------------------
+template <int WR, int WT, int FR, int FT, int NS, bool WIDE>
+__global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs a) {
+  constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma;
+  constexpr int kW = BM * 128, kX = BN * 128, kS = NW * 256, kStage = kW + kX + kS;
+  constexpr int kWl = BM / 8 / NW, kXl = BN / 8 / NW, kLoads = kWl + kXl + 1;
+  constexpr int kXWaves = (BN + kWave - 1) / kWave;          // waves that load scales of x
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole loads a wave");
+  static_assert(kXWaves < NW && FR * kMfma <= kFp8Block, "the scales' loads");
+  // the stages give way to the waves' results at the end
+  constexpr int kResults = NW * tile_bytes<FR, FT>();
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > kResults ? NS * kStage : kResults];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
+  if (block_id() >= a.blocks) return;
+  const int64_t id = by_die(block_id(), a.blocks), tiles = a.blocks / a.split;
+  const int part = (int)(id / tiles);
+  // tiles go in bands of kBand token tiles by all row blocks, the band's token tiles innermost, so that
+  // a die's run of tiles shares rows of x and weights alike
+  constexpr int kBand = 4;
+  const int64_t n_tok = tiles / a.row_blocks, in_part = id % tiles, band = in_part / (kBand * a.row_blocks);
+  const int64_t in_band = in_part - band * kBand * a.row_blocks;
+  const int64_t wide = n_tok - band * kBand < kBand ? n_tok - band * kBand : kBand;
+  const int64_t rb = in_band / wide, tile = band * kBand + in_band % wide;
+  int e;
+  int64_t t0, t1;
+  if (!find_tile(a.offsets, a.E, a.T, BN, tile, e, t0, t1)) return;
+  const int64_t r0 = rb * BM;
+  const int nr = (int)(a.R - r0 < BM ? a.R - r0 : BM), nt = (int)(t1 - t0 < BN ? t1 - t0 : BN);
+  const int64_t cb = fp8_blocks(a.C), rbs = fp8_blocks(a.R);
+  // buffers end with the 16-byte piece that holds their last column
+  const u32x4 wr = rows_buffer(a.codes + ((int64_t)e * a.R + r0) * a.ldw,
+                               ((nr - 1) * a.ldw + a.C + 15) & ~(int64_t)15);
+  const int64_t x0 = a.pick ? 0 : t0, xn = a.pick ? a.Tx : nt;
+  const u32x4 xr = rows_buffer(static_cast<const uint8_t*>(a.x) + x0 * a.ldx,
+                               ((xn - 1) * a.ldx + a.C + 15) & ~(int64_t)15);
+  const int first = (int)(cb * part / a.split), steps = (int)(cb * (part + 1) / a.split);
+  uint32_t woff[kWl], xoff[kXl];
+  int wcol[kWl], xcol[kXl];
+#pragma unroll
+  for (int i = 0; i < kWl; ++i) {
+    const int row = (wave * kWl + i) * 8 + (lane >> 3);
+    wcol[i] = ((lane & 7) ^ piece_turn(row)) * 16;
+    woff[i] = row < nr ? row * (uint32_t)a.ldw + wcol[i] : kOutside;
+  }
+#pragma unroll
+  for (int i = 0; i < kXl; ++i) {
+    const int row = (wave * kXl + i) * 8 + (lane >> 3);
+    const int64_t x = row < nt ? x_row(a, t0 + row) : -1;
+    xcol[i] = ((lane & 7) ^ piece_turn(row)) * 16;
+    xoff[i] = x >= 0 ? (uint32_t)(x - x0) * (uint32_t)a.ldx + xcol[i] : kOutside;
+  }
+  // this wave's scales: 64 rows of x, or the tile's blocks of weight rows
+  const bool of_x = wave < kXWaves;
+  const float* sbase;
+  int64_t sstep, sbytes;
+  uint32_t soff = kOutside;
+  if (of_x) {
+    const int row = wave * kWave + lane;
+    const int64_t x = row < nt ? x_row(a, t0 + row) : -1;
+    if (x >= 0) soff = (uint32_t)((x - x0) * a.xs_row) * 4u;
+    sbase = a.x_blocks + x0 * a.xs_row;
+    sstep = a.xs_blk;
+    sbytes = ((xn - 1) * a.xs_row + 1) * 4;
+  } else {
+    const int64_t r = r0 / kFp8Block, left = rbs - r;
+    const int n = left < (BM + kFp8Block - 1) / kFp8Block ? (int)left : (BM + kFp8Block - 1) / kFp8Block;
+    if (wave == kXWaves && lane < n) soff = (uint32_t)(lane * cb) * 4u;
+    sbase = static_cast<const float*>(a.scales) + ((int64_t)e * rbs + r) * cb;
+    sstep = 1;
+    sbytes = ((n - 1) * cb + 1) * 4;
+  }
+  const uint32_t lds0 = lds_address(&lds[0]);
+  auto load = [&](int slot, int kt) __attribute__((always_inline)) {
+    const uint32_t dst = lds0 + slot * kStage;
+    const bool cut = kt * kFp8Block + kFp8Block > a.C;       // the row's last, short block, or past it
+    const int left = (int)a.C - kt * kFp8Block;
+    const uint32_t more = kt < steps ? (uint32_t)kt * kFp8Block : 0u;
+#pragma unroll
+    for (int i = 0; i < kWl; ++i)
+      load_lds16(wr, (cut && wcol[i] >= left) || kt >= steps ? kOutside : woff[i], more,
+                 dst + (wave * kWl + i) * 1024);
+#pragma unroll
+    for (int i = 0; i < kXl; ++i)
+      load_lds16(xr, (cut && xcol[i] >= left) || kt >= steps ? kOutside : xoff[i], more,
+                 dst + kW + (wave * kXl + i) * 1024);
+    load_lds4(rows_buffer(sbase + (kt < steps ? kt : 0) * sstep, sbytes), kt < steps ? soff : kOutside,
+              dst + kW + kX + wave * 256);
+  };
+  f32x4 acc[FR][FT];
+#pragma unroll
+  for (int i = 0; i < FR; ++i)
+#pragma unroll
+    for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  // neighbouring waves, on different SIMDs, share their rows of x; those past a partial tile's last
+  // row only help to load
+  const int wm = (wave % WR) * FR * kMfma, wn = (wave / WR) * FT * kMfma;
+  const bool busy = wn < nt;
+  const int l = lane & 15, q = lane >> 4;
+  const int p0 = ((2 * q) ^ piece_turn(l)) * 16, p1 = ((2 * q + 1) ^ piece_turn(l)) * 16;
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) load(s, first + s);
+  auto walk = [&](auto with_products) __attribute__((always_inline)) {
+    int slot = 0;
+    for (int kt = first; kt < steps; ++kt) {
+      wait_loads<(NS - 2) * kLoads>();
+      step_barrier();
+      uint8_t* base = lds + slot * kStage;
+      if ((a.C & 15) && kt == (int)cb - 1) {
+        // the row's last piece keeps the columns that exist
+        for (int row = tid; row < BM + BN; row += NW * kWave) {
+          const int r = row < BM ? row : row - BM, piece = ((int)a.C & 127) >> 4;
+          u32x4* p = reinterpret_cast<u32x4*>(base + row * 128 + (piece ^ piece_turn(r)) * 16);
+          *p = first_bytes(*p, (int)a.C & 15);
+        }
+        step_barrier();
+      }
+      load(slot == 0 ? NS - 1 : slot - 1, kt + NS - 1);
+      slot = slot + 1 == NS ? 0 : slot + 1;
+      if (decltype(with_products)::value == 0) continue;
+      const uint8_t* wb = base + (wm + l) * 128;
+      const uint8_t* xb = base + kW + (wn + l) * 128;
+      const float* sb = reinterpret_cast<const float*>(base + kW + kX);
+      const float fw = sb[kXWaves * kWave + wm / kFp8Block];
+      auto read = [&](const uint8_t* p) __attribute__((always_inline)) {
+        return frag<WIDE>(*reinterpret_cast<const u32x4*>(p + p0), *reinterpret_cast<const u32x4*>(p + p1));
+      };
+      Frag<WIDE> xf[FT], wf[2];
+      float f[FT];
+      f32x4 p[2][FT];
+#pragma unroll
+      for (int j = 0; j < FT; ++j) xf[j] = read(xb + j * kMfma * 128);
+      wf[0] = read(wb);
+#pragma unroll
+      for (int j = 0; j < FT; ++j) f[j] = sb[wn + j * kMfma + l] * fw;
+#pragma unroll
+      for (int i = 0; i < FR; ++i) {
+        if (i + 1 < FR) wf[(i + 1) & 1] = read(wb + (i + 1) * kMfma * 128);
+#pragma unroll
+        for (int j = 0; j < FT; ++j) p[i & 1][j] = block_sum<WIDE>(wf[i & 1], xf[j]);
+        if (i > 0) {
+#pragma unroll
+          for (int j = 0; j < FT; ++j) acc[i - 1][j] += p[(i - 1) & 1][j] * f[j];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int j = 0; j < FT; ++j) acc[FR - 1][j] += p[(FR - 1) & 1][j] * f[j];
+    }
+  };
+  if (busy) walk(Int<1>());
+  else walk(Int<0>());
+  wait_loads<0>();
+  step_barrier();
+  store_tile<FR, FT>(a, part, acc, &lds[0] + wave * tile_bytes<FR, FT>(), t0 + wn, t1, r0 + wm);
+}
+
+template <int WR, int WT, int FR, int FT, int NS, bool WIDE>
+hipError_t tile_fp8(MatmulArgs a, hipStream_t stream) {
+  constexpr int BM = WR * FR * kMfma, BN = WT * FT * kMfma;
+  a.row_blocks = (a.R + BM - 1) / BM;
+  a.blocks = a.row_blocks * token_tiles(a, BN) * a.split;
+  hipLaunchKernelGGL((tile_fp8_kernel<WR, WT, FR, FT, NS, WIDE>), grid_of(a.blocks),
+                     dim3(WR * WT * kWave), 0, stream, a);
+  return hipGetLastError();
+}
+
+template <bool WIDE>
+hipError_t tile_fp8_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  switch (p.bn) {
+    case 64:
+      return p.bm == 64 ? tile_fp8<1, 4, 4, 1, 3, WIDE>(a, stream) : tile_fp8<2, 2, 4, 2, 3, WIDE>(a, stream);
+    case 128: return tile_fp8<2, 2, 4, 4, 2, WIDE>(a, stream);
+    default:
+      // fragments of bf16 numbers leave no registers for more
+      if constexpr (WIDE) return tile_fp8<2, 2, 4, 4, 2, WIDE>(a, stream);
+      else return tile_fp8<2, 4, 8, 4, 2, WIDE>(a, stream);
+  }
+}
+
+}  // namespace
+
+hipError_t launch_few_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  if (p.nt == 1) return p.rt == 2 ? few_fp8<2, 1, 8>(a, stream) : few_fp8<1, 1, 8>(a, stream);
+  return p.rt == 2 ? few_fp8<2, 2, 8>(a, stream) : few_fp8<1, 2, 8>(a, stream);
+}
+
+hipError_t launch_tile_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
+  return a.y_type == AAAC_F32 ? tile_fp8_any<true>(a, p, stream) : tile_fp8_any<false>(a, p, stream);
+}
+
+}  // namespace aaac

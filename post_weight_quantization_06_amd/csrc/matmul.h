@@ -163,6 +163,101 @@ __device__ __forceinline__ void store_part(const MatmulArgs& a, int part, int64_
   else *reinterpret_cast<f32x4*>(a.parts + ((int64_t)part * a.T + t) * part_row(a.R) + r) = v;
 }
 
+// A wave's result, FR * 16 weight rows by FT * 16 rows of x, into y. A lane holds four neighbours of
+// 16 rows of x at a time, 32 bytes of a row together in 16 bits; through `lds` (tile_bytes, this
+// wave's own) a row's FR * 32 bytes go out together, 16 a lane (4096 x 14336 x 4096 in MXFP4, all of
+// the call: 164 us with, 177 without). Parts and fp32 leave directly, 64 bytes of a row together.
+template <int FR, int FT>
+constexpr int tile_bytes() { return FT * kMfma * (FR * 32 + 16); }
+template <int FR, int FT>
+__device__ __forceinline__ void store_tile(const MatmulArgs& a, int part, const f32x4 (&acc)[FR][FT],
+                                           uint8_t* lds, int64_t t0, int64_t t1, int64_t r0) {
+  const int lane = threadIdx.x & (kWave - 1), l = lane & 15, q = lane >> 4;
+  if (!a.y_row || a.split > 1) {
+#pragma unroll
+    for (int j = 0; j < FT; ++j) {
+      const int64_t t = t0 + j * kMfma + l;
+      if (t >= t1) continue;
+#pragma unroll
+      for (int i = 0; i < FR; ++i) {
+        const int64_t r = r0 + i * kMfma + 4 * q;
+        if (r < a.R) store_part(a, part, t, r, acc[i][j]);
+      }
+    }
+    return;
+  }
+  constexpr int kRow = FR * 32 + 16, kLanes = FR * 2;        // bytes and 16-byte pieces of a row
+#pragma unroll
+  for (int j = 0; j < FT; ++j)
+#pragma unroll
+    for (int i = 0; i < FR; ++i) {
+      const f32x4 v = acc[i][j];
+      const uint2 w = a.y_type == AAAC_BF16 ? make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w))
+                                            : make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
+      *reinterpret_cast<uint2*>(lds + (j * kMfma + l) * kRow + i * 32 + q * 8) = w;
+    }
+  const int64_t r = r0 + 8 * (lane % kLanes);
+  uint16_t* y = static_cast<uint16_t*>(a.y) + r;
+  for (int k = lane / kLanes; k < FT * kMfma; k += kWave / kLanes) {
+    if (t0 + k >= t1) break;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + k * kRow + 16 * (lane % kLanes));
+    uint16_t* p = y + (t0 + k) * a.ldy;
+    if (r + 8 <= a.R) {
+      // results larger than the L2s together are not kept there
+      if (a.y_row == 2) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+      else *reinterpret_cast<u32x4*>(p) = v;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (r + c < a.R) p[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
+    }
+  }
+}
+
+// Workgroups go to the eight dies in turn. Renumbered so that a die gets runs of kRun consecutive
+// tiles, as many as it works on at once, its L2 serves the rows that neighbouring tiles share. Runs
+// and not an eighth of the tiles each: a grouped call's last tiles are empty, and the dies share them
+// (8 experts of 14336 x 4096, 4093 rows: 637 us, 767 in eighths).
+constexpr int kDies = 8, kRun = 32;
+__device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
+  const int64_t whole = n / (kDies * kRun) * (kDies * kRun);
+  if (b >= whole) return b;
+  const int64_t d = b % kDies, i = b / kDies;
+  return (i / kRun * kDies + d) * kRun + i % kRun;
+}
+
+// Adds the waves' sums acc[RT][NT] in wave order and stores them. red: join_bytes of LDS.
+template <int RT, int NT, int W>
+constexpr int join_bytes() { return W * NT * kMfma * (RT * kMfma + 4) * 4; }
+template <int RT, int NT, int W>
+__device__ __forceinline__ void join_and_store(const MatmulArgs& a, const f32x4 (&acc)[RT][NT],
+                                               int64_t r0, int64_t t0, int64_t t1, float* red) {
+  constexpr int kRow = RT * kMfma + 4;           // floats between x rows
+  constexpr int kPart = NT * kMfma * kRow;       // and between waves
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *reinterpret_cast<f32x4*>(red + wave * kPart + (j * kMfma + (lane & 15)) * kRow + i * kMfma +
+                                4 * (lane >> 4)) = acc[i][j];
+  __syncthreads();
+  for (int u = tid; u < NT * kMfma * RT * 4; u += W * kWave) {
+    const int t = u / (RT * 4), r = 4 * (u % (RT * 4));
+    const float* p = red + t * kRow + r;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += *reinterpret_cast<const f32x4*>(p + w * kPart);
+    if (t0 + t < t1 && r0 + r < a.R) store4(a, t0 + t, r0 + r, v);
+  }
+}
+
+// How the eight 16-byte pieces of a 128-byte row lie permuted in LDS, by row bits 1 to 3: pieces of
+// neighbouring rows then fall on different banks.
+__device__ __forceinline__ int piece_turn(int row) {
+  return (row >> 1 & 1) ^ (row & 4) ^ (row >> 3 & 1) * 6;
+}
+
 inline int can_store4(const MatmulArgs& a) {
   const int b = a.y_type == AAAC_F32 ? 4 : 2;
   return (uintptr_t)a.y % (4 * b) == 0 && a.ldy % 4 == 0;

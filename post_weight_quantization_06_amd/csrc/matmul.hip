@@ -1,5 +1,6 @@
 // How a product call is run: the choice of kernel and tile, and the kernel that adds the parts of a
 // sum that was split over workgroups.
+#include "fp8.h"
 #include "matmul.h"
 
 namespace aaac {
@@ -47,6 +48,8 @@ constexpr TileCost kBf16Tiles[] = {{128, 32, 0.70, true}, {128, 64, 0.77, true},
                                    {128, 128, 0.96, true}, {256, 256, 1.85, false}};
 constexpr TileCost kMxTiles[] = {{64, 64, 0.45, true}, {128, 64, 0.60, true},
                                  {128, 128, 0.75, true}, {256, 256, 1.90, false}};
+constexpr TileCost kFp8Tiles[] = {{64, 64, 0.45, true}, {128, 64, 0.60, true},
+                                  {128, 128, 0.75, true}, {256, 256, 1.90, false}};
 constexpr double kTile = 2.3, kTwoBf16 = 0.80, kTwoMx = 0.95, kLaunch = 3.0;
 constexpr double kPartBytes = 6e6;
 
@@ -83,6 +86,17 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
   MatmulPlan p = {};
   p.split = 1;
   const int64_t rows = (a.T + a.E - 1) / a.E;    // rows of x an expert, on average
+  if (kind == kFp8) {
+    if (rows <= kMfma || (a.E == 1 && rows <= 2 * kMfma)) {
+      const int64_t blocks = (a.R + kMfma - 1) / kMfma * (a.E < a.T ? a.E : a.T);
+      p.nt = rows <= kMfma ? 1 : 2;
+      p.rt = blocks > 2 * device_cu_count() ? 2 : 1;
+      p.chunks = 1;
+      return p;
+    }
+    plan_tiles(a, kFp8Tiles, kTwoMx, kFp8Block, can_split, p);
+    return p;
+  }
   if (rows <= kMfma || (kind == kMxMxfp4 && a.E == 1 && rows <= 2 * kMfma)) {
     const int64_t blocks = (a.R + kMfma - 1) / kMfma * (a.E < a.T ? a.E : a.T);
     p.nt = rows <= kMfma ? 1 : 2;
@@ -107,9 +121,11 @@ hipError_t launch_matmul(MatmulArgs a, MatmulKind kind, const MatmulPlan& p, hip
   hipError_t e;
   if (p.bn == 0)
     e = kind == kPacked ? launch_few_packed(a, p, stream)
+        : kind == kFp8 ? launch_few_fp8(a, p, stream)
         : kind == kMxMxfp4 ? launch_few_mxfp4(a, p, stream) : launch_few_mx_bf16(a, p, stream);
   else
     e = kind == kPacked ? launch_tile_packed(a, p, stream)
+        : kind == kFp8 ? launch_tile_fp8(a, p, stream)
         : kind == kMxMxfp4 ? launch_tile_mxfp4(a, p, stream) : launch_tile_mx_bf16(a, p, stream);
   if (e != hipSuccess || p.split == 1) return e;
   const int64_t items = a.T * (part_row(a.R) / 4);

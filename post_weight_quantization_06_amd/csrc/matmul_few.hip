@@ -17,32 +17,6 @@ template <class X, class Y> struct Pick<false, X, Y> { typedef Y type; };
 
 constexpr int64_t kXLds = 64 << 10;              // LDS bytes for rows of x
 
-// Adds the waves' sums acc[RT][NT] in wave order and stores them. red: join_bytes of LDS.
-template <int RT, int NT, int W>
-constexpr int join_bytes() { return W * NT * kMfma * (RT * kMfma + 4) * 4; }
-template <int RT, int NT, int W>
-__device__ __forceinline__ void join_and_store(const MatmulArgs& a, const f32x4 (&acc)[RT][NT],
-                                               int64_t r0, int64_t t0, int64_t t1, float* red) {
-  constexpr int kRow = RT * kMfma + 4;           // floats between x rows
-  constexpr int kPart = NT * kMfma * kRow;       // and between waves
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      *reinterpret_cast<f32x4*>(red + wave * kPart + (j * kMfma + (lane & 15)) * kRow + i * kMfma +
-                                4 * (lane >> 4)) = acc[i][j];
-  __syncthreads();
-  for (int u = tid; u < NT * kMfma * RT * 4; u += W * kWave) {
-    const int t = u / (RT * 4), r = 4 * (u % (RT * 4));
-    const float* p = red + t * kRow + r;
-    f32x4 v = *reinterpret_cast<const f32x4*>(p);
-#pragma unroll
-    for (int w = 1; w < W; ++w) v += *reinterpret_cast<const f32x4*>(p + w * kPart);
-    if (t0 + t < t1 && r0 + r < a.R) store4(a, t0 + t, r0 + r, v);
-  }
-}
-
 // Bytes between the rows of x in LDS: whole 1 KB pieces, and 16 more to spread a column over banks.
 __host__ __device__ __forceinline__ int64_t x_row_bytes(int64_t C) {
   return (2 * C + 1023) / 1024 * 1024 + 16;

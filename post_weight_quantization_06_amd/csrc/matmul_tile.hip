@@ -6,69 +6,6 @@ namespace aaac {
 
 namespace {
 
-// A wave's result, FR * 16 weight rows by FT * 16 rows of x, into y. A lane holds four neighbours of
-// 16 rows of x at a time, 32 bytes of a row together in 16 bits; through `lds` (tile_bytes, this
-// wave's own) a row's FR * 32 bytes go out together, 16 a lane (4096 x 14336 x 4096 in MXFP4, all of
-// the call: 164 us with, 177 without). Parts and fp32 leave directly, 64 bytes of a row together.
-template <int FR, int FT>
-constexpr int tile_bytes() { return FT * kMfma * (FR * 32 + 16); }
-template <int FR, int FT>
-__device__ __forceinline__ void store_tile(const MatmulArgs& a, int part, const f32x4 (&acc)[FR][FT],
-                                           uint8_t* lds, int64_t t0, int64_t t1, int64_t r0) {
-  const int lane = threadIdx.x & (kWave - 1), l = lane & 15, q = lane >> 4;
-  if (!a.y_row || a.split > 1) {
-#pragma unroll
-    for (int j = 0; j < FT; ++j) {
-      const int64_t t = t0 + j * kMfma + l;
-      if (t >= t1) continue;
-#pragma unroll
-      for (int i = 0; i < FR; ++i) {
-        const int64_t r = r0 + i * kMfma + 4 * q;
-        if (r < a.R) store_part(a, part, t, r, acc[i][j]);
-      }
-    }
-    return;
-  }
-  constexpr int kRow = FR * 32 + 16, kLanes = FR * 2;        // bytes and 16-byte pieces of a row
-#pragma unroll
-  for (int j = 0; j < FT; ++j)
-#pragma unroll
-    for (int i = 0; i < FR; ++i) {
-      const f32x4 v = acc[i][j];
-      const uint2 w = a.y_type == AAAC_BF16 ? make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w))
-                                            : make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
-      *reinterpret_cast<uint2*>(lds + (j * kMfma + l) * kRow + i * 32 + q * 8) = w;
-    }
-  const int64_t r = r0 + 8 * (lane % kLanes);
-  uint16_t* y = static_cast<uint16_t*>(a.y) + r;
-  for (int k = lane / kLanes; k < FT * kMfma; k += kWave / kLanes) {
-    if (t0 + k >= t1) break;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + k * kRow + 16 * (lane % kLanes));
-    uint16_t* p = y + (t0 + k) * a.ldy;
-    if (r + 8 <= a.R) {
-      // results larger than the L2s together are not kept there
-      if (a.y_row == 2) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
-      else *reinterpret_cast<u32x4*>(p) = v;
-    } else {
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (r + c < a.R) p[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
-    }
-  }
-}
-
-// Workgroups go to the eight dies in turn. Renumbered so that a die gets runs of kRun consecutive
-// tiles, as many as it works on at once, its L2 serves the rows that neighbouring tiles share. Runs
-// and not an eighth of the tiles each: a grouped call's last tiles are empty, and the dies share them
-// (8 experts of 14336 x 4096, 4093 rows: 637 us, 767 in eighths).
-constexpr int kDies = 8, kRun = 32;
-__device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
-  const int64_t whole = n / (kDies * kRun) * (kDies * kRun);
-  if (b >= whole) return b;
-  const int64_t d = b % kDies, i = b / kDies;
-  return (i / kRun * kDies + d) * kRun + i % kRun;
-}
-
 // ------------------------------------------------------------------------------------------------
 // MXFP4 x times MXFP4 weights. A tile is BM weight rows by BN rows of x; a step takes 256 columns
 // (128 bytes of codes and 8 scale bytes a row). Lane l of a matrix instruction holds blocks 2 q and
@@ -89,9 +26,6 @@ __device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
 // one through registers, and each waits for memory, the next stage's loads among it, in every step: half
 // the rate (2048 x 2880 with 2816 columns 23 us, with 2880 or 2944 46 us; 32 experts, 4096 rows, 60 and 119).
 // ------------------------------------------------------------------------------------------------
-__device__ __forceinline__ int piece_turn(int row) {
-  return (row >> 1 & 1) ^ (row & 4) ^ (row >> 3 & 1) * 6;
-}
 template <int WR, int WT, int FR, int FT, bool WHOLE>
 __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_mxfp4_kernel(MatmulArgs a) {
   constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma;

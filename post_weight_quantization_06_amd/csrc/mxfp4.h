@@ -50,6 +50,11 @@ struct MatmulArgs {
   const void* x;               // bf16 rows of ldx elements, or codes [T, Cp / 2]
   const uint8_t* x_scales;     // with codes: [T, Cp / 32]
   int64_t T, ldx;
+  const int32_t* pick;         // FP8: [T] row of x for each row of y, or NULL
+  int64_t Tx;                  // FP8: rows of x
+  int64_t ldw;                 // FP8: bytes between rows of codes of the weights
+  const float* x_blocks;       // FP8: scale of row t, block b at t * xs_row + b * xs_blk
+  int64_t xs_row, xs_blk;
   void* y;                     // [T, R] of y_type, rows of ldy elements
   int y_type;
   int64_t ldy;
@@ -79,7 +84,7 @@ struct MatmulPlan {
   int rt, nt, chunks;
 };
 
-enum MatmulKind { kMxBf16, kMxMxfp4, kPacked };
+enum MatmulKind { kMxBf16, kMxMxfp4, kPacked, kFp8 };
 
 // can_split: a workspace for parts may be used.
 MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split);
@@ -92,5 +97,7 @@ hipError_t launch_few_packed(const MatmulArgs& a, const MatmulPlan& p, hipStream
 hipError_t launch_tile_mxfp4(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
 hipError_t launch_tile_mx_bf16(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
 hipError_t launch_tile_packed(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
+hipError_t launch_few_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
+hipError_t launch_tile_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream);
 
 }  // namespace aaac

@@ -1,9 +1,12 @@
-"""Products on 4-bit weights for any number of rows, dense and grouped by expert, and the MXFP4 format.
+"""Products on 4-bit and 8-bit weights for any number of rows, dense and grouped by expert, the MXFP4
+and FP8 formats, and the routing of rows to experts.
 
-Two weight formats take part: the packed dual-codebook format of the quantizer (`QuantizedMatrix`,
-`PackedExperts`) and MXFP4 (`MXFP4Matrix`, one matrix or a stack of experts). Rows of x that belong
-to experts are sorted by expert and described by `offsets`, int32 [E + 1] on the device: expert e has
-the rows offsets[e] <= t < offsets[e + 1]. The weights are frozen: nothing here has a gradient.
+Three weight formats take part: the packed dual-codebook format of the quantizer (`QuantizedMatrix`,
+`PackedExperts`), MXFP4 (`MXFP4Matrix`) and FP8 with a scale for each block of 128 (`FP8Matrix`), the last
+two for one matrix or a stack of experts. Rows of x that belong to experts are sorted by expert and
+described by `offsets`, int32 [E + 1] on the device: expert e has the rows offsets[e] <= t <
+offsets[e + 1]. `route` makes them from a router's logits; its result moves rows to that order and back.
+The weights are frozen: nothing here has a gradient.
 
 Every call enqueues its kernels on the current stream of the tensors' device and returns.
 """
@@ -150,3 +153,157 @@ class PackedExperts:
         """Each row of x times its expert's transposed matrix (see packed_matmul)."""
         return packed_matmul(self.codes, self.scales, self.bitmap, self.tables_bf16, x, self.g,
                              self.S, self.n, offsets, out, dtype)
+
+
+def fp8_quantize(x: torch.Tensor, tile: bool = False) -> Tuple[torch.Tensor, torch.Tensor]:
+    """FP8 codes (float8_e4m3fn, shaped as x) and fp32 scales of x (bf16, fp16 or fp32): a scale for each
+    128 columns of a row, [..., ceil(C/128)]; with tile for each 128 x 128 of a matrix [R, C] or a stack
+    [E, R, C], [..., ceil(R/128), ceil(C/128)]. Rows of codes start on 16 bytes, as the products need
+    them: for a C that is no multiple of 16 the result is a view of wider rows."""
+    lead, C = x.shape[:-1], x.shape[-1]
+    if tile and x.dim() not in (2, 3):
+        raise ValueError("tile needs [R, C] or [E, R, C] (got %d-D)" % x.dim())
+    wide = (C + 15) // 16 * 16
+    codes = torch.empty(*lead, wide, dtype=torch.float8_e4m3fn, device=x.device)
+    if wide != C:
+        codes = codes[..., :C]
+    blocks = (C + 127) // 128
+    if tile:
+        scales = torch.empty(*lead[:-1], (lead[-1] + 127) // 128, blocks, dtype=torch.float32,
+                             device=x.device)
+        L.aaac_fp8_quantize(x, codes, scales, True)
+    else:
+        scales = torch.empty(*lead, blocks, dtype=torch.float32, device=x.device)
+        x2 = x if x.dim() == 2 else x.reshape(-1, C)
+        L.aaac_fp8_quantize(x2, codes if x.dim() == 2 else codes.view(-1, C), scales)
+    return codes, scales
+
+
+def fp8_dequant(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values of FP8 codes, in `out` (then of its type) or a new tensor of `dtype`. The scales' shape
+    says whether they are those of rows or of tiles (fp8_quantize)."""
+    lead, C = codes.shape[:-1], codes.shape[-1]
+    if out is None:
+        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
+    elif out.shape != codes.shape:
+        raise ValueError("out must be shaped as the codes (got %s and %s)" % (
+            tuple(out.shape), tuple(codes.shape)))
+    blocks = (C + 127) // 128
+    if scales.shape == (*lead, blocks):
+        flat = codes.dim() == 2
+        L.aaac_fp8_dequant(codes if flat else codes.view(-1, C), scales, out if flat else out.view(-1, C))
+    elif len(lead) in (1, 2) and scales.shape == (*lead[:-1], (lead[-1] + 127) // 128, blocks):
+        L.aaac_fp8_dequant(codes, scales, out, True)
+    else:
+        raise ValueError("scales %s fit neither the rows nor the tiles of codes %s" % (
+            tuple(scales.shape), tuple(codes.shape)))
+    return out
+
+
+def fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
+               offsets: Optional[torch.Tensor] = None, rows: Optional[torch.Tensor] = None,
+               x_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+               dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """[..., R] = x [..., C] times the transposed FP8 matrix (codes [R, C], scales of its tiles), or with
+    offsets each row times its expert's (codes [E, R, C]). x is bf16, fp16 or fp32 and is quantized first,
+    or codes with x_scales from fp8_quantize. rows: int32 [T], the result's row t multiplies row rows[t]
+    of x [Tx, C] (a routing's `rows`: tokens need not be copied to their experts; rows outside x stand
+    for zeros). Without `out`, rows outside the offsets hold nothing defined; with it they stay as they
+    were."""
+    if rows is not None:
+        if x.dim() != 2:
+            raise ValueError("with rows, x must be [Tx, C] (got %d-D)" % x.dim())
+        if out is None:
+            out = torch.empty(rows.shape[0], codes.shape[-2], dtype=dtype, device=x.device)
+        x2, y2 = x, out
+    else:
+        x2, y2, out = _rows_of(x, codes.shape[-2], out, dtype)
+    L.aaac_fp8_matmul(codes, scales, x2, y2, offsets, rows, x_scales)
+    return out
+
+
+@dataclasses.dataclass
+class FP8Matrix:
+    """One weight matrix in FP8 with a scale for each tile of 128 x 128, or a stack of experts."""
+    codes: torch.Tensor          # float8_e4m3fn [R, C] or [E, R, C], rows on 16 bytes
+    scales: torch.Tensor         # float32 [ceil(R/128), ceil(C/128)] or [E, .., ..]
+
+    @classmethod
+    def quantize(cls, W: torch.Tensor) -> "FP8Matrix":
+        """W [R, C], or [E, R, C] for a stack of experts."""
+        return cls(*fp8_quantize(W, tile=True))
+
+    def dequant(self, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+        return fp8_dequant(self.codes, self.scales, dtype)
+
+    def matmul(self, x: torch.Tensor, offsets: Optional[torch.Tensor] = None,
+               rows: Optional[torch.Tensor] = None, x_scales: Optional[torch.Tensor] = None,
+               out: Optional[torch.Tensor] = None,
+               dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+        """x times the transposed matrix (see fp8_matmul)."""
+        return fp8_matmul(self.codes, self.scales, x, offsets, rows, x_scales, out, dtype)
+
+
+@dataclasses.dataclass
+class Routing:
+    """Which experts T tokens go to, and the places of their rows in expert order."""
+    experts: torch.Tensor        # int32 [T, k], best first, -1 where none is left
+    weights: torch.Tensor        # float32 [T, k], 0 there
+    offsets: torch.Tensor        # int32 [E + 1]: expert e has the places offsets[e] .. offsets[e + 1] - 1
+    rows: torch.Tensor           # int32 [T k]: the token of each place, -1 behind the last expert's
+    places: torch.Tensor         # int32 [T, k]: the place of each slot, -1 without an expert
+
+    def to_experts(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """[T k, C]: the rows of x [T, C] in expert order (see rows_to_experts)."""
+        return rows_to_experts(x, self.places, out)
+
+    def from_experts(self, y: torch.Tensor, out: Optional[torch.Tensor] = None,
+                     dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+        """[T, C]: each token's weighted sum of its experts' rows of y [T k, C]."""
+        return rows_from_experts(y, self.places, self.weights, out, dtype)
+
+
+def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+          groups: int = 1, top_groups: Optional[int] = None, group_top: int = 1,
+          renormalize: bool = True, scale: float = 1.0) -> Routing:
+    """The k best of E experts for each token of logits [T, E] (bf16, fp16 or fp32).
+
+    Scores are softmax(logits) over the experts or sigmoid(logits). Experts are chosen by score + bias
+    (fp32 [E], for balance), weighted by the score alone: divided by its sum over the chosen ones with
+    renormalize, times scale. With groups, the experts form that many groups of neighbours, and only the
+    top_groups (default: all) with the largest best value (group_top 1) or sum of the two best (2) take
+    part. Equals go to the lowest index. An expert whose logit or bias is -inf is left out, so a row of
+    -inf (a padded batch's) gets no expert; the type's lowest value is a number like any other."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E] (got %d-D)" % logits.dim())
+    if not isinstance(k, int) or k < 1:
+        raise ValueError("k must be a positive whole number (got %r)" % (k,))
+    T, E = logits.shape
+    like = dict(dtype=torch.int32, device=logits.device)
+    r = Routing(torch.empty(T, k, **like), torch.empty(T, k, dtype=torch.float32, device=logits.device),
+                torch.empty(E + 1, **like), torch.empty(T * k, **like), torch.empty(T, k, **like))
+    L.aaac_route(logits, k, r.experts, r.weights, r.offsets, r.rows, r.places, score, bias, groups,
+                 top_groups, group_top, renormalize, scale)
+    return r
+
+
+def rows_to_experts(x: torch.Tensor, places: torch.Tensor,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """out [T k, C] with out[places[t, j]] = x[t], x [T, C] of any type of up to 4 bytes. Without `out`,
+    rows that no place names hold nothing defined; with it they stay as they were."""
+    if out is None:
+        out = torch.empty(places.numel(), x.shape[-1], dtype=x.dtype, device=x.device)
+    L.aaac_rows_to_experts(x, places, out)
+    return out
+
+
+def rows_from_experts(y: torch.Tensor, places: torch.Tensor, weights: torch.Tensor,
+                      out: Optional[torch.Tensor] = None,
+                      dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """[T, C] = the sum over j of weights[t, j] y[places[t, j]], in `out` or a new tensor of `dtype`
+    (default: y's). Places of -1 add nothing."""
+    if out is None:
+        out = torch.empty(places.shape[0], y.shape[-1], dtype=dtype or y.dtype, device=y.device)
+    L.aaac_rows_from_experts(y, places, weights, out)
+    return out

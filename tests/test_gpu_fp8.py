@@ -1,0 +1,417 @@
+"""GPU parity of FP8 in blocks of 128 (quantize, dequant, products) against the fp64 oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import aaac_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+P = pytest.importorskip("post_weight_quantization_06_amd")
+L = P._lib
+
+DEV = "cuda"
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+EPS = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+
+
+def _say(*a):
+    print("[case]", *a, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a visible GPU")
+    L.load()
+    yield
+
+
+def _gen(*key):
+    return torch.Generator().manual_seed(sum(int(k) * 7919 ** i for i, k in enumerate(key)) % (1 << 62))
+
+
+def _bytes(codes):
+    return codes.contiguous().view(torch.uint8).cpu().numpy()
+
+
+# ------------------------------------------------------------------ quantize and dequant
+
+def _check(x, tile):
+    """Quantise x [M, C] on the GPU; codes and scales bit for bit against the oracle, and the values."""
+    codes, scales = P.fp8_quantize(x, tile=tile)
+    want_c, want_s = ref.fp8_encode(x.double().cpu().numpy(), tile)
+    assert codes.shape == x.shape and codes.stride(0) % 16 == 0 and codes.data_ptr() % 16 == 0
+    assert np.array_equal(scales.cpu().numpy(), want_s, equal_nan=True)
+    assert np.array_equal(_bytes(codes), want_c)
+    # fp32 product of code and scale, rounded to the type
+    value = torch.from_numpy(ref.fp8_decode(want_c, np.ones_like(want_s), tile)).float()
+    value *= torch.from_numpy(ref._fp8_spread(want_s, *x.shape, tile))
+    for dt in TYPES:
+        got = P.fp8_dequant(codes, scales, dtype=dt).cpu()
+        assert torch.equal(torch.nan_to_num(got.float(), 7e7, 8e7, 9e7),
+                           torch.nan_to_num(value.to(dt).float(), 7e7, 8e7, 9e7))
+    return codes, scales
+
+
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,C", [(1, 1), (1, 15), (3, 16), (2, 127), (5, 129), (1, 4096), (129, 264),
+                                 (257, 1000), (300, 515)])
+def test_quantize_matches_the_oracle(dtype, M, C, tile):
+    _say("fp8", dtype, M, C, tile)
+    x = torch.randn(M, C, generator=_gen(M, C)) * torch.exp(2 * torch.randn(M, 1, generator=_gen(C, M)))
+    _check(x.to(dtype).to(DEV), tile)
+
+
+def test_every_bf16_value_beside_several_largest_ones():
+    _say("fp8 all bf16")
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    for top in (0.0, 2.0 ** -126, 2.0 ** -90, 1.0, 448.0, 450.0, 3e38):
+        x = bits.view(512, 128).clone()
+        big = x.float().abs() > top              # the block's largest is top, where it is not 0
+        if top:
+            x[big] = torch.tensor(top).to(torch.bfloat16)
+            x[:, 5] = top
+        _check(x.to(DEV), False)
+
+
+def test_fp32_ties_and_neighbours_of_ties():
+    # scale 1 (the largest is 448) and powers of two: every midpoint of two codes, and its neighbours
+    _say("fp8 ties")
+    t = ref._e4m3_table()[:127]
+    mid = ((t[1:] + t[:-1]) / 2).astype(np.float32)
+    v = np.concatenate([mid, np.nextafter(mid, np.float32(0)), np.nextafter(mid, np.float32(999))])
+    v = np.concatenate([v, -v, [0.0, -0.0, 1e-30, -1e-30, 2.0 ** -10, 2.0 ** -10 * 1.0001]])
+    v = np.resize(v, (7, 127)).astype(np.float32)
+    rows = []
+    for e in (-126, -100, -81, -80, -79, -3, 0, 5, 100, 119):
+        with np.errstate(under="ignore"):
+            rows.append(np.ldexp(np.concatenate([v, np.full((7, 1), 448, np.float32)], 1), e))
+    _check(torch.from_numpy(np.concatenate(rows).astype(np.float32)).to(DEV), False)
+
+
+@pytest.mark.parametrize("exp", [-140, -127, -110, -82, -60, 0, 100])
+def test_quotients_by_scales_of_every_size(exp):
+    # scales that are no powers of two, down to the least one: quotients are the rounded ones
+    _say("fp8 scales", exp)
+    x = torch.randn(300, 256, generator=_gen(exp + 200), dtype=torch.float64)
+    x = torch.ldexp(x * (1 + torch.rand(300, 1, generator=_gen(exp + 201), dtype=torch.float64)),
+                    torch.tensor(exp))
+    _check(x.float().to(DEV), False)
+
+
+def test_infinities_nan_and_zero_blocks():
+    _say("fp8 inf nan")
+    for dt in TYPES:
+        for tile in (False, True):
+            x = torch.randn(260, 300, generator=_gen(5)).to(dt)
+            x[0, 0], x[1, 140], x[2, 299], x[3, 128:256] = float("inf"), float("-inf"), float("nan"), 0.0
+            x[128:256, :128] = -0.0
+            codes, scales = _check(x.to(DEV), tile)
+            # the three bad elements lie in three rows' blocks, and in three tiles of the first row
+            assert (~torch.isfinite(scales)).sum() == 3
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("C,ld,start", [(64, 96, 0), (64, 100, 3), (150, 177, 1), (256, 264, 8)])
+def test_strided_rows_in_and_out(dtype, C, ld, start):
+    _say("fp8 strides", dtype, C, ld, start)
+    base = torch.randn(9 * ld + 16, generator=_gen(C)).to(dtype).to(DEV)
+    x = base[start:start + 9 * ld].view(9, ld)[:, :C]
+    for tile in (False, True):
+        codes, scales = _check(x, tile)
+        out = torch.full((9 * ld + 16,), 77.0, dtype=dtype, device=DEV)
+        y = out[start:start + 9 * ld].view(9, ld)[:, :C]
+        P.fp8_dequant(codes, scales, out=y)
+        assert torch.equal(y, P.fp8_dequant(codes, scales, dtype=dtype))
+        y.fill_(77.0)
+        assert (out == 77.0).all()               # nothing between the rows was written
+    # codes into wider rows: what follows the next 16 bytes stays
+    wide = (C + 15) // 16 * 16
+    buf = torch.full((9, wide + 32), 0x55, dtype=torch.uint8, device=DEV)
+    codes = buf.view(torch.float8_e4m3fn)[:, :C]
+    scales = torch.empty(9, (C + 127) // 128, device=DEV)
+    L.aaac_fp8_quantize(x, codes, scales)
+    assert np.array_equal(_bytes(codes), ref.fp8_encode(x.double().cpu().numpy())[0])
+    assert (buf[:, C:wide] == 0).all() and (buf[:, wide:] == 0x55).all()
+
+
+def test_codes_on_any_address_are_read_back():
+    _say("fp8 dequant addresses")
+    x = torch.randn(7, 203, generator=_gen(9)).to(DEV)
+    codes, scales = P.fp8_quantize(x)
+    flat = torch.empty(7 * 203 + 5, dtype=torch.uint8, device=DEV)
+    for at in (0, 1, 5):
+        v = flat[at:at + 7 * 203].view(7, 203)
+        v.copy_(codes.view(torch.uint8))
+        got = P.fp8_dequant(v.view(torch.float8_e4m3fn), scales, dtype=torch.float32)
+        assert torch.equal(got, P.fp8_dequant(codes, scales, dtype=torch.float32))
+
+
+def test_stack_of_experts_is_its_matrices():
+    W = torch.randn(3, 150, 70, generator=_gen(1)).to(torch.bfloat16).to(DEV)
+    m = P.FP8Matrix.quantize(W)
+    assert m.codes.shape == (3, 150, 70) and m.scales.shape == (3, 2, 1)
+    for e in range(3):
+        c, s = P.fp8_quantize(W[e], tile=True)
+        assert np.array_equal(_bytes(m.codes[e]), _bytes(c)) and torch.equal(m.scales[e], s)
+    assert torch.equal(m.dequant()[1], P.fp8_dequant(m.codes[1], m.scales[1]))
+    part = P.FP8Matrix.quantize(W[:, 10:140, 3:67])  # matrices further apart than their rows
+    c, s = P.fp8_quantize(W[2, 10:140, 3:67].contiguous(), tile=True)
+    assert np.array_equal(_bytes(part.codes[2]), _bytes(c)) and torch.equal(part.scales[2], s)
+
+
+def test_leading_axes_and_no_rows():
+    x = torch.randn(2, 3, 5, 130, generator=_gen(3)).to(DEV)
+    c, s = P.fp8_quantize(x)
+    assert c.shape == x.shape and s.shape == (2, 3, 5, 2)
+    c1, s1 = P.fp8_quantize(x[1, 2])
+    assert np.array_equal(_bytes(c[1, 2]), _bytes(c1)) and torch.equal(s[1, 2], s1)
+    assert torch.equal(P.fp8_dequant(c, s)[1, 2], P.fp8_dequant(c1, s1))
+    for tile in (False, True):
+        c, s = P.fp8_quantize(torch.empty(0, 40, device=DEV), tile=tile)
+        assert c.shape == (0, 40) and s.shape == (0, 1) and P.fp8_dequant(c, s).shape == (0, 40)
+
+
+# ------------------------------------------------------------------ products
+
+def _whole(shape, gen, top=2):
+    """Whole numbers up to `top` as e4m3: every sum of their products is exact in fp32."""
+    return torch.randint(-top, top + 1, shape, generator=gen).float().to(torch.float8_e4m3fn)
+
+
+def _aligned(codes, junk=None):
+    """The codes on the GPU in rows of whole 16 bytes; junk: what the bytes behind a row hold."""
+    C = codes.shape[-1]
+    wide = (C + 15) // 16 * 16 + (16 if junk is not None else 0)
+    buf = torch.full((*codes.shape[:-1], wide), junk or 0, dtype=torch.uint8)
+    buf[..., :C] = codes.view(torch.uint8)
+    return buf.to(DEV).view(torch.float8_e4m3fn)[..., :C]
+
+
+def _pow2(shape, gen):
+    return torch.exp2(torch.randint(-2, 3, shape, generator=gen).float())
+
+
+def _offsets(E, T, gen):
+    cut = torch.randint(0, T + 1, (E - 1,), generator=gen).sort().values
+    return torch.cat([torch.zeros(1), cut.float(), torch.full((1,), float(T))]).int()
+
+
+def _exact_case(E, R, C, T, dtype=torch.float32, tokens=None, junk=0x7f, grouped=None):
+    """A product whose every term and sum is exact, compared bit for bit. E = 0: one matrix, no offsets.
+    tokens: rows of x, picked by an index with some outside x. junk 0x7f: NaN codes behind the rows."""
+    g = _gen(E, R, C, T)
+    n = max(E, 1)
+    wc, ws = _whole((n, R, C), g), _pow2((n, -(-R // 128), -(-C // 128)), g)
+    Tx = tokens or T
+    xc, xs = _whole((Tx, C), g), _pow2((Tx, -(-C // 128)), g)
+    off = _offsets(E, T, g) if E else None
+    rows = torch.randint(-1, Tx + 1, (T,), generator=g).int() if tokens else None
+    wv = torch.stack([torch.from_numpy(ref.fp8_decode(wc[e].view(torch.uint8).numpy(), ws[e].numpy(), True))
+                      for e in range(n)])
+    xv = torch.from_numpy(ref.fp8_decode(xc.view(torch.uint8).numpy(), xs.numpy()))
+    if tokens:
+        ok = (rows >= 0) & (rows < Tx)
+        xv = torch.where(ok[:, None], xv[rows.long().clamp(0, Tx - 1)], torch.zeros(()).double())
+    want = torch.full((T, R), 55.0, dtype=torch.float64)
+    for e in range(n):
+        a, b = (int(off[e]), int(off[e + 1])) if E else (0, T)
+        want[a:b] = xv[a:b] @ wv[e].t()
+    assert want.abs().max() < 2 ** 19            # and every partial sum: 24 bits hold steps of 2^-4
+    codes = _aligned(wc if E else wc[0], junk)
+    out = torch.full((T, R), 55.0, dtype=dtype, device=DEV)
+    y = P.fp8_matmul(codes, (ws if E else ws[0]).to(DEV), _aligned(xc, junk),
+                     None if off is None else off.to(DEV), None if rows is None else rows.to(DEV),
+                     xs.to(DEV), out)
+    assert torch.equal(y.cpu(), want.float().to(dtype))
+
+
+# (E, R, C, T): the few-row kernels and every tile, whole and short in every direction
+FORMS = [(0, 16, 128, 1), (0, 1, 1, 1), (0, 40, 16, 16), (0, 129, 200, 7), (0, 4096, 256, 3),
+         (0, 12000, 130, 9), (0, 300, 1030, 32), (0, 12000, 260, 20), (0, 64, 128, 33), (0, 200, 4096, 40),
+         (0, 8192, 384, 64), (0, 1000, 640, 100), (0, 515, 2048, 129), (0, 2048, 1031, 500),
+         (0, 4096, 520, 777), (0, 4000, 896, 2000), (1, 256, 256, 5), (7, 130, 300, 40), (40, 64, 129, 200),
+         (5, 200, 256, 300), (3, 1030, 272, 900), (9, 2048, 384, 3000), (64, 256, 128, 64)]
+
+
+@pytest.mark.parametrize("E,R,C,T", FORMS)
+def test_products_of_whole_numbers_are_exact(E, R, C, T):
+    _say("fp8 product", E, R, C, T, L.fp8_matmul_plan(max(E, 1), R, C, T))
+    _exact_case(E, R, C, T)
+
+
+@pytest.mark.parametrize("E,R,C,T,tokens", [(0, 64, 128, 5, 3), (0, 130, 260, 50, 9), (6, 130, 260, 50, 9),
+                                            (4, 1030, 272, 900, 301), (8, 2048, 1040, 2048, 600)])
+def test_rows_of_x_by_an_index(E, R, C, T, tokens):
+    _say("fp8 rows", E, R, C, T, tokens, L.fp8_matmul_plan(max(E, 1), R, C, T))
+    _exact_case(E, R, C, T, tokens=tokens)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,R,C,T", [(0, 130, 300, 3), (0, 131, 300, 200), (4, 1000, 256, 700)])
+def test_result_types(dtype, E, R, C, T):
+    _exact_case(E, R, C, T, dtype)
+
+
+def test_every_tile_and_kernel_is_reached():
+    got = set()
+    for E, R, C, T in FORMS + [(0, 14336, 4096, 4096), (0, 14336, 4096, 1024), (0, 1024, 8192, 256)]:
+        bm, bn, split, rt, nt, _ = L.fp8_matmul_plan(max(E, 1), R, C, T)
+        got.add((bm, bn, split > 1, rt, nt))
+    few = {(0, 0, False, rt, nt) for rt in (1, 2) for nt in (1, 2)}
+    assert few <= got, got
+
+
+def _bound(xv, wv, dtype, want):
+    """Half a step of the result, and the sums: 128 exact products a block, each addition rounded or cut to
+    24 bits (2^-23 of the sum of magnitudes), the block's factor and its addition round once each, blocks
+    and the parts of waves and workgroups (up to 64) add up in fp32. Results of 16 bits may come from the
+    FP8 instruction, which adds eight products aligned to the largest: each may lose what lies below 2^-13
+    of it, seven beside the largest at most, so 8 * 2^-13 of the magnitudes' sum."""
+    blocks = -(-xv.shape[1] // 128)
+    mag = xv.abs() @ wv.abs().t()
+    cut = 0.0 if dtype is torch.float32 else 8 * 2.0 ** -13
+    return EPS[dtype] * want.abs() + mag * (128 * 2.0 ** -23 + (blocks + 66) * 2.0 ** -24 + cut)
+
+
+@pytest.mark.parametrize("xtype", TYPES)
+@pytest.mark.parametrize("R,C,T", [(200, 130, 1), (1000, 4096, 5), (515, 1000, 100), (2048, 2048, 700)])
+def test_quantized_in_the_call(xtype, R, C, T):
+    _say("fp8 quantize in the call", xtype, R, C, T)
+    g = _gen(R, C, T)
+    x = (torch.randn(T, C, generator=g) * torch.exp(torch.randn(C, generator=g))).to(xtype)
+    W = torch.randn(R, C, generator=g).mul_(0.02).to(torch.bfloat16)
+    m = P.FP8Matrix.quantize(W.to(DEV))
+    xv = torch.from_numpy(ref.fp8_decode(*ref.fp8_encode(x.double().numpy())))
+    wv = torch.from_numpy(ref.fp8_decode(*ref.fp8_encode(W.double().numpy(), True), True))
+    want = xv @ wv.t()
+    for dt in TYPES:
+        y = m.matmul(x.to(DEV), dtype=dt)
+        off = (y.double().cpu() - want).abs()
+        assert bool((off <= _bound(xv, wv, dt, want)).all()), float((off / _bound(xv, wv, dt, want)).max())
+        # as a whole: half steps, and at most 2^-15 beside them (1.4e-5 measured for normal values)
+        assert off.norm() <= (EPS[dt] + (0 if dt is torch.float32 else 2.0 ** -15)) * want.norm() + \
+            (1e-6 * want.norm() if dt is torch.float32 else 0)
+    # the same bits as the two calls
+    codes, scales = P.fp8_quantize(x.to(DEV))
+    assert torch.equal(m.matmul(codes, x_scales=scales, dtype=torch.float32), m.matmul(x.to(DEV), dtype=torch.float32))
+
+
+def test_nan_blocks_reach_only_their_products():
+    _say("fp8 nan")
+    g = _gen(77)
+    for T in (4, 90):
+        x = torch.randn(T, 300, generator=g).to(DEV)
+        W = torch.randn(200, 300, generator=g).to(DEV)
+        x[1, 200] = float("nan")
+        W[150, 3] = float("inf")                 # its tile: rows 128 .. 199
+        y = P.FP8Matrix.quantize(W).matmul(x, dtype=torch.float32)
+        bad = torch.zeros(T, 200, dtype=torch.bool)
+        bad[1], bad[:, 128:] = True, True
+        assert torch.equal(torch.isnan(y).cpu(), bad)
+
+
+def test_rows_of_no_expert_are_left_alone_and_bad_offsets_stay_inside():
+    _say("fp8 offsets")
+    g = _gen(8)
+    for T, R in ((30, 130), (600, 300)):
+        W = P.FP8Matrix.quantize(torch.randn(3, R, 256, generator=g).to(DEV))
+        x = torch.randn(T, 256, generator=g).to(DEV)
+        off = torch.tensor([2, 5, 5, T - 4], dtype=torch.int32, device=DEV)
+        out = torch.full((T, R), 9.0, device=DEV)
+        W.matmul(x, off, out=out)
+        one = [P.FP8Matrix(W.codes[e], W.scales[e]).matmul(x, dtype=torch.float32) for e in range(3)]
+        assert (out[:2] == 9).all() and (out[T - 4:] == 9).all()
+        torch.testing.assert_close(out[2:5], one[0][2:5], rtol=1e-5, atol=1e-4)
+        torch.testing.assert_close(out[5:T - 4], one[2][5:T - 4], rtol=1e-5, atol=1e-4)
+        for bad in ([-7, 3, 1 << 30, -1], [5, 2, 1, 0], [T + 9, T + 9, T + 9, T + 9]):
+            guard = torch.full((T + 2, R), 9.0, device=DEV)
+            W.matmul(x, torch.tensor(bad, dtype=torch.int32, device=DEV), out=guard[1:T + 1])
+            assert (guard[0] == 9).all() and (guard[T + 1] == 9).all()
+
+
+def test_results_do_not_depend_on_the_workspace_or_other_rows():
+    g = _gen(4)
+    W = P.FP8Matrix.quantize(torch.randn(1024, 4096, generator=g).to(DEV))
+    x, xs = P.fp8_quantize(torch.randn(256, 4096, generator=g).to(DEV))
+    need = L.fp8_matmul_workspace_bytes(1, 1024, 4096, 256, 256, False)
+    y = [torch.empty(256, 1024, device=DEV) for _ in range(2)]
+    for i, fill in enumerate((0, 0xFF)):
+        ws = torch.full((max(need, 256),), fill, dtype=torch.uint8, device=DEV)
+        L.aaac_fp8_matmul(W.codes, W.scales, x, y[i], x_scales=xs, ws=ws)
+    assert torch.equal(y[0], y[1])
+
+
+def test_strided_results_and_leading_axes():
+    g = _gen(6)
+    W = P.FP8Matrix.quantize(torch.randn(70, 200, generator=g).to(DEV))
+    for T in (3, 80):
+        x = torch.randn(T, 200, generator=g).to(DEV)
+        y = W.matmul(x)
+        buf = torch.full((T, 91), 7.0, dtype=torch.bfloat16, device=DEV)
+        W.matmul(x, out=buf[:, 3:73])
+        assert torch.equal(buf[:, 3:73], y) and (buf[:, :3] == 7).all() and (buf[:, 73:] == 7).all()
+        assert torch.equal(W.matmul(x.view(1, T, 200)), y.view(1, T, 70))
+        assert W.matmul(x[:0]).shape == (0, 70)
+
+
+def test_on_another_stream_and_captured():
+    _say("fp8 graph")
+    g = _gen(2)
+    W = P.FP8Matrix.quantize(torch.randn(2, 300, 512, generator=g).to(DEV))
+    x = torch.randn(90, 512, generator=g).to(DEV)
+    off = torch.tensor([0, 40, 90], dtype=torch.int32, device=DEV)
+    rows = torch.randperm(90, generator=g).int().to(DEV)
+    want = W.matmul(x, off, rows)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y = W.matmul(x, off, rows)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y, want)
+    graphs, outs = [], []
+    for _ in range(2):                           # two graphs: each has its own workspace
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(W.matmul(x, off, rows))
+        graphs.append(gr)
+    for i in range(3):
+        x.normal_()
+        want = W.matmul(x, off, rows)
+        for gr in graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+def test_refusals_of_the_calls():
+    W = P.FP8Matrix.quantize(torch.randn(64, 200, device=DEV))
+    x = torch.randn(4, 200, device=DEV)
+    with pytest.raises(ValueError, match="gradient"):
+        W.matmul(x.clone().requires_grad_())
+    with pytest.raises(ValueError, match="gradient"):
+        P.fp8_quantize(x.clone().requires_grad_())
+    with pytest.raises(ValueError, match="columns"):
+        W.matmul(torch.randn(4, 201, device=DEV))
+    with pytest.raises(TypeError):
+        W.matmul(x.double())
+    with pytest.raises(TypeError):
+        P.fp8_quantize(x.double())
+    with pytest.raises(ValueError):              # codes without scales are no numbers
+        W.matmul(P.fp8_quantize(x)[0], x_scales=torch.ones(4, 1, device=DEV))
+    with pytest.raises(TypeError):
+        W.matmul(P.fp8_quantize(x)[0])
+    with pytest.raises(ValueError, match="every tensor must be on the GPU"):
+        W.matmul(x.cpu())
+    with pytest.raises(L.AAACError):             # rows of codes off 16 bytes
+        flat = torch.zeros(64 * 200, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+        P.fp8_matmul(flat.view(64, 200), W.scales, x)
+    with pytest.raises(ValueError):
+        P.fp8_dequant(W.codes, torch.ones(3, 3, device=DEV))
+    with pytest.raises(ValueError):
+        W.matmul(x, rows=torch.zeros(4, dtype=torch.int64, device=DEV))
+    with pytest.raises(L.AAACError):             # every row the same memory
+        P.fp8_quantize(torch.zeros(1, 64, device=DEV).expand(4, 64))

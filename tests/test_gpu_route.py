@@ -1,0 +1,391 @@
+"""GPU parity of routing to experts and of the rows' way there and back against the fp64 oracle, and a
+layer of experts from all of them."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import aaac_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+P = pytest.importorskip("post_weight_quantization_06_amd")
+L = P._lib
+
+DEV = "cuda"
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+INF = float("inf")
+
+
+def _say(*a):
+    print("[case]", *a, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a visible GPU")
+    L.load()
+    yield
+
+
+def _gen(*key):
+    return torch.Generator().manual_seed(sum(int(k) * 7919 ** i for i, k in enumerate(key)) % (1 << 62))
+
+
+def _check(logits, k, bias=None, **kw):
+    """Experts, offsets, rows and places equal to the oracle's; weights within two roundings of fp32 and
+    what a float32 sum over a token's experts may be off (a non-renormalised softmax)."""
+    r = P.route(logits.to(DEV), k, bias=None if bias is None else bias.to(DEV), **kw)
+    e, w, off, rows, places = ref.route(logits.double().numpy(), k,
+                                        bias=None if bias is None else bias.double().numpy(), **kw)
+    assert np.array_equal(r.experts.cpu().numpy(), e)
+    assert np.array_equal(r.offsets.cpu().numpy(), off)
+    assert np.array_equal(r.rows.cpu().numpy(), rows)
+    assert np.array_equal(r.places.cpu().numpy(), places)
+    # exp and the sum of up to 512 terms: each exp within 2 units, the sum is in 64 bits
+    tol = 4 * 2.0 ** -24 * np.abs(w) + 2.0 ** -149
+    assert (np.abs(r.weights.double().cpu().numpy() - w) <= tol).all()
+    return r
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 60, 4), (8, 256, 8), (9, 64, 6), (61, 60, 4),
+                                   (100, 33, 33), (300, 128, 1), (70, 512, 8), (64, 300, 64),
+                                   (2100, 16, 3)])
+def test_plain_routing(score, dtype, T, E, k):
+    _say("route", score, dtype, T, E, k)
+    x = torch.randn(T, E, generator=_gen(T, E, k)).mul_(2).to(dtype)
+    _check(x, k, score=score)
+    _check(x, k, score=score, renormalize=False, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,top,gt", [
+    (5, 256, 8, 8, 4, 2), (40, 256, 8, 8, 4, 1), (7, 160, 6, 8, 3, 1), (33, 60, 4, 3, 2, 2),
+    (20, 64, 8, 64, 8, 2), (50, 510, 7, 5, 1, 2), (12, 96, 12, 6, 6, 2), (9, 24, 2, 12, 1, 2),
+    (300, 64, 4, 1, 1, 2)])
+def test_groups_and_bias(score, T, E, k, groups, top, gt):
+    _say("route groups", score, T, E, k, groups, top, gt)
+    g = _gen(T, E, k, groups)
+    x = torch.randn(T, E, generator=g)
+    bias = torch.randn(E, generator=g).mul_(0.1)
+    kw = dict(score=score, groups=groups, top_groups=top, group_top=gt)
+    _check(x, k, bias, **kw)
+    _check(x, k, bias, renormalize=False, **kw)
+    _check(x, k, **kw)
+
+
+def test_equal_values_go_to_the_lowest_index():
+    x = torch.randint(0, 3, (200, 64), generator=_gen(1)).float()
+    x[x == 0] = -0.0
+    x[::2] = x[::2].abs()                        # zeros of both signs are equal
+    for kw in ({}, {"score": "sigmoid", "bias": torch.zeros(64)},
+               {"score": "sigmoid", "bias": torch.zeros(64), "groups": 8, "top_groups": 3, "group_top": 2},
+               {"groups": 16, "top_groups": 5}):
+        _check(x, 6, **kw)
+
+
+def test_values_that_single_precision_would_confuse():
+    # scores + bias that differ by less than a float32's step near 1
+    g = _gen(12)
+    x = torch.randn(400, 64, generator=g).mul_(1e-4)
+    bias = 1.0 + torch.randint(0, 3, (64,), generator=g).float() * 2.0 ** -23
+    _check(x, 8, bias, score="sigmoid")
+    _check(x, 8, bias, score="sigmoid", groups=8, top_groups=2, group_top=2)
+    _check(x, 8, bias, score="softmax")
+
+
+def test_masked_experts_and_padded_tokens():
+    _say("route masks")
+    g = _gen(3)
+    for T in (6, 90):
+        x = torch.randn(T, 48, generator=g)
+        x[torch.rand(T, 48, generator=g) < 0.5] = -INF
+        x[1] = -INF                              # nobody is left
+        x[2, 1:] = -INF                          # one is
+        x[T - 2:] = -INF
+        x[3] = torch.finfo(torch.float32).min    # the lowest value is a number like any other
+        x[4, :40] = torch.finfo(torch.float32).min
+        bias = torch.randn(48, generator=g).mul_(0.1)
+        bias[5] = -INF
+        for b in (None, bias):
+            for kw in ({}, {"groups": 6, "top_groups": 2, "group_top": 2}, {"groups": 4, "top_groups": 1}):
+                for score in ("softmax", "sigmoid"):
+                    r = _check(x, 7, b, score=score, **kw)
+                    assert (r.experts[1] == -1).all() and (r.weights[1] == 0).all()
+    r = _check(torch.full((4, 16), -INF), 2)     # no token has an expert
+    assert (r.offsets == 0).all() and (r.rows == -1).all()
+    r = _check(torch.full((300, 16), -INF), 2, score="sigmoid")
+    assert (r.offsets == 0).all() and (r.rows == -1).all() and (r.places == -1).all()
+
+
+def test_scores_that_vanish():
+    x = torch.full((3, 8), -2000.0)              # sigmoid is 0 in 64 bits: no weight, no NaN
+    r = P.route(x.to(DEV), 2, score="sigmoid")
+    assert (r.weights == 0).all() and r.experts.tolist() == [[0, 1]] * 3
+    x = torch.randn(5, 8, generator=_gen(2)) - 300       # 0 in 32 bits only
+    _check(x, 3, score="sigmoid")
+    _check(torch.randn(5, 8, generator=_gen(4)) * 1000, 3, score="softmax")
+
+
+def test_nan_ranks_first_and_shows():
+    for dt in TYPES:
+        x = torch.randn(20, 40, generator=_gen(5)).to(dt)
+        x[3, 17], x[7, 2], x[7, 30] = float("nan"), float("nan"), INF
+        for kw in ({"score": "softmax"}, {"score": "sigmoid"},
+                   {"score": "sigmoid", "bias": torch.zeros(40, device=DEV)}):
+            r = P.route(x.to(DEV), 4, **kw)
+            assert r.experts[3, 0] == 17 and r.experts[7, 0] == 2
+            assert torch.isnan(r.weights[3]).all() and torch.isnan(r.weights[7]).all()
+            ok = [i for i in range(20) if i not in (3, 7)]
+            assert torch.isfinite(r.weights[ok]).all()
+
+
+def test_strided_logits_no_tokens_and_reused_workspaces():
+    base = torch.randn(50, 100, generator=_gen(6)).to(DEV)
+    for x in (base[:, 3:67], base[::2, :64], base.to(torch.bfloat16)[1:, 1:65]):
+        r, q = P.route(x, 5), P.route(x.contiguous(), 5)
+        for a, b in zip(vars(r).values(), vars(q).values()):
+            assert torch.equal(a, b)
+    r = P.route(base[:0], 5)
+    assert r.experts.shape == (0, 5) and r.offsets.tolist() == [0] * 101 and r.rows.shape == (0,)
+    need = L.load().aaac_route_workspace_bytes(50, 100)
+    for fill in (0, 255):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device=DEV)
+        out = [torch.empty_like(t) for t in vars(P.route(base, 5)).values()]
+        L.aaac_route(base, 5, *out, ws=ws)
+        for a, b in zip(out, vars(P.route(base, 5)).values()):
+            assert torch.equal(a, b)
+
+
+def test_many_tokens_against_a_sort():
+    _say("route many")
+    for T, E, k in ((20011, 128, 6), (70000, 8, 2)):
+        x = torch.randn(T, E, generator=_gen(T)).to(DEV)
+        x[::97] = -INF
+        r = P.route(x, k)
+        top = torch.sort(x, dim=1, descending=True, stable=True)
+        want = top.indices[:, :k].masked_fill(torch.isneginf(top.values[:, :k]), -1)
+        assert torch.equal(r.experts.long(), want)
+        key = want.reshape(-1).masked_fill(want.reshape(-1) < 0, E)
+        at = torch.sort(key, stable=True).indices
+        n = int((key < E).sum())
+        assert torch.equal(r.rows[:n].long(), at[:n] // k) and (r.rows[n:] == -1).all()
+        places = torch.full((T * k,), -1, device=DEV)
+        places[at[:n]] = torch.arange(n, device=DEV)
+        assert torch.equal(r.places.reshape(-1).long(), places)
+        counts = torch.bincount(key, minlength=E + 1)[:E]
+        assert r.offsets[0] == 0 and torch.equal(r.offsets[1:].long(), counts.cumsum(0))
+
+
+# ------------------------------------------------------------------ rows to experts and back
+
+@pytest.mark.parametrize("dtype", TYPES + [torch.uint8, torch.int32])
+@pytest.mark.parametrize("T,C,k", [(1, 1, 1), (3, 8, 2), (5, 33, 4), (61, 2882, 4), (7, 4096, 8), (300, 70, 3)])
+def test_rows_to_experts(dtype, T, C, k):
+    _say("rows to", dtype, T, C, k)
+    g = _gen(T, C, k)
+    x = torch.randint(0, 200, (T, C), generator=g).to(dtype).to(DEV)
+    places = torch.randperm(T * k + 5, generator=g)[:T * k].view(T, k).int()
+    places[0, 0] = -1
+    places[-1, -1] = T * k + 100
+    out = torch.full((T * k + 5, C), 99, dtype=dtype, device=DEV)
+    want = out.clone()
+    for t in range(T):
+        for p in places[t].tolist():
+            if 0 <= p < T * k + 5:
+                want[p] = x[t]
+    P.rows_to_experts(x, places.to(DEV), out)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("ytype", TYPES)
+@pytest.mark.parametrize("otype", TYPES)
+@pytest.mark.parametrize("T,C,k", [(1, 1, 1), (3, 8, 2), (5, 33, 4), (61, 2882, 4), (7, 4096, 8)])
+def test_rows_from_experts(ytype, otype, T, C, k):
+    _say("rows from", ytype, otype, T, C, k)
+    g = _gen(T, C, k)
+    y = torch.randn(T * k, C, generator=g).to(ytype)
+    w = torch.rand(T, k, generator=g)
+    places = torch.randperm(T * k, generator=g).view(T, k).int()
+    places[0, 0] = -1
+    places[-1, -1] = T * k
+    ok = (places >= 0) & (places < T * k)
+    part = y.double()[places.long().clamp(0, T * k - 1)] * torch.where(ok, w, torch.zeros(())).double()[..., None]
+    want = part.sum(1)
+    got = P.rows_from_experts(y.to(DEV), places.to(DEV), w.to(DEV), dtype=otype)
+    # k fused multiply-adds in fp32, then half a step of the result
+    eps = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}[otype]
+    tol = k * 2.0 ** -24 * part.abs().sum(1) * (1 + eps) + eps * want.abs() + (2.0 ** -25 if otype is torch.float16 else 0)
+    assert got.dtype is otype and ((got.double().cpu() - want).abs() <= tol).all()
+
+
+def test_rows_in_strided_tensors():
+    g = _gen(9)
+    base = torch.randn(30, 100, generator=g).to(torch.bfloat16).to(DEV)
+    places = torch.randperm(60, generator=g).view(30, 2).int().to(DEV)
+    w = torch.rand(30, 2, generator=g).to(DEV)
+    for a, b in ((0, 64), (1, 65), (2, 60), (8, 72)):
+        x = base[:, a:b]
+        buf = torch.full((60, 90), 3.0, dtype=torch.bfloat16, device=DEV)
+        view = buf[:, 5:5 + b - a]
+        P.rows_to_experts(x, places, view)
+        ys = P.rows_to_experts(x.contiguous(), places)
+        assert torch.equal(view, ys)
+        assert torch.equal(P.rows_from_experts(view, places, w), P.rows_from_experts(ys, places, w))
+        view.fill_(3.0)
+        assert (buf == 3).all()
+    assert P.rows_from_experts(base[:0], torch.full((4, 2), -1, dtype=torch.int32, device=DEV),
+                               torch.ones(4, 2, device=DEV)).abs().max() == 0
+    assert P.rows_to_experts(base[:0], places[:0]).shape == (0, 100)
+
+
+def test_infinite_rows_count_only_where_they_are_placed():
+    y = torch.ones(4, 64, device=DEV)
+    y[2] = INF
+    places = torch.tensor([[0, 1], [-1, 3], [2, 3]], dtype=torch.int32, device=DEV)
+    w = torch.tensor([[0.5, 0.25], [0.0, 1.0], [1.0, 1.0]], device=DEV)
+    got = P.rows_from_experts(y, places, w)
+    assert got[:, 0].tolist() == [0.75, 1.0, INF]
+
+
+# ------------------------------------------------------------------ a layer of experts
+
+def _experts(kind, W):
+    if kind == "fp8":
+        return P.FP8Matrix.quantize(W)
+    return P.MXFP4Matrix.quantize(W)
+
+
+def _layer(x, logits, up, down, rows, **kw):
+    r = P.route(logits, 4, **kw)
+    if rows:
+        h = up.matmul(x, r.offsets, rows=r.rows)
+    else:
+        h = up.matmul(r.to_experts(x), r.offsets)
+    a, b = h.chunk(2, dim=-1)
+    s = torch.nn.functional.silu(a) * b
+    y = down.matmul(s, r.offsets)
+    return r, h, s, y, r.from_experts(y)
+
+
+def _near(got, x, W, kind):
+    """A product's row, bf16, against 64 bits: half a step (2^-8), and fp32 sums of exact products, every
+    addition cut or rounded to 24 bits (2^-23), with a factor and a few joins (40) more. The FP8 instruction
+    adds eight products aligned to the largest and cut below 2^-13 of it: 8 * 2^-13 of the magnitudes."""
+    x = x.double()
+    if kind == "fp8":
+        x = torch.from_numpy(ref.fp8_decode(*ref.fp8_encode(x[None].numpy())))[0]
+    want, mag = W @ x, W.abs() @ x.abs()
+    cut = 8 * 2.0 ** -13 if kind == "fp8" else 0.0
+    assert ((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + ((len(x) + 40) * 2.0 ** -23 + cut) * mag).all()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("T", [1, 5, 64, 700])
+def test_a_layer_of_experts(kind, T):
+    """Routing, both products and the way back, each step against 64 bits on the step's own inputs."""
+    _say("layer", kind, T)
+    E, C, F = 12, 256, 192
+    g = _gen(T, 3)
+    up, down = (_experts(kind, torch.randn(E, a, b, generator=g).mul_(0.05).to(torch.bfloat16).to(DEV))
+                for a, b in ((2 * F, C), (C, F)))
+    x = torch.randn(T, C, generator=g).to(torch.bfloat16).to(DEV)
+    logits = torch.randn(T, E, generator=g).to(DEV)
+    if T > 1:
+        logits[-1] = -INF                        # a padded batch
+    kw = dict(score="sigmoid", scale=1.5)
+    r, h, s, y, out = _layer(x, logits, up, down, kind == "fp8", **kw)
+    n = int(r.offsets[-1])
+    assert n == 4 * (T - 1 if T > 1 else 1)
+    if kind == "fp8":                            # the index and the copied rows agree bit for bit
+        _, h2, _, y2, out2 = _layer(x, logits, up, down, False, **kw)
+        assert torch.equal(h[:n], h2[:n]) and torch.equal(y[:n], y2[:n]) and torch.equal(out, out2)
+    e64, w64, _, _, places = ref.route(logits.double().cpu().numpy(), 4, **kw)
+    assert np.array_equal(r.experts.cpu().numpy(), e64) and np.array_equal(r.places.cpu().numpy(), places)
+    uv, dv = up.dequant(torch.float32).double().cpu(), down.dequant(torch.float32).double().cpu()
+    x, h, s, y, out = x.cpu(), h.cpu(), s.cpu(), y.cpu(), out.cpu()
+    for t in range(0, T, 1 + T // 60):
+        want, mag = torch.zeros(C, dtype=torch.float64), torch.zeros(C, dtype=torch.float64)
+        for j in range(4):
+            e, p = int(e64[t, j]), int(places[t, j])
+            if e >= 0:
+                _near(h[p], x[t], uv[e], kind)
+                _near(y[p], s[p], dv[e], kind)
+                want += w64[t, j] * y[p].double()
+                mag += (w64[t, j] * y[p].double()).abs()
+        # the weights' roundings and four fused multiply-adds, then half a step
+        assert ((out[t].double() - want).abs() <= 2.0 ** -8 * want.abs() + 16 * 2.0 ** -24 * mag).all()
+    if T > 1:
+        assert (out[-1] == 0).all() and (r.experts[-1] == -1).all()
+
+
+def test_layer_captured_and_replayed():
+    _say("layer graph")
+    E, C, F, T = 8, 256, 128, 20
+    g = _gen(31)
+    up, down = (P.FP8Matrix.quantize(torch.randn(E, a, b, generator=g).mul_(0.05).to(DEV))
+                for a, b in ((2 * F, C), (C, F)))
+    x = torch.randn(T, C, generator=g).to(torch.bfloat16).to(DEV)
+    logits = torch.randn(T, E, generator=g).to(DEV)
+    _layer(x, logits, up, down, True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        _layer(x, logits, up, down, True)
+    torch.cuda.current_stream().wait_stream(side)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        r, _, _, _, out = _layer(x, logits, up, down, True)
+    for i in range(4):
+        x.normal_()
+        logits.normal_()
+        if i == 2:
+            logits[T // 2:] = -INF               # a shorter batch in the same graph
+        r2, _, _, _, want = _layer(x, logits, up, down, True)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(r.experts, r2.experts) and torch.equal(r.places, r2.places)
+        assert torch.equal(out, want)
+
+
+def test_refusals_of_the_calls():
+    x = torch.randn(4, 16, device=DEV)
+    with pytest.raises(ValueError, match="gradient"):
+        P.route(x.clone().requires_grad_(), 2)
+    with pytest.raises(ValueError, match="gradient"):
+        P.route(x, 2, bias=torch.zeros(16, device=DEV, requires_grad=True))
+    with pytest.raises(ValueError, match="score"):
+        P.route(x, 2, score="tanh")
+    for bad in (0, -1, 1.5):
+        with pytest.raises(ValueError):
+            P.route(x, bad)
+    for kw in (dict(k=17), dict(k=2, groups=3), dict(k=5, groups=4, top_groups=1), dict(k=2, groups=0),
+               dict(k=2, groups=4, top_groups=5), dict(k=2, groups=4, top_groups=2, group_top=3)):
+        with pytest.raises(L.AAACError):
+            P.route(x, **kw)
+    with pytest.raises(L.AAACError):
+        P.route(torch.randn(2, 513, device=DEV), 2)
+    with pytest.raises(TypeError):
+        P.route(x.double(), 2)
+    with pytest.raises(ValueError):
+        P.route(x, 2, bias=torch.zeros(15, device=DEV))
+    with pytest.raises(ValueError):
+        P.route(x.t(), 2)
+    places = torch.zeros(4, 2, dtype=torch.int32, device=DEV)
+    with pytest.raises(ValueError):
+        P.rows_to_experts(x, places[:3])
+    with pytest.raises(ValueError):
+        P.rows_to_experts(x, places.long())
+    with pytest.raises(TypeError):
+        P.rows_to_experts(x.double(), places)
+    with pytest.raises(ValueError, match="gradient"):
+        P.rows_to_experts(x.clone().requires_grad_(), places)
+    with pytest.raises(ValueError):
+        P.rows_from_experts(x, places, torch.ones(4, 3, device=DEV))
+    with pytest.raises(ValueError, match="gradient"):
+        P.rows_from_experts(x, places, torch.ones(4, 2, device=DEV, requires_grad=True))
+    with pytest.raises(ValueError):
+        P.rows_from_experts(x, places, torch.ones(4, 2, device=DEV), out=torch.empty(4, 15, device=DEV))
