@@ -201,36 +201,47 @@ hipError_t few_fp8(MatmulArgs a, hipStream_t stream) {
 
 // ------------------------------------------------------------------------------------------------
 // More rows: tiles of BM weight rows by BN rows of x, both staged through LDS, a block of 128 columns a
-// step. Loads run NS - 1 steps ahead and go to LDS asynchronously. The 16-byte pieces of a row lie
-// permuted by row bits 1 to 3 (piece_turn). A stage ends with the step's scales: those of the tile's rows
-// of x, then of its blocks of weight rows.
+// step, in a ring of NS stages. The 16-byte pieces of a row lie permuted by row bits 1 to 3 (piece_turn). A
+// stage ends with the step's scales: those of the tile's rows of x, then of its blocks of weight rows.
+//
+// A wave holds its fragments of x for the whole step and takes its FR fragments of weights in turn, each
+// read while the one before is multiplied. A stage is given back in two parts, so that loads run NS - 1/2
+// steps ahead: once the first half of the weights' fragments and those of x are read (point A, before the
+// products of the half's last fragment), the step NS later loads these parts; once the second half is read
+// (point B, before the products of the last fragment), the rest. The products at these points come from
+// registers, so the matrix units work through the barriers. At either point all but the (NS - 1) kLoads
+// youngest loads of a wave have to have arrived, and the loads that follow it are spread between the
+// products: 64 lanes of 16 bytes take the address unit 16 cycles, all of a step's at once half of a step.
+// Loads past the last step lie outside their buffers, so every step has the same count.
 // ------------------------------------------------------------------------------------------------
 template <int WR, int WT, int FR, int FT, int NS, bool WIDE>
 __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs a) {
   constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma;
   constexpr int kW = BM * 128, kX = BN * 128, kS = NW * 256, kStage = kW + kX + kS;
-  constexpr int kWl = BM / 8 / NW, kXl = BN / 8 / NW, kLoads = kWl + kXl + 1;
+  constexpr int kWl = BM / 8 / NW / 2, kXl = BN / 8 / NW;    // loads a wave: half of the weights; x
+  constexpr int kA = kWl + kXl + 1, kLoads = kA + kWl;
   constexpr int kXWaves = (BN + kWave - 1) / kWave;          // waves that load scales of x
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "whole loads a wave");
+  static_assert(BM % (16 * NW) == 0 && BN % (8 * NW) == 0 && FR % 2 == 0, "whole loads a wave");
   static_assert(kXWaves < NW && FR * kMfma <= kFp8Block, "the scales' loads");
   // the stages give way to the waves' results at the end
   constexpr int kResults = NW * tile_bytes<FR, FT>();
   __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > kResults ? NS * kStage : kResults];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
   if (block_id() >= a.blocks) return;
-  const int64_t id = by_die(block_id(), a.blocks), tiles = a.blocks / a.split;
-  const int part = (int)(id / tiles);
+  // fewer than 2^32 workgroups have a tile (2^31 tiles of 16 x 16 at most)
+  const uint32_t id = (uint32_t)by_die(block_id(), a.blocks), tiles = (uint32_t)a.blocks / (uint32_t)a.split;
+  const uint32_t part = id / tiles, row_blocks = (uint32_t)a.row_blocks;
   // tiles go in bands of kBand token tiles by all row blocks, the band's token tiles innermost, so that
   // a die's run of tiles shares rows of x and weights alike
-  constexpr int kBand = 4;
-  const int64_t n_tok = tiles / a.row_blocks, in_part = id % tiles, band = in_part / (kBand * a.row_blocks);
-  const int64_t in_band = in_part - band * kBand * a.row_blocks;
-  const int64_t wide = n_tok - band * kBand < kBand ? n_tok - band * kBand : kBand;
-  const int64_t rb = in_band / wide, tile = band * kBand + in_band % wide;
+  constexpr uint32_t kBand = 4;
+  const uint32_t n_tok = tiles / row_blocks, in_part = id - part * tiles;
+  const uint32_t band = in_part / (kBand * row_blocks), in_band = in_part - band * kBand * row_blocks;
+  const uint32_t wide = n_tok - band * kBand < kBand ? n_tok - band * kBand : kBand;
+  const uint32_t rb = in_band / wide, tile = band * kBand + (in_band - rb * wide);
   int e;
   int64_t t0, t1;
   if (!find_tile(a.offsets, a.E, a.T, BN, tile, e, t0, t1)) return;
-  const int64_t r0 = rb * BM;
+  const int64_t r0 = (int64_t)rb * BM;
   const int nr = (int)(a.R - r0 < BM ? a.R - r0 : BM), nt = (int)(t1 - t0 < BN ? t1 - t0 : BN);
   const int64_t cb = fp8_blocks(a.C), rbs = fp8_blocks(a.R);
   // buffers end with the 16-byte piece that holds their last column
@@ -240,27 +251,33 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
   const u32x4 xr = rows_buffer(static_cast<const uint8_t*>(a.x) + x0 * a.ldx,
                                ((xn - 1) * a.ldx + a.C + 15) & ~(int64_t)15);
   const int first = (int)(cb * part / a.split), steps = (int)(cb * (part + 1) / a.split);
-  uint32_t woff[kWl], xoff[kXl];
-  int wcol[kWl], xcol[kXl];
+  // the tile row of eight rows' load i of half h of the weights: halves of every wave row's fragments
+  auto w_row = [&](int h, int i) {
+    constexpr int kHalf = FR / 2 * kMfma;
+    const int r = (wave * kWl + i) * 8;
+    return r / kHalf * (2 * kHalf) + h * kHalf + r % kHalf;
+  };
+  // the column of a lane's 16 bytes in rows from an even and from an odd multiple of eight on
+  const int col[2] = {((lane & 7) ^ piece_turn(lane >> 3)) * 16, ((lane & 7) ^ piece_turn((lane >> 3) + 8)) * 16};
+  uint32_t woff[2][kWl], xoff[kXl];
 #pragma unroll
-  for (int i = 0; i < kWl; ++i) {
-    const int row = (wave * kWl + i) * 8 + (lane >> 3);
-    wcol[i] = ((lane & 7) ^ piece_turn(row)) * 16;
-    woff[i] = row < nr ? row * (uint32_t)a.ldw + wcol[i] : kOutside;
-  }
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < kWl; ++i) {
+      const int row = w_row(h, i);
+      woff[h][i] = row + (lane >> 3) < nr ? (row + (lane >> 3)) * (uint32_t)a.ldw + col[row >> 3 & 1] : kOutside;
+    }
 #pragma unroll
   for (int i = 0; i < kXl; ++i) {
-    const int row = (wave * kXl + i) * 8 + (lane >> 3);
-    const int64_t x = row < nt ? x_row(a, t0 + row) : -1;
-    xcol[i] = ((lane & 7) ^ piece_turn(row)) * 16;
-    xoff[i] = x >= 0 ? (uint32_t)(x - x0) * (uint32_t)a.ldx + xcol[i] : kOutside;
+    const int row = (wave * kXl + i) * 8;
+    const int64_t x = row + (lane >> 3) < nt ? x_row(a, t0 + row + (lane >> 3)) : -1;
+    xoff[i] = x >= 0 ? (uint32_t)(x - x0) * (uint32_t)a.ldx + col[row >> 3 & 1] : kOutside;
   }
   // this wave's scales: 64 rows of x, or the tile's blocks of weight rows
-  const bool of_x = wave < kXWaves;
   const float* sbase;
   int64_t sstep, sbytes;
   uint32_t soff = kOutside;
-  if (of_x) {
+  if (wave < kXWaves) {
     const int row = wave * kWave + lane;
     const int64_t x = row < nt ? x_row(a, t0 + row) : -1;
     if (x >= 0) soff = (uint32_t)((x - x0) * a.xs_row) * 4u;
@@ -276,21 +293,48 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
     sbytes = ((n - 1) * cb + 1) * 4;
   }
   const uint32_t lds0 = lds_address(&lds[0]);
-  auto load = [&](int slot, int kt) __attribute__((always_inline)) {
+  // Loads of a step, one at a time: 0 .. kA - 1 its part A, kA .. kLoads - 1 its part B.
+  auto load = [&](int slot, int kt, int n) __attribute__((always_inline)) {
     const uint32_t dst = lds0 + slot * kStage;
-    const bool cut = kt * kFp8Block + kFp8Block > a.C;       // the row's last, short block, or past it
-    const int left = (int)a.C - kt * kFp8Block;
-    const uint32_t more = kt < steps ? (uint32_t)kt * kFp8Block : 0u;
+    const bool in = kt < steps;
+    const uint32_t more = in ? (uint32_t)kt * kFp8Block : 0u;
+    // columns from the step's first on; a row's last step may have fewer
+    const int left = in ? (int)a.C - kt * kFp8Block : 0;
+    auto at = [&](uint32_t off, int row) { return left >= kFp8Block || col[row >> 3 & 1] < left ? off : kOutside; };
+    if (n == kWl + kXl) {
+      load_lds4(rows_buffer(sbase + (in ? kt : 0) * sstep, sbytes), in ? soff : kOutside,
+                dst + kW + kX + wave * 256);
+    } else if (n >= kWl && n < kWl + kXl) {
+      const int i = n - kWl, row = (wave * kXl + i) * 8;
+      load_lds16(xr, at(xoff[i], row), more, dst + kW + row * 128);
+    } else {
+      const int h = n < kWl ? 0 : 1, i = h ? n - kA : n, row = w_row(h, i);
+      load_lds16(wr, at(woff[h][i], row), more, dst + row * 128);
+    }
+  };
+  // Loads n0 .. n1 - 1, part `at` of `of` of them.
+  auto loads = [&](int slot, int kt, int n0, int n1, int at, int of) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < kWl; ++i)
-      load_lds16(wr, (cut && wcol[i] >= left) || kt >= steps ? kOutside : woff[i], more,
-                 dst + (wave * kWl + i) * 1024);
-#pragma unroll
-    for (int i = 0; i < kXl; ++i)
-      load_lds16(xr, (cut && xcol[i] >= left) || kt >= steps ? kOutside : xoff[i], more,
-                 dst + kW + (wave * kXl + i) * 1024);
-    load_lds4(rows_buffer(sbase + (kt < steps ? kt : 0) * sstep, sbytes), kt < steps ? soff : kOutside,
-              dst + kW + kX + wave * 256);
+    for (int n = 0; n < kLoads; ++n)
+      if (n >= n0 + (n1 - n0) * at / of && n < n0 + (n1 - n0) * (at + 1) / of) load(slot, kt, n);
+  };
+  // Arrived are all but the youngest (NS - 1) kLoads. Where step kt is the row's last and ends inside a
+  // 16-byte piece, that piece keeps the columns that exist: in half h of the weights, and x with half 0.
+  auto arrive = [&](int slot, int kt, int h) __attribute__((always_inline)) {
+    wait_loads<(NS - 1) * kLoads>();
+    step_barrier();
+    if ((a.C & 15) && kt == (int)cb - 1) {
+      int from = tid;
+      asm volatile("" : "+v"(from));             // keeps what this needs out of the loop's registers
+      for (int r = from; r < BM + BN; r += NW * kWave) {
+        if (r < BM ? (r / kMfma % FR >= FR / 2) != h : h) continue;
+        const int piece = ((int)a.C & 127) >> 4;
+        u32x4* p = reinterpret_cast<u32x4*>(lds + slot * kStage + r * 128 +
+                                            (piece ^ piece_turn(r < BM ? r : r - BM)) * 16);
+        *p = first_bytes(*p, (int)a.C & 15);
+      }
+      step_barrier();
+    }
   };
   f32x4 acc[FR][FT];
 #pragma unroll
@@ -302,55 +346,69 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
   const int wm = (wave % WR) * FR * kMfma, wn = (wave / WR) * FT * kMfma;
   const bool busy = wn < nt;
   const int l = lane & 15, q = lane >> 4;
-  const int p0 = ((2 * q) ^ piece_turn(l)) * 16, p1 = ((2 * q + 1) ^ piece_turn(l)) * 16;
-#pragma unroll
-  for (int s = 0; s < NS - 1; ++s) load(s, first + s);
+  const int p0 = ((2 * q) ^ piece_turn(l)) * 16, p1 = p0 ^ 16;
+  auto read = [&](const uint8_t* p) __attribute__((always_inline)) {
+    return frag<WIDE>(*reinterpret_cast<const u32x4*>(p + p0), *reinterpret_cast<const u32x4*>(p + p1));
+  };
   auto walk = [&](auto with_products) __attribute__((always_inline)) {
+    constexpr bool kMul = decltype(with_products)::value != 0;
+    Frag<WIDE> xf[FT], wf[2];
+    f32x4 p[FT];                                 // sums of the fragment of weights before
+    float f[FT], last[FT];                       // factors of this step and of the one before
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int n = 0; n < kLoads; ++n) load(s, first + s, n);
+    arrive(0, first, 0);
+    if (kMul) {
+#pragma unroll
+      for (int j = 0; j < FT; ++j) {
+        xf[j] = read(lds + kW + (wn + j * kMfma + l) * 128);
+        p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        last[j] = 0.0f;
+      }
+      wf[0] = read(lds + (wm + l) * 128);
+    }
     int slot = 0;
     for (int kt = first; kt < steps; ++kt) {
-      wait_loads<(NS - 2) * kLoads>();
-      step_barrier();
-      uint8_t* base = lds + slot * kStage;
-      if ((a.C & 15) && kt == (int)cb - 1) {
-        // the row's last piece keeps the columns that exist
-        for (int row = tid; row < BM + BN; row += NW * kWave) {
-          const int r = row < BM ? row : row - BM, piece = ((int)a.C & 127) >> 4;
-          u32x4* p = reinterpret_cast<u32x4*>(base + row * 128 + (piece ^ piece_turn(r)) * 16);
-          *p = first_bytes(*p, (int)a.C & 15);
-        }
-        step_barrier();
+      const int next = slot + 1 == NS ? 0 : slot + 1;
+      const uint8_t* wb = lds + slot * kStage + (wm + l) * 128;
+      const uint8_t* nb = lds + next * kStage;
+      const float* sb = reinterpret_cast<const float*>(lds + slot * kStage + kW + kX);
+      if (kMul) {
+        const float fw = sb[kXWaves * kWave + wm / kFp8Block];
+#pragma unroll
+        for (int j = 0; j < FT; ++j) f[j] = sb[wn + j * kMfma + l] * fw;
       }
-      load(slot == 0 ? NS - 1 : slot - 1, kt + NS - 1);
-      slot = slot + 1 == NS ? 0 : slot + 1;
-      if (decltype(with_products)::value == 0) continue;
-      const uint8_t* wb = base + (wm + l) * 128;
-      const uint8_t* xb = base + kW + (wn + l) * 128;
-      const float* sb = reinterpret_cast<const float*>(base + kW + kX);
-      const float fw = sb[kXWaves * kWave + wm / kFp8Block];
-      auto read = [&](const uint8_t* p) __attribute__((always_inline)) {
-        return frag<WIDE>(*reinterpret_cast<const u32x4*>(p + p0), *reinterpret_cast<const u32x4*>(p + p1));
-      };
-      Frag<WIDE> xf[FT], wf[2];
-      float f[FT];
-      f32x4 p[2][FT];
-#pragma unroll
-      for (int j = 0; j < FT; ++j) xf[j] = read(xb + j * kMfma * 128);
-      wf[0] = read(wb);
-#pragma unroll
-      for (int j = 0; j < FT; ++j) f[j] = sb[wn + j * kMfma + l] * fw;
 #pragma unroll
       for (int i = 0; i < FR; ++i) {
-        if (i + 1 < FR) wf[(i + 1) & 1] = read(wb + (i + 1) * kMfma * 128);
+        if (i == FR / 2 - 1) arrive(slot, kt, 1);            // A
+        if (i == FR - 1) arrive(next, kt + 1, 0);            // B
+        if (kMul) {
+          wf[(i + 1) & 1] = read(i + 1 < FR ? wb + (i + 1) * kMfma * 128 : nb + (wm + l) * 128);
 #pragma unroll
-        for (int j = 0; j < FT; ++j) p[i & 1][j] = block_sum<WIDE>(wf[i & 1], xf[j]);
-        if (i > 0) {
-#pragma unroll
-          for (int j = 0; j < FT; ++j) acc[i - 1][j] += p[(i - 1) & 1][j] * f[j];
+          for (int j = 0; j < FT; ++j) {
+            f32x4& sum = acc[i > 0 ? i - 1 : FR - 1][j];
+            sum += p[j] * (i > 0 ? f[j] : last[j]);
+            asm volatile("" : "+v"(sum));        // here, not behind the barriers that follow
+            p[j] = block_sum<WIDE>(wf[i & 1], xf[j]);
+            if (i == FR - 1) xf[j] = read(nb + kW + (wn + j * kMfma + l) * 128);
+          }
         }
+        // after A: part A of the step NS later, after B of the step before: its part B
+        if (i >= FR / 2 - 1 && i < FR - 1) loads(slot, kt + NS, 0, kA, i - (FR / 2 - 1), FR / 2);
+        else if (i == FR - 1) loads(slot, kt + NS, kA, kLoads, 0, 1);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if (kMul) {
 #pragma unroll
-      for (int j = 0; j < FT; ++j) acc[FR - 1][j] += p[(FR - 1) & 1][j] * f[j];
+        for (int j = 0; j < FT; ++j) last[j] = f[j];
+      }
+      slot = next;
+    }
+    if (kMul) {
+#pragma unroll
+      for (int j = 0; j < FT; ++j) acc[FR - 1][j] += p[j] * last[j];
     }
   };
   if (busy) walk(Int<1>());
