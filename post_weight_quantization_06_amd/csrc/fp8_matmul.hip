@@ -46,6 +46,11 @@ __device__ __forceinline__ Frag<WIDE> frag(u32x4 a, u32x4 b) {
   return f;
 }
 
+__device__ __forceinline__ i32x8 operand(const Frag<false>& f) {
+  return i32x8{(int)f.v[0].x, (int)f.v[0].y, (int)f.v[0].z, (int)f.v[0].w,
+               (int)f.v[1].x, (int)f.v[1].y, (int)f.v[1].z, (int)f.v[1].w};
+}
+
 // The sum over a block.
 template <bool WIDE>
 __device__ __forceinline__ f32x4 block_sum(const Frag<WIDE>& w, const Frag<WIDE>& x) {
@@ -55,13 +60,8 @@ __device__ __forceinline__ f32x4 block_sum(const Frag<WIDE>& w, const Frag<WIDE>
     for (int i = 0; i < 4; ++i) c = mfma_bf16(w.v[i], x.v[i], c);
     return c;
   } else {
-    const u32x4 *a = w.v, *b = x.v;
-    const i32x8 wa = {(int)a[0].x, (int)a[0].y, (int)a[0].z, (int)a[0].w,
-                      (int)a[1].x, (int)a[1].y, (int)a[1].z, (int)a[1].w};
-    const i32x8 xa = {(int)b[0].x, (int)b[0].y, (int)b[0].z, (int)b[0].w,
-                      (int)b[1].x, (int)b[1].y, (int)b[1].z, (int)b[1].w};
     // e4m3 on both sides, no scales (zeros select the instruction without)
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, xa, c, 0, 0, 0, 0, 0, 0);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(x), c, 0, 0, 0, 0, 0, 0);
   }
 }
 
@@ -204,28 +204,82 @@ hipError_t few_fp8(MatmulArgs a, hipStream_t stream) {
 // step, in a ring of NS stages. The 16-byte pieces of a row lie permuted by row bits 1 to 3 (piece_turn). A
 // stage ends with the step's scales: those of the tile's rows of x, then of its blocks of weight rows.
 //
-// A wave holds its fragments of x for the whole step and takes its FR fragments of weights in turn, each
-// read while the one before is multiplied. A stage is given back in two parts, so that loads run NS - 1/2
-// steps ahead: once the first half of the weights' fragments and those of x are read (point A, before the
-// products of the half's last fragment), the step NS later loads these parts; once the second half is read
-// (point B, before the products of the last fragment), the rest. The products at these points come from
-// registers, so the matrix units work through the barriers. At either point all but the (NS - 1) kLoads
-// youngest loads of a wave have to have arrived, and the loads that follow it are spread between the
-// products: 64 lanes of 16 bytes take the address unit 16 cycles, all of a step's at once half of a step.
-// Loads past the last step lie outside their buffers, so every step has the same count.
+// The instruction is that of 32 x 32 results and 64 columns, two of them a block. Its operands take 16 of
+// its 64 cycles to read, in which no vector instruction starts; the one of 16 x 16 by 128 columns takes as
+// long for its 32 cycles, and the four multiply-adds and the rest of a block's vector work do not fit into
+// what is left (4 vector instructions to one take 35 cycles, 6 take 47, 8 take 54; in the other, 12 to 64
+// cycles take 68).
+//
+// A wave holds its fragments of x for the whole step and takes the 2 FR half fragments of weights in
+// turn, two of them in registers: the products of one run while the next is there and the one after it is
+// read. A stage is given back in two parts, so that loads run NS - 1/2 steps ahead: point A, before the
+// products of the first half of the weight rows' last two half fragments (everything of that half and of x
+// has been read), frees these for the step NS later, and point B, before the last two, the rest. The
+// products at these points come from registers, so the matrix units work through the barriers. At either
+// point all but the (NS - 1) kLoads youngest loads of a wave have to have arrived, and the loads that follow
+// it are spread between the products: 64 lanes of 16 bytes take the address unit 16 cycles, all of a step's
+// at once half of a step. Loads past the last step lie outside their buffers, so every step has the same
+// count. A wave with one fragment of weights (FR = 1) has no first half and only point B.
 // ------------------------------------------------------------------------------------------------
+constexpr int kBig = 32;                         // rows and columns of the tiles' matrix instruction
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Half of a block: 64 columns, 32 codes a lane.
+template <bool WIDE>
+__device__ __forceinline__ f32x16 half_sum(const Frag<WIDE>& w, const Frag<WIDE>& x, f32x16 c) {
+  if constexpr (WIDE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w.v[i]),
+                                                  __builtin_bit_cast(bf16x8, x.v[i]), c, 0, 0, 0);
+    return c;
+  } else {
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(w), operand(x), c, 0, 0, 0, 0, 0, 0);
+  }
+}
+
+// A wave's result, FR * 32 weight rows by FT * 32 rows of x, as store_tile: a lane has row lane & 31 of x
+// and, in registers 4 g .. 4 g + 3 of a fragment, weight rows 8 g + 4 (lane >> 5) and the next three.
+template <int FR, int FT>
+__device__ __forceinline__ void store_big(const MatmulArgs& a, int part, const f32x16 (&acc)[FR][FT],
+                                          uint8_t* lds, int64_t t0, int64_t t1, int64_t r0) {
+  const int lane = threadIdx.x & (kWave - 1), l = lane & 31, q = lane >> 5;
+  const bool through = a.y_row && a.split == 1;
+#pragma unroll
+  for (int j = 0; j < FT; ++j) {
+    const int64_t t = t0 + j * kBig + l;
+#pragma unroll
+    for (int i = 0; i < FR; ++i)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x16 c = acc[i][j];
+        const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
+        const int row = i * kBig + 8 * g + 4 * q;
+        if (through)
+          *reinterpret_cast<uint2*>(lds + (j * kBig + l) * row_bytes<FR * kBig>() + row * 2) = pack_16(a, v);
+        else if (t < t1 && r0 + row < a.R)
+          store_part(a, part, t, r0 + row, v);
+      }
+  }
+  if (through) store_rows<FR * kBig, FT * kBig>(a, lds, t0, t1, r0);
+}
+
 template <int WR, int WT, int FR, int FT, int NS, bool WIDE>
 __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs a) {
-  constexpr int NW = WR * WT, BM = WR * FR * kMfma, BN = WT * FT * kMfma;
+  constexpr int NW = WR * WT, BM = WR * FR * kBig, BN = WT * FT * kBig;
   constexpr int kW = BM * 128, kX = BN * 128, kS = NW * 256, kStage = kW + kX + kS;
-  constexpr int kWl = BM / 8 / NW / 2, kXl = BN / 8 / NW;    // loads a wave: half of the weights; x
-  constexpr int kA = kWl + kXl + 1, kLoads = kA + kWl;
+  // fragments of a wave's weight rows in the first half, loads a wave of either half and of x
+  constexpr bool kTwo = FR > 1;
+  constexpr int kFirst = kTwo ? FR / 2 : FR;
+  constexpr int kW0 = kFirst * WR * kBig / 8 / NW, kW1 = (FR - kFirst) * WR * kBig / 8 / NW, kXl = BN / 8 / NW;
+  constexpr int kA = kW0 + kXl + 1, kLoads = kA + kW1;
   constexpr int kXWaves = (BN + kWave - 1) / kWave;          // waves that load scales of x
-  static_assert(BM % (16 * NW) == 0 && BN % (8 * NW) == 0 && FR % 2 == 0, "whole loads a wave");
-  static_assert(kXWaves < NW && FR * kMfma <= kFp8Block, "the scales' loads");
+  static_assert(kFirst * WR * kBig % (8 * NW) == 0 && (FR - kFirst) * WR * kBig % (8 * NW) == 0 &&
+                BN % (8 * NW) == 0, "whole loads a wave");
+  static_assert(kXWaves < NW && FR * kBig <= kFp8Block, "the scales' loads");
   // the stages give way to the waves' results at the end
-  constexpr int kResults = NW * tile_bytes<FR, FT>();
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > kResults ? NS * kStage : kResults];
+  constexpr int kResult = FT * kBig * row_bytes<FR * kBig>();
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > NW * kResult ? NS * kStage : NW * kResult];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
   if (block_id() >= a.blocks) return;
   // fewer than 2^32 workgroups have a tile (2^31 tiles of 16 x 16 at most)
@@ -251,22 +305,21 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
   const u32x4 xr = rows_buffer(static_cast<const uint8_t*>(a.x) + x0 * a.ldx,
                                ((xn - 1) * a.ldx + a.C + 15) & ~(int64_t)15);
   const int first = (int)(cb * part / a.split), steps = (int)(cb * (part + 1) / a.split);
-  // the tile row of eight rows' load i of half h of the weights: halves of every wave row's fragments
-  auto w_row = [&](int h, int i) {
-    constexpr int kHalf = FR / 2 * kMfma;
-    const int r = (wave * kWl + i) * 8;
-    return r / kHalf * (2 * kHalf) + h * kHalf + r % kHalf;
+  // the tile row where load n of the weights starts: the first half of every wave row's fragments, then
+  // the second
+  auto w_row = [&](int n) {
+    const int h = n < kW0 ? 0 : 1, rows = (h ? FR - kFirst : kFirst) * kBig;
+    const int r = h ? (wave * kW1 + n - kW0) * 8 : (wave * kW0 + n) * 8;
+    return r / rows * (FR * kBig) + h * kFirst * kBig + r % rows;
   };
   // the column of a lane's 16 bytes in rows from an even and from an odd multiple of eight on
   const int col[2] = {((lane & 7) ^ piece_turn(lane >> 3)) * 16, ((lane & 7) ^ piece_turn((lane >> 3) + 8)) * 16};
-  uint32_t woff[2][kWl], xoff[kXl];
+  uint32_t woff[kW0 + kW1], xoff[kXl];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < kWl; ++i) {
-      const int row = w_row(h, i);
-      woff[h][i] = row + (lane >> 3) < nr ? (row + (lane >> 3)) * (uint32_t)a.ldw + col[row >> 3 & 1] : kOutside;
-    }
+  for (int i = 0; i < kW0 + kW1; ++i) {
+    const int row = w_row(i);
+    woff[i] = row + (lane >> 3) < nr ? (row + (lane >> 3)) * (uint32_t)a.ldw + col[row >> 3 & 1] : kOutside;
+  }
 #pragma unroll
   for (int i = 0; i < kXl; ++i) {
     const int row = (wave * kXl + i) * 8;
@@ -301,15 +354,15 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
     // columns from the step's first on; a row's last step may have fewer
     const int left = in ? (int)a.C - kt * kFp8Block : 0;
     auto at = [&](uint32_t off, int row) { return left >= kFp8Block || col[row >> 3 & 1] < left ? off : kOutside; };
-    if (n == kWl + kXl) {
+    if (n == kW0 + kXl) {
       load_lds4(rows_buffer(sbase + (in ? kt : 0) * sstep, sbytes), in ? soff : kOutside,
                 dst + kW + kX + wave * 256);
-    } else if (n >= kWl && n < kWl + kXl) {
-      const int i = n - kWl, row = (wave * kXl + i) * 8;
+    } else if (n >= kW0 && n < kW0 + kXl) {
+      const int i = n - kW0, row = (wave * kXl + i) * 8;
       load_lds16(xr, at(xoff[i], row), more, dst + kW + row * 128);
     } else {
-      const int h = n < kWl ? 0 : 1, i = h ? n - kA : n, row = w_row(h, i);
-      load_lds16(wr, at(woff[h][i], row), more, dst + row * 128);
+      const int i = n < kW0 ? n : n - kXl - 1, row = w_row(i);
+      load_lds16(wr, at(woff[i], row), more, dst + row * 128);
     }
   };
   // Loads n0 .. n1 - 1, part `at` of `of` of them.
@@ -318,16 +371,16 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
     for (int n = 0; n < kLoads; ++n)
       if (n >= n0 + (n1 - n0) * at / of && n < n0 + (n1 - n0) * (at + 1) / of) load(slot, kt, n);
   };
-  // Arrived are all but the youngest (NS - 1) kLoads. Where step kt is the row's last and ends inside a
-  // 16-byte piece, that piece keeps the columns that exist: in half h of the weights, and x with half 0.
-  auto arrive = [&](int slot, int kt, int h) __attribute__((always_inline)) {
-    wait_loads<(NS - 1) * kLoads>();
+  // Arrived are all but the youngest N loads. Where step kt is the row's last and ends inside a 16-byte
+  // piece, that piece keeps the columns that exist: of half h of the weights, and of x with half 0.
+  auto arrive = [&](auto n, int slot, int kt, int h) __attribute__((always_inline)) {
+    wait_loads<decltype(n)::value>();
     step_barrier();
     if ((a.C & 15) && kt == (int)cb - 1) {
       int from = tid;
       asm volatile("" : "+v"(from));             // keeps what this needs out of the loop's registers
       for (int r = from; r < BM + BN; r += NW * kWave) {
-        if (r < BM ? (r / kMfma % FR >= FR / 2) != h : h) continue;
+        if (r < BM ? (r / kBig % FR >= kFirst) != h : h) continue;
         const int piece = ((int)a.C & 127) >> 4;
         u32x4* p = reinterpret_cast<u32x4*>(lds + slot * kStage + r * 128 +
                                             (piece ^ piece_turn(r < BM ? r : r - BM)) * 16);
@@ -336,91 +389,107 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
       step_barrier();
     }
   };
-  f32x4 acc[FR][FT];
+  typedef Int<kTwo ? (NS - 1) * kLoads : (NS - 2) * kLoads> Younger;
+  f32x16 acc[FR][FT];
 #pragma unroll
   for (int i = 0; i < FR; ++i)
 #pragma unroll
-    for (int j = 0; j < FT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < FT; ++j) acc[i][j] = f32x16{};
   // neighbouring waves, on different SIMDs, share their rows of x; those past a partial tile's last
   // row only help to load
-  const int wm = (wave % WR) * FR * kMfma, wn = (wave / WR) * FT * kMfma;
+  const int wm = (wave % WR) * FR * kBig, wn = (wave / WR) * FT * kBig;
   const bool busy = wn < nt;
-  const int l = lane & 15, q = lane >> 4;
-  const int p0 = ((2 * q) ^ piece_turn(l)) * 16, p1 = p0 ^ 16;
-  auto read = [&](const uint8_t* p) __attribute__((always_inline)) {
-    return frag<WIDE>(*reinterpret_cast<const u32x4*>(p + p0), *reinterpret_cast<const u32x4*>(p + p1));
+  const int l = lane & 31, q = lane >> 5;
+  // the first piece of a lane's half fragment s: pieces 4 s + 2 q and the next
+  const int p0 = ((2 * q) ^ piece_turn(l)) * 16;
+  auto read = [&](const uint8_t* row, int s) __attribute__((always_inline)) {
+    return frag<WIDE>(*reinterpret_cast<const u32x4*>(row + (p0 ^ (64 * s))),
+                      *reinterpret_cast<const u32x4*>(row + (p0 ^ (64 * s + 16))));
   };
   auto walk = [&](auto with_products) __attribute__((always_inline)) {
     constexpr bool kMul = decltype(with_products)::value != 0;
-    Frag<WIDE> xf[FT], wf[2];
-    f32x4 p[FT];                                 // sums of the fragment of weights before
-    float f[FT], last[FT];                       // factors of this step and of the one before
+    constexpr int G = 2 * FR;                    // half fragments of weights: fragment g / 2, half g % 2
+    Frag<WIDE> xf[FT][2], wf[2];
+    f32x16 p[FT];                                // a fragment of weights' sums over the block
+    float f[FT], sx[FT], fw = 0.0f;              // factors of the block; scales of the next step's
 #pragma unroll
     for (int s = 0; s < NS; ++s)
 #pragma unroll
       for (int n = 0; n < kLoads; ++n) load(s, first + s, n);
-    arrive(0, first, 0);
+    arrive(Int<(NS - 1) * kLoads>(), 0, first, 0);
+    auto scales = [&](const uint8_t* stage) __attribute__((always_inline)) {
+      const float* sb = reinterpret_cast<const float*>(stage + kW + kX);
+      fw = sb[kXWaves * kWave + wm / kFp8Block];
+#pragma unroll
+      for (int j = 0; j < FT; ++j) sx[j] = sb[wn + j * kBig + l];
+    };
     if (kMul) {
+      scales(lds);
 #pragma unroll
       for (int j = 0; j < FT; ++j) {
-        xf[j] = read(lds + kW + (wn + j * kMfma + l) * 128);
-        p[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        last[j] = 0.0f;
+        xf[j][0] = read(lds + kW + (wn + j * kBig + l) * 128, 0);
+        xf[j][1] = read(lds + kW + (wn + j * kBig + l) * 128, 1);
+        p[j] = f32x16{};
+        f[j] = 0.0f;
       }
-      wf[0] = read(lds + (wm + l) * 128);
+      wf[0] = read(lds + (wm + l) * 128, 0);
+      wf[1] = read(lds + (wm + l) * 128, 1);
     }
     int slot = 0;
     for (int kt = first; kt < steps; ++kt) {
       const int next = slot + 1 == NS ? 0 : slot + 1;
       const uint8_t* wb = lds + slot * kStage + (wm + l) * 128;
       const uint8_t* nb = lds + next * kStage;
-      const float* sb = reinterpret_cast<const float*>(lds + slot * kStage + kW + kX);
-      if (kMul) {
-        const float fw = sb[kXWaves * kWave + wm / kFp8Block];
 #pragma unroll
-        for (int j = 0; j < FT; ++j) f[j] = sb[wn + j * kMfma + l] * fw;
-      }
-#pragma unroll
-      for (int i = 0; i < FR; ++i) {
-        if (i == FR / 2 - 1) arrive(slot, kt, 1);            // A
-        if (i == FR - 1) arrive(next, kt + 1, 0);            // B
+      for (int g = 0; g < G; ++g) {
+        constexpr int kPointA = kTwo ? 2 * kFirst - 2 : -1, kPointB = G - 2;
+        if (g == kPointA) arrive(Younger(), slot, kt, 1);
+        if (g == kPointB) arrive(Younger(), next, kt + 1, 0);
         if (kMul) {
-          wf[(i + 1) & 1] = read(i + 1 < FR ? wb + (i + 1) * kMfma * 128 : nb + (wm + l) * 128);
+          const int i = g / 2, s = g % 2;
 #pragma unroll
           for (int j = 0; j < FT; ++j) {
-            f32x4& sum = acc[i > 0 ? i - 1 : FR - 1][j];
-            sum += p[j] * (i > 0 ? f[j] : last[j]);
-            asm volatile("" : "+v"(sum));        // here, not behind the barriers that follow
-            p[j] = block_sum<WIDE>(wf[i & 1], xf[j]);
-            if (i == FR - 1) xf[j] = read(nb + kW + (wn + j * kMfma + l) * 128);
+            if (s == 0) {
+              // the sums of the fragment before; its factors are the step before's for the last one
+              f32x16& sum = acc[i > 0 ? i - 1 : FR - 1][j];
+              sum += p[j] * f[j];
+              asm volatile("" : "+v"(sum));      // here, not behind the barriers that follow
+              if (i == 0) f[j] = sx[j] * fw;
+              p[j] = half_sum<WIDE>(wf[0], xf[j][0], f32x16{});
+            } else {
+              p[j] = half_sum<WIDE>(wf[1], xf[j][1], p[j]);
+            }
+            if (g >= kPointB) xf[j][s] = read(nb + kW + (wn + j * kBig + l) * 128, s);
           }
+          wf[s] = g + 2 < G ? read(wb + (i + 1) * kBig * 128, s) : read(nb + (wm + l) * 128, s);
+          if (g == G - 1) scales(nb);
         }
-        // after A: part A of the step NS later, after B of the step before: its part B
-        if (i >= FR / 2 - 1 && i < FR - 1) loads(slot, kt + NS, 0, kA, i - (FR / 2 - 1), FR / 2);
-        else if (i == FR - 1) loads(slot, kt + NS, kA, kLoads, 0, 1);
+        if (kTwo) {
+          // after A: part A of the step NS later; after B: its part B
+          if (g >= kPointA && g < kPointB) loads(slot, kt + NS, 0, kA, g - kPointA, kPointB - kPointA);
+          if (g >= kPointB) loads(slot, kt + NS, kA, kLoads, g - kPointB, 2);
+        } else {
+          loads(slot, kt + NS, 0, kLoads, g, 2);
+        }
         __builtin_amdgcn_sched_barrier(0);
-      }
-      if (kMul) {
-#pragma unroll
-        for (int j = 0; j < FT; ++j) last[j] = f[j];
       }
       slot = next;
     }
     if (kMul) {
 #pragma unroll
-      for (int j = 0; j < FT; ++j) acc[FR - 1][j] += p[j] * last[j];
+      for (int j = 0; j < FT; ++j) acc[FR - 1][j] += p[j] * f[j];
     }
   };
   if (busy) walk(Int<1>());
   else walk(Int<0>());
   wait_loads<0>();
   step_barrier();
-  store_tile<FR, FT>(a, part, acc, &lds[0] + wave * tile_bytes<FR, FT>(), t0 + wn, t1, r0 + wm);
+  store_big<FR, FT>(a, (int)part, acc, &lds[0] + wave * kResult, t0 + wn, t1, r0 + wm);
 }
 
 template <int WR, int WT, int FR, int FT, int NS, bool WIDE>
 hipError_t tile_fp8(MatmulArgs a, hipStream_t stream) {
-  constexpr int BM = WR * FR * kMfma, BN = WT * FT * kMfma;
+  constexpr int BM = WR * FR * kBig, BN = WT * FT * kBig;
   a.row_blocks = (a.R + BM - 1) / BM;
   a.blocks = a.row_blocks * token_tiles(a, BN) * a.split;
   hipLaunchKernelGGL((tile_fp8_kernel<WR, WT, FR, FT, NS, WIDE>), grid_of(a.blocks),
@@ -432,12 +501,12 @@ template <bool WIDE>
 hipError_t tile_fp8_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
   switch (p.bn) {
     case 64:
-      return p.bm == 64 ? tile_fp8<1, 4, 4, 1, 3, WIDE>(a, stream) : tile_fp8<2, 2, 4, 2, 3, WIDE>(a, stream);
-    case 128: return tile_fp8<2, 2, 4, 4, 2, WIDE>(a, stream);
+      return p.bm == 64 ? tile_fp8<2, 2, 1, 1, 4, WIDE>(a, stream) : tile_fp8<2, 2, 2, 1, 3, WIDE>(a, stream);
+    case 128: return tile_fp8<2, 2, 2, 2, 2, WIDE>(a, stream);
     default:
       // fragments of bf16 numbers leave no registers for more
-      if constexpr (WIDE) return tile_fp8<2, 2, 4, 4, 2, WIDE>(a, stream);
-      else return tile_fp8<2, 4, 8, 4, 2, WIDE>(a, stream);
+      if constexpr (WIDE) return tile_fp8<2, 2, 2, 2, 2, WIDE>(a, stream);
+      else return tile_fp8<2, 4, 4, 2, 2, WIDE>(a, stream);
   }
 }
 

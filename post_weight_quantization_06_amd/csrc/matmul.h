@@ -163,12 +163,43 @@ __device__ __forceinline__ void store_part(const MatmulArgs& a, int part, int64_
   else *reinterpret_cast<f32x4*>(a.parts + ((int64_t)part * a.T + t) * part_row(a.R) + r) = v;
 }
 
-// A wave's result, FR * 16 weight rows by FT * 16 rows of x, into y. A lane holds four neighbours of
-// 16 rows of x at a time, 32 bytes of a row together in 16 bits; through `lds` (tile_bytes, this
-// wave's own) a row's FR * 32 bytes go out together, 16 a lane (4096 x 14336 x 4096 in MXFP4, all of
-// the call: 164 us with, 177 without). Parts and fp32 leave directly, 64 bytes of a row together.
+// A wave's result of KT rows of x by KR weight rows in 16 bits, gathered in `lds` (row_bytes a row), into
+// y: a row's KR * 2 bytes go out together, 16 a lane (4096 x 14336 x 4096 in MXFP4, all of the call: 164 us
+// with, 177 with the lanes' own 8 bytes each).
+template <int KR>
+constexpr int row_bytes() { return KR * 2 + 16; }
+template <int KR, int KT>
+__device__ __forceinline__ void store_rows(const MatmulArgs& a, const uint8_t* lds, int64_t t0, int64_t t1,
+                                           int64_t r0) {
+  constexpr int kLanes = KR / 8;                 // 16-byte pieces of a row
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t r = r0 + 8 * (lane % kLanes);
+  uint16_t* y = static_cast<uint16_t*>(a.y) + r;
+  for (int k = lane / kLanes; k < KT; k += kWave / kLanes) {
+    if (t0 + k >= t1) break;
+    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + k * row_bytes<KR>() + 16 * (lane % kLanes));
+    uint16_t* p = y + (t0 + k) * a.ldy;
+    if (r + 8 <= a.R) {
+      // results larger than the L2s together are not kept there
+      if (a.y_row == 2) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+      else *reinterpret_cast<u32x4*>(p) = v;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        if (r + c < a.R) p[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
+    }
+  }
+}
+__device__ __forceinline__ uint2 pack_16(const MatmulArgs& a, f32x4 v) {
+  return a.y_type == AAAC_BF16 ? make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w))
+                               : make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
+}
+
+// A wave's result, FR * 16 weight rows by FT * 16 rows of x, into y, in 16 bits through `lds`
+// (tile_bytes, this wave's own). A lane holds four neighbours of 16 rows of x at a time. Parts and fp32
+// leave directly, 64 bytes of a row together.
 template <int FR, int FT>
-constexpr int tile_bytes() { return FT * kMfma * (FR * 32 + 16); }
+constexpr int tile_bytes() { return FT * kMfma * row_bytes<FR * kMfma>(); }
 template <int FR, int FT>
 __device__ __forceinline__ void store_tile(const MatmulArgs& a, int part, const f32x4 (&acc)[FR][FT],
                                            uint8_t* lds, int64_t t0, int64_t t1, int64_t r0) {
@@ -186,32 +217,13 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, int part, const 
     }
     return;
   }
-  constexpr int kRow = FR * 32 + 16, kLanes = FR * 2;        // bytes and 16-byte pieces of a row
 #pragma unroll
   for (int j = 0; j < FT; ++j)
 #pragma unroll
-    for (int i = 0; i < FR; ++i) {
-      const f32x4 v = acc[i][j];
-      const uint2 w = a.y_type == AAAC_BF16 ? make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w))
-                                            : make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
-      *reinterpret_cast<uint2*>(lds + (j * kMfma + l) * kRow + i * 32 + q * 8) = w;
-    }
-  const int64_t r = r0 + 8 * (lane % kLanes);
-  uint16_t* y = static_cast<uint16_t*>(a.y) + r;
-  for (int k = lane / kLanes; k < FT * kMfma; k += kWave / kLanes) {
-    if (t0 + k >= t1) break;
-    const u32x4 v = *reinterpret_cast<const u32x4*>(lds + k * kRow + 16 * (lane % kLanes));
-    uint16_t* p = y + (t0 + k) * a.ldy;
-    if (r + 8 <= a.R) {
-      // results larger than the L2s together are not kept there
-      if (a.y_row == 2) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
-      else *reinterpret_cast<u32x4*>(p) = v;
-    } else {
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (r + c < a.R) p[c] = (uint16_t)(v[c >> 1] >> (16 * (c & 1)));
-    }
-  }
+    for (int i = 0; i < FR; ++i)
+      *reinterpret_cast<uint2*>(lds + (j * kMfma + l) * row_bytes<FR * kMfma>() + i * 32 + q * 8) =
+          pack_16(a, acc[i][j]);
+  store_rows<FR * kMfma, FT * kMfma>(a, lds, t0, t1, r0);
 }
 
 // Workgroups go to the eight dies in turn. Renumbered so that a die gets runs of kRun consecutive
