@@ -972,6 +972,33 @@ def aaac_fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, 
             x.data_ptr(), xt, xs, Tx, ldx, T, y.data_ptr(), yt, ldy, wp, wn)
 
 
+def _route_inputs(logits: torch.Tensor, bias, score: str):
+    """(device, type, T, E, row stride) after the checks of a routing's inputs."""
+    what = "aaac_route"
+    dev = _on_gpu(what, logits, bias)
+    _no_grad(what, logits)
+    lt = _float_type(logits, "logits")
+    T, E, ldl = _rows(logits, "logits")
+    if score not in SCORES:
+        raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
+    if bias is not None:
+        _no_grad(what, bias)
+        _f32(bias, "bias", E)
+    return dev, lt, T, E, ldl
+
+
+def _route(inputs, logits, k, experts, weights, offsets, rows, places, score, bias, groups, top_groups,
+           group_top, renormalize, scale, ws=None, stream=None):
+    dev, lt, T, E, ldl = inputs
+    need = (_lib or load()).aaac_route_workspace_bytes(T, E)
+    ws, wp, wn = _own_ws(need, ws, logits, stream, "aaac_route")
+    _launch("aaac_route", dev, stream, logits.data_ptr(), lt, T, E, ldl,
+            None if bias is None else bias.data_ptr(), SCORES[score], k, groups,
+            groups if top_groups is None else top_groups, group_top, bool(renormalize), scale,
+            experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
+            places.data_ptr(), wp, wn)
+
+
 def aaac_route(logits: torch.Tensor, k: int, experts: torch.Tensor, weights: torch.Tensor,
                offsets: torch.Tensor, rows: torch.Tensor, places: torch.Tensor,
                score: str = "softmax", bias: Optional[torch.Tensor] = None, groups: int = 1,
@@ -979,29 +1006,15 @@ def aaac_route(logits: torch.Tensor, k: int, experts: torch.Tensor, weights: tor
                scale: float = 1.0, ws: Optional[torch.Tensor] = None, stream=None):
     """Routing of logits [T, E] (bf16, fp16 or fp32, any row stride) into experts int32 [T, k], weights
     fp32 [T, k], offsets int32 [E + 1], rows int32 [T k] and places int32 [T, k] (see aaac.h)."""
-    what = "aaac_route"
-    dev = _on_gpu(what, logits, experts, weights, offsets, rows, places, bias, ws)
-    _no_grad(what, logits)
-    if bias is not None:
-        _no_grad(what, bias)
-    lt = _float_type(logits, "logits")
-    T, E, ldl = _rows(logits, "logits")
-    if score not in SCORES:
-        raise ValueError("score must be 'softmax' or 'sigmoid' (got %r)" % (score,))
-    if bias is not None:
-        _f32(bias, "bias", E)
-    _i32(experts, "experts", T * k)
+    _on_gpu("aaac_route", logits, experts, weights, offsets, rows, places, bias, ws)
+    inputs = _route_inputs(logits, bias, score)
+    T, E = inputs[2:4]
+    for t, name in ((experts, "experts"), (rows, "rows"), (places, "places")):
+        _i32(t, name, T * k)
     _f32(weights, "weights", T * k)
     _i32(offsets, "offsets", E + 1)
-    _i32(rows, "rows", T * k)
-    _i32(places, "places", T * k)
-    need = int((_lib or load()).aaac_route_workspace_bytes(T, E))
-    ws, wp, wn = _own_ws(need, ws, logits, stream, what)
-    _launch(what, dev, stream, logits.data_ptr(), lt, T, E, ldl,
-            None if bias is None else bias.data_ptr(), SCORES[score], k, groups,
-            groups if top_groups is None else top_groups, group_top, int(renormalize), scale,
-            experts.data_ptr(), weights.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-            places.data_ptr(), wp, wn)
+    _route(inputs, logits, k, experts, weights, offsets, rows, places, score, bias, groups, top_groups,
+           group_top, renormalize, scale, ws, stream)
 
 
 def _any_rows(t: torch.Tensor, name: str):

@@ -568,10 +568,13 @@ bool fp8_query_args(int64_t E, int64_t R, int64_t C, int64_t T, MatmulArgs& a) {
 }
 
 // Where an FP8 product's workspace holds what: the parts of split sums, then quantized rows of x (codes
-// [Tx, Cp], zeros past C, and scales a block at a time, [Cp / 128, Tx]).
+// [Tx, Cp], zeros past C, and scales a block at a time, [Cp / 128, Tx]) where the product does not
+// quantize them itself.
 MatmulWs fp8_matmul_ws(const MatmulArgs& a, int64_t Tx, bool quantize) {
   MatmulWs w;
-  const size_t parts = parts_bytes(a, plan_matmul(a, kFp8, true));
+  const MatmulPlan p = plan_matmul(a, kFp8, true);
+  const size_t parts = parts_bytes(a, p);
+  quantize = quantize && !p.quantize;
   w.codes = (parts + 255) / 256 * 256;
   w.scales = w.codes + (size_t)Tx * (size_t)a.Cp;
   w.bytes = quantize ? w.scales + (size_t)Tx * (size_t)(a.Cp / kFp8Block) * sizeof(float) : parts;
@@ -1085,15 +1088,18 @@ aaac_status aaac_fp8_matmul(const uint8_t* w_codes, int64_t ldw, const float* w_
   a.x_blocks = x_scales;
   a.xs_row = fp8_blocks(C);
   a.xs_blk = 1;
-  if (ws || quantize) {
-    const MatmulWs w = fp8_matmul_ws(a, Tx, quantize);
+  a.x_type = x_type;
+  const MatmulPlan p = plan_matmul(a, kFp8, ws != nullptr);
+  const bool first = quantize && !p.quantize;    // x is quantized by a kernel of its own
+  if (ws || first) {
+    const MatmulWs w = fp8_matmul_ws(a, Tx, first);
     if (!ws || !aligned(ws, 256))
       return fail(AAAC_ERR_INVALID_ARG, "%s: ws null or not 256-byte aligned", who);
     if (ws_bytes < w.bytes)
       return fail(AAAC_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", who, ws_bytes,
                   w.bytes);
     a.parts = static_cast<float*>(ws);
-    if (quantize) {
+    if (first) {
       uint8_t* codes = static_cast<uint8_t*>(ws) + w.codes;
       float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + w.scales);
       const hipError_t e = launch_fp8_quantize(x, x_type, 1, Tx, C, ldx, 0, false, codes, a.Cp, a.Cp,
@@ -1104,9 +1110,10 @@ aaac_status aaac_fp8_matmul(const uint8_t* w_codes, int64_t ldw, const float* w_
       a.x_blocks = scales;
       a.xs_row = 1;
       a.xs_blk = Tx;
+      a.x_type = AAAC_FP8;
     }
   }
-  return hip_status(launch_matmul(a, kFp8, plan_matmul(a, kFp8, ws != nullptr), s), who);
+  return hip_status(launch_matmul(a, kFp8, p, s), who);
 }
 
 size_t aaac_route_workspace_bytes(int64_t T, int64_t E) {

@@ -9,6 +9,7 @@
 // Both directions move each byte once and are bound by memory.
 #include "aaac.h"
 #include "fp8.h"
+#include "fp8_encode.h"
 
 namespace aaac {
 
@@ -17,103 +18,11 @@ namespace {
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kLane = 16;                        // columns a lane: eight lanes make a block
 constexpr int kSteps = 2;                        // lane pieces in flight per thread
-
-template <int TYPE> struct Elem;
-template <> struct Elem<AAAC_BF16> { typedef uint16_t T; };
-template <> struct Elem<AAAC_F16> { typedef uint16_t T; };
-template <> struct Elem<AAAC_F32> { typedef uint32_t T; };
-
-template <int TYPE>
-__device__ __forceinline__ float to_f32(typename Elem<TYPE>::T v) {
-  if (TYPE == AAAC_F32) return __uint_as_float((uint32_t)v);
-  if (TYPE == AAAC_BF16) return __uint_as_float((uint32_t)v << 16);
-  return (float)__builtin_bit_cast(_Float16, (uint16_t)v);
-}
-
-// Sixteen consecutive elements as fp32; those at or past `valid` read as zero. VEC: p is aligned to 16
-// bytes.
-template <int TYPE, bool VEC>
-__device__ __forceinline__ void load16(const typename Elem<TYPE>::T* p, int valid, float (&v)[kLane]) {
-  typedef typename Elem<TYPE>::T T;
-  if (valid < kLane) {
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) v[i] = i < valid ? to_f32<TYPE>(p[i]) : 0.0f;
-    return;
-  }
-  constexpr int kWords = kLane * sizeof(T) / 16;
-  u32x4 w[kWords];
-#pragma unroll
-  for (int i = 0; i < kWords; ++i) {
-    if (VEC) w[i] = reinterpret_cast<const u32x4*>(p)[i];
-    else __builtin_memcpy(&w[i], reinterpret_cast<const uint8_t*>(p) + 16 * i, 16);
-  }
-#pragma unroll
-  for (int i = 0; i < kLane; ++i) {
-    if (sizeof(T) == 4) v[i] = __uint_as_float(w[i >> 2][i & 3]);
-    else v[i] = to_f32<TYPE>((T)(w[i >> 3][(i >> 1) & 3] >> (16 * (i & 1))));
-  }
-}
-
-__device__ __forceinline__ uint32_t top_bits(const float (&v)[kLane]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kLane; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-  return top;
-}
-
-__device__ __forceinline__ float scale_of(uint32_t top) {
-  if (top >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
-  return fmaxf(__uint_as_float(top) / 448.0f, 0x1p-126f);
-}
-
-// The codes of sixteen elements. Their quotients are the correctly rounded ones: with r the rounded
-// reciprocal of the scale, x r is within two units of the quotient, one correction by its remainder
-// brings it within one and the second one rounds it correctly (Markstein). Scales so small that a
-// remainder may underflow are divided by.
-__device__ __forceinline__ u32x4 encode16(const float (&v)[kLane], float scale) {
-  float q[kLane];
-  if (scale >= 0x1p-80f) {
-    const float r = 1.0f / scale;
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) {
-      float u = v[i] * r;
-      u = __builtin_fmaf(__builtin_fmaf(-u, scale, v[i]), r, u);
-      q[i] = __builtin_fmaf(__builtin_fmaf(-u, scale, v[i]), r, u);
-      // a zero keeps its sign
-      q[i] = v[i] == 0.0f ? v[i] : q[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < kLane; ++i) q[i] = v[i] / scale;
-  }
-  u32x4 w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    int p = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i], q[4 * i + 1], 0, false);
-    p = __builtin_amdgcn_cvt_pk_fp8_f32(q[4 * i + 2], q[4 * i + 3], p, true);
-    w[i] = (uint32_t)p;
-  }
-  // no number: the scale of a block with an infinity or a NaN
-  if (!(scale == scale)) w = u32x4{0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
-  return w;
-}
 
 __device__ __forceinline__ int64_t divide(int64_t i, int64_t n, int64_t total) {
   return total <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)n) : i / n;
-}
-
-// Codes past a row's last column are zeros, of a NaN block too.
-__device__ __forceinline__ u32x4 keep_first(u32x4 w, int valid) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = valid - 4 * i;
-    if (n < 4) w[i] = n <= 0 ? 0u : w[i] & ((1u << (8 * n)) - 1u);
-  }
-  return w;
 }
 
 // Blocks of 1 x 128: eight neighbouring lanes hold a block.
@@ -140,9 +49,9 @@ __global__ __launch_bounds__(kBlock) void fp8_quantize_rows_kernel(
     const float s = scale_of(block_max_u32_t<8>(top_bits(v[u]), 8));
     const int64_t left = C - col[u];
     if (col[u] < Cw) {
-      u32x4 w = encode16(v[u], s);
+      Words4 w = encode16(v[u], s);
       if (left < kLane) w = keep_first(w, (int)left);
-      *reinterpret_cast<u32x4*>(codes + row[u] * ldq + col[u]) = w;
+      *reinterpret_cast<Words4*>(codes + row[u] * ldq + col[u]) = w;
     }
     if ((threadIdx.x & 7) == 0) scales[row[u] * s_row + col[u] / kFp8Block * s_blk] = s;
   }
@@ -182,9 +91,9 @@ __global__ __launch_bounds__(kBlock) void fp8_quantize_tiles_kernel(
   for (int u = 0; u < kEach; ++u) {
     const int64_t r = row0 + u * kRows;
     if (r >= M) break;
-    u32x4 w = encode16(v[u], s);
+    Words4 w = encode16(v[u], s);
     if (valid < kLane) w = keep_first(w, valid);
-    *reinterpret_cast<u32x4*>(codes + (e * M + r) * ldq + col) = w;
+    *reinterpret_cast<Words4*>(codes + (e * M + r) * ldq + col) = w;
   }
 }
 
@@ -193,7 +102,7 @@ template <int TYPE, bool VEC>
 __device__ __forceinline__ void store16(typename Elem<TYPE>::T* p, int valid, const float (&v)[kLane]) {
   typedef typename Elem<TYPE>::T T;
   constexpr int kWords = kLane * sizeof(T) / 16;
-  u32x4 w[kWords];
+  Words4 w[kWords];
 #pragma unroll
   for (int i = 0; i < kLane * (int)sizeof(T) / 4; ++i) {
     if (TYPE == AAAC_F32) {
@@ -208,7 +117,7 @@ __device__ __forceinline__ void store16(typename Elem<TYPE>::T* p, int valid, co
   if (valid == kLane) {
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
-      if (VEC) reinterpret_cast<u32x4*>(p)[i] = w[i];
+      if (VEC) reinterpret_cast<Words4*>(p)[i] = w[i];
       else __builtin_memcpy(reinterpret_cast<uint8_t*>(p) + 16 * i, &w[i], 16);
     }
     return;
@@ -230,7 +139,7 @@ __global__ __launch_bounds__(kBlock) void fp8_dequant_kernel(
     int64_t ldy) {
   const int64_t i0 = block_id() * (kBlock * kSteps) + threadIdx.x;
   const int64_t cb = fp8_blocks(C), rb = (M + per - 1) / per;
-  u32x4 w[kSteps];
+  Words4 w[kSteps];
   float s[kSteps];
   int64_t row[kSteps], col[kSteps];
 #pragma unroll
@@ -242,10 +151,10 @@ __global__ __launch_bounds__(kBlock) void fp8_dequant_kernel(
     const uint8_t* p = codes + row[u] * ldq + col[u];
     const int64_t left = C - col[u];
     if (left >= kLane) {
-      if (CV) w[u] = *reinterpret_cast<const u32x4*>(p);
+      if (CV) w[u] = *reinterpret_cast<const Words4*>(p);
       else __builtin_memcpy(&w[u], p, 16);
     } else {
-      w[u] = u32x4{0u, 0u, 0u, 0u};
+      w[u] = Words4{0u, 0u, 0u, 0u};
 #pragma unroll
       for (int k = 0; k < kLane; ++k)
         if (k < left) w[u][k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));

@@ -7,6 +7,7 @@
 // columns, and in the result four neighbouring weight rows of x row l & 15; a sum does not depend on
 // which lane holds which columns.
 #include "fp8.h"
+#include "fp8_encode.h"
 #include "matmul.h"
 
 namespace aaac {
@@ -51,18 +52,12 @@ __device__ __forceinline__ i32x8 operand(const Frag<false>& f) {
                (int)f.v[1].x, (int)f.v[1].y, (int)f.v[1].z, (int)f.v[1].w};
 }
 
-// The sum over a block.
-template <bool WIDE>
-__device__ __forceinline__ f32x4 block_sum(const Frag<WIDE>& w, const Frag<WIDE>& x) {
+// The sum over a block by the bf16 instruction.
+__device__ __forceinline__ f32x4 block_sum(const Frag<true>& w, const Frag<true>& x) {
   f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-  if constexpr (WIDE) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c = mfma_bf16(w.v[i], x.v[i], c);
-    return c;
-  } else {
-    // e4m3 on both sides, no scales (zeros select the instruction without)
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(x), c, 0, 0, 0, 0, 0, 0);
-  }
+  for (int i = 0; i < 4; ++i) c = mfma_bf16(w.v[i], x.v[i], c);
+  return c;
 }
 
 // A 16-byte piece without its bytes at or past `valid`.
@@ -85,11 +80,45 @@ __device__ __forceinline__ int64_t x_row(const MatmulArgs& a, int64_t t) {
 // ------------------------------------------------------------------------------------------------
 // Few rows of x per matrix: the weights are read once, straight into registers, and bound the time.
 // A workgroup owns RT * 16 rows of one expert's matrix and up to NT * 16 rows of x; its waves take the
-// blocks of columns in turn and add their sums in wave order through LDS.
+// blocks of columns in turn, U at a time, the next U or 2 U on their way while these are multiplied, and add
+// their sums in wave order through LDS.
+// QUANTIZE: x is bf16, fp16 or fp32. Its rows are quantised into LDS, eight lanes a block, while the first
+// weights are on their way; the same codes and scales that the quantiser writes.
 // ------------------------------------------------------------------------------------------------
-template <int RT, int NT, int W>
+constexpr int few_x_bytes(int64_t C) { return (int)(fp8_blocks(C) * kFp8Block + 16); }   // of a row in LDS
+
+// meanwhile: called once the thread's first elements are on their way (loads return in order, so what it
+// loads does not hold them up).
+template <int TYPE, class F>
+__device__ __forceinline__ void quantize_rows(const MatmulArgs& a, int64_t t0, int nt, int cb, uint8_t* codes,
+                                              int row_bytes, float* scales, int threads, F meanwhile) {
+  typedef typename Elem<TYPE>::T T;
+  const int per_row = cb * (kFp8Block / kLane);
+  float v[kLane];
+  auto load = [&](int i) __attribute__((always_inline)) {
+    if (i >= nt * per_row) return;
+    const int row = i / per_row, col = (i - row * per_row) * kLane, left = (int)a.C - col;
+    const int64_t x = x_row(a, t0 + row);
+    load16<TYPE, false>(static_cast<const T*>(a.x) + (x < 0 ? 0 : x) * a.ldx + col,
+                        x < 0 || left < 0 ? 0 : left > kLane ? kLane : left, v);
+  };
+  load(threadIdx.x);
+  meanwhile();
+  for (int i = threadIdx.x; i < nt * per_row; i += threads) {
+    const int row = i / per_row, col = (i - row * per_row) * kLane, left = (int)a.C - col;
+    if (i >= threads) load(i);
+    const float s = scale_of(block_max_u32_t<8>(top_bits(v), 8));
+    Words4 w = encode16(v, s);
+    if (left < kLane) w = keep_first(w, left);
+    *reinterpret_cast<Words4*>(codes + row * row_bytes + col) = w;
+    if ((threadIdx.x & 7) == 0) scales[row * cb + col / kFp8Block] = s;
+  }
+}
+
+template <int RT, int NT, int W, bool QUANTIZE>
 __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
-  constexpr int U = 4;                           // blocks in flight
+  constexpr int U = RT + NT > 2 ? 2 : 4;         // two groups' weights fit the registers
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
   const int64_t id = block_id(), tile = id / a.row_blocks, rb = id % a.row_blocks;
   int e;
@@ -97,7 +126,7 @@ __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
   if (!find_tile(a.offsets, a.E, a.T, NT * kMfma, tile, e, t0, t1)) return;
   const int64_t r0 = rb * (RT * kMfma);
   const int l = lane & 15, q = lane >> 4;
-  const int64_t cb = fp8_blocks(a.C);
+  const int cb = (int)fp8_blocks(a.C), whole = (int)(a.C / kFp8Block);
   const uint8_t* wp[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
@@ -106,96 +135,128 @@ __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
   }
   const float* sw = static_cast<const float*>(a.scales) +
                     ((int64_t)e * fp8_blocks(a.R) + r0 / kFp8Block) * cb;
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  // lane group q takes the 16-byte pieces q and q + 4 of a block: 64 neighbouring bytes of a row a load.
+  // The row's last, short block keeps the columns that exist.
+  typedef u32x4 Group[U][RT][2];
+  auto load = [&](Group& w, int b0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < U; ++n) {
+      const int b = b0 + n * W;
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const u32x4* p = reinterpret_cast<const u32x4*>(wp[i] + (int64_t)b * kFp8Block + 64 * h);
+          w[n][i][h] = zero;
+          if (b < whole) {
+            w[n][i][h] = *p;
+          } else if (b < cb) {
+            const int left = (int)a.C - b * kFp8Block - 64 * h - 16 * q;
+            if (left > 0) w[n][i][h] = first_bytes(*p, left < 16 ? left : 16);
+          }
+        }
+    }
+  };
+  Group w[2];
+  const int nt = (int)(t1 - t0 < NT * kMfma ? t1 - t0 : NT * kMfma);
+  const int row_bytes = few_x_bytes(a.C);
   const uint8_t* xp[NT];
   const float* sx[NT];
   bool in[NT];
+  int64_t xs_blk = 1;
+  if constexpr (QUANTIZE) {
+    uint8_t* codes = smem;
+    float* scales = reinterpret_cast<float*>(smem + a.x_rows * row_bytes);
+    auto first = [&]() __attribute__((always_inline)) { load(w[0], wave); };
+    constexpr int kThreads = W * kWave;
+    if (a.x_type == AAAC_BF16)
+      quantize_rows<AAAC_BF16>(a, t0, nt, cb, codes, row_bytes, scales, kThreads, first);
+    else if (a.x_type == AAAC_F16)
+      quantize_rows<AAAC_F16>(a, t0, nt, cb, codes, row_bytes, scales, kThreads, first);
+    else
+      quantize_rows<AAAC_F32>(a, t0, nt, cb, codes, row_bytes, scales, kThreads, first);
+    load(w[1], wave + U * W);
+    step_barrier();                              // does not wait for the weights
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t t = t0 + j * kMfma + l, x = t < t1 ? x_row(a, t) : -1;
-    in[j] = x >= 0;
-    xp[j] = static_cast<const uint8_t*>(a.x) + (in[j] ? x : 0) * a.ldx + 16 * q;
-    sx[j] = a.x_blocks + (in[j] ? x : 0) * a.xs_row;
+    for (int j = 0; j < NT; ++j) {
+      const int t = j * kMfma + l;
+      in[j] = t < nt;
+      xp[j] = codes + (in[j] ? t : 0) * row_bytes + 16 * q;
+      sx[j] = scales + (in[j] ? t : 0) * cb;
+    }
+  } else {
+    load(w[0], wave);
+    load(w[1], wave + U * W);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int64_t t = t0 + j * kMfma + l, x = t < t1 ? x_row(a, t) : -1;
+      in[j] = x >= 0;
+      xp[j] = static_cast<const uint8_t*>(a.x) + (in[j] ? x : 0) * a.ldx + 16 * q;
+      sx[j] = a.x_blocks + (in[j] ? x : 0) * a.xs_row;
+    }
+    xs_blk = a.xs_blk;
   }
   f32x4 acc[RT][NT];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const u32x4 zero = {0u, 0u, 0u, 0u};
-  auto multiply = [&](const u32x4 (&w)[RT][2], const u32x4 (&x)[NT][2], const float (&f)[NT])
-      __attribute__((always_inline)) {
-    Frag<true> xf[NT];
+  auto multiply = [&](const Group& w, int b0) __attribute__((always_inline)) {
+    u32x4 x[U][NT][2];
+    float f[U][NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) xf[j] = frag<true>(x[j][0], x[j][1]);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const Frag<true> wf = frag<true>(w[i][0], w[i][1]);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) acc[i][j] += block_sum<true>(wf, xf[j]) * f[j];
-    }
-  };
-  // lane group q takes the 16-byte pieces q and q + 4 of a block: 64 neighbouring bytes of a row a load
-  auto blocks = [&](int64_t b0, auto count, auto step) __attribute__((always_inline)) {
-    constexpr int N = decltype(count)::value;
-    u32x4 w[N][RT][2], x[N][NT][2];
-    float fw[N], fx[N][NT];
-#pragma unroll
-    for (int n = 0; n < N; ++n) {
-      const int64_t b = b0 + n * decltype(step)::value;
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          w[n][i][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wp[i] + b * kFp8Block + 64 * h));
+    for (int n = 0; n < U; ++n) {
+      const int b = b0 + n * W;
+      const float fw = b < cb ? sw[b] : 0.0f;
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          x[n][j][h] = in[j] ? *reinterpret_cast<const u32x4*>(xp[j] + b * kFp8Block + 64 * h) : zero;
-        fx[n][j] = in[j] ? sx[j][b * a.xs_blk] : 0.0f;
+        for (int h = 0; h < 2; ++h) {
+          const u32x4* p = reinterpret_cast<const u32x4*>(xp[j] + (int64_t)b * kFp8Block + 64 * h);
+          x[n][j][h] = zero;
+          if (QUANTIZE ? b < cb : b < whole) {
+            if (in[j]) x[n][j][h] = *p;
+          } else if (b < cb) {
+            const int left = (int)a.C - b * kFp8Block - 64 * h - 16 * q;
+            if (left > 0 && in[j]) x[n][j][h] = first_bytes(*p, left < 16 ? left : 16);
+          }
+        }
+        f[n][j] = b < cb && in[j] ? sx[j][b * xs_blk] * fw : 0.0f;
       }
-      fw[n] = sw[b];
     }
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-      float f[NT];
+    for (int n = 0; n < U; ++n) {
+      Frag<true> xf[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) f[j] = fx[n][j] * fw[n];
-      multiply(w[n], x[n], f);
+      for (int j = 0; j < NT; ++j) xf[j] = frag<true>(x[n][j][0], x[n][j][1]);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const Frag<true> wf = frag<true>(w[n][i][0], w[n][i][1]);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] += block_sum(wf, xf[j]) * f[n][j];
+      }
     }
   };
-  const int64_t whole = a.C / kFp8Block;
-  int64_t b = wave;
-  for (; b + (U - 1) * W < whole; b += U * W) blocks(b, Int<U>(), Int<W>());
-  for (; b < whole; b += W) blocks(b, Int<1>(), Int<W>());
-  if (b == whole && whole < cb) {                // the row's last, short block, by one wave
-    u32x4 w[RT][2], x[NT][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t c = whole * kFp8Block + 64 * h;
-      const int64_t left = a.C - c - 16 * q;
-      const int valid = left > 16 ? 16 : left < 0 ? 0 : (int)left;
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-        w[i][h] = valid > 0 ? first_bytes(*reinterpret_cast<const u32x4*>(wp[i] + c), valid) : zero;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        x[j][h] = valid > 0 && in[j] ? first_bytes(*reinterpret_cast<const u32x4*>(xp[j] + c), valid) : zero;
-    }
-    float f[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) f[j] = (in[j] ? sx[j][whole * a.xs_blk] : 0.0f) * sw[whole];
-    multiply(w, x, f);
+  for (int b = wave; b < cb; b += 2 * U * W) {
+    multiply(w[0], b);
+    if (b + U * W >= cb) break;
+    load(w[0], b + 2 * U * W);
+    multiply(w[1], b + U * W);
+    load(w[1], b + 3 * U * W);
   }
-  __shared__ float red[join_bytes<RT, NT, W>() / 4];
-  join_and_store<RT, NT, W>(a, acc, r0, t0, t1, red);
+  if (QUANTIZE) __syncthreads();                 // the rows of x give way to the waves' sums
+  join_and_store<RT, NT, W>(a, acc, r0, t0, t1, reinterpret_cast<float*>(smem));
 }
 
-template <int RT, int NT, int W>
+template <int RT, int NT, int W, bool QUANTIZE>
 hipError_t few_fp8(MatmulArgs a, hipStream_t stream) {
   a.row_blocks = (a.R + RT * kMfma - 1) / (RT * kMfma);
   const int64_t grid = a.row_blocks * token_tiles(a, NT * kMfma);
-  hipLaunchKernelGGL((few_fp8_kernel<RT, NT, W>), grid_of(grid), dim3(W * kWave), 0, stream, a);
+  a.x_rows = (int)(a.T < NT * kMfma ? a.T : NT * kMfma);
+  const int x_lds = QUANTIZE ? a.x_rows * (few_x_bytes(a.C) + 4 * (int)fp8_blocks(a.C)) : 0;
+  const int lds = x_lds > join_bytes<RT, NT, W>() ? x_lds : join_bytes<RT, NT, W>();
+  hipLaunchKernelGGL((few_fp8_kernel<RT, NT, W, QUANTIZE>), grid_of(grid), dim3(W * kWave), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -513,8 +574,10 @@ hipError_t tile_fp8_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t st
 }  // namespace
 
 hipError_t launch_few_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
-  if (p.nt == 1) return p.rt == 2 ? few_fp8<2, 1, 8>(a, stream) : few_fp8<1, 1, 8>(a, stream);
-  return p.rt == 2 ? few_fp8<2, 2, 8>(a, stream) : few_fp8<1, 2, 8>(a, stream);
+  if (a.x_type != AAAC_FP8)
+    return p.rt == 2 ? few_fp8<2, 1, 8, true>(a, stream) : few_fp8<1, 1, 8, true>(a, stream);
+  if (p.nt == 1) return p.rt == 2 ? few_fp8<2, 1, 8, false>(a, stream) : few_fp8<1, 1, 8, false>(a, stream);
+  return p.rt == 2 ? few_fp8<2, 2, 8, false>(a, stream) : few_fp8<1, 2, 8, false>(a, stream);
 }
 
 hipError_t launch_tile_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {

@@ -34,6 +34,10 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // and 12. Four chunks at a time pay on long rows: 12.6 us down to 11.9 at 14336 columns, 7.3 up to 7.8
 // at 4096.
 //
+// FP8 rows of x given in another type: a workgroup of the few-row kernels quantises its own where they have
+// up to kFewQuantize elements (64 a thread), which saves a launch; more take longer than the launch does.
+constexpr int64_t kFewQuantize = 32768;
+
 // Tiles: the least estimated time over tile widths and splits. A tile takes its steps times kStep
 // (measured with every CU at work) and kTile to start and end; the busiest CU runs
 // ceil(workgroups / CUs) of them, two at a time where LDS holds two, which takes kTwo of one after the
@@ -92,6 +96,7 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
       p.nt = rows <= kMfma ? 1 : 2;
       p.rt = blocks > 2 * device_cu_count() ? 2 : 1;
       p.chunks = 1;
+      p.quantize = p.nt == 1 && (a.E == 1 && rows < kMfma ? rows : kMfma) * a.C <= kFewQuantize;
       return p;
     }
     plan_tiles(a, kFp8Tiles, kTwoMx, kFp8Block, can_split, p);

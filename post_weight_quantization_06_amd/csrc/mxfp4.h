@@ -65,6 +65,7 @@ struct MatmulArgs {
   int64_t row_blocks;          // set by the launcher: row blocks of one expert
   int64_t blocks;              // set by the launcher of tiles: workgroups that have one
   int x_rows;                  // set by the launcher: rows of x that the workgroup's LDS holds
+  int x_type;                  // FP8 with plan.quantize: x as it was given, quantised by every workgroup
 };
 
 __host__ __device__ __forceinline__ int64_t part_row(int64_t R) { return (R + 3) & ~(int64_t)3; }
@@ -82,6 +83,7 @@ inline int64_t token_tiles(const MatmulArgs& a, int BN) {
 struct MatmulPlan {
   int bm, bn, split;
   int rt, nt, chunks;
+  bool quantize;               // FP8: the few-row kernels can quantise their rows of x themselves
 };
 
 enum MatmulKind { kMxBf16, kMxMxfp4, kPacked, kFp8 };

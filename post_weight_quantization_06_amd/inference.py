@@ -275,16 +275,15 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[t
     top_groups (default: all) with the largest best value (group_top 1) or sum of the two best (2) take
     part. Equals go to the lowest index. An expert whose logit or bias is -inf is left out, so a row of
     -inf (a padded batch's) gets no expert; the type's lowest value is a number like any other."""
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E] (got %d-D)" % logits.dim())
     if not isinstance(k, int) or k < 1:
         raise ValueError("k must be a positive whole number (got %r)" % (k,))
-    T, E = logits.shape
-    like = dict(dtype=torch.int32, device=logits.device)
-    r = Routing(torch.empty(T, k, **like), torch.empty(T, k, dtype=torch.float32, device=logits.device),
-                torch.empty(E + 1, **like), torch.empty(T * k, **like), torch.empty(T, k, **like))
-    L.aaac_route(logits, k, r.experts, r.weights, r.offsets, r.rows, r.places, score, bias, groups,
-                 top_groups, group_top, renormalize, scale)
+    inputs = L._route_inputs(logits, bias, score)
+    T, E, dev = inputs[2], inputs[3], logits.device
+    experts, places, rows = torch.empty(3, T, k, dtype=torch.int32, device=dev).unbind(0)
+    r = Routing(experts, torch.empty(T, k, dtype=torch.float32, device=dev),
+                torch.empty(E + 1, dtype=torch.int32, device=dev), rows.view(-1), places)
+    L._route(inputs, logits, k, experts, r.weights, r.offsets, rows, places, score, bias, groups,
+             top_groups, group_top, renormalize, scale)
     return r
 
 
