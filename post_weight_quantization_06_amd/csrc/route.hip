@@ -20,9 +20,11 @@ namespace aaac {
 namespace {
 
 constexpr int kMaxBlocks = 256;                  // blocks of tokens, each counted on its own
-constexpr int kWaves = 8;                        // waves of a block
+constexpr int kWaves = 16;                       // waves of a block: four a SIMD hide what one waits for
 
 template <int N> struct Int { static constexpr int value = N; };
+template <bool B, class X, class Y> struct Pick { typedef X type; };
+template <class X, class Y> struct Pick<false, X, Y> { typedef Y type; };
 
 template <int TYPE>
 __device__ __forceinline__ float load_f32(const void* p, int64_t i) {
@@ -51,6 +53,10 @@ __device__ __forceinline__ uint64_t key_of(double v) {
 __device__ __forceinline__ double value_of(uint64_t key) {
   const uint64_t sign = 1ull << 63;
   return __longlong_as_double((long long)(key & sign ? key ^ sign : ~key));
+}
+
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
 // The largest of the wave's values, in a scalar register. Lanes shift within their rows of 16, then
@@ -86,131 +92,237 @@ __device__ __forceinline__ uint64_t top_lanes(uint64_t key) {
   return lanes;
 }
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) v += __shfl_xor(v, d);
-  return v;
+// The partner's key in a block of 2 D lanes whose halves are alike within themselves.
+template <int D>
+__device__ __forceinline__ uint32_t other(uint32_t v) {
+  if (D == 1) return dpp_u32<kDppQuadXor1>(v);
+  if (D == 2) return dpp_u32<kDppQuadXor2>(v);
+  if (D == 4) return dpp_u32<kDppRowHalfMirror>(v);
+  if (D == 8) return dpp_u32<kDppRowMirror>(v);
+  return (uint32_t)__shfl_xor((int)v, D);
 }
-__device__ __forceinline__ float wave_top(float v) {
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const float o = __shfl_xor(v, d);
-    v = v != v ? v : o != o ? o : fmaxf(v, o);   // a NaN stays
-  }
-  return v;
+template <int D>
+__device__ __forceinline__ uint64_t other(uint64_t v) {
+  return (uint64_t)other<D>((uint32_t)(v >> 32)) << 32 | other<D>((uint32_t)v);
 }
 
-// One token by one wave. Groups take 64 / 2^ceil(log2 G) neighbouring lanes each, NV neighbouring
-// experts a lane, so that lane order is expert order and a group is a power of two of lanes.
-// Returns the expert of slot `lane`, or -1, and its weight.
+// e^x for x <= 0 in 64 bits: x = n ln 2 + r with |r| <= ln 2 / 2, and the Taylor polynomial of e^r up to
+// r^13 (what follows is below 2^-57). NaN gives some number: callers look for it in x.
+__device__ __forceinline__ double exp64(double x) {
+  x = fmax(x, -750.0);                           // 0 from there on
+  const double n = rint(x * 1.4426950408889634);
+  double r = __builtin_fma(-n, 0.6931471805599453, x);
+  r = __builtin_fma(-n, 2.3190468138462996e-17, r);
+  double p = 1.0 / 6227020800.0;
+#pragma unroll
+  for (int i = 0; i < 13; ++i) {
+    const double c[] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0, 1.0 / 40320.0,
+                        1.0 / 5040.0, 1.0 / 720.0, 1.0 / 120.0, 1.0 / 24.0, 1.0 / 6.0, 0.5, 1.0, 1.0};
+    double k = c[i];
+    if (i < 10) asm("" : "+s"(k));               // a scalar operand: in vector registers each is copied first
+    p = __builtin_fma(p, r, k);
+  }
+  return ldexp(p, (int)n);
+}
+// 1 / d, d normal: the instruction's estimate and two steps of Newton's method.
+__device__ __forceinline__ double reciprocal(double d) {
+  double r = __builtin_amdgcn_rcp(d);
+  r = __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+  return __builtin_fma(__builtin_fma(-d, r, 1.0), r, r);
+}
+__device__ __forceinline__ double sigmoid64(float l) {
+  const double e = exp64(-fabs((double)l)), r = reciprocal(1.0 + e);
+  return l > 0.0f ? r : e * r;
+}
+
+// NV neighbouring logits; those at or past n are -inf. VEC: n is 0 or NV and they lie on their whole size.
+template <int TYPE, int NV, bool VEC>
+__device__ __forceinline__ void load_logits(const void* p, int64_t at, int n, float (&l)[NV]) {
+  if (VEC) {
+    typedef typename Pick<TYPE == AAAC_F32, uint32_t, uint16_t>::type T;
+    T v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = -INFINITY;
+    if (n > 0) {
+      __builtin_memcpy(v, __builtin_assume_aligned(static_cast<const T*>(p) + at, sizeof(v) < 16 ? sizeof(v) : 16),
+                       sizeof(v));
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        l[i] = TYPE == AAAC_F32 ? __uint_as_float((uint32_t)v[i])
+               : TYPE == AAAC_BF16 ? __uint_as_float((uint32_t)v[i] << 16)
+                                   : (float)__builtin_bit_cast(_Float16, (uint16_t)v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] = i < n ? load_f32<TYPE>(p, at + i) : -INFINITY;
+  }
+}
+
+// One token by one wave. Groups take 64 / 2^ceil(log2 G) neighbouring lanes each, NV neighbouring experts a
+// lane, so that lane order is expert order and a group is a power of two of lanes. bias: of the lane's
+// experts, -inf past the last. Returns the expert of slot `lane`, or -1, and its weight.
+//
+// Bound by vector instructions, some 780 a token with 256 experts in groups, a bias and k = 8 (16384 tokens:
+// 32 us, 22 of them at full issue; the logits' bytes would take 3). A lane's few keys are sorted once, so that
+// the k rounds of selection only look at each lane's first. Two tokens side by side in a wave took 30 us,
+// and 11 instead of 8 us for one token.
 template <int NV, bool EXACT>
-__device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lanes_per_group, float& weight) {
+__device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lanes_per_group,
+                                      const float (&bias)[NV], float& weight) {
   typedef typename Keys<EXACT>::T Key;
+  constexpr bool kSorted = NV <= 4;
   const int lane = threadIdx.x & (kWave - 1);
   const int per_group = a.E / a.groups, group = lane / lanes_per_group;
   const int j0 = (lane % lanes_per_group) * NV, e0 = group * per_group + j0;
   const int n = group < a.groups ? per_group - j0 : 0;      // experts of this lane: NV, or fewer
-  float l[NV];
   const int64_t at = t * a.ldl;
+  float l[NV];
   auto load = [&](auto type) __attribute__((always_inline)) {
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-      l[v] = v < n ? load_f32<decltype(type)::value>(a.logits, at + e0 + v) : -INFINITY;
+    if (a.vec) load_logits<decltype(type)::value, NV, true>(a.logits, at + e0, n, l);
+    else load_logits<decltype(type)::value, NV, false>(a.logits, at + e0, n, l);
   };
   if (a.type == AAAC_F32) load(Int<AAAC_F32>());
   else if (a.type == AAAC_BF16) load(Int<AAAC_BF16>());
   else load(Int<AAAC_F16>());
   float top = 0.0f;
-  double total = 1.0;
+  double over = 1.0;
   if (!a.sigmoid && (EXACT || !a.renormalize)) {
-    top = l[0];
+    uint32_t best = 0;
 #pragma unroll
-    for (int v = 1; v < NV; ++v) top = top != top ? top : l[v] != l[v] ? l[v] : fmaxf(top, l[v]);
-    top = wave_top(top);
-    total = 0.0;
-    if (top != -INFINITY) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        if (v < n) total += EXACT ? exp((double)l[v] - top) : (double)expf(l[v] - top);
-      }
-    }
-    total = wave_sum(total);
-  }
-  Key key[NV];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    key[v] = 0;
-    if (EXACT) {
-      double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l[v])) : exp((double)l[v] - top) / total;
-      const float b = a.bias && v < n ? a.bias[e0 + v] : 0.0f;
-      if (v < n && l[v] != -INFINITY && b != -INFINITY) key[v] = (Key)key_of(s + b);
-    } else if (v < n && l[v] != -INFINITY) {
-      key[v] = (Key)key_of(l[v]);
-    }
-  }
-  if (a.top_groups < a.groups) {
-    Key best = 0, next = 0;
+    for (int v = 0; v < NV; ++v) best = max(best, key_of(l[v]));
+    top = value_of(wave_max(best));
+    double total = 0.0;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
+      const double x = (double)l[v] - top;
+      total += x != x ? x : EXACT ? exp64(x) : (double)expf((float)x);
+    }
+    // a row of -inf has no scores; its x are NaN
+    over = top == -INFINITY ? 0.0 : 1.0 / block_sum_f64(total, kWave);
+  }
+  Key key[NV];
+  int which[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) which[v] = v;
+  // l or bias -inf: 0, also past the lane's last expert
+  if constexpr (EXACT) {
+    auto take = [&](int v, double s) __attribute__((always_inline)) {
+      const Key k = key_of(s + (double)bias[v]);
+      key[v] = l[v] != l[v] ? ~(Key)0 : fminf(l[v], bias[v]) == -INFINITY ? 0 : k;
+    };
+    if (a.sigmoid) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) take(v, sigmoid64(l[v]));
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const double x = (double)l[v] - top;
+        take(v, x != x ? x : exp64(x) * over);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) key[v] = l[v] == -INFINITY ? 0 : (Key)key_of(l[v]);
+  }
+  if (kSorted) {
+    // neighbours in turn; equals keep their order
+#pragma unroll
+    for (int i = NV - 1; i > 0; --i)
+#pragma unroll
+      for (int v = 0; v < i; ++v) {
+        const bool swap = key[v + 1] > key[v];
+        const Key k = swap ? key[v] : key[v + 1];
+        const int w = swap ? which[v] : which[v + 1];
+        key[v] = swap ? key[v + 1] : key[v];
+        which[v] = swap ? which[v + 1] : which[v];
+        key[v + 1] = k;
+        which[v + 1] = w;
+      }
+  }
+  if (a.top_groups < a.groups) {
+    Key best = key[0], next = 0;
+#pragma unroll
+    for (int v = 1; v < NV; ++v) {
       next = max(next, min(best, key[v]));
       best = max(best, key[v]);
+      if (kSorted) break;
     }
-    for (int d = 1; d < lanes_per_group; d <<= 1) {
-      const Key ob = (Key)__shfl_xor((unsigned long long)best, d);
-      const Key on = (Key)__shfl_xor((unsigned long long)next, d);
-      next = max(min(best, ob), max(next, on));
+    auto join = [&](auto d) __attribute__((always_inline)) {
+      constexpr int D = decltype(d)::value;
+      if (D >= lanes_per_group) return;
+      const Key ob = other<D>(best);
+      if (EXACT) next = max(min(best, ob), max(next, other<D>(next)));
       best = max(best, ob);
+    };
+    join(Int<1>());
+    join(Int<2>());
+    join(Int<4>());
+    join(Int<8>());
+    join(Int<16>());
+    join(Int<32>());
+    if constexpr (EXACT) {
+      if (a.group_top == 2 && next != 0) best = key_of(value_of(best) + value_of(next));
     }
-    if (EXACT && a.group_top == 2 && next != 0)
-      best = (Key)key_of(value_of(best) + value_of(next));
     // a group's place among the groups, the lower index first among equals
     int place = 0;
     for (int g = 0; g < a.groups; ++g) {
-      const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)best, g * lanes_per_group);
-      Key o = lo;
-      if (EXACT)
-        o |= (Key)__builtin_amdgcn_readlane((uint32_t)((uint64_t)best >> 32), g * lanes_per_group) << (EXACT ? 32 : 0);
+      Key o = (uint32_t)__builtin_amdgcn_readlane((uint32_t)best, g * lanes_per_group);
+      if constexpr (EXACT) {
+        const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(best >> 32), g * lanes_per_group);
+        o |= (Key)hi << 32;
+      }
       place += o > best || (o == best && g < group) ? 1 : 0;
     }
-    if (place >= a.top_groups) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) key[v] = 0;
-    }
+    for (int v = 0; v < NV; ++v) key[v] = place >= a.top_groups ? 0 : key[v];
   }
   int mine = -1;
-  Key best = 0;
-  int which = 0;
+  Key best = key[0];
+  int first = which[0];
+  if (!kSorted) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v)
-    if (key[v] > best) best = key[v], which = v;
+    for (int v = 1; v < NV; ++v)
+      if (key[v] > best) best = key[v], first = v;
+  }
 #pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
     const uint64_t lanes = top_lanes(best);
     if (!lanes) break;
     const int from = __builtin_ctzll(lanes);
-    const int e = __builtin_amdgcn_readlane(e0 + which, from);
+    const int e = __builtin_amdgcn_readlane(e0 + first, from);
     if (lane == j) mine = e;
     if (lane == from) {
+      if (kSorted) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (v == which) key[v] = 0;
-      best = 0;
+        for (int v = 0; v + 1 < NV; ++v) key[v] = key[v + 1], which[v] = which[v + 1];
+        key[NV - 1] = 0;
+        best = key[0];
+        first = which[0];
+      } else {
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
-        if (key[v] > best) best = key[v], which = v;
+        for (int v = 0; v < NV; ++v)
+          if (v == first) key[v] = 0;
+        best = 0;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          if (key[v] > best) best = key[v], first = v;
+      }
     }
   }
-  // weights in 64 bits, a lane each
+  // weights in 64 bits, a lane each; `lanes`, a power of two, hold all of them
+  int lanes = 1;
+  while (lanes < a.k) lanes <<= 1;
   double s = 0.0;
   const float lm = mine >= 0 ? load_any(a.type, a.logits, at + mine) : -INFINITY;
   if (a.sigmoid) {
-    s = mine >= 0 ? 1.0 / (1.0 + exp(-(double)lm)) : 0.0;
+    s = lm != lm ? (double)lm : mine >= 0 ? sigmoid64(lm) : 0.0;
   } else {
-    if (!EXACT && a.renormalize) top = wave_top(lm);
-    s = mine >= 0 ? exp((double)lm - (double)top) / total : 0.0;
+    if (!EXACT && a.renormalize) top = value_of(block_max_u32(key_of(lm), lanes));
+    const double x = (double)lm - (double)top;
+    s = mine < 0 ? 0.0 : x != x ? x : exp64(x) * over;
   }
   if (a.renormalize) {
-    const double sum = wave_sum(s);
+    const double sum = block_sum_f64(s, lanes);
     s = sum == 0.0 ? 0.0 : s / sum;
   }
   weight = (float)(s * (double)a.scale);
@@ -247,47 +359,58 @@ __device__ __forceinline__ void place_slots(const RouteArgs& a, volatile int* ne
 // Everything after the choice for one block of tokens: counts and their sums in LDS, then the places.
 // lds: int [place_ints]. The rows of each expert in earlier blocks and in every block are read from
 // a.counts; with one block (`alone`) they are its own.
-__host__ __device__ constexpr int place_ints(int E) { return kWaves * E + kWaves; }
+__host__ __device__ constexpr int count_row(int E) { return (E + 3) & ~3; }
+constexpr int kThreads = kWaves * kWave;
+__host__ __device__ constexpr int place_ints(int E) { return kWaves * E + kWaves + 2 * 4 * kThreads; }
 __device__ __forceinline__ void place_block(const RouteArgs& a, int* lds, int block, int blocks,
                                             bool alone) {
+  static_assert(kMaxExperts <= kThreads, "an expert a thread");
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
-  constexpr int kThreads = kWaves * kWave, kShare = kMaxExperts / kThreads;
-  int* hist = lds;                               // [kWaves][E]: slots of each wave, then their places
-  int* sums = lds + kWaves * a.E;                // [kWaves]
+  int* sum = lds;                                // [kThreads][2][4]: a thread's part of the counts
+  int* hist = lds + 2 * 4 * kThreads;            // [kWaves][E]: slots of each wave, then their places
+  int* sums = hist + kWaves * a.E;               // [kWaves]
   const int64_t slots = a.T * a.k, per = (int64_t)a.per_block * a.k, b0 = block * per;
   const int64_t b1 = b0 + per < slots ? b0 + per : slots;
   const int64_t each = (b1 - b0 + kWaves - 1) / kWaves;
   const int64_t s0 = b0 + wave * each < b1 ? b0 + wave * each : b1;
   const int64_t s1 = s0 + each < b1 ? s0 + each : b1;
   for (int i = tid; i < kWaves * a.E; i += kThreads) hist[i] = 0;
+  // four experts a thread, the blocks dealt out over what threads that leaves
+  const int cols = count_row(a.E) / 4, room = kThreads / cols < 8 ? kThreads / cols : 8;
+  const int ways = blocks < room ? blocks : room;
+  if (!alone) {
+    int4 all = {0, 0, 0, 0}, before = {0, 0, 0, 0};
+    if (tid < cols * ways) {
+      const int4* c = reinterpret_cast<const int4*>(a.counts) + tid % cols;
+#pragma unroll 8
+      for (int b = tid / cols; b < blocks; b += ways) {
+        const int4 n = c[(int64_t)b * cols];
+        const int m = b < block ? -1 : 0;
+        all.x += n.x, all.y += n.y, all.z += n.z, all.w += n.w;
+        before.x += n.x & m, before.y += n.y & m, before.z += n.z & m, before.w += n.w & m;
+      }
+    }
+    reinterpret_cast<int4*>(sum)[2 * tid] = all;
+    reinterpret_cast<int4*>(sum)[2 * tid + 1] = before;
+  }
   __syncthreads();
   for (int64_t s = s0 + lane; s < s1; s += kWave) {
     const int e = a.experts[s];
     if (e >= 0) atomicAdd(&hist[wave * a.E + e], 1);
   }
   __syncthreads();
-  // a thread's experts: kShare neighbours
-  int all[kShare], before[kShare], mine = 0;
-#pragma unroll
-  for (int i = 0; i < kShare; ++i) {
-    const int e = tid * kShare + i;
-    all[i] = before[i] = 0;
-    if (e < a.E) {
-      if (alone) {
-        for (int w = 0; w < kWaves; ++w) all[i] += hist[w * a.E + e];
-      } else {
-        const int32_t* c = a.counts + e;
-#pragma unroll 8
-        for (int b = 0; b < blocks; ++b) {
-          const int n = c[(int64_t)b * a.E];
-          all[i] += n;
-          before[i] += b < block ? n : 0;
-        }
+  int all = 0, before = 0;                       // of expert tid
+  if (tid < a.E) {
+    if (alone) {
+      for (int w = 0; w < kWaves; ++w) all += hist[w * a.E + tid];
+    } else {
+      for (int i = tid / 4; i < cols * ways; i += cols) {
+        all += sum[8 * i + (tid & 3)];
+        before += sum[8 * i + 4 + (tid & 3)];
       }
-      mine += all[i];
     }
   }
-  int run = mine;                                // inclusive over the wave
+  int run = all;                                 // inclusive over the wave
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
     const int o = __shfl_up(run, d);
@@ -295,23 +418,20 @@ __device__ __forceinline__ void place_block(const RouteArgs& a, int* lds, int bl
   }
   if (lane == kWave - 1) sums[wave] = run;
   __syncthreads();
-  int first = run - mine, total = 0;
+  int first = run - all, total = 0;
+#pragma unroll
   for (int w = 0; w < kWaves; ++w) {
     if (w < wave) first += sums[w];
     total += sums[w];
   }
+  if (tid < a.E) {
+    if (block == 0) a.offsets[tid] = first;
+    int at = first + before;
 #pragma unroll
-  for (int i = 0; i < kShare; ++i) {
-    const int e = tid * kShare + i;
-    if (e < a.E) {
-      if (block == 0) a.offsets[e] = first;
-      int at = first + before[i];
-      for (int w = 0; w < kWaves; ++w) {
-        const int n = hist[w * a.E + e];
-        hist[w * a.E + e] = at;
-        at += n;
-      }
-      first += all[i];
+    for (int w = 0; w < kWaves; ++w) {
+      const int n = hist[w * a.E + tid];
+      hist[w * a.E + tid] = at;
+      at += n;
     }
   }
   if (block == 0 && tid == 0) a.offsets[a.E] = total;
@@ -326,19 +446,27 @@ __device__ __forceinline__ void place_block(const RouteArgs& a, int* lds, int bl
 
 // alone: the one block of a call with few tokens orders its slots too.
 template <int NV, bool EXACT>
-__global__ __launch_bounds__(kWaves * kWave) void route_kernel(RouteArgs a, int lanes_per_group,
-                                                               bool alone) {
+__global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs a, int lanes_per_group, bool alone) {
   extern __shared__ int lds[];
   const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
   const int64_t t0 = (int64_t)blockIdx.x * a.per_block;
   const int64_t t1 = t0 + a.per_block < a.T ? t0 + a.per_block : a.T;
   if (!alone) {
-    for (int i = threadIdx.x; i < a.E; i += kWaves * kWave) lds[i] = 0;
+    for (int i = threadIdx.x; i < a.E; i += kThreads) lds[i] = 0;
     __syncthreads();
+  }
+  float bias[NV];
+  {
+    const int group = lane / lanes_per_group, per_group = a.E / a.groups, j0 = lane % lanes_per_group * NV;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const bool in = group < a.groups && j0 + v < per_group;
+      bias[v] = !in ? -INFINITY : EXACT && a.bias ? a.bias[group * per_group + j0 + v] : 0.0f;
+    }
   }
   for (int64_t t = t0 + wave; t < t1; t += kWaves) {
     float weight;
-    const int e = choose<NV, EXACT>(a, t, lanes_per_group, weight);
+    const int e = choose<NV, EXACT>(a, t, lanes_per_group, bias, weight);
     if (lane < a.k) {
       a.experts[t * a.k + lane] = e;
       a.weights[t * a.k + lane] = weight;
@@ -349,12 +477,13 @@ __global__ __launch_bounds__(kWaves * kWave) void route_kernel(RouteArgs a, int 
   if (alone) {
     place_block(a, lds, 0, 1, true);
   } else {
-    for (int i = threadIdx.x; i < a.E; i += kWaves * kWave)
-      a.counts[(int64_t)blockIdx.x * a.E + i] = lds[i];
+    // a row of counts ends on 16 bytes; what follows the experts is never used
+    for (int i = threadIdx.x; i < a.E; i += kThreads)
+      a.counts[(int64_t)blockIdx.x * count_row(a.E) + i] = lds[i];
   }
 }
 
-__global__ __launch_bounds__(kWaves * kWave) void place_kernel(RouteArgs a, int blocks) {
+__global__ __launch_bounds__(kThreads) void place_kernel(RouteArgs a, int blocks) {
   extern __shared__ int lds[];
   place_block(a, lds, blockIdx.x, blocks, false);
 }
@@ -366,15 +495,17 @@ int tokens_per_block(int64_t T) {
 }
 
 template <int NV, bool EXACT>
-hipError_t route_n(const RouteArgs& a, int lanes_per_group, hipStream_t stream) {
+hipError_t route_n(RouteArgs a, int lanes_per_group, hipStream_t stream) {
+  const int b = a.type == AAAC_F32 ? 4 : 2, whole = NV * b < 16 ? NV * b : 16;
+  a.vec = (uintptr_t)a.logits % whole == 0 && a.ldl % NV == 0 && a.E / a.groups % NV == 0;
   const int blocks = (int)((a.T + a.per_block - 1) / a.per_block);
   const bool alone = blocks == 1;
   const size_t lds = sizeof(int) * place_ints(a.E);
-  hipLaunchKernelGGL((route_kernel<NV, EXACT>), dim3(blocks), dim3(kWaves * kWave),
+  hipLaunchKernelGGL((route_kernel<NV, EXACT>), dim3(blocks), dim3(kThreads),
                      alone ? lds : sizeof(int) * a.E, stream, a, lanes_per_group, alone);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || alone) return e;
-  hipLaunchKernelGGL(place_kernel, dim3(blocks), dim3(kWaves * kWave), lds, stream, a, blocks);
+  hipLaunchKernelGGL(place_kernel, dim3(blocks), dim3(kThreads), lds, stream, a, blocks);
   return hipGetLastError();
 }
 
@@ -518,7 +649,7 @@ hipError_t to_experts(const void* x, int64_t T, int64_t bytes, int64_t ldx, cons
 
 size_t route_workspace_bytes(int64_t T, int E) {
   const int64_t per = tokens_per_block(T);
-  return T <= per ? 0 : sizeof(int32_t) * (size_t)((T + per - 1) / per) * (size_t)E;
+  return T <= per ? 0 : sizeof(int32_t) * (size_t)((T + per - 1) / per) * (size_t)count_row(E);
 }
 
 hipError_t launch_route(RouteArgs a, hipStream_t stream) {
