@@ -527,121 +527,152 @@ __global__ void no_offsets_kernel(int32_t* offsets, int n) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Rows to experts and back: bound by memory. A workgroup takes one token and 256 words of its row: the
-// row is read once and written to each of its places, in words of 16, 4 or 2 bytes as the rows' addresses
-// allow. Places outside [0, N) are skipped.
+// Rows to experts and back: bound by memory. A workgroup takes one token and 256 pieces of 16 bytes of its
+// row, which is read once and written to each of its places. Rows that do not start on 16 bytes are read and
+// written in the same pieces, unaligned (1003 x 3 rows of 5003 in bf16 there: 17 us in words of two bytes).
+// Places outside [0, N) are skipped. 8192 x 8 rows of 4096 in bf16: 119 us either way, 5.1 TB/s.
 // ------------------------------------------------------------------------------------------------
-template <class Word>
-__global__ __launch_bounds__(kBlock) void rows_to_experts_kernel(
-    const uint8_t* __restrict__ x, int64_t words, int64_t ldx, const int32_t* __restrict__ places, int k,
-    uint8_t* __restrict__ out, int64_t N, int64_t ldo, int64_t chunks, int64_t blocks) {
-  const int64_t id = block_id();
-  if (id >= blocks) return;
-  const int64_t t = id / chunks, w = (id - t * chunks) * kBlock + threadIdx.x;
-  if (w >= words) return;
-  const Word v = reinterpret_cast<const Word*>(x + t * ldx)[w];
-  for (int j = 0; j < k; ++j) {
-    const int64_t p = places[t * k + j];
-    if (p >= 0 && p < N) reinterpret_cast<Word*>(out + p * ldo)[w] = v;
-  }
-}
-
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// V neighbours of a row as fp32.
-template <int TYPE, int V>
-__device__ __forceinline__ void load_v(const void* p, int64_t i, float (&v)[V]) {
-  if (V == 1) {
-    v[0] = load_f32<TYPE>(p, i);
-  } else if (TYPE == AAAC_F32) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
+// VEC: on 16 bytes. Of the row's last piece there may be only `bytes` < 16, a multiple of the element's.
+template <bool VEC>
+__device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int bytes, int element) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (VEC) return *reinterpret_cast<const u32x4*>(p);
+  if (bytes >= 16) {
+    __builtin_memcpy(&v, p, 16);
+    return v;
+  }
 #pragma unroll
-    for (int c = 0; c < V; ++c) v[c] = __uint_as_float(w[c & 3]);
+  for (int i = 0; i < 16; ++i) {
+    if (i >= bytes) break;
+    if (element == 1) v[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
+    else if (i % 4 == 0 && element == 4) v[i >> 2] = *reinterpret_cast<const uint32_t*>(p + i);
+    else if (i % 2 == 0 && element == 2)
+      v[i >> 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(p + i) << (8 * (i & 3));
+  }
+  return v;
+}
+template <bool VEC>
+__device__ __forceinline__ void store_piece(uint8_t* p, int bytes, int element, u32x4 v) {
+  if (VEC) {
+    *reinterpret_cast<u32x4*>(p) = v;
+  } else if (bytes >= 16) {
+    __builtin_memcpy(p, &v, 16);
   } else {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const uint16_t b = (uint16_t)(w[(c >> 1) & 3] >> (16 * (c & 1)));
-      v[c] = TYPE == AAAC_BF16 ? __uint_as_float((uint32_t)b << 16)
-                               : (float)__builtin_bit_cast(_Float16, b);
+    for (int i = 0; i < 16; ++i) {
+      if (i >= bytes) break;
+      if (element == 1) p[i] = (uint8_t)(v[i >> 2] >> (8 * (i & 3)));
+      else if (i % 4 == 0 && element == 4) *reinterpret_cast<uint32_t*>(p + i) = v[i >> 2];
+      else if (i % 2 == 0 && element == 2)
+        *reinterpret_cast<uint16_t*>(p + i) = (uint16_t)(v[i >> 2] >> (8 * (i & 3)));
     }
   }
 }
-__device__ __forceinline__ uint16_t to_16(int type, float v) {
+
+template <bool VEC>
+__global__ __launch_bounds__(kBlock) void rows_to_experts_kernel(
+    const uint8_t* __restrict__ x, int64_t bytes, int64_t ldx, const int32_t* __restrict__ places, int k,
+    uint8_t* __restrict__ out, int64_t N, int64_t ldo, int element, int64_t chunks, int64_t blocks) {
+  const int64_t id = block_id();
+  if (id >= blocks) return;
+  const int64_t t = id / chunks, at = ((id - t * chunks) * kBlock + threadIdx.x) * 16;
+  if (at >= bytes) return;
+  const int left = bytes - at < 16 ? (int)(bytes - at) : 16;
+  const u32x4 v = load_piece<VEC>(x + t * ldx + at, left, element);
+  for (int j = 0; j < k; ++j) {
+    const int64_t p = places[t * k + j];
+    if (p >= 0 && p < N) store_piece<VEC>(out + p * ldo + at, left, element, v);
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ float value_at(u32x4 w, int i) {
+  if (TYPE == AAAC_F32) return __uint_as_float(w[i & 3]);
+  const uint16_t b = (uint16_t)(w[(i >> 1) & 3] >> (16 * (i & 1)));
+  return TYPE == AAAC_BF16 ? __uint_as_float((uint32_t)b << 16) : (float)__builtin_bit_cast(_Float16, b);
+}
+__device__ __forceinline__ uint32_t to_16(int type, float v) {
   return type == AAAC_BF16 ? __builtin_bit_cast(uint16_t, (__bf16)v)
                            : __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-template <int TYPE, int V>
+// VEC: whole pieces of y and of out on their own size.
+template <int TYPE, bool VEC>
 __global__ __launch_bounds__(kBlock) void rows_from_experts_kernel(
-    const void* __restrict__ y, int64_t N, int64_t C, int64_t ldy, const int32_t* __restrict__ places,
-    const float* __restrict__ weights, int k, void* __restrict__ out, int out_type, int64_t ldo,
+    const uint8_t* __restrict__ y, int64_t N, int64_t C, int64_t ldy, const int32_t* __restrict__ places,
+    const float* __restrict__ weights, int k, uint8_t* __restrict__ out, int out_type, int64_t ldo,
     int64_t chunks, int64_t blocks) {
+  constexpr int B = TYPE == AAAC_F32 ? 4 : 2, V = 16 / B;
   const int64_t id = block_id();
   if (id >= blocks) return;
   const int64_t t = id / chunks, c = ((id - t * chunks) * kBlock + threadIdx.x) * V;
   if (c >= C) return;
+  const int left = C - c < V ? (int)(C - c) : V;
   float sum[V] = {};
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int64_t p = places[t * k + j];
-    if (p < 0 || p >= N) continue;
-    const float w = weights[t * k + j];
-    float v[V];
-    load_v<TYPE, V>(y, p * ldy + c, v);
+  constexpr int U = 8;                           // rows on their way together
+  for (int j0 = 0; j0 < k; j0 += U) {
+    u32x4 v[U];
+    float w[U];
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum[i] = __builtin_fmaf(w, v[i], sum[i]);
+    for (int u = 0; u < U; ++u) {
+      v[u] = u32x4{0u, 0u, 0u, 0u};
+      w[u] = 0.0f;
+      if (j0 + u < k) {
+        const int64_t p = places[t * k + j0 + u];
+        if (p >= 0 && p < N) {
+          w[u] = weights[t * k + j0 + u];
+          v[u] = load_piece<VEC>(y + (p * ldy + c) * B, left * B, B);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum[i] = __builtin_fmaf(w[u], value_at<TYPE>(v[u], i), sum[i]);
   }
-  const int64_t at = t * ldo + c;
-  if (out_type == AAAC_F32) {
-    float* o = static_cast<float*>(out) + at;
-    if (V == 1) {
-      o[0] = sum[0];
-    } else {
+  const int ob = out_type == AAAC_F32 ? 4 : 2;
+  uint8_t* o = out + (t * ldo + c) * ob;
+  if (ob == 4) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4)
-        *reinterpret_cast<u32x4*>(o + i) =
-            u32x4{__float_as_uint(sum[i % V]), __float_as_uint(sum[(i + 1) % V]),
-                  __float_as_uint(sum[(i + 2) % V]), __float_as_uint(sum[(i + 3) % V])};
+    for (int i = 0; i < V; i += 4) {
+      const u32x4 w = {__float_as_uint(sum[i]), __float_as_uint(sum[i + 1]), __float_as_uint(sum[i + 2]),
+                       __float_as_uint(sum[i + 3])};
+      if (left > i) store_piece<VEC>(o + 4 * i, (left - i) * 4, 4, w);
     }
     return;
   }
-  uint16_t* o = static_cast<uint16_t*>(out) + at;
-  uint32_t w[(V + 1) / 2];
+  u32x4 w = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int i = 0; i < V; i += 2)
-    w[i / 2] = to_16(out_type, sum[i]) | (V > 1 ? (uint32_t)to_16(out_type, sum[(i + 1) % V]) << 16 : 0u);
-  if (V == 8) *reinterpret_cast<u32x4*>(o) = u32x4{w[0], w[1 % ((V + 1) / 2)], w[2 % ((V + 1) / 2)], w[3 % ((V + 1) / 2)]};
-  else if (V == 4) *reinterpret_cast<u32x2*>(o) = u32x2{w[0], w[1 % ((V + 1) / 2)]};
-  else o[0] = (uint16_t)w[0];
+  for (int i = 0; i < V; i += 2) w[i / 2] = to_16(out_type, sum[i]) | to_16(out_type, sum[i + 1]) << 16;
+  if (V == 8) {
+    store_piece<VEC>(o, left * 2, 2, w);
+  } else if (VEC) {
+    *reinterpret_cast<u32x2*>(o) = u32x2{w.x, w.y};
+  } else {
+    store_piece<false>(o, left * 2, 2, w);       // eight bytes at most
+  }
 }
 
 template <int TYPE>
 hipError_t from_experts(const void* y, int64_t N, int64_t C, int64_t ldy, const int32_t* places,
                         const float* weights, int64_t T, int k, void* out, int out_type, int64_t ldo,
                         hipStream_t stream) {
-  constexpr int V = TYPE == AAAC_F32 ? 4 : 8;    // 16 bytes of y
+  constexpr int V = TYPE == AAAC_F32 ? 4 : 8;
   const int ob = out_type == AAAC_F32 ? 4 : 2, store = V * ob < 16 ? V * ob : 16;
   const bool vec = (uintptr_t)y % 16 == 0 && ldy % V == 0 && C % V == 0 && (uintptr_t)out % store == 0 &&
                    (ldo * ob) % store == 0;
-  const int64_t chunks = (C + kBlock * (vec ? V : 1) - 1) / (kBlock * (vec ? V : 1)), blocks = T * chunks;
+  const int64_t chunks = (C + kBlock * V - 1) / (kBlock * V), blocks = T * chunks;
+  const uint8_t* in = static_cast<const uint8_t*>(y);
+  uint8_t* to = static_cast<uint8_t*>(out);
   if (vec)
-    hipLaunchKernelGGL((rows_from_experts_kernel<TYPE, V>), grid_of(blocks), dim3(kBlock), 0, stream, y, N,
-                       C, ldy, places, weights, k, out, out_type, ldo, chunks, blocks);
+    hipLaunchKernelGGL((rows_from_experts_kernel<TYPE, true>), grid_of(blocks), dim3(kBlock), 0, stream, in, N,
+                       C, ldy, places, weights, k, to, out_type, ldo, chunks, blocks);
   else
-    hipLaunchKernelGGL((rows_from_experts_kernel<TYPE, 1>), grid_of(blocks), dim3(kBlock), 0, stream, y, N,
-                       C, ldy, places, weights, k, out, out_type, ldo, chunks, blocks);
-  return hipGetLastError();
-}
-
-template <class Word>
-hipError_t to_experts(const void* x, int64_t T, int64_t bytes, int64_t ldx, const int32_t* places, int k,
-                      void* out, int64_t N, int64_t ldo, hipStream_t stream) {
-  const int64_t words = bytes / sizeof(Word), chunks = (words + kBlock - 1) / kBlock, blocks = T * chunks;
-  hipLaunchKernelGGL((rows_to_experts_kernel<Word>), grid_of(blocks), dim3(kBlock), 0, stream,
-                     static_cast<const uint8_t*>(x), words, ldx, places, k, static_cast<uint8_t*>(out), N,
-                     ldo, chunks, blocks);
+    hipLaunchKernelGGL((rows_from_experts_kernel<TYPE, false>), grid_of(blocks), dim3(kBlock), 0, stream, in,
+                       N, C, ldy, places, weights, k, to, out_type, ldo, chunks, blocks);
   return hipGetLastError();
 }
 
@@ -667,10 +698,16 @@ hipError_t launch_rows_to_experts(const void* x, int64_t T, int64_t bytes, int64
                                   int element, hipStream_t stream) {
   if (T == 0 || bytes == 0) return hipSuccess;
   const uint64_t low = (uintptr_t)x | (uintptr_t)out | (uint64_t)bytes | (uint64_t)ldx | (uint64_t)ldo;
-  if (low % 16 == 0) return to_experts<u32x4>(x, T, bytes, ldx, places, k, out, N, ldo, stream);
-  if (low % 4 == 0) return to_experts<uint32_t>(x, T, bytes, ldx, places, k, out, N, ldo, stream);
-  if (element == 1) return to_experts<uint8_t>(x, T, bytes, ldx, places, k, out, N, ldo, stream);
-  return to_experts<uint16_t>(x, T, bytes, ldx, places, k, out, N, ldo, stream);
+  const int64_t chunks = (bytes + kBlock * 16 - 1) / (kBlock * 16), blocks = T * chunks;
+  const uint8_t* in = static_cast<const uint8_t*>(x);
+  uint8_t* to = static_cast<uint8_t*>(out);
+  if (low % 16 == 0)
+    hipLaunchKernelGGL((rows_to_experts_kernel<true>), grid_of(blocks), dim3(kBlock), 0, stream, in, bytes,
+                       ldx, places, k, to, N, ldo, element, chunks, blocks);
+  else
+    hipLaunchKernelGGL((rows_to_experts_kernel<false>), grid_of(blocks), dim3(kBlock), 0, stream, in, bytes,
+                       ldx, places, k, to, N, ldo, element, chunks, blocks);
+  return hipGetLastError();
 }
 
 hipError_t launch_rows_from_experts(const void* y, int type, int64_t N, int64_t C, int64_t ldy,
