@@ -601,6 +601,7 @@ def _current_stream(dev: int) -> int:
 
 # the current stream's handle; torch's own shortcut saves 1 us of a call
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on_gpu(what: str, *tensors):
@@ -635,7 +636,7 @@ def _launch(name: str, dev: int, stream, *args):
         if stream.device.index != dev:
             raise ValueError("%s: stream on %s, tensors on cuda:%d" % (name, stream.device, dev))
         raw = stream.cuda_stream
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -878,22 +879,29 @@ def _blocks(n: int) -> int:
     return (n + 127) // 128
 
 
+def _fp8_quantize(X: torch.Tensor, codes: torch.Tensor, ldq: int, scales: torch.Tensor, tile: bool,
+                  dev: int, stream=None):
+    """The call for codes and scales that fit X."""
+    what = "aaac_fp8_quantize"
+    _no_grad(what, X)
+    xt = _float_type(X, "X")
+    E, M, C, ldx, step = _stacked(X, "X")
+    _launch(what, dev, stream, X.data_ptr(), xt, E, M, C, ldx, step, tile, codes.data_ptr(), ldq,
+            scales.data_ptr())
+
+
 def aaac_fp8_quantize(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tile: bool = False,
                       stream=None):
     """codes e4m3 like X [M, C] (or with tile [E, M, C]) in rows whose stride is a multiple of 16, and
     scales fp32 [M, ceil(C/128)] (with tile [E, ceil(M/128), ceil(C/128)])."""
     what = "aaac_fp8_quantize"
     dev = _on_gpu(what, X, codes, scales)
-    _no_grad(what, X)
-    xt = _float_type(X, "X")
-    E, M, C, ldx, step = _stacked(X, "X")
-    Eq, Mq, Cq, ldq = _fp8_codes(codes, "codes")
-    if (Eq, Mq, Cq) != (E, M, C):
+    if codes.shape != X.shape:
         raise ValueError("%s: codes must be shaped as X (got %s and %s)" % (
             what, tuple(codes.shape), tuple(X.shape)))
+    E, M, C, ldq = _fp8_codes(codes, "codes")
     _f32(scales, "scales", (E * _blocks(M) if tile else E * M) * _blocks(C))
-    _launch(what, dev, stream, X.data_ptr(), xt, E, M, C, ldx, step, int(tile), codes.data_ptr(), ldq,
-            scales.data_ptr())
+    _fp8_quantize(X, codes, ldq, scales, tile, dev, stream)
 
 
 def aaac_fp8_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tensor, tile: bool = False,
@@ -910,8 +918,8 @@ def aaac_fp8_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tensor,
     _f32(scales, "scales", (E * _blocks(M) if tile else E * M) * _blocks(C))
     if not tile:
         E, M = 1, E * M
-    _launch(what, dev, stream, codes.data_ptr(), ldq, scales.data_ptr(), E, M, C, int(tile),
-            Y.data_ptr(), yt, ldy)
+    _launch(what, dev, stream, codes.data_ptr(), ldq, scales.data_ptr(), E, M, C, tile, Y.data_ptr(), yt,
+            ldy)
 
 
 @functools.lru_cache(maxsize=4096)

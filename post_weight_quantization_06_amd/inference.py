@@ -160,23 +160,20 @@ def fp8_quantize(x: torch.Tensor, tile: bool = False) -> Tuple[torch.Tensor, tor
     128 columns of a row, [..., ceil(C/128)]; with tile for each 128 x 128 of a matrix [R, C] or a stack
     [E, R, C], [..., ceil(R/128), ceil(C/128)]. Rows of codes start on 16 bytes, as the products need
     them: for a C that is no multiple of 16 the result is a view of wider rows."""
+    dev = L._on_gpu("fp8_quantize", x)
     lead, C = x.shape[:-1], x.shape[-1]
-    if tile and x.dim() not in (2, 3):
-        raise ValueError("tile needs [R, C] or [E, R, C] (got %d-D)" % x.dim())
-    wide = (C + 15) // 16 * 16
+    wide, blocks = (C + 15) // 16 * 16, (C + 127) // 128
     codes = torch.empty(*lead, wide, dtype=torch.float8_e4m3fn, device=x.device)
-    if wide != C:
-        codes = codes[..., :C]
-    blocks = (C + 127) // 128
     if tile:
+        if len(lead) not in (1, 2):
+            raise ValueError("tile needs [R, C] or [E, R, C] (got %d-D)" % x.dim())
         scales = torch.empty(*lead[:-1], (lead[-1] + 127) // 128, blocks, dtype=torch.float32,
                              device=x.device)
-        L.aaac_fp8_quantize(x, codes, scales, True)
+        L._fp8_quantize(x, codes, wide, scales, True, dev)
     else:
         scales = torch.empty(*lead, blocks, dtype=torch.float32, device=x.device)
-        x2 = x if x.dim() == 2 else x.reshape(-1, C)
-        L.aaac_fp8_quantize(x2, codes if x.dim() == 2 else codes.view(-1, C), scales)
-    return codes, scales
+        L._fp8_quantize(x if len(lead) == 1 else x.reshape(-1, C), codes, wide, scales, False, dev)
+    return (codes if wide == C else codes[..., :C]), scales
 
 
 def fp8_dequant(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16,
