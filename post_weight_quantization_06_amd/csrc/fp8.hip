@@ -20,63 +20,61 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kSteps = 2;                        // lane pieces in flight per thread
+constexpr int kCols = 16;                        // columns a lane
 
 __device__ __forceinline__ int64_t divide(int64_t i, int64_t n, int64_t total) {
   return total <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)n) : i / n;
 }
 
-// Blocks of 1 x 128: eight neighbouring lanes hold a block.
+// Blocks of 1 x 128.
 template <int TYPE, bool VEC>
 __global__ __launch_bounds__(kBlock) void fp8_quantize_rows_kernel(
     const typename Elem<TYPE>::T* __restrict__ X, int64_t C, int64_t ldx, int64_t per_row,
     int64_t total, uint8_t* __restrict__ codes, int64_t ldq, int64_t Cw, float* __restrict__ scales,
     int64_t s_row, int64_t s_blk) {
+  constexpr int V = kCols, kLanes = kFp8Block / V;
   const int64_t i0 = block_id() * (kBlock * kSteps) + threadIdx.x;
-  float v[kSteps][kLane];
+  float v[kSteps][V];
   int64_t row[kSteps], col[kSteps];
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
     const int64_t i = i0 + u * kBlock;
     if (i >= total) break;
     row[u] = divide(i, per_row, total);
-    col[u] = (i - row[u] * per_row) * kLane;
+    col[u] = (i - row[u] * per_row) * V;
     const int64_t left = C - col[u];
-    load16<TYPE, VEC>(X + row[u] * ldx + col[u], left > kLane ? kLane : left < 0 ? 0 : (int)left, v[u]);
+    load_lane<TYPE, VEC>(X + row[u] * ldx + col[u], left > V ? V : left < 0 ? 0 : (int)left, v[u]);
   }
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
-    if (i0 + u * kBlock >= total) break;         // total is a multiple of 8: whole blocks leave
-    const float s = scale_of(block_max_u32_t<8>(top_bits(v[u]), 8));
+    if (i0 + u * kBlock >= total) break;         // total is a multiple of kLanes: whole blocks leave
+    const float s = scale_of(block_max_u32_t<kLanes>(top_bits(v[u]), kLanes));
     const int64_t left = C - col[u];
-    if (col[u] < Cw) {
-      Words4 w = encode16(v[u], s);
-      if (left < kLane) w = keep_first(w, (int)left);
-      *reinterpret_cast<Words4*>(codes + row[u] * ldq + col[u]) = w;
-    }
-    if ((threadIdx.x & 7) == 0) scales[row[u] * s_row + col[u] / kFp8Block * s_blk] = s;
+    if (col[u] < Cw) store_codes(v[u], s, left > V ? V : (int)left, codes + row[u] * ldq + col[u]);
+    if (threadIdx.x % kLanes == 0) scales[row[u] * s_row + col[u] / kFp8Block * s_blk] = s;
   }
 }
 
-// Blocks of 128 x 128: one a workgroup, four rows of a lane piece a thread.
+// Blocks of 128 x 128, one a workgroup.
 template <int TYPE, bool VEC>
 __global__ __launch_bounds__(kBlock) void fp8_quantize_tiles_kernel(
     const typename Elem<TYPE>::T* __restrict__ X, int64_t M, int64_t C, int64_t ldx, int64_t stride_x,
     int64_t tiles, uint8_t* __restrict__ codes, int64_t ldq, int64_t Cw, float* __restrict__ scales) {
-  constexpr int kRows = kBlock / 8, kEach = kFp8Block / kRows;
+  constexpr int V = kCols, kLanes = kFp8Block / V, kRows = kBlock / kLanes, kEach = kFp8Block / kRows;
   __shared__ uint32_t tops[kWavesPerBlock];
   const int64_t id = block_id();
   if (id >= tiles) return;
   const int64_t cb = fp8_blocks(C), rb = fp8_blocks(M);
   const int64_t e = id / (cb * rb), tr = id / cb % rb, tc = id % cb;
-  const int64_t col = tc * kFp8Block + (threadIdx.x & 7) * kLane, row0 = tr * kFp8Block + (threadIdx.x >> 3);
-  const int64_t left = C - col;
-  const int valid = left > kLane ? kLane : left < 0 ? 0 : (int)left;
-  float v[kEach][kLane];
+  const int64_t col = tc * kFp8Block + threadIdx.x % kLanes * V;
+  const int64_t row0 = tr * kFp8Block + threadIdx.x / kLanes, left = C - col;
+  const int valid = left > V ? V : left < 0 ? 0 : (int)left;
+  float v[kEach][V];
   uint32_t top = 0;
 #pragma unroll
   for (int u = 0; u < kEach; ++u) {
     const int64_t r = row0 + u * kRows;
-    load16<TYPE, VEC>(X + e * stride_x + r * ldx + col, r < M ? valid : 0, v[u]);
+    load_lane<TYPE, VEC>(X + e * stride_x + r * ldx + col, r < M ? valid : 0, v[u]);
   }
 #pragma unroll
   for (int u = 0; u < kEach; ++u) top = max(top, top_bits(v[u]));
@@ -91,55 +89,26 @@ __global__ __launch_bounds__(kBlock) void fp8_quantize_tiles_kernel(
   for (int u = 0; u < kEach; ++u) {
     const int64_t r = row0 + u * kRows;
     if (r >= M) break;
-    Words4 w = encode16(v[u], s);
-    if (valid < kLane) w = keep_first(w, valid);
-    *reinterpret_cast<Words4*>(codes + (e * M + r) * ldq + col) = w;
+    store_codes(v[u], s, valid, codes + (e * M + r) * ldq + col);
   }
-}
-
-// fp32 product of code and scale, rounded once more to a 16-bit type.
-template <int TYPE, bool VEC>
-__device__ __forceinline__ void store16(typename Elem<TYPE>::T* p, int valid, const float (&v)[kLane]) {
-  typedef typename Elem<TYPE>::T T;
-  constexpr int kWords = kLane * sizeof(T) / 16;
-  Words4 w[kWords];
-#pragma unroll
-  for (int i = 0; i < kLane * (int)sizeof(T) / 4; ++i) {
-    if (TYPE == AAAC_F32) {
-      w[i >> 2][i & 3] = __float_as_uint(v[i]);
-    } else {
-      const f32x2 f = {v[2 * i], v[2 * i + 1]};
-      w[i >> 2][i & 3] = TYPE == AAAC_BF16
-                             ? __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2))
-                             : __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
-    }
-  }
-  if (valid == kLane) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      if (VEC) reinterpret_cast<Words4*>(p)[i] = w[i];
-      else __builtin_memcpy(reinterpret_cast<uint8_t*>(p) + 16 * i, &w[i], 16);
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < kLane; ++i)
-    if (i < valid) {
-      if (sizeof(T) == 4) p[i] = (T)w[i >> 2][i & 3];
-      else p[i] = (T)(w[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
-    }
 }
 
 // per: rows that share a row of scales (128 with tiles, else 1). VEC: rows of Y start on 16 bytes; CV:
-// rows of codes do.
+// rows of codes do. Values are the fp32 products of code and scale, rounded once more to a 16-bit type.
+// fp32 values leave 16 bytes a lane, so that a wave's stores lie together (1003 x 5003: 7.9 us, with 64 bytes
+// a lane 12.7); in 16 bits 32 bytes a lane are as good (4096 x 14336: 27 us, with 16 bytes a lane 30).
+template <int TYPE> constexpr int kOutCols = TYPE == AAAC_F32 ? 4 : 16;
+template <int TYPE> constexpr int kOutSteps = TYPE == AAAC_F32 ? 4 : 2;
 template <int TYPE, bool VEC, bool CV>
 __global__ __launch_bounds__(kBlock) void fp8_dequant_kernel(
     const uint8_t* __restrict__ codes, int64_t ldq, const float* __restrict__ scales, int64_t M,
     int64_t C, int per, int64_t per_row, int64_t total, typename Elem<TYPE>::T* __restrict__ Y,
     int64_t ldy) {
+  typedef typename Elem<TYPE>::T T;
+  constexpr int V = kOutCols<TYPE>, kWords = V / 4, kOut = V * sizeof(T) / 16, kSteps = kOutSteps<TYPE>;
   const int64_t i0 = block_id() * (kBlock * kSteps) + threadIdx.x;
   const int64_t cb = fp8_blocks(C), rb = (M + per - 1) / per;
-  Words4 w[kSteps];
+  uint32_t w[kSteps][kWords];
   float s[kSteps];
   int64_t row[kSteps], col[kSteps];
 #pragma unroll
@@ -147,16 +116,17 @@ __global__ __launch_bounds__(kBlock) void fp8_dequant_kernel(
     const int64_t i = i0 + u * kBlock;
     if (i >= total) break;
     row[u] = divide(i, per_row, total);
-    col[u] = (i - row[u] * per_row) * kLane;
+    col[u] = (i - row[u] * per_row) * V;
     const uint8_t* p = codes + row[u] * ldq + col[u];
     const int64_t left = C - col[u];
-    if (left >= kLane) {
-      if (CV) w[u] = *reinterpret_cast<const Words4*>(p);
-      else __builtin_memcpy(&w[u], p, 16);
+    if (left >= V) {
+      if (CV) __builtin_memcpy(w[u], __builtin_assume_aligned(p, V), V);
+      else __builtin_memcpy(w[u], p, V);
     } else {
-      w[u] = Words4{0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int k = 0; k < kLane; ++k)
+      for (int k = 0; k < kWords; ++k) w[u][k] = 0;
+#pragma unroll
+      for (int k = 0; k < V; ++k)
         if (k < left) w[u][k >> 2] |= (uint32_t)p[k] << (8 * (k & 3));
     }
     int64_t at = row[u];
@@ -169,9 +139,9 @@ __global__ __launch_bounds__(kBlock) void fp8_dequant_kernel(
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
     if (i0 + u * kBlock >= total) break;
-    float v[kLane];
+    float v[V];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kWords; ++k) {
       const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u][k], false);
       const f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[u][k], true);
       v[4 * k] = a.x * s[u];
@@ -179,8 +149,32 @@ __global__ __launch_bounds__(kBlock) void fp8_dequant_kernel(
       v[4 * k + 2] = b.x * s[u];
       v[4 * k + 3] = b.y * s[u];
     }
+    Words4 o[kOut];
+#pragma unroll
+    for (int k = 0; k < 4 * kOut; ++k) {
+      if (TYPE == AAAC_F32) {
+        o[k >> 2][k & 3] = __float_as_uint(v[k]);
+      } else {
+        const f32x2 f = {v[(2 * k) % V], v[(2 * k + 1) % V]};
+        o[k >> 2][k & 3] = TYPE == AAAC_BF16
+                               ? __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2))
+                               : __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+      }
+    }
+    T* p = Y + row[u] * ldy + col[u];
     const int64_t left = C - col[u];
-    store16<TYPE, VEC>(Y + row[u] * ldy + col[u], left > kLane ? kLane : (int)left, v);
+    if (left >= V) {
+#pragma unroll
+      for (int k = 0; k < kOut; ++k) {
+        if (VEC) reinterpret_cast<Words4*>(p)[k] = o[k];
+        else __builtin_memcpy(reinterpret_cast<uint8_t*>(p) + 16 * k, &o[k], 16);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < V; ++k)
+        if (k < left)
+          p[k] = sizeof(T) == 4 ? (T)o[0][k & 3] : (T)(o[(k >> 3) % kOut][(k >> 1) & 3] >> (16 * (k & 1)));
+    }
   }
 }
 
@@ -201,7 +195,7 @@ hipError_t quantize_t(const void* X, int64_t E, int64_t M, int64_t C, int64_t ld
                          stream, x, M, C, ldx, stride_x, tiles, codes, ldq, Cw, scales);
     return hipGetLastError();
   }
-  const int64_t per_row = fp8_blocks(C) * (kFp8Block / kLane), total = M * per_row;
+  const int64_t per_row = fp8_blocks(C) * (kFp8Block / kCols), total = M * per_row;
   const dim3 grid = grid_of((total + kBlock * kSteps - 1) / (kBlock * kSteps));
   if (vec)
     hipLaunchKernelGGL((fp8_quantize_rows_kernel<TYPE, true>), grid, dim3(kBlock), 0, stream, x, C, ldx,
@@ -219,8 +213,9 @@ hipError_t dequant_t(const uint8_t* codes, int64_t ldq, const float* scales, int
   T* y = static_cast<T*>(Y);
   const bool vec = (uintptr_t)Y % 16 == 0 && (ldy * sizeof(T)) % 16 == 0;
   const bool cv = (uintptr_t)codes % 16 == 0 && ldq % 16 == 0;
-  const int64_t per_row = (C + kLane - 1) / kLane, total = E * M * per_row;
-  const dim3 grid = grid_of((total + kBlock * kSteps - 1) / (kBlock * kSteps));
+  const int64_t per_row = (C + kOutCols<TYPE> - 1) / kOutCols<TYPE>, total = E * M * per_row;
+  const int64_t each = kBlock * kOutSteps<TYPE>;
+  const dim3 grid = grid_of((total + each - 1) / each);
   const int per = tile ? kFp8Block : 1;
   if (vec && cv)
     hipLaunchKernelGGL((fp8_dequant_kernel<TYPE, true, true>), grid, dim3(kBlock), 0, stream, codes,

@@ -93,25 +93,24 @@ template <int TYPE, class F>
 __device__ __forceinline__ void quantize_rows(const MatmulArgs& a, int64_t t0, int nt, int cb, uint8_t* codes,
                                               int row_bytes, float* scales, int threads, F meanwhile) {
   typedef typename Elem<TYPE>::T T;
-  const int per_row = cb * (kFp8Block / kLane);
-  float v[kLane];
+  constexpr int V = 16, kLanes = kFp8Block / V;
+  const int per_row = cb * kLanes;
+  float v[V];
   auto load = [&](int i) __attribute__((always_inline)) {
     if (i >= nt * per_row) return;
-    const int row = i / per_row, col = (i - row * per_row) * kLane, left = (int)a.C - col;
+    const int row = i / per_row, col = (i - row * per_row) * V, left = (int)a.C - col;
     const int64_t x = x_row(a, t0 + row);
-    load16<TYPE, false>(static_cast<const T*>(a.x) + (x < 0 ? 0 : x) * a.ldx + col,
-                        x < 0 || left < 0 ? 0 : left > kLane ? kLane : left, v);
+    load_lane<TYPE, false>(static_cast<const T*>(a.x) + (x < 0 ? 0 : x) * a.ldx + col,
+                           x < 0 || left < 0 ? 0 : left > V ? V : left, v);
   };
   load(threadIdx.x);
   meanwhile();
   for (int i = threadIdx.x; i < nt * per_row; i += threads) {
-    const int row = i / per_row, col = (i - row * per_row) * kLane, left = (int)a.C - col;
+    const int row = i / per_row, col = (i - row * per_row) * V, left = (int)a.C - col;
     if (i >= threads) load(i);
-    const float s = scale_of(block_max_u32_t<8>(top_bits(v), 8));
-    Words4 w = encode16(v, s);
-    if (left < kLane) w = keep_first(w, left);
-    *reinterpret_cast<Words4*>(codes + row * row_bytes + col) = w;
-    if ((threadIdx.x & 7) == 0) scales[row * cb + col / kFp8Block] = s;
+    const float s = scale_of(block_max_u32_t<kLanes>(top_bits(v), kLanes));
+    store_codes(v, s, left > V ? V : left, codes + row * row_bytes + col);
+    if (threadIdx.x % kLanes == 0) scales[row * cb + col / kFp8Block] = s;
   }
 }
 
