@@ -464,10 +464,10 @@ aaac_status aaac_fp8_dequant(const uint8_t* codes, int64_t ldq, const float* sca
 /* Workspace bytes of one aaac_fp8_matmul call, 0 for an unsupported shape or where it uses none. The
  * workspace needs no particular contents and keeps none that matter. quantize: x is not FP8. */
 size_t aaac_fp8_matmul_workspace_bytes(int64_t E, int64_t R, int64_t C, int64_t T, int64_t Tx,
-                                       int quantize);
+                                       int quantize, int y_type);
 
 /* How one such call runs on the current device, as aaac_matmul_plan. */
-aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int has_ws,
+aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int y_type, int has_ws,
                                  int32_t plan[6]);
 
 /*
@@ -482,8 +482,8 @@ aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int
  *          a routed slot. Values outside [0, Tx) stand for a row of zeros. NULL: Tx = T.
  * x        AAAC_FP8: codes [Tx, ldx bytes] (16-byte aligned, ldx % 16 == 0, C <= ldx < 2^22) with x_scales
  *          fp32 [Tx, ceil(C / 128)]; else AAAC_BF16, AAAC_F16 or AAAC_F32 [Tx, C], any row stride ldx >= C,
- *          x_scales NULL: the call runs aaac_fp8_quantize into ws (which it then needs) and multiplies the
- *          result, the same bits as two calls with a workspace give.
+ *          x_scales NULL: the call quantizes x as aaac_fp8_quantize does, into ws where it needs one for
+ *          that, and multiplies the result: the same bits as two calls with a workspace give.
  * y, ws    as above. y must not overlap an input.
  * Shapes: 1 <= E <= 65535, 1 <= R < 2^31, 1 <= C < 2^21, E * R * C < 2^40, 0 <= T, Tx < 2^31, at most
  * 2^31 output tiles of 16 x 16; with rows, codes and scales of x below 2^31 bytes each.

@@ -115,8 +115,8 @@ def load(path: str = LIB_PATH):
                                       c_i64, c_vp, c_vp]),
         "aaac_fp8_dequant": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_int, c_vp, c_int,
                                      c_i64, c_vp]),
-        "aaac_fp8_matmul_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i64, c_int]),
-        "aaac_fp8_matmul_plan": (c_int, [c_i64, c_i64, c_i64, c_i64, c_int, P(ctypes.c_int32)]),
+        "aaac_fp8_matmul_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i64, c_int, c_int]),
+        "aaac_fp8_matmul_plan": (c_int, [c_i64, c_i64, c_i64, c_i64, c_int, c_int, P(ctypes.c_int32)]),
         "aaac_fp8_matmul": (c_int, [c_vp, c_i64, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_int,
                                     c_vp, c_i64, c_i64, c_i64, c_vp, c_int, c_i64, c_vp, c_size,
                                     c_vp]),
@@ -924,19 +924,21 @@ def aaac_fp8_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tensor,
 
 @functools.lru_cache(maxsize=4096)
 def fp8_matmul_workspace_bytes(E: int, R: int, C: int, T: int, Tx: int, quantize: bool,
-                               dev: int = 0) -> int:
-    """Workspace bytes of an FP8 product on GPU dev."""
+                               dtype: torch.dtype = torch.bfloat16, dev: int = 0) -> int:
+    """Workspace bytes of an FP8 product with results of dtype on GPU dev."""
     fn = (_lib or load()).aaac_fp8_matmul_workspace_bytes
     if torch.cuda.is_available():
         with torch.cuda.device(dev):
-            return int(fn(E, R, C, T, Tx, int(quantize)))
-    return int(fn(E, R, C, T, Tx, int(quantize)))
+            return int(fn(E, R, C, T, Tx, int(quantize), FLOAT_TYPES[dtype]))
+    return int(fn(E, R, C, T, Tx, int(quantize), FLOAT_TYPES[dtype]))
 
 
-def fp8_matmul_plan(E: int, R: int, C: int, T: int, has_ws: bool = True):
+def fp8_matmul_plan(E: int, R: int, C: int, T: int, has_ws: bool = True,
+                    dtype: torch.dtype = torch.bfloat16):
     """matmul_plan of an FP8 product."""
     plan = (ctypes.c_int32 * 6)()
-    _check(load().aaac_fp8_matmul_plan(E, R, C, T, int(has_ws), plan), "aaac_fp8_matmul_plan")
+    _check(load().aaac_fp8_matmul_plan(E, R, C, T, FLOAT_TYPES[dtype], int(has_ws), plan),
+           "aaac_fp8_matmul_plan")
     return tuple(plan)
 
 
@@ -973,7 +975,7 @@ def aaac_fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, 
         _i32(offsets, "offsets", E + 1)
     if rows is not None:
         _i32(rows, "rows", T)
-    need = fp8_matmul_workspace_bytes(E, R, C, T, Tx, xs is None, dev)
+    need = fp8_matmul_workspace_bytes(E, R, C, T, Tx, xs is None, y.dtype, dev)
     ws, wp, wn = _own_ws(need, ws, y, stream, what)
     _launch(what, dev, stream, codes.data_ptr(), ldw, scales.data_ptr(), E, R, C,
             None if offsets is None else offsets.data_ptr(), None if rows is None else rows.data_ptr(),

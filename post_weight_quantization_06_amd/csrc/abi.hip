@@ -555,8 +555,8 @@ aaac_status check_fp8_shape(int64_t E, int64_t M, int64_t C, int64_t ld, int64_t
 }
 
 // The sizes of an FP8 product that the queries are asked about; false for an unsupported one.
-bool fp8_query_args(int64_t E, int64_t R, int64_t C, int64_t T, MatmulArgs& a) {
-  if (E < 1 || E > 65535 || R < 1 || R >= ((int64_t)1 << 31) || C < 1 || C >= kMaxMatmulCols || T < 1 ||
+bool fp8_query_args(int64_t E, int64_t R, int64_t C, int64_t T, int y_type, MatmulArgs& a) {
+  if (!type_bytes(y_type) || E < 1 || E > 65535 || R < 1 || R >= ((int64_t)1 << 31) || C < 1 || C >= kMaxMatmulCols || T < 1 ||
       T >= ((int64_t)1 << 31))
     return false;
   a.E = (int)E;
@@ -564,6 +564,7 @@ bool fp8_query_args(int64_t E, int64_t R, int64_t C, int64_t T, MatmulArgs& a) {
   a.C = C;
   a.Cp = fp8_blocks(C) * kFp8Block;
   a.T = T;
+  a.y_type = y_type;
   return true;
 }
 
@@ -1012,17 +1013,18 @@ aaac_status aaac_fp8_dequant(const uint8_t* codes, int64_t ldq, const float* sca
 }
 
 size_t aaac_fp8_matmul_workspace_bytes(int64_t E, int64_t R, int64_t C, int64_t T, int64_t Tx,
-                                       int quantize) {
+                                       int quantize, int y_type) {
   MatmulArgs a = {};
-  if (!fp8_query_args(E, R, C, T, a) || Tx < 0 || Tx >= ((int64_t)1 << 31)) return 0;
+  if (!fp8_query_args(E, R, C, T, y_type, a) || Tx < 0 || Tx >= ((int64_t)1 << 31)) return 0;
   return fp8_matmul_ws(a, Tx, quantize != 0).bytes;
 }
 
-aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int has_ws,
+aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int y_type, int has_ws,
                                  int32_t plan[6]) {
   const char* who = "aaac_fp8_matmul_plan";
   MatmulArgs a = {};
-  if (!fp8_query_args(E, R, C, T, a))
+  if (!type_bytes(y_type)) return fail(AAAC_ERR_INVALID_ARG, "%s: y_type %d", who, y_type);
+  if (!fp8_query_args(E, R, C, T, y_type, a))
     return fail(AAAC_ERR_UNSUPPORTED_SHAPE, "%s: E=%lld R=%lld C=%lld T=%lld", who, (long long)E,
                 (long long)R, (long long)C, (long long)T);
   if (!plan) return fail(AAAC_ERR_INVALID_ARG, "%s: plan null", who);

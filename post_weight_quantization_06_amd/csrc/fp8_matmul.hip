@@ -21,8 +21,8 @@ namespace {
 // (measured: 2^16 + 2^2 gives 2^16, 2^16 + 2^3 does not), then in fp32: its sums are off by 2^-19.4 of the
 // sum of magnitudes on average over normal values, 2^-15.8 at most. That is a hundredth of half a step of
 // bf16 and a thirtieth of fp16's, so results of these types use it. fp32 results take the bf16 instruction, whose
-// sums of the same exact products are fp32 sums, at half the rate; so do the few-row kernels, which wait for
-// memory.
+// sums of the same exact products are fp32 sums, at half the rate and with a conversion for every two codes
+// (4096 x 14336 and one row of bf16, in workgroups of eight waves: 17.3 us, with the FP8 instruction 15.5).
 template <bool WIDE> struct Frag;
 template <> struct Frag<false> { u32x4 v[2]; };
 template <> struct Frag<true> { u32x4 v[4]; };
@@ -60,6 +60,11 @@ __device__ __forceinline__ f32x4 block_sum(const Frag<true>& w, const Frag<true>
   return c;
 }
 
+__device__ __forceinline__ f32x4 block_sum(const Frag<false>& w, const Frag<false>& x) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(w), operand(x), f32x4{0.0f, 0.0f, 0.0f, 0.0f},
+                                                          0, 0, 0, 0, 0, 0);
+}
+
 // A 16-byte piece without its bytes at or past `valid`.
 __device__ __forceinline__ u32x4 first_bytes(u32x4 v, int valid) {
 #pragma unroll
@@ -79,9 +84,9 @@ __device__ __forceinline__ int64_t x_row(const MatmulArgs& a, int64_t t) {
 
 // ------------------------------------------------------------------------------------------------
 // Few rows of x per matrix: the weights are read once, straight into registers, and bound the time.
-// A workgroup owns RT * 16 rows of one expert's matrix and up to NT * 16 rows of x; its waves take the
-// blocks of columns in turn, U at a time, the next U or 2 U on their way while these are multiplied, and add
-// their sums in wave order through LDS.
+// A workgroup owns RT * 16 rows of one expert's matrix and up to 16 rows of x; its waves take the blocks of
+// columns in turn, U at a time, the next U or 2 U on their way while these are multiplied, and add their sums
+// in wave order through LDS.
 // QUANTIZE: x is bf16, fp16 or fp32. Its rows are quantised into LDS, eight lanes a block, while the first
 // weights are on their way; the same codes and scales that the quantiser writes.
 // ------------------------------------------------------------------------------------------------
@@ -114,15 +119,14 @@ __device__ __forceinline__ void quantize_rows(const MatmulArgs& a, int64_t t0, i
   }
 }
 
-template <int RT, int NT, int W, bool QUANTIZE>
+template <int RT, int U, int W, bool QUANTIZE, bool WIDE>
 __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
-  constexpr int U = RT + NT > 2 ? 2 : 4;         // two groups' weights fit the registers
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = threadIdx.x & (kWave - 1), wave = wave_index();
   const int64_t id = block_id(), tile = id / a.row_blocks, rb = id % a.row_blocks;
   int e;
   int64_t t0, t1;
-  if (!find_tile(a.offsets, a.E, a.T, NT * kMfma, tile, e, t0, t1)) return;
+  if (!find_tile(a.offsets, a.E, a.T, kMfma, tile, e, t0, t1)) return;
   const int64_t r0 = rb * (RT * kMfma);
   const int l = lane & 15, q = lane >> 4;
   const int cb = (int)fp8_blocks(a.C), whole = (int)(a.C / kFp8Block);
@@ -158,11 +162,11 @@ __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
     }
   };
   Group w[2];
-  const int nt = (int)(t1 - t0 < NT * kMfma ? t1 - t0 : NT * kMfma);
+  const int nt = (int)(t1 - t0 < kMfma ? t1 - t0 : kMfma);
   const int row_bytes = few_x_bytes(a.C);
-  const uint8_t* xp[NT];
-  const float* sx[NT];
-  bool in[NT];
+  const uint8_t* xp;
+  const float* sx;
+  bool in;
   int64_t xs_blk = 1;
   if constexpr (QUANTIZE) {
     uint8_t* codes = smem;
@@ -177,64 +181,46 @@ __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
       quantize_rows<AAAC_F32>(a, t0, nt, cb, codes, row_bytes, scales, kThreads, first);
     load(w[1], wave + U * W);
     step_barrier();                              // does not wait for the weights
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int t = j * kMfma + l;
-      in[j] = t < nt;
-      xp[j] = codes + (in[j] ? t : 0) * row_bytes + 16 * q;
-      sx[j] = scales + (in[j] ? t : 0) * cb;
-    }
+    in = l < nt;
+    xp = codes + (in ? l : 0) * row_bytes + 16 * q;
+    sx = scales + (in ? l : 0) * cb;
   } else {
     load(w[0], wave);
     load(w[1], wave + U * W);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int64_t t = t0 + j * kMfma + l, x = t < t1 ? x_row(a, t) : -1;
-      in[j] = x >= 0;
-      xp[j] = static_cast<const uint8_t*>(a.x) + (in[j] ? x : 0) * a.ldx + 16 * q;
-      sx[j] = a.x_blocks + (in[j] ? x : 0) * a.xs_row;
-    }
+    const int64_t x = t0 + l < t1 ? x_row(a, t0 + l) : -1;
+    in = x >= 0;
+    xp = static_cast<const uint8_t*>(a.x) + (in ? x : 0) * a.ldx + 16 * q;
+    sx = a.x_blocks + (in ? x : 0) * a.xs_row;
     xs_blk = a.xs_blk;
   }
-  f32x4 acc[RT][NT];
+  f32x4 acc[RT][1];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < RT; ++i) acc[i][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   auto multiply = [&](const Group& w, int b0) __attribute__((always_inline)) {
-    u32x4 x[U][NT][2];
-    float f[U][NT];
+    u32x4 x[U][2];
+    float f[U];
 #pragma unroll
     for (int n = 0; n < U; ++n) {
       const int b = b0 + n * W;
-      const float fw = b < cb ? sw[b] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4* p = reinterpret_cast<const u32x4*>(xp[j] + (int64_t)b * kFp8Block + 64 * h);
-          x[n][j][h] = zero;
-          if (QUANTIZE ? b < cb : b < whole) {
-            if (in[j]) x[n][j][h] = *p;
-          } else if (b < cb) {
-            const int left = (int)a.C - b * kFp8Block - 64 * h - 16 * q;
-            if (left > 0 && in[j]) x[n][j][h] = first_bytes(*p, left < 16 ? left : 16);
-          }
+      for (int h = 0; h < 2; ++h) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(xp + (int64_t)b * kFp8Block + 64 * h);
+        x[n][h] = zero;
+        if (QUANTIZE ? b < cb : b < whole) {
+          if (in) x[n][h] = *p;
+        } else if (b < cb) {
+          const int left = (int)a.C - b * kFp8Block - 64 * h - 16 * q;
+          if (left > 0 && in) x[n][h] = first_bytes(*p, left < 16 ? left : 16);
         }
-        f[n][j] = b < cb && in[j] ? sx[j][b * xs_blk] * fw : 0.0f;
       }
+      f[n] = b < cb && in ? sx[b * xs_blk] * sw[b] : 0.0f;
     }
 #pragma unroll
     for (int n = 0; n < U; ++n) {
-      Frag<true> xf[NT];
+      const Frag<WIDE> xf = frag<WIDE>(x[n][0], x[n][1]);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) xf[j] = frag<true>(x[n][j][0], x[n][j][1]);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const Frag<true> wf = frag<true>(w[n][i][0], w[n][i][1]);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] += block_sum(wf, xf[j]) * f[n][j];
-      }
+      for (int i = 0; i < RT; ++i)
+        acc[i][0] += block_sum(frag<WIDE>(w[n][i][0], w[n][i][1]), xf) * f[n];
     }
   };
   for (int b = wave; b < cb; b += 2 * U * W) {
@@ -245,17 +231,21 @@ __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
     load(w[1], b + 3 * U * W);
   }
   if (QUANTIZE) __syncthreads();                 // the rows of x give way to the waves' sums
-  join_and_store<RT, NT, W>(a, acc, r0, t0, t1, reinterpret_cast<float*>(smem));
+  join_and_store<RT, 1, W>(a, acc, r0, t0, t1, reinterpret_cast<float*>(smem));
 }
 
-template <int RT, int NT, int W, bool QUANTIZE>
+template <int RT, int U, int W>
 hipError_t few_fp8(MatmulArgs a, hipStream_t stream) {
+  const bool quantize = a.x_type != AAAC_FP8, wide = a.y_type == AAAC_F32;
   a.row_blocks = (a.R + RT * kMfma - 1) / (RT * kMfma);
-  const int64_t grid = a.row_blocks * token_tiles(a, NT * kMfma);
-  a.x_rows = (int)(a.T < NT * kMfma ? a.T : NT * kMfma);
-  const int x_lds = QUANTIZE ? a.x_rows * (few_x_bytes(a.C) + 4 * (int)fp8_blocks(a.C)) : 0;
-  const int lds = x_lds > join_bytes<RT, NT, W>() ? x_lds : join_bytes<RT, NT, W>();
-  hipLaunchKernelGGL((few_fp8_kernel<RT, NT, W, QUANTIZE>), grid_of(grid), dim3(W * kWave), lds, stream, a);
+  const int64_t grid = a.row_blocks * token_tiles(a, kMfma);
+  a.x_rows = (int)(a.T < kMfma ? a.T : kMfma);
+  const int x_lds = quantize ? a.x_rows * (few_x_bytes(a.C) + 4 * (int)fp8_blocks(a.C)) : 0;
+  const int lds = x_lds > join_bytes<RT, 1, W>() ? x_lds : join_bytes<RT, 1, W>();
+  const auto kernel =
+      quantize ? (wide ? few_fp8_kernel<RT, U, W, true, true> : few_fp8_kernel<RT, U, W, true, false>)
+               : (wide ? few_fp8_kernel<RT, U, W, false, true> : few_fp8_kernel<RT, U, W, false, false>);
+  hipLaunchKernelGGL(kernel, grid_of(grid), dim3(W * kWave), lds, stream, a);
   return hipGetLastError();
 }
 
@@ -298,30 +288,48 @@ __device__ __forceinline__ f32x16 half_sum(const Frag<WIDE>& w, const Frag<WIDE>
   }
 }
 
-// A wave's result, FR * 32 weight rows by FT * 32 rows of x, as store_tile: a lane has row lane & 31 of x
-// and, in registers 4 g .. 4 g + 3 of a fragment, weight rows 8 g + 4 (lane >> 5) and the next three.
+// A wave's result, FR * 32 weight rows by FT * 32 rows of x. A lane has row lane & 31 of x and, in registers
+// 4 g .. 4 g + 3 of a fragment, weight rows 8 g + 4 (lane >> 5) and the next three. In 16 bits the two lanes of
+// a row of x exchange halves, so that each stores eight neighbours.
 template <int FR, int FT>
 __device__ __forceinline__ void store_big(const MatmulArgs& a, int part, const f32x16 (&acc)[FR][FT],
-                                          uint8_t* lds, int64_t t0, int64_t t1, int64_t r0) {
+                                          int64_t t0, int64_t t1, int64_t r0) {
   const int lane = threadIdx.x & (kWave - 1), l = lane & 31, q = lane >> 5;
-  const bool through = a.y_row && a.split == 1;
+  const bool pairs = a.y_row && a.split == 1;
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int64_t t = t0 + j * kBig + l;
 #pragma unroll
-    for (int i = 0; i < FR; ++i)
+    for (int i = 0; i < FR; ++i) {
+      const f32x16 c = acc[i][j];
+      if (pairs) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x16 c = acc[i][j];
-        const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
-        const int row = i * kBig + 8 * g + 4 * q;
-        if (through)
-          *reinterpret_cast<uint2*>(lds + (j * kBig + l) * row_bytes<FR * kBig>() + row * 2) = pack_16(a, v);
-        else if (t < t1 && r0 + row < a.R)
-          store_part(a, part, t, r0 + row, v);
+        for (int g = 0; g < 4; g += 2) {
+          const uint2 u = pack_16(a, f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]});
+          const uint2 v = pack_16(a, f32x4{c[4 * g + 4], c[4 * g + 5], c[4 * g + 6], c[4 * g + 7]});
+          const auto x = __builtin_amdgcn_permlane32_swap(u.x, v.x, false, false);
+          const auto y = __builtin_amdgcn_permlane32_swap(u.y, v.y, false, false);
+          const u32x4 w = {x[0], y[0], x[1], y[1]};
+          const int64_t r = r0 + i * kBig + 8 * (g + q);
+          uint16_t* p = static_cast<uint16_t*>(a.y) + t * a.ldy + r;
+          if (t < t1 && r + 8 <= a.R) {
+            *reinterpret_cast<u32x4*>(p) = w;
+          } else if (t < t1) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (r + k < a.R) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int64_t r = r0 + i * kBig + 8 * g + 4 * q;
+          if (t < t1 && r < a.R)
+            store_part(a, part, t, r, f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]});
+        }
       }
+    }
   }
-  if (through) store_rows<FR * kBig, FT * kBig>(a, lds, t0, t1, r0);
 }
 
 template <int WR, int WT, int FR, int FT, int NS, bool WIDE>
@@ -337,9 +345,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
   static_assert(kFirst * WR * kBig % (8 * NW) == 0 && (FR - kFirst) * WR * kBig % (8 * NW) == 0 &&
                 BN % (8 * NW) == 0, "whole loads a wave");
   static_assert(kXWaves < NW && FR * kBig <= kFp8Block, "the scales' loads");
-  // the stages give way to the waves' results at the end
-  constexpr int kResult = FT * kBig * row_bytes<FR * kBig>();
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage > NW * kResult ? NS * kStage : NW * kResult];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[NS * kStage];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = wave_index();
   if (block_id() >= a.blocks) return;
   // fewer than 2^32 workgroups have a tile (2^31 tiles of 16 x 16 at most)
@@ -542,9 +548,8 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
   };
   if (busy) walk(Int<1>());
   else walk(Int<0>());
-  wait_loads<0>();
-  step_barrier();
-  store_big<FR, FT>(a, (int)part, acc, &lds[0] + wave * kResult, t0 + wn, t1, r0 + wm);
+  wait_loads<0>();                               // none may reach LDS after the workgroup has ended
+  store_big<FR, FT>(a, (int)part, acc, t0 + wn, t1, r0 + wm);
 }
 
 template <int WR, int WT, int FR, int FT, int NS, bool WIDE>
@@ -573,10 +578,8 @@ hipError_t tile_fp8_any(const MatmulArgs& a, const MatmulPlan& p, hipStream_t st
 }  // namespace
 
 hipError_t launch_few_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
-  if (a.x_type != AAAC_FP8)
-    return p.rt == 2 ? few_fp8<2, 1, 8, true>(a, stream) : few_fp8<1, 1, 8, true>(a, stream);
-  if (p.nt == 1) return p.rt == 2 ? few_fp8<2, 1, 8, false>(a, stream) : few_fp8<1, 1, 8, false>(a, stream);
-  return p.rt == 2 ? few_fp8<2, 2, 8, false>(a, stream) : few_fp8<1, 2, 8, false>(a, stream);
+  if (p.rt == 4) return few_fp8<4, 1, 8>(a, stream);
+  return p.rt == 2 ? few_fp8<2, 2, 8>(a, stream) : few_fp8<1, 2, 16>(a, stream);
 }
 
 hipError_t launch_tile_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {

@@ -34,9 +34,23 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // and 12. Four chunks at a time pay on long rows: 12.6 us down to 11.9 at 14336 columns, 7.3 up to 7.8
 // at 4096.
 //
+// FP8, whose tiles stream weights as fast: the few-row kernels where they save more than a second pass over an
+// expert's weights costs. Those of an expert with more than 16 rows are read again, and the tile kernels read
+// x from LDS, so up to kFewOne rows for one matrix and kFewMean rows an expert on average, and twice as many
+// for fp32 results, whose tiles are slower. 64 experts of 2048 x 2048, bf16 x: 33 us with 100 rows (tiles 36),
+// 41 with 200 (43), 53 with 400 (46); 4096 x 14336, FP8 x: 16 us with 1 row (tiles 16), 17.6 with 8 (16.6), 21
+// with 16 (17). Up to kFewWeights codes a call is all latency, and no launch for the quantised x or the parts
+// counts more: 16 experts of 1000 x 1000 with 200 rows 12.5 us (16), 4096 x 4096 with 16 rows 15.5 (17).
+// 16 weight rows a workgroup of 16 waves where that makes no more workgroups than the CUs, 32 up to twice as
+// many, else 64, the longest run of loads for the time it takes to start and end: 4096 x 14336 with one row
+// 13.4 us (32: 18, 64: 30), 8000 x 8000 14.7 (16: 15.4, 64: 17.6), 14336 x 4096 13.1 (15.7, 14.1), 28672 x 8192
+// 40 (63, 56).
+//
 // FP8 rows of x given in another type: a workgroup of the few-row kernels quantises its own where they have
-// up to kFewQuantize elements (64 a thread), which saves a launch; more take longer than the launch does.
-constexpr int64_t kFewQuantize = 32768;
+// up to kFewQuantize elements, which saves a launch; more take longer than the launch does. An expert may have
+// four times the average, and LDS holds 16 of its rows.
+constexpr int64_t kFewOne = 8, kFewMean = 4, kFewWeights = (int64_t)1 << 25;
+constexpr int64_t kFewQuantize = 32768, kFewLds = 65536;
 
 // Tiles: the least estimated time over tile widths and splits. A tile takes its steps times kStep
 // (measured with every CU at work) and kTile to start and end; the busiest CU runs
@@ -47,32 +61,44 @@ constexpr int64_t kFewQuantize = 32768;
 // double the workgroups of a short MXFP4 product: 48 rows against 14336 x 4096 in 16.2 us, 17.0 in 128.
 // The MXFP4 step times are those of rows of whole steps; the other form's steps (tile_mxfp4_kernel) take
 // about twice as long in every tile and have no table of their own.
-struct TileCost { int bm, bn; double step; bool two; };
-constexpr TileCost kBf16Tiles[] = {{128, 32, 0.70, true}, {128, 64, 0.77, true},
-                                   {128, 128, 0.96, true}, {256, 256, 1.85, false}};
-constexpr TileCost kMxTiles[] = {{64, 64, 0.45, true}, {128, 64, 0.60, true},
-                                 {128, 128, 0.75, true}, {256, 256, 1.90, false}};
-constexpr TileCost kFp8Tiles[] = {{64, 64, 0.45, true}, {128, 64, 0.60, true},
-                                  {128, 128, 0.75, true}, {256, 256, 1.90, false}};
+//
+// The FP8 tiles' times are their own, by results: 16 bits or fp32 (which take another instruction). They
+// count that a chip at work in part runs faster (kIdle) and, on average over the experts, half a tile that is
+// empty (kLastFp8). Measured: 14336 x 4096 with 300 rows 38 us in 128 wide tiles (128 by 64: 44, 256 wide: 52,
+// split in two: 48), with 1024 rows 65 in 256 wide ones (128 wide: 79); 4096 x 14336 with 512 rows 50 in 128
+// wide ones split in two (unsplit 71, 256 wide split 8: 54); 64 experts of 2048 x 2048 with 4000 rows 62 in 128
+// wide ones (256 wide: 92), 32 of 4096 x 2048 with 16380 rows 192 in 256 wide ones (213).
+struct TileCost { int bm, bn; double step, two, tile; };
+constexpr double kOne = 0.0;                     // LDS holds one tile
 constexpr double kTile = 2.3, kTwoBf16 = 0.80, kTwoMx = 0.95, kLaunch = 3.0;
-constexpr double kPartBytes = 6e6;
+constexpr TileCost kBf16Tiles[] = {{128, 32, 0.70, kTwoBf16, kTile}, {128, 64, 0.77, kTwoBf16, kTile},
+                                   {128, 128, 0.96, kTwoBf16, kTile}, {256, 256, 1.85, kOne, kTile}};
+constexpr TileCost kMxTiles[] = {{64, 64, 0.45, kTwoMx, kTile}, {128, 64, 0.60, kTwoMx, kTile},
+                                 {128, 128, 0.75, kTwoMx, kTile}, {256, 256, 1.90, kOne, kTile}};
+constexpr TileCost kFp8Tiles[] = {{64, 64, 0.33, 0.73, 2.5}, {128, 64, 0.48, 0.72, 4.0},
+                                  {128, 128, 0.66, 0.79, 4.0}, {256, 256, 1.60, kOne, 12.0}};
+constexpr TileCost kFp8Fp32Tiles[] = {{64, 64, 0.49, 0.73, 3.5}, {128, 64, 0.66, 0.80, 6.0},
+                                      {128, 128, 1.00, 0.88, 7.0}};
+constexpr double kPartBytes = 6e6, kIdle = 0.4, kLast = 0.75, kLastFp8 = 0.5;
 
 template <int N>
-void plan_tiles(const MatmulArgs& a, const TileCost (&tiles)[N], double two, int cols, bool can_split,
-                MatmulPlan& p) {
+void plan_tiles(const MatmulArgs& a, const TileCost (&tiles)[N], int cols, double idle, double last,
+                bool can_split, MatmulPlan& p) {
   const int cus = device_cu_count();
   const int64_t steps = (a.Cp + cols - 1) / cols;
   // experts' last tiles: some are empty, and the split of the rows over the experts is not known here
-  const double extra = a.E > 1 ? 0.75 * (double)(a.E < a.T ? a.E : a.T) : 0.0;
+  const double extra = a.E > 1 ? last * (double)(a.E < a.T ? a.E : a.T) : 0.0;
   double best = 1e30;
   for (const TileCost& t : tiles) {
     const double across = a.E > 1 ? (double)a.T / t.bn + extra : (double)((a.T + t.bn - 1) / t.bn);
     const double n = (double)((a.R + t.bm - 1) / t.bm) * across;
     for (int split = 1; split <= (can_split ? 16 : 1); ++split) {
       if (split > 1 && (steps < 4 * split || n * split > 4.0 * cus)) break;
-      const double each = (double)((steps + split - 1) / split) * t.step + kTile;
+      const double each = (double)((steps + split - 1) / split) * t.step + t.tile;
       const double on_cu = n * split / cus;
-      double time = on_cu <= 1 ? each : (double)(int64_t)(on_cu + 0.999) * each * (t.two ? two : 1.0);
+      const double turns = on_cu <= 1 ? 1.0 : (double)(int64_t)(on_cu + 0.999);
+      double time = turns * each * (on_cu > 1 && t.two > 0 ? t.two : 1.0);
+      if (on_cu < 1) time *= 1.0 - idle * (1.0 - on_cu);
       if (split > 1) time += kLaunch + 8.0 * split * (double)a.T * (double)a.R / kPartBytes;
       if (time < best) {
         best = time;
@@ -91,15 +117,20 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
   p.split = 1;
   const int64_t rows = (a.T + a.E - 1) / a.E;    // rows of x an expert, on average
   if (kind == kFp8) {
-    if (rows <= kMfma || (a.E == 1 && rows <= 2 * kMfma)) {
+    const bool wide = a.y_type == AAAC_F32;
+    const int64_t most = (a.E == 1 ? kFewOne : kFewMean) * (wide ? 2 : 1);
+    if (rows <= (a.E * a.R * a.C <= kFewWeights ? kMfma : most)) {
       const int64_t blocks = (a.R + kMfma - 1) / kMfma * (a.E < a.T ? a.E : a.T);
-      p.nt = rows <= kMfma ? 1 : 2;
-      p.rt = blocks > 2 * device_cu_count() ? 2 : 1;
+      const int cus = device_cu_count();
+      const int64_t each = a.E == 1 ? rows : rows < kMfma / 4 ? 4 * rows : kMfma;
+      p.nt = 1;
+      p.rt = blocks <= cus ? 1 : blocks <= 2 * cus ? 2 : 4;
       p.chunks = 1;
-      p.quantize = p.nt == 1 && (a.E == 1 && rows < kMfma ? rows : kMfma) * a.C <= kFewQuantize;
+      p.quantize = each * a.C <= kFewQuantize && (a.T < kMfma ? a.T : kMfma) * a.C <= kFewLds;
       return p;
     }
-    plan_tiles(a, kFp8Tiles, kTwoMx, kFp8Block, can_split, p);
+    if (wide) plan_tiles(a, kFp8Fp32Tiles, kFp8Block, kIdle, kLastFp8, can_split, p);
+    else plan_tiles(a, kFp8Tiles, kFp8Block, kIdle, kLastFp8, can_split, p);
     return p;
   }
   if (rows <= kMfma || (kind == kMxMxfp4 && a.E == 1 && rows <= 2 * kMfma)) {
@@ -109,8 +140,8 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
     p.chunks = a.C >= 8192 ? 4 : 1;
     return p;
   }
-  if (kind == kMxMxfp4) plan_tiles(a, kMxTiles, kTwoMx, 256, can_split, p);
-  else plan_tiles(a, kBf16Tiles, kTwoBf16, 64, can_split, p);
+  if (kind == kMxMxfp4) plan_tiles(a, kMxTiles, 256, 0.0, kLast, can_split, p);
+  else plan_tiles(a, kBf16Tiles, 64, 0.0, kLast, can_split, p);
   return p;
 }
 

@@ -27,7 +27,7 @@ def lib():
     L = ctypes.CDLL(LIB)
     L.aaac_last_error.restype = ctypes.c_char_p
     L.aaac_fp8_matmul_workspace_bytes.restype = ctypes.c_size_t
-    L.aaac_fp8_matmul_workspace_bytes.argtypes = [i64] * 5 + [ctypes.c_int]
+    L.aaac_fp8_matmul_workspace_bytes.argtypes = [i64] * 5 + [ctypes.c_int] * 2
     L.aaac_route_workspace_bytes.restype = ctypes.c_size_t
     L.aaac_route_workspace_bytes.argtypes = [i64, i64]
     return L
@@ -144,24 +144,25 @@ def test_product_workspaces_and_plans(lib):
     need = lib.aaac_fp8_matmul_workspace_bytes
     for bad in ((0, 16, 64, 4, 4), (1, 0, 64, 4, 4), (1, 16, 0, 4, 4), (1, 16, 64, 0, 0), (1, 16, 64, 4, -1),
                 (1, 16, 1 << 21, 4, 4), (65536, 16, 64, 4, 4)):
-        assert need(*bad, 1) == 0
-    assert need(1, 16, 64, 4, 4, 0) == 0
-    assert need(1, 64, 200, 4, 4, 1) == 0        # few rows are quantized by the product itself
-    n = need(1, 64, 200, 40, 40, 1)
+        assert need(*bad, 1, BF16) == 0
+    assert need(1, 16, 64, 4, 4, 0, BF16) == need(1, 16, 64, 400, 400, 1, FP8) == 0
+    assert need(1, 64, 200, 4, 4, 1, BF16) == 0        # few rows are quantized by the product itself
+    n = need(1, 64, 200, 40, 40, 1, BF16)
     assert n >= 40 * (256 + 8)                   # codes of whole blocks and their scales
-    assert need(1, 64, 200, 40, 90, 1) > n       # of the rows of x
+    assert need(1, 64, 200, 40, 90, 1, BF16) > n       # of the rows of x
     args = dict(xt=BF16, xs=None, ldx=200, T=40, Tx=40)
     assert _mm(lib, work=FAKE, nwork=n - 1, **args) == WS_SMALL
     assert _mm(lib, work=vp((1 << 20) + 128), nwork=n, **args) == INVALID
-    split = need(1, 1024, 8192, 256, 256, 0)
+    split = need(1, 1024, 8192, 256, 256, 0, BF16)
     assert split >= 2 * 256 * 1024 * 4
     plan = (ctypes.c_int32 * 6)()
     f = lib.aaac_fp8_matmul_plan
-    assert f(i64(1), i64(1024), i64(8192), i64(256), 1, plan) == OK and plan[2] > 1
-    assert f(i64(1), i64(1024), i64(8192), i64(256), 0, plan) == OK and plan[2] == 1
-    assert f(i64(1), i64(16), i64(64), i64(4), 1, plan) == OK and list(plan[:2]) == [0, 0]
-    assert f(i64(1), i64(16), i64(64), i64(4), 1, None) == INVALID
-    assert f(i64(1), i64(16), i64(64), i64(0), 1, plan) == SHAPE
+    assert f(i64(1), i64(1024), i64(8192), i64(256), BF16, 1, plan) == OK and plan[2] > 1
+    assert f(i64(1), i64(1024), i64(8192), i64(256), BF16, 0, plan) == OK and plan[2] == 1
+    assert f(i64(1), i64(16), i64(64), i64(4), BF16, 1, plan) == OK and list(plan[:2]) == [0, 0]
+    assert f(i64(1), i64(16), i64(64), i64(4), BF16, 1, None) == INVALID
+    assert f(i64(1), i64(16), i64(64), i64(0), BF16, 1, plan) == SHAPE
+    assert f(i64(1), i64(16), i64(64), i64(4), FP8, 1, plan) == INVALID
 
 
 def _route(L, x=FAKE, xt=F32, T=4, E=64, ldl=64, bias=None, score=0, k=4, groups=1, top=1, gt=1, e=FAKE,

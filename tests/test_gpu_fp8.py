@@ -230,17 +230,21 @@ def _exact_case(E, R, C, T, dtype=torch.float32, tokens=None, junk=0x7f, grouped
 
 
 # (E, R, C, T): the few-row kernels and every tile, whole and short in every direction
-FORMS = [(0, 16, 128, 1), (0, 1, 1, 1), (0, 40, 16, 16), (0, 129, 200, 7), (0, 4096, 256, 3),
+FORMS = [(0, 16, 128, 1), (0, 1, 1, 1), (0, 40, 16, 16), (0, 129, 200, 7), (0, 4096, 256, 3), (0, 6000, 300, 5),
          (0, 12000, 130, 9), (0, 300, 1030, 32), (0, 12000, 260, 20), (0, 64, 128, 33), (0, 200, 4096, 40),
          (0, 8192, 384, 64), (0, 1000, 640, 100), (0, 515, 2048, 129), (0, 2048, 1031, 500),
-         (0, 4096, 520, 777), (0, 4000, 896, 2000), (1, 256, 256, 5), (7, 130, 300, 40), (40, 64, 129, 200),
-         (5, 200, 256, 300), (3, 1030, 272, 900), (9, 2048, 384, 3000), (64, 256, 128, 64)]
+         (0, 4096, 520, 777), (0, 4000, 896, 2000), (0, 4000, 1030, 2100), (0, 500, 8200, 1000),
+         (0, 1500, 8200, 700), (0, 3000, 8000, 600), (0, 250, 6000, 8000), (0, 3000, 8000, 1500),
+         (1, 256, 256, 5), (7, 130, 300, 40), (40, 64, 129, 200), (5, 200, 256, 300), (3, 1030, 272, 900),
+         (4, 1030, 8200, 300), (8, 1500, 1031, 500), (20, 130, 4100, 1000), (9, 2048, 384, 3000),
+         (64, 256, 128, 64)]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("E,R,C,T", FORMS)
-def test_products_of_whole_numbers_are_exact(E, R, C, T):
-    _say("fp8 product", E, R, C, T, L.fp8_matmul_plan(max(E, 1), R, C, T))
-    _exact_case(E, R, C, T)
+def test_products_of_whole_numbers_are_exact(E, R, C, T, dtype):
+    _say("fp8 product", E, R, C, T, dtype, L.fp8_matmul_plan(max(E, 1), R, C, T, dtype=dtype))
+    _exact_case(E, R, C, T, dtype)
 
 
 @pytest.mark.parametrize("E,R,C,T,tokens", [(0, 64, 128, 5, 3), (0, 130, 260, 50, 9), (6, 130, 260, 50, 9),
@@ -256,13 +260,18 @@ def test_result_types(dtype, E, R, C, T):
     _exact_case(E, R, C, T, dtype)
 
 
-def test_every_tile_and_kernel_is_reached():
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_every_tile_and_kernel_is_reached(dtype):
     got = set()
-    for E, R, C, T in FORMS + [(0, 14336, 4096, 4096), (0, 14336, 4096, 1024), (0, 1024, 8192, 256)]:
-        bm, bn, split, rt, nt, _ = L.fp8_matmul_plan(max(E, 1), R, C, T)
-        got.add((bm, bn, split > 1, rt, nt))
-    few = {(0, 0, False, rt, nt) for rt in (1, 2) for nt in (1, 2)}
-    assert few <= got, got
+    for E, R, C, T in FORMS:
+        bm, bn, split, rt, _, _ = L.fp8_matmul_plan(max(E, 1), R, C, T, dtype=dtype)
+        got.add((bm, bn, split > 1, rt))
+    want = {(0, 0, False, rt) for rt in (1, 2, 4)}
+    want |= {(64, 64, False, 0), (64, 64, True, 0), (128, 128, False, 0), (128, 128, True, 0), (128, 64, False, 0),
+             (128, 64, True, 0)}
+    if dtype is not torch.float32:               # fp32 results have no larger tile
+        want |= {(256, 256, False, 0), (256, 256, True, 0)}
+    assert want <= got, want - got
 
 
 def _bound(xv, wv, dtype, want):
@@ -337,7 +346,7 @@ def test_results_do_not_depend_on_the_workspace_or_other_rows():
     g = _gen(4)
     W = P.FP8Matrix.quantize(torch.randn(1024, 4096, generator=g).to(DEV))
     x, xs = P.fp8_quantize(torch.randn(256, 4096, generator=g).to(DEV))
-    need = L.fp8_matmul_workspace_bytes(1, 1024, 4096, 256, 256, False)
+    need = L.fp8_matmul_workspace_bytes(1, 1024, 4096, 256, 256, False, torch.float32)
     y = [torch.empty(256, 1024, device=DEV) for _ in range(2)]
     for i, fill in enumerate((0, 0xFF)):
         ws = torch.full((max(need, 256),), fill, dtype=torch.uint8, device=DEV)
