@@ -309,6 +309,74 @@ def test_quantized_in_the_call(xtype, R, C, T):
     assert torch.equal(m.matmul(codes, x_scales=scales, dtype=torch.float32), m.matmul(x.to(DEV), dtype=torch.float32))
 
 
+@pytest.mark.parametrize("xtype", TYPES)
+@pytest.mark.parametrize("E,R,C,tokens,n", [(0, 300, 4096, 8, 0), (0, 300, 4000, 3, 16), (6, 70, 200, 11, 0),
+                                            (8, 130, 4096, 16, 0), (8, 4096, 4096, 16, 0), (9, 130, 3900, 5, 17),
+                                            (20, 200, 1031, 300, 0), (8, 130, 264, 60, 400)])
+def test_quantized_in_the_call_by_experts(xtype, E, R, C, tokens, n):
+    """The same bits as the two calls, quantised by the product's own workgroups or before it. n: slots that
+    pick their row of x, some outside x."""
+    _say("fp8 quantize in the call", xtype, E, R, C, tokens, n)
+    g = _gen(E, R, C, n)
+    x = (torch.randn(tokens, C, generator=g) * torch.exp(torch.randn(C, generator=g))).to(xtype).to(DEV)
+    m = P.FP8Matrix.quantize(torch.randn(*([E] if E else []), R, C, generator=g).mul_(0.02).to(DEV))
+    codes, scales = P.fp8_quantize(x)
+    for off in [_offsets(E, n or tokens, g), torch.tensor([0] * E + [n or tokens]).int()] if E else [None]:
+        off = None if off is None else off.to(DEV)
+        rows = torch.randint(-1, tokens + 1, (n,), generator=g).int().to(DEV) if n else None
+        for dt in TYPES:
+            got = m.matmul(x, off, rows, dtype=dt)
+            assert torch.equal(got, m.matmul(codes, off, rows, x_scales=scales, dtype=dt))
+
+
+def test_rows_far_apart():
+    """Rows and matrices whose offsets pass 2^31 and 2^32 bytes."""
+    g = _gen(55)
+    far, R, C = (1 << 22) - 16, 1100, 200
+    wide = torch.empty(2 * R * far, dtype=torch.uint8, device=DEV)
+    w = wide.view(torch.float8_e4m3fn).as_strided((R, C), (far, 1))
+    x = wide.view(torch.float8_e4m3fn)[R * far:].as_strided((R, C), (far, 1))
+    w.view(torch.uint8).copy_(_whole((R, C), g).view(torch.uint8))
+    x.view(torch.uint8).copy_(_whole((R, C), g).view(torch.uint8))
+    ws, xs = _pow2((-(-R // 128), 2), g).to(DEV), _pow2((R, 2), g).to(DEV)
+    assert R * far > 1 << 32
+    y = torch.empty(R * far, dtype=torch.bfloat16, device=DEV).as_strided((R, R), (far, 1))
+    wc, xc = _aligned(w.cpu(), 0x7f), _aligned(x.cpu(), 0x7f)
+    for T in (5, 300, R):
+        _say("fp8 far", T)
+        want = P.fp8_matmul(wc, ws, xc[R - T:], x_scales=xs[R - T:])
+        got = P.fp8_matmul(w, ws, x[R - T:], x_scales=xs[R - T:], out=y[R - T:])
+        assert torch.equal(got, want)
+    codes = wide.view(torch.float8_e4m3fn).as_strided((R, R), (far, 1))
+    scales = torch.empty(R, -(-R // 128), device=DEV)
+    L.aaac_fp8_quantize(y, codes, scales)
+    cc, sc = P.fp8_quantize(y.contiguous())
+    assert torch.equal(codes.view(torch.uint8), cc.view(torch.uint8)) and torch.equal(scales, sc)
+    P.fp8_dequant(codes, scales, out=y)
+    assert torch.equal(y, P.fp8_dequant(cc, sc))
+
+
+def test_two_streams_at_once():
+    """Calls that overlap do not share what they write."""
+    _say("fp8 streams")
+    g = _gen(91)
+    W = P.FP8Matrix.quantize(torch.randn(512, 8192, generator=g).to(DEV))
+    xs = [torch.randn(T, 8192, generator=g).to(DEV) for T in (3, 40, 200, 200)]
+    want = [W.matmul(x) for x in xs]
+    sides = [torch.cuda.Stream() for _ in xs]
+    for s in sides:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[] for _ in xs]
+    for _ in range(5):
+        for i, (s, x) in enumerate(zip(sides, xs)):
+            with torch.cuda.stream(s):
+                got[i].append(W.matmul(x))
+    torch.cuda.synchronize()
+    for w, ys in zip(want, got):
+        for y in ys:
+            assert torch.equal(y, w)
+
+
 def test_nan_blocks_reach_only_their_products():
     _say("fp8 nan")
     g = _gen(77)

@@ -242,6 +242,26 @@ def test_rows_in_strided_tensors():
     assert P.rows_to_experts(base[:0], places[:0]).shape == (0, 100)
 
 
+def test_rows_far_apart():
+    """Row offsets past 2^31 elements and 2^32 bytes, of logits too."""
+    _say("rows far")
+    g = _gen(12)
+    far, T = (1 << 24) + 8, 150
+    x = torch.empty(T * far, dtype=torch.bfloat16, device=DEV).as_strided((T, 70), (far, 1))
+    out = torch.empty(2 * T * far, dtype=torch.bfloat16, device=DEV).as_strided((2 * T, 70), (far, 1))
+    x.copy_(torch.randn(T, 70, generator=g))
+    places = torch.randperm(2 * T, generator=g).view(T, 2).int().to(DEV)
+    w = torch.rand(T, 2, generator=g).to(DEV)
+    near = x.contiguous()
+    P.rows_to_experts(x, places, out)
+    assert torch.equal(out, P.rows_to_experts(near, places))
+    want = P.rows_from_experts(out.contiguous(), places, w)
+    assert torch.equal(P.rows_from_experts(out, places, w, out=x), want)
+    a, b = P.route(x, 4), P.route(x.contiguous(), 4)
+    assert torch.equal(a.experts, b.experts) and torch.equal(a.weights, b.weights)
+    assert torch.equal(a.places, b.places) and torch.equal(a.offsets, b.offsets)
+
+
 def test_infinite_rows_count_only_where_they_are_placed():
     y = torch.ones(4, 64, device=DEV)
     y[2] = INF
