@@ -843,14 +843,21 @@ def _own_ws(need: int, ws, like: torch.Tensor, stream, what: str):
 
 def _stacked(t: torch.Tensor, name: str):
     """(E, rows, columns, row stride, matrix stride) of a 2-D or 3-D tensor with unit column stride."""
-    if t.dim() not in (2, 3):
-        raise ValueError("%s must be 2-D or 3-D (got %d-D)" % (name, t.dim()))
-    M, C = t.shape[-2:]
-    if t.stride(-1) != 1 and C > 1:
+    n = t.dim()
+    if n == 2:
+        E, step = 1, 0
+        M, C = t.shape
+        ld, unit = t.stride()
+    elif n == 3:
+        E, M, C = t.shape
+        step, ld, unit = t.stride()
+    else:
+        raise ValueError("%s must be 2-D or 3-D (got %d-D)" % (name, n))
+    if unit != 1 and C > 1:
         raise ValueError("%s must have unit column stride" % name)
-    E = t.shape[0] if t.dim() == 3 else 1
-    ld = t.stride(-2) if M > 1 else (t.stride(0) if E > 1 else (C + 15) // 16 * 16)
-    return E, M, C, ld, t.stride(0) if E > 1 else 0
+    if M <= 1:                 # the stride of a single row carries nothing
+        ld = step if E > 1 else (C + 15) // 16 * 16
+    return E, M, C, ld, step if E > 1 else 0
 
 
 def _fp8_codes(t: torch.Tensor, name: str):

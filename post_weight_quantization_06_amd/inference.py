@@ -180,15 +180,14 @@ def fp8_dequant(codes: torch.Tensor, scales: torch.Tensor, dtype: torch.dtype = 
                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of FP8 codes, in `out` (then of its type) or a new tensor of `dtype`. The scales' shape
     says whether they are those of rows or of tiles (fp8_quantize)."""
-    lead, C = codes.shape[:-1], codes.shape[-1]
+    *lead, C = shape = codes.shape
     if out is None:
-        out = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-    elif out.shape != codes.shape:
-        raise ValueError("out must be shaped as the codes (got %s and %s)" % (
-            tuple(out.shape), tuple(codes.shape)))
+        out = torch.empty(shape, dtype=dtype, device=codes.device)
+    elif out.shape != shape:
+        raise ValueError("out must be shaped as the codes (got %s and %s)" % (tuple(out.shape), tuple(shape)))
     blocks = (C + 127) // 128
     if scales.shape == (*lead, blocks):
-        flat = codes.dim() == 2
+        flat = len(lead) == 1
         L.aaac_fp8_dequant(codes if flat else codes.view(-1, C), scales, out if flat else out.view(-1, C))
     elif len(lead) in (1, 2) and scales.shape == (*lead[:-1], (lead[-1] + 127) // 128, blocks):
         L.aaac_fp8_dequant(codes, scales, out, True)
