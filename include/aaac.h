@@ -550,7 +550,7 @@ aaac_status aaac_rows_to_experts(const void* x, int element, int64_t T, int64_t 
 /*
  * And back: out[t] = sum over j of weights[t, j] y[places[t, j]], in fp32 in the order of j, rounded once
  * to out_type; places outside [0, N) add nothing. y [N, C] of y_type, out [T, C] of out_type (AAAC_BF16,
- * AAAC_F16, AAAC_F32); weights fp32 [T, k]. Shapes as above.
+ * AAAC_F16, AAAC_F32); weights fp32 [T, k]; out must not overlap y. Shapes as above.
  */
 aaac_status aaac_rows_from_experts(const void* y, int y_type, int64_t N, int64_t C, int64_t ldy,
                                    const int32_t* places, const float* weights, int64_t T, int64_t k,

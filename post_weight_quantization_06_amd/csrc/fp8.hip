@@ -26,7 +26,8 @@ __device__ __forceinline__ int64_t divide(int64_t i, int64_t n, int64_t total) {
   return total <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)n) : i / n;
 }
 
-// Blocks of 1 x 128.
+// Blocks of 1 x 128. 16 columns a lane, so that a store of codes is 16 bytes (4096 x 4096 of bf16: 13 us, 8 of
+// it the bytes' at a copy's rate, with 8 columns a lane 15; 1003 x 5003 of fp32 8.0, with 4 columns 9.6).
 template <int TYPE, bool VEC>
 __global__ __launch_bounds__(kBlock) void fp8_quantize_rows_kernel(
     const typename Elem<TYPE>::T* __restrict__ X, int64_t C, int64_t ldx, int64_t per_row,
@@ -55,7 +56,8 @@ __global__ __launch_bounds__(kBlock) void fp8_quantize_rows_kernel(
   }
 }
 
-// Blocks of 128 x 128, one a workgroup.
+// Blocks of 128 x 128, one a workgroup, which holds it in registers between its maximum and its codes. 4096 x
+// 14336 of bf16: 37 us, 4.8 TB/s (with 8 columns a lane 41).
 template <int TYPE, bool VEC>
 __global__ __launch_bounds__(kBlock) void fp8_quantize_tiles_kernel(
     const typename Elem<TYPE>::T* __restrict__ X, int64_t M, int64_t C, int64_t ldx, int64_t stride_x,
