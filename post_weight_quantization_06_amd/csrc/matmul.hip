@@ -51,6 +51,17 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // four times the average, and LDS holds 16 of its rows.
 constexpr int64_t kFewOne = 8, kFewMean = 4, kFewWeights = (int64_t)1 << 25;
 constexpr int64_t kFewQuantize = 32768, kFewLds = 65536;
+//
+// With weights that every die's L2 holds (kFewAgain) they also take more rows, 16 a workgroup, where that takes
+// less than a launch (kQuantise, for rows of x in another type) more than the tiles do: 1000 x 1000 with 64 rows
+// of bf16 10.8 us (tiles 15.4), with 250 10.7 (15.4), 2000 x 2000 with 128 rows 13.1 (15.4), with 250 17.1
+// (15.2), 16 experts of 500 x 500 with 600 rows 10.9 (15.9); larger weights cost more to read again: 12866 x
+// 2022 with 27 rows 22 (16). The times of a workgroup are measured ones, `two` those of more than one a CU. The
+// choice does not look at the type of x, so that quantising inside the call and before it give the same bits.
+constexpr int64_t kFewAgain = (int64_t)1 << 23;
+struct FewCost { int rt; double start, block, two; };
+constexpr FewCost kFewFp8[] = {{1, 2.2, 0.24, 1.00}, {2, 3.0, 0.27, 0.75}, {4, 3.0, 0.36, 0.72}};
+constexpr double kQuantise = 5.0;
 
 // Tiles: the least estimated time over tile widths and splits. A tile takes its steps times kStep
 // (measured with every CU at work) and kTile to start and end; the busiest CU runs
@@ -75,14 +86,15 @@ constexpr TileCost kBf16Tiles[] = {{128, 32, 0.70, kTwoBf16, kTile}, {128, 64, 0
                                    {128, 128, 0.96, kTwoBf16, kTile}, {256, 256, 1.85, kOne, kTile}};
 constexpr TileCost kMxTiles[] = {{64, 64, 0.45, kTwoMx, kTile}, {128, 64, 0.60, kTwoMx, kTile},
                                  {128, 128, 0.75, kTwoMx, kTile}, {256, 256, 1.90, kOne, kTile}};
-constexpr TileCost kFp8Tiles[] = {{64, 64, 0.33, 0.73, 2.5}, {128, 64, 0.48, 0.72, 4.0},
-                                  {128, 128, 0.66, 0.79, 4.0}, {256, 256, 1.60, kOne, 12.0}};
+constexpr TileCost kFp8Tiles[] = {{64, 64, 0.30, 0.73, 3.5}, {128, 64, 0.46, 0.72, 4.5},
+                                  {128, 128, 0.60, 0.79, 6.0}, {256, 256, 1.60, kOne, 12.0}};
 constexpr TileCost kFp8Fp32Tiles[] = {{64, 64, 0.49, 0.73, 3.5}, {128, 64, 0.66, 0.80, 6.0},
-                                      {128, 128, 1.00, 0.88, 7.0}};
+                                      {128, 128, 1.00, 0.88, 8.5}};
 constexpr double kPartBytes = 6e6, kIdle = 0.4, kLast = 0.75, kLastFp8 = 0.5;
 
+// The estimated time, and the plan.
 template <int N>
-void plan_tiles(const MatmulArgs& a, const TileCost (&tiles)[N], int cols, double idle, double last,
+double plan_tiles(const MatmulArgs& a, const TileCost (&tiles)[N], int cols, double idle, double last,
                 bool can_split, MatmulPlan& p) {
   const int cus = device_cu_count();
   const int64_t steps = (a.Cp + cols - 1) / cols;
@@ -94,11 +106,11 @@ void plan_tiles(const MatmulArgs& a, const TileCost (&tiles)[N], int cols, doubl
     const double n = (double)((a.R + t.bm - 1) / t.bm) * across;
     for (int split = 1; split <= (can_split ? 16 : 1); ++split) {
       if (split > 1 && (steps < 4 * split || n * split > 4.0 * cus)) break;
-      const double each = (double)((steps + split - 1) / split) * t.step + t.tile;
       const double on_cu = n * split / cus;
+      const double step = t.step * (on_cu < 1 ? 1.0 - idle * (1.0 - on_cu) : 1.0);
+      const double each = (double)((steps + split - 1) / split) * step + t.tile;
       const double turns = on_cu <= 1 ? 1.0 : (double)(int64_t)(on_cu + 0.999);
       double time = turns * each * (on_cu > 1 && t.two > 0 ? t.two : 1.0);
-      if (on_cu < 1) time *= 1.0 - idle * (1.0 - on_cu);
       if (split > 1) time += kLaunch + 8.0 * split * (double)a.T * (double)a.R / kPartBytes;
       if (time < best) {
         best = time;
@@ -108,6 +120,25 @@ void plan_tiles(const MatmulArgs& a, const TileCost (&tiles)[N], int cols, doubl
       }
     }
   }
+  return best;
+}
+
+// The same of the few-row kernels for any number of rows.
+double plan_few_fp8(const MatmulArgs& a, int& rt) {
+  const int cus = device_cu_count();
+  const double tiles = a.E > 1 ? (double)a.T / kMfma + kLastFp8 * (double)(a.E < a.T ? a.E : a.T)
+                               : (double)((a.T + kMfma - 1) / kMfma);
+  double best = 1e30;
+  for (const FewCost& f : kFewFp8) {
+    const double on_cu = (double)((a.R + f.rt * kMfma - 1) / (f.rt * kMfma)) * tiles / cus;
+    const double each = f.start + f.block * (double)fp8_blocks(a.C);
+    const double time = on_cu <= 1 ? each : each * f.two * (double)(int64_t)(on_cu + 0.999);
+    if (time < best) {
+      best = time;
+      rt = f.rt;
+    }
+  }
+  return best;
 }
 
 }  // namespace
@@ -129,8 +160,16 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
       p.quantize = each * a.C <= kFewQuantize && (a.T < kMfma ? a.T : kMfma) * a.C <= kFewLds;
       return p;
     }
-    if (wide) plan_tiles(a, kFp8Fp32Tiles, kFp8Block, kIdle, kLastFp8, can_split, p);
-    else plan_tiles(a, kFp8Tiles, kFp8Block, kIdle, kLastFp8, can_split, p);
+    const double time = wide ? plan_tiles(a, kFp8Fp32Tiles, kFp8Block, kIdle, kLastFp8, can_split, p)
+                             : plan_tiles(a, kFp8Tiles, kFp8Block, kIdle, kLastFp8, can_split, p);
+    int rt;
+    if (a.E * a.R * a.C <= kFewAgain && kMfma * a.C <= kFewQuantize && plan_few_fp8(a, rt) < time + kQuantise) {
+      p = {};
+      p.split = 1;
+      p.rt = rt;
+      p.nt = p.chunks = 1;
+      p.quantize = true;
+    }
     return p;
   }
   if (rows <= kMfma || (kind == kMxMxfp4 && a.E == 1 && rows <= 2 * kMfma)) {

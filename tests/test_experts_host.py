@@ -135,7 +135,7 @@ def test_product_refusals(lib):
     for bad in (dict(E=2), dict(off=OFF2), dict(rows=OFF2), dict(w=None), dict(w=OFF8), dict(ws_=None),
                 dict(ws_=OFF2), dict(x=None), dict(x=OFF8), dict(xs=None), dict(xs=OFF2), dict(y=None),
                 dict(y=OFF2), dict(yt=FP8), dict(xt=MXFP4), dict(xt=7), dict(xt=BF16, ldx=200),
-                dict(xt=BF16, xs=None, ldx=200, T=40, Tx=40), dict(xt=F32, xs=None, ldx=200, x=OFF2)):
+                dict(xt=BF16, xs=None, C=2200, ldw=2208, ldx=2200, T=40, Tx=40), dict(xt=F32, xs=None, ldx=200, x=OFF2)):
         assert _mm(lib, **bad) == INVALID, bad
     assert _mm(lib, xt=BF16, xs=None, ldx=199, work=FAKE, nwork=1 << 20) == SHAPE
 
@@ -147,10 +147,10 @@ def test_product_workspaces_and_plans(lib):
         assert need(*bad, 1, BF16) == 0
     assert need(1, 16, 64, 4, 4, 0, BF16) == need(1, 16, 64, 400, 400, 1, FP8) == 0
     assert need(1, 64, 200, 4, 4, 1, BF16) == 0        # few rows are quantized by the product itself
-    n = need(1, 64, 200, 40, 40, 1, BF16)
-    assert n >= 40 * (256 + 8)                   # codes of whole blocks and their scales
-    assert need(1, 64, 200, 40, 90, 1, BF16) > n       # of the rows of x
-    args = dict(xt=BF16, xs=None, ldx=200, T=40, Tx=40)
+    n = need(1, 64, 2200, 40, 40, 1, BF16)
+    assert n >= 40 * (2304 + 72)                 # codes of whole blocks and their scales
+    assert need(1, 64, 2200, 40, 90, 1, BF16) > n      # of the rows of x
+    args = dict(xt=BF16, xs=None, C=2200, ldw=2208, ldx=2200, T=40, Tx=40)
     assert _mm(lib, work=FAKE, nwork=n - 1, **args) == WS_SMALL
     assert _mm(lib, work=vp((1 << 20) + 128), nwork=n, **args) == INVALID
     split = need(1, 1024, 8192, 256, 256, 0, BF16)

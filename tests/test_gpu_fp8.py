@@ -237,7 +237,8 @@ FORMS = [(0, 16, 128, 1), (0, 1, 1, 1), (0, 40, 16, 16), (0, 129, 200, 7), (0, 4
          (0, 1500, 8200, 700), (0, 3000, 8000, 600), (0, 250, 6000, 8000), (0, 3000, 8000, 1500),
          (1, 256, 256, 5), (7, 130, 300, 40), (40, 64, 129, 200), (5, 200, 256, 300), (3, 1030, 272, 900),
          (4, 1030, 8200, 300), (8, 1500, 1031, 500), (20, 130, 4100, 1000), (9, 2048, 384, 3000),
-         (64, 256, 128, 64)]
+         (64, 256, 128, 64), (0, 70, 2200, 33), (0, 515, 2100, 129), (0, 1000, 2090, 100), (5, 200, 2080, 300),
+         (40, 64, 2100, 200), (0, 300, 260, 600)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
