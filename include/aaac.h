@@ -528,7 +528,7 @@ size_t aaac_route_workspace_bytes(int64_t T, int64_t E);
  *          256-byte aligned, no particular contents.
  * Shapes: T >= 0 with T k < 2^31 (T = 0: the offsets are zeroed), 1 <= E <= 512, 1 <= k <= min(64,
  * top_groups E / groups), 1 <= top_groups <= groups <= 64, E % groups == 0. Results are bitwise
- * reproducible. One kernel up to 16 tokens, two above.
+ * reproducible. One kernel for few tokens (16 to 64, by E), two above.
  */
 aaac_status aaac_route(const void* logits, int type, int64_t T, int64_t E, int64_t ldl,
                        const float* bias, int score, int64_t k, int groups, int top_groups,

@@ -53,7 +53,8 @@ def _check(logits, k, bias=None, **kw):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 60, 4), (8, 256, 8), (9, 64, 6), (61, 60, 4),
                                    (100, 33, 33), (300, 128, 1), (70, 512, 8), (64, 300, 64),
-                                   (2100, 16, 3)])
+                                   (2100, 16, 3), (64, 64, 6), (65, 64, 6), (48, 128, 8), (49, 65, 2), (24, 256, 8),
+                                   (25, 129, 8), (16, 512, 8), (17, 257, 8)])
 def test_plain_routing(score, dtype, T, E, k):
     _say("route", score, dtype, T, E, k)
     x = torch.randn(T, E, generator=_gen(T, E, k)).mul_(2).to(dtype)
@@ -65,7 +66,8 @@ def test_plain_routing(score, dtype, T, E, k):
 @pytest.mark.parametrize("T,E,k,groups,top,gt", [
     (5, 256, 8, 8, 4, 2), (40, 256, 8, 8, 4, 1), (7, 160, 6, 8, 3, 1), (33, 60, 4, 3, 2, 2),
     (20, 64, 8, 64, 8, 2), (50, 510, 7, 5, 1, 2), (12, 96, 12, 6, 6, 2), (9, 24, 2, 12, 1, 2),
-    (300, 64, 4, 1, 1, 2)])
+    (300, 64, 4, 1, 1, 2), (24, 256, 8, 8, 4, 2), (25, 256, 8, 8, 4, 2), (64, 64, 6, 8, 3, 2),
+    (48, 128, 8, 4, 2, 2), (17, 512, 8, 8, 4, 2)])
 def test_groups_and_bias(score, T, E, k, groups, top, gt):
     _say("route groups", score, T, E, k, groups, top, gt)
     g = _gen(T, E, k, groups)
