@@ -298,43 +298,83 @@ __device__ __forceinline__ f32x16 half_sum(const Frag<WIDE>& w, const Frag<WIDE>
 
 // A wave's result, FR * 32 weight rows by FT * 32 rows of x. A lane has row lane & 31 of x and, in registers
 // 4 g .. 4 g + 3 of a fragment, weight rows 8 g + 4 (lane >> 5) and the next three. In 16 bits the two lanes of
-// a row of x exchange halves, so that each stores eight neighbours.
+// a row of x exchange halves, so that each stores eight neighbours, 16 bytes. Where they do not start on four
+// bytes (every second row of y where R is odd) a lane stores those from the second on, with the next lane's
+// first: 4096 rows against 14335 x 4096 take 243 us, with the 16 bytes on odd addresses 272, element by element
+// 366, and against 14336 x 4096 231.
 template <int FR, int FT>
 __device__ __forceinline__ void store_big(const MatmulArgs& a, int part, const f32x16 (&acc)[FR][FT],
                                           int64_t t0, int64_t t1, int64_t r0) {
   const int lane = threadIdx.x & (kWave - 1), l = lane & 31, q = lane >> 5;
-  const bool pairs = a.y_row && a.split == 1;
+  if (a.y_type == AAAC_F32 || a.split > 1) {
+#pragma unroll
+    for (int j = 0; j < FT; ++j)
+#pragma unroll
+      for (int i = 0; i < FR; ++i)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x16 c = acc[i][j];
+          const f32x4 v = {c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]};
+          const int64_t t = t0 + j * kBig + l, r = r0 + i * kBig + 8 * g + 4 * q;
+          if (t < t1 && r + 4 <= a.R && a.split == 1 && !a.y_vec)
+            __builtin_memcpy(static_cast<float*>(a.y) + t * a.ldy + r, &v, 16);
+          else if (t < t1 && r < a.R)
+            store_part(a, part, t, r, v);
+        }
+    return;
+  }
+  constexpr int kPieces = 2 * FR;                // a lane's pieces of a row of x
+  const bool shift = !a.y_row && (((uintptr_t)a.y & 2) || (a.ldy & 1)) && r0 + FR * kBig <= a.R;
 #pragma unroll
   for (int j = 0; j < FT; ++j) {
     const int64_t t = t0 + j * kBig + l;
+    uint16_t* y = static_cast<uint16_t*>(a.y) + t * a.ldy + r0;
+    auto piece = [&](int n) __attribute__((always_inline)) {
+      const f32x16 c = acc[n / 2][j];
+      const int k = n % 2 * 8;
+      const uint2 u = pack_16(a, f32x4{c[k], c[k + 1], c[k + 2], c[k + 3]});
+      const uint2 v = pack_16(a, f32x4{c[k + 4], c[k + 5], c[k + 6], c[k + 7]});
+      const auto lo = __builtin_amdgcn_permlane32_swap(u.x, v.x, false, false);
+      const auto hi = __builtin_amdgcn_permlane32_swap(u.y, v.y, false, false);
+      return u32x4{lo[0], hi[0], lo[1], hi[1]};
+    };
+    u32x4 w = piece(0);
+    if (shift) {
+      const uint32_t odd = (uintptr_t)y >> 1 & 1, bits = 16 * odd;
+      if (t < t1 && odd && q == 0) y[0] = (uint16_t)w.x;
+      y += odd + 8 * q;
 #pragma unroll
-    for (int i = 0; i < FR; ++i) {
-      const f32x16 c = acc[i][j];
-      if (pairs) {
-#pragma unroll
-        for (int g = 0; g < 4; g += 2) {
-          const uint2 u = pack_16(a, f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]});
-          const uint2 v = pack_16(a, f32x4{c[4 * g + 4], c[4 * g + 5], c[4 * g + 6], c[4 * g + 7]});
-          const auto x = __builtin_amdgcn_permlane32_swap(u.x, v.x, false, false);
-          const auto y = __builtin_amdgcn_permlane32_swap(u.y, v.y, false, false);
-          const u32x4 w = {x[0], y[0], x[1], y[1]};
-          const int64_t r = r0 + i * kBig + 8 * (g + q);
-          uint16_t* p = static_cast<uint16_t*>(a.y) + t * a.ldy + r;
-          if (t < t1 && r + 8 <= a.R) {
-            *reinterpret_cast<u32x4*>(p) = w;
-          } else if (t < t1) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (r + k < a.R) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
+      for (int n = 0; n < kPieces; ++n) {
+        const u32x4 after = n + 1 < kPieces ? piece(n + 1) : u32x4{0u, 0u, 0u, 0u};
+        // the next eight neighbours' first: the other lane's, of its next piece for the upper one
+        const auto firsts = __builtin_amdgcn_permlane32_swap(w.x, after.x, false, false);
+        const uint32_t first = q ? firsts[0] : firsts[1];
+        const u32x4 v = {__builtin_amdgcn_alignbit(w.y, w.x, bits), __builtin_amdgcn_alignbit(w.z, w.y, bits),
+                         __builtin_amdgcn_alignbit(w.w, w.z, bits), __builtin_amdgcn_alignbit(first, w.w, bits)};
+        if (t < t1) {
+          if (n + 1 < kPieces || !(odd && q)) {
+            __builtin_memcpy(y + 16 * n, &v, 16);
+          } else {
+            __builtin_memcpy(y + 16 * n, &v, 12);
+            y[16 * n + 6] = (uint16_t)v.w;
           }
         }
-      } else {
+        w = after;
+      }
+      continue;
+    }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int64_t r = r0 + i * kBig + 8 * g + 4 * q;
-          if (t < t1 && r < a.R)
-            store_part(a, part, t, r, f32x4{c[4 * g], c[4 * g + 1], c[4 * g + 2], c[4 * g + 3]});
-        }
+    for (int n = 0; n < kPieces; ++n) {
+      if (n > 0) w = piece(n);
+      const int64_t r = r0 + 16 * n + 8 * q;
+      uint16_t* p = y + 16 * n + 8 * q;
+      if (t < t1 && r + 8 <= a.R) {
+        if (a.y_row) *reinterpret_cast<u32x4*>(p) = w;
+        else __builtin_memcpy(p, &w, 16);
+      } else if (t < t1) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (r + k < a.R) p[k] = (uint16_t)(w[k >> 1] >> (16 * (k & 1)));
       }
     }
   }
