@@ -226,18 +226,6 @@ __device__ __forceinline__ void store_tile(const MatmulArgs& a, int part, const 
   store_rows<FR * kMfma, FT * kMfma>(a, lds, t0, t1, r0);
 }
 
-// Workgroups go to the eight dies in turn. Renumbered so that a die gets runs of kRun consecutive
-// tiles, as many as it works on at once, its L2 serves the rows that neighbouring tiles share. Runs
-// and not an eighth of the tiles each: a grouped call's last tiles are empty, and the dies share them
-// (8 experts of 14336 x 4096, 4093 rows: 637 us, 767 in eighths).
-constexpr int kDies = 8, kRun = 32;
-__device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
-  const int64_t whole = n / (kDies * kRun) * (kDies * kRun);
-  if (b >= whole) return b;
-  const int64_t d = b % kDies, i = b / kDies;
-  return (i / kRun * kDies + d) * kRun + i % kRun;
-}
-
 // Adds the waves' sums acc[RT][NT] in wave order and stores them. red: join_bytes of LDS.
 template <int RT, int NT, int W>
 constexpr int join_bytes() { return W * NT * kMfma * (RT * kMfma + 4) * 4; }

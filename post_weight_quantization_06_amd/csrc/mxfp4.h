@@ -29,6 +29,18 @@ __device__ __forceinline__ int64_t block_id() {
   return (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
 }
 
+// Workgroups go to the eight dies in turn. Renumbered so that a die gets runs of kRun consecutive
+// tiles, as many as it works on at once, its L2 serves the rows that neighbouring tiles share. Runs
+// and not an eighth of the tiles each: a grouped call's last tiles are empty, and the dies share them
+// (8 experts of 14336 x 4096, 4093 rows: 637 us, 767 in eighths).
+constexpr int kDies = 8, kRun = 32;
+__device__ __forceinline__ int64_t by_die(int64_t b, int64_t n) {
+  const int64_t whole = n / (kDies * kRun) * (kDies * kRun);
+  if (b >= whole) return b;
+  const int64_t d = b % kDies, i = b / kDies;
+  return (i / kRun * kDies + d) * kRun + i % kRun;
+}
+
 hipError_t launch_mxfp4_quantize(const void* X, int x_type, int64_t M, int64_t C, int64_t ldx,
                                  uint8_t* codes, uint8_t* scales, hipStream_t stream);
 hipError_t launch_mxfp4_dequant(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t C,
