@@ -436,6 +436,26 @@ def test_strided_results_and_leading_axes():
         assert W.matmul(x[:0]).shape == (0, 70)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("R,C,T", [(33, 300, 40), (515, 2100, 129), (192, 2100, 70), (1031, 2100, 700), (2049, 300, 777),
+                                   (4001, 1030, 2100), (4224, 1030, 2050), (515, 8200, 300)])
+def test_results_on_any_address(dtype, R, C, T):
+    """Rows of y that start anywhere hold the same, and nothing beside them is touched."""
+    _say("fp8 addresses", dtype, R, C, T, L.fp8_matmul_plan(1, R, C, T, dtype=dtype))
+    g = _gen(R, C, T)
+    W = P.FP8Matrix.quantize(torch.randn(R, C, generator=g).to(DEV))
+    x, xs = P.fp8_quantize(torch.randn(T, C, generator=g).to(DEV))
+    want = None
+    for start, ld in ((0, (R + 7) // 8 * 8 + 8), (0, R + 3), (1, R + 4 + R % 2), (2, R + 5), (3, R + 3 + (R + 1) % 2)):
+        buf = torch.full((T + 1, ld), 7.0, dtype=dtype, device=DEV)
+        y = buf.view(-1)[start:start + T * ld].view(T, ld)[:, :R]
+        W.matmul(x, x_scales=xs, out=y)
+        want = y.clone() if want is None else want
+        assert torch.equal(y, want)
+        y.fill_(7.0)
+        assert (buf == 7).all()
+
+
 def test_on_another_stream_and_captured():
     _say("fp8 graph")
     g = _gen(2)
