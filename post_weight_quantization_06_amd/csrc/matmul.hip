@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // for fp32 results, whose tiles are slower. 64 experts of 2048 x 2048, bf16 x: 33 us with 100 rows (tiles 36),
 // 41 with 200 (43), 53 with 400 (46); 4096 x 14336, FP8 x: 16 us with 1 row (tiles 16), 17.6 with 8 (16.6), 21
 // with 16 (17). Up to kFewWeights codes a call is all latency, and no launch for the quantised x or the parts
-// counts more: 16 experts of 1000 x 1000 with 200 rows 12.5 us (16), 4096 x 4096 with 16 rows 15.5 (17).
+// counts more: 4096 x 4096 with 16 rows 15.5 us (17).
 // 16 weight rows a workgroup of 16 waves where that makes no more workgroups than the CUs, 32 up to twice as
 // many, else 64, the longest run of loads for the time it takes to start and end: 4096 x 14336 with one row
 // 13.4 us (32: 18, 64: 30), 8000 x 8000 14.7 (16: 15.4, 64: 17.6), 14336 x 4096 13.1 (15.7, 14.1), 28672 x 8192
@@ -51,8 +51,9 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // four times the average, and LDS holds 16 of its rows.
 constexpr int64_t kFewOne = 8, kFewMean = 4, kFewWeights = (int64_t)1 << 25;
 constexpr int64_t kFewQuantize = 32768, kFewLds = 65536;
-//
-// With weights that every die's L2 holds (kFewAgain) they also take more rows, 16 a workgroup, where that takes
+
+// With small weights (kFewAgain; kFewWeights up to 16 rows an expert on average: 16 of 1000 x 1000 with 200
+// rows 12.5 us, 16 in tiles) they also take more rows, 16 a workgroup, where that takes
 // less than a launch (kQuantise, for rows of x in another type) more than the tiles do: 1000 x 1000 with 64 rows
 // of bf16 10.8 us (tiles 15.4), with 250 10.7 (15.4), 2000 x 2000 with 128 rows 13.1 (15.4), with 250 17.1
 // (15.2), 16 experts of 500 x 500 with 600 rows 10.9 (15.9); larger weights cost more to read again: 12866 x
@@ -150,7 +151,8 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
   if (kind == kFp8) {
     const bool wide = a.y_type == AAAC_F32;
     const int64_t most = (a.E == 1 ? kFewOne : kFewMean) * (wide ? 2 : 1);
-    if (rows <= (a.E * a.R * a.C <= kFewWeights ? kMfma : most)) {
+    const int64_t weights = a.E * a.R * a.C;
+    if (rows <= (a.E == 1 && weights <= kFewWeights ? kMfma : most)) {
       const int64_t blocks = (a.R + kMfma - 1) / kMfma * (a.E < a.T ? a.E : a.T);
       const int cus = device_cu_count();
       const int64_t each = a.E == 1 ? rows : rows < kMfma / 4 ? 4 * rows : kMfma;
@@ -163,7 +165,8 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
     const double time = wide ? plan_tiles(a, kFp8Fp32Tiles, kFp8Block, kIdle, kLastFp8, can_split, p)
                              : plan_tiles(a, kFp8Tiles, kFp8Block, kIdle, kLastFp8, can_split, p);
     int rt;
-    if (a.E * a.R * a.C <= kFewAgain && kMfma * a.C <= kFewQuantize && plan_few_fp8(a, rt) < time + kQuantise) {
+    if (weights <= (rows <= kMfma ? kFewWeights : kFewAgain) && kMfma * a.C <= kFewQuantize &&
+        plan_few_fp8(a, rt) < time + kQuantise) {
       p = {};
       p.split = 1;
       p.rt = rt;
