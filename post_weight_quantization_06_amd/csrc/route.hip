@@ -531,14 +531,48 @@ __global__ void no_offsets_kernel(int32_t* offsets, int n) {
 }
 
 // ------------------------------------------------------------------------------------------------
-// Rows to experts and back: bound by memory. A workgroup takes one token and 256 pieces of 16 bytes of its
-// row, which is read once and written to each of its places. Rows that do not start on 16 bytes are read and
-// written in the same pieces, unaligned (1003 x 3 rows of 5003 in bf16 there: 17 us in words of two bytes).
+// Rows to experts and back: bound by memory. A thread takes 16 bytes of a token's row, which are read once and
+// written to each of the row's places; a workgroup one token or, where rows are short, several (16384 x 4 rows
+// of 130 in bf16: 8 us there and 8 back, with one 23 and 21). Rows that do not start on 16 bytes but on four are
+// moved by words, neighbouring ones by a wave's lanes (4096 x 4 rows of 4094: 27 and 28 us, in pieces of 16
+// unaligned bytes 34 and 32, rows of 4096 26); those on any address in such pieces (rows of 4095: 37 and 34).
 // Places outside [0, N) are skipped. 8192 x 8 rows of 4096 in bf16: 87 us there and 161 back, together 4.9
 // TB/s (some of what the first writes reaches memory while the second runs).
 // ------------------------------------------------------------------------------------------------
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// What a thread takes: token t, and of its row the piece of `size` units that starts at `at`. A workgroup has
+// one token's kBlock pieces, or several tokens where rows have fewer.
+struct RowGrid {
+  int64_t T, chunks, blocks;   // workgroups a token, all workgroups
+  int per, tokens;             // threads a token, tokens a workgroup
+};
+RowGrid row_grid(int64_t T, int64_t pieces) {
+  RowGrid g;
+  g.T = T;
+  g.chunks = (pieces + kBlock - 1) / kBlock;
+  g.per = pieces < kBlock ? (int)pieces : kBlock;
+  g.tokens = kBlock / g.per;
+  g.blocks = (T + g.tokens - 1) / g.tokens * g.chunks;
+  return g;
+}
+// The thread's token, and its number among the row's; false where it has none. ONE: one token a workgroup,
+// whose places and weights are then scalar loads (8192 x 8 rows of 4096 back: 121 us, 133 otherwise).
+template <bool ONE>
+__device__ __forceinline__ bool row_place(const RowGrid& g, int64_t& t, int64_t& i) {
+  const int64_t id = block_id();
+  if (id >= g.blocks) return false;
+  if (ONE) {
+    t = id / g.chunks;
+    i = (id - t * g.chunks) * kBlock + threadIdx.x;
+    return true;
+  }
+  const int first = threadIdx.x / g.per;
+  t = id / g.chunks * g.tokens + first;
+  i = id % g.chunks * kBlock + threadIdx.x - first * g.per;
+  return first < g.tokens && t < g.T;
+}
 
 // VEC: on 16 bytes. Of the row's last piece there may be only `bytes` < 16, a multiple of the element's.
 template <bool VEC>
@@ -577,19 +611,41 @@ __device__ __forceinline__ void store_piece(uint8_t* p, int bytes, int element, 
   }
 }
 
-template <bool VEC>
+template <bool VEC, bool ONE>
 __global__ __launch_bounds__(kBlock) void rows_to_experts_kernel(
     const uint8_t* __restrict__ x, int64_t bytes, int64_t ldx, const int32_t* __restrict__ places, int k,
-    uint8_t* __restrict__ out, int64_t N, int64_t ldo, int element, int64_t chunks, int64_t blocks) {
-  const int64_t id = block_id();
-  if (id >= blocks) return;
-  const int64_t t = id / chunks, at = ((id - t * chunks) * kBlock + threadIdx.x) * 16;
+    uint8_t* __restrict__ out, int64_t N, int64_t ldo, int element, RowGrid grid) {
+  int64_t t, at;
+  if (!row_place<ONE>(grid, t, at)) return;
+  at *= 16;
   if (at >= bytes) return;
   const int left = bytes - at < 16 ? (int)(bytes - at) : 16;
   const u32x4 v = load_piece<VEC>(x + t * ldx + at, left, element);
   for (int j = 0; j < k; ++j) {
     const int64_t p = places[t * k + j];
     if (p >= 0 && p < N) store_piece<VEC>(out + p * ldo + at, left, element, v);
+  }
+}
+
+// Rows on four bytes: a wave's 64 lanes take neighbouring words, four times.
+template <bool ONE>
+__global__ __launch_bounds__(kBlock) void rows_to_experts_words_kernel(
+    const uint32_t* __restrict__ x, int64_t words, int64_t ldx, const int32_t* __restrict__ places, int k,
+    uint32_t* __restrict__ out, int64_t N, int64_t ldo, RowGrid grid) {
+  int64_t t, at;
+  if (!row_place<ONE>(grid, t, at)) return;
+  const int step = ONE ? kBlock : grid.per;
+  at += at / kBlock * (3 * kBlock);
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (at + i * step < words) v[i] = x[t * ldx + at + i * step];
+  for (int j = 0; j < k; ++j) {
+    const int64_t p = places[t * k + j];
+    if (p < 0 || p >= N) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (at + i * step < words) out[p * ldo + at + i * step] = v[i];
   }
 }
 
@@ -605,15 +661,15 @@ __device__ __forceinline__ uint32_t to_16(int type, float v) {
 }
 
 // VEC: whole pieces of y and of out on their own size.
-template <int TYPE, bool VEC>
+template <int TYPE, bool VEC, bool ONE>
 __global__ __launch_bounds__(kBlock) void rows_from_experts_kernel(
     const uint8_t* __restrict__ y, int64_t N, int64_t C, int64_t ldy, const int32_t* __restrict__ places,
     const float* __restrict__ weights, int k, uint8_t* __restrict__ out, int out_type, int64_t ldo,
-    int64_t chunks, int64_t blocks) {
+    RowGrid grid) {
   constexpr int B = TYPE == AAAC_F32 ? 4 : 2, V = 16 / B;
-  const int64_t id = block_id();
-  if (id >= blocks) return;
-  const int64_t t = id / chunks, c = ((id - t * chunks) * kBlock + threadIdx.x) * V;
+  int64_t t, c;
+  if (!row_place<ONE>(grid, t, c)) return;
+  c *= V;
   if (c >= C) return;
   const int left = C - c < V ? (int)(C - c) : V;
   float sum[V] = {};
@@ -661,23 +717,91 @@ __global__ __launch_bounds__(kBlock) void rows_from_experts_kernel(
   }
 }
 
-template <int TYPE>
+// The same for rows on four bytes, a word or its one or two columns at a time.
+template <int TYPE, bool ONE>
+__global__ __launch_bounds__(kBlock) void rows_from_experts_words_kernel(
+    const uint32_t* __restrict__ y, int64_t N, int64_t words, int64_t ldy, const int32_t* __restrict__ places,
+    const float* __restrict__ weights, int k, uint8_t* __restrict__ out, int out_type, int64_t ldo,
+    RowGrid grid) {
+  constexpr int V = TYPE == AAAC_F32 ? 1 : 2, W = 4, U = 8;
+  int64_t t, at;
+  if (!row_place<ONE>(grid, t, at)) return;
+  const int step = ONE ? kBlock : grid.per;
+  at += at / kBlock * ((W - 1) * kBlock);
+  float sum[W][V] = {};
+  for (int j0 = 0; j0 < k; j0 += U) {
+    uint32_t v[U][W];
+    float w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t p = j0 + u < k ? places[t * k + j0 + u] : -1;
+      const bool in = p >= 0 && p < N;
+      w[u] = in ? weights[t * k + j0 + u] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) v[u][i] = in && at + i * step < words ? y[p * ldy + at + i * step] : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+#pragma unroll
+        for (int c = 0; c < V; ++c)
+          sum[i][c] = __builtin_fmaf(w[u], value_at<TYPE>(u32x4{v[u][i], 0u, 0u, 0u}, c), sum[i][c]);
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    if (at + i * step >= words) break;
+    const int64_t c = (at + i * step) * V;
+    if (out_type == AAAC_F32) {
+      __builtin_memcpy(out + 4 * (t * ldo + c), sum[i], 4 * V);
+    } else {
+      uint32_t o = to_16(out_type, sum[i][0]);
+      if (V == 2) o |= to_16(out_type, sum[i][V - 1]) << 16;
+      __builtin_memcpy(out + 2 * (t * ldo + c), &o, 2 * V);
+    }
+  }
+}
+
+template <int TYPE, bool ONE>
 hipError_t from_experts(const void* y, int64_t N, int64_t C, int64_t ldy, const int32_t* places,
-                        const float* weights, int64_t T, int k, void* out, int out_type, int64_t ldo,
+                        const float* weights, int k, void* out, int out_type, int64_t ldo, const RowGrid& grid,
                         hipStream_t stream) {
-  constexpr int V = TYPE == AAAC_F32 ? 4 : 8;
+  constexpr int B = TYPE == AAAC_F32 ? 4 : 2, V = 16 / B, P = 4 / B;   // bytes a column; columns of 16, of 4
   const int ob = out_type == AAAC_F32 ? 4 : 2, store = V * ob < 16 ? V * ob : 16;
   const bool vec = (uintptr_t)y % 16 == 0 && ldy % V == 0 && C % V == 0 && (uintptr_t)out % store == 0 &&
                    (ldo * ob) % store == 0;
-  const int64_t chunks = (C + kBlock * V - 1) / (kBlock * V), blocks = T * chunks;
+  const bool word = (uintptr_t)y % 4 == 0 && ldy % P == 0 && C % P == 0;
   const uint8_t* in = static_cast<const uint8_t*>(y);
   uint8_t* to = static_cast<uint8_t*>(out);
   if (vec)
-    hipLaunchKernelGGL((rows_from_experts_kernel<TYPE, true>), grid_of(blocks), dim3(kBlock), 0, stream, in, N,
-                       C, ldy, places, weights, k, to, out_type, ldo, chunks, blocks);
+    hipLaunchKernelGGL((rows_from_experts_kernel<TYPE, true, ONE>), grid_of(grid.blocks), dim3(kBlock), 0,
+                       stream, in, N, C, ldy, places, weights, k, to, out_type, ldo, grid);
+  else if (word)
+    hipLaunchKernelGGL((rows_from_experts_words_kernel<TYPE, ONE>), grid_of(grid.blocks), dim3(kBlock), 0,
+                       stream, static_cast<const uint32_t*>(y), N, C / P, ldy / P, places, weights, k, to,
+                       out_type, ldo, grid);
   else
-    hipLaunchKernelGGL((rows_from_experts_kernel<TYPE, false>), grid_of(blocks), dim3(kBlock), 0, stream, in,
-                       N, C, ldy, places, weights, k, to, out_type, ldo, chunks, blocks);
+    hipLaunchKernelGGL((rows_from_experts_kernel<TYPE, false, ONE>), grid_of(grid.blocks), dim3(kBlock), 0,
+                       stream, in, N, C, ldy, places, weights, k, to, out_type, ldo, grid);
+  return hipGetLastError();
+}
+
+template <bool ONE>
+hipError_t to_experts(const void* x, int64_t bytes, int64_t ldx, const int32_t* places, int k, void* out,
+                      int64_t N, int64_t ldo, int element, const RowGrid& grid, hipStream_t stream) {
+  const uint64_t low = (uintptr_t)x | (uintptr_t)out | (uint64_t)bytes | (uint64_t)ldx | (uint64_t)ldo;
+  const uint8_t* in = static_cast<const uint8_t*>(x);
+  uint8_t* to = static_cast<uint8_t*>(out);
+  if (low % 16 == 0)
+    hipLaunchKernelGGL((rows_to_experts_kernel<true, ONE>), grid_of(grid.blocks), dim3(kBlock), 0, stream, in,
+                       bytes, ldx, places, k, to, N, ldo, element, grid);
+  else if (low % 4 == 0)
+    hipLaunchKernelGGL((rows_to_experts_words_kernel<ONE>), grid_of(grid.blocks), dim3(kBlock), 0, stream,
+                       static_cast<const uint32_t*>(x), bytes / 4, ldx / 4, places, k,
+                       static_cast<uint32_t*>(out), N, ldo / 4, grid);
+  else
+    hipLaunchKernelGGL((rows_to_experts_kernel<false, ONE>), grid_of(grid.blocks), dim3(kBlock), 0, stream, in,
+                       bytes, ldx, places, k, to, N, ldo, element, grid);
   return hipGetLastError();
 }
 
@@ -702,17 +826,20 @@ hipError_t launch_rows_to_experts(const void* x, int64_t T, int64_t bytes, int64
                                   const int32_t* places, int k, void* out, int64_t N, int64_t ldo,
                                   int element, hipStream_t stream) {
   if (T == 0 || bytes == 0) return hipSuccess;
-  const uint64_t low = (uintptr_t)x | (uintptr_t)out | (uint64_t)bytes | (uint64_t)ldx | (uint64_t)ldo;
-  const int64_t chunks = (bytes + kBlock * 16 - 1) / (kBlock * 16), blocks = T * chunks;
-  const uint8_t* in = static_cast<const uint8_t*>(x);
-  uint8_t* to = static_cast<uint8_t*>(out);
-  if (low % 16 == 0)
-    hipLaunchKernelGGL((rows_to_experts_kernel<true>), grid_of(blocks), dim3(kBlock), 0, stream, in, bytes,
-                       ldx, places, k, to, N, ldo, element, chunks, blocks);
-  else
-    hipLaunchKernelGGL((rows_to_experts_kernel<false>), grid_of(blocks), dim3(kBlock), 0, stream, in, bytes,
-                       ldx, places, k, to, N, ldo, element, chunks, blocks);
-  return hipGetLastError();
+  const RowGrid grid = row_grid(T, (bytes + 15) / 16);
+  return grid.tokens == 1 ? to_experts<true>(x, bytes, ldx, places, k, out, N, ldo, element, grid, stream)
+                          : to_experts<false>(x, bytes, ldx, places, k, out, N, ldo, element, grid, stream);
+}
+
+template <int TYPE>
+static hipError_t from_experts_of(const void* y, int64_t N, int64_t C, int64_t ldy, const int32_t* places,
+                                  const float* weights, int64_t T, int k, void* out, int out_type,
+                                  int64_t ldo, hipStream_t stream) {
+  constexpr int V = TYPE == AAAC_F32 ? 4 : 8;
+  const RowGrid grid = row_grid(T, (C + V - 1) / V);
+  return grid.tokens == 1
+             ? from_experts<TYPE, true>(y, N, C, ldy, places, weights, k, out, out_type, ldo, grid, stream)
+             : from_experts<TYPE, false>(y, N, C, ldy, places, weights, k, out, out_type, ldo, grid, stream);
 }
 
 hipError_t launch_rows_from_experts(const void* y, int type, int64_t N, int64_t C, int64_t ldy,
@@ -720,10 +847,10 @@ hipError_t launch_rows_from_experts(const void* y, int type, int64_t N, int64_t 
                                     void* out, int out_type, int64_t ldo, hipStream_t stream) {
   if (T == 0) return hipSuccess;
   if (type == AAAC_F32)
-    return from_experts<AAAC_F32>(y, N, C, ldy, places, weights, T, k, out, out_type, ldo, stream);
+    return from_experts_of<AAAC_F32>(y, N, C, ldy, places, weights, T, k, out, out_type, ldo, stream);
   if (type == AAAC_BF16)
-    return from_experts<AAAC_BF16>(y, N, C, ldy, places, weights, T, k, out, out_type, ldo, stream);
-  return from_experts<AAAC_F16>(y, N, C, ldy, places, weights, T, k, out, out_type, ldo, stream);
+    return from_experts_of<AAAC_BF16>(y, N, C, ldy, places, weights, T, k, out, out_type, ldo, stream);
+  return from_experts_of<AAAC_F16>(y, N, C, ldy, places, weights, T, k, out, out_type, ldo, stream);
 }
 
 }  // namespace aaac

@@ -185,7 +185,8 @@ def test_many_tokens_against_a_sort():
 # ------------------------------------------------------------------ rows to experts and back
 
 @pytest.mark.parametrize("dtype", TYPES + [torch.uint8, torch.int32])
-@pytest.mark.parametrize("T,C,k", [(1, 1, 1), (3, 8, 2), (5, 33, 4), (61, 2882, 4), (7, 4096, 8), (300, 70, 3)])
+@pytest.mark.parametrize("T,C,k", [(1, 1, 1), (3, 8, 2), (5, 33, 4), (61, 2882, 4), (7, 4096, 8), (300, 70, 3), (700, 130, 2),
+                                   (37, 1001, 3), (90, 2002, 2), (45, 2040, 1)])
 def test_rows_to_experts(dtype, T, C, k):
     _say("rows to", dtype, T, C, k)
     g = _gen(T, C, k)
@@ -205,7 +206,8 @@ def test_rows_to_experts(dtype, T, C, k):
 
 @pytest.mark.parametrize("ytype", TYPES)
 @pytest.mark.parametrize("otype", TYPES)
-@pytest.mark.parametrize("T,C,k", [(1, 1, 1), (3, 8, 2), (5, 33, 4), (61, 2882, 4), (7, 4096, 8)])
+@pytest.mark.parametrize("T,C,k", [(1, 1, 1), (3, 8, 2), (5, 33, 4), (61, 2882, 4), (7, 4096, 8), (700, 130, 2),
+                                   (37, 1001, 3), (90, 2002, 10), (45, 2040, 1)])
 def test_rows_from_experts(ytype, otype, T, C, k):
     _say("rows from", ytype, otype, T, C, k)
     g = _gen(T, C, k)
