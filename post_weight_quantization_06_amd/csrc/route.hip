@@ -535,7 +535,8 @@ __global__ void no_offsets_kernel(int32_t* offsets, int n) {
 // written to each of the row's places; a workgroup one token or, where rows are short, several (16384 x 4 rows
 // of 130 in bf16: 8 us there and 8 back, with one 23 and 21). Rows that do not start on 16 bytes but on four are
 // moved by words, neighbouring ones by a wave's lanes (4096 x 4 rows of 4094: 27 and 28 us, in pieces of 16
-// unaligned bytes 34 and 32, rows of 4096 26); those on any address in such pieces (rows of 4095: 37 and 34).
+// unaligned bytes 34 and 32, rows of 4096 26); two-byte elements on any address are put together to words there
+// (rows of 4095: 28 us, 37 in unaligned pieces), and the rest goes in such pieces (back: 34).
 // Places outside [0, N) are skipped. 8192 x 8 rows of 4096 in bf16: 87 us there and 161 back, together 4.9
 // TB/s (some of what the first writes reaches memory while the second runs).
 // ------------------------------------------------------------------------------------------------
@@ -646,6 +647,58 @@ __global__ __launch_bounds__(kBlock) void rows_to_experts_words_kernel(
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (at + i * step < words) out[p * ldo + at + i * step] = v[i];
+  }
+}
+
+// Rows of two-byte elements on any address: words at either end, put together from a thread's three elements.
+template <bool ONE>
+__global__ __launch_bounds__(kBlock) void rows_to_experts_halves_kernel(
+    const uint16_t* __restrict__ x, int64_t C, int64_t ldx, const int32_t* __restrict__ places, int k,
+    uint16_t* __restrict__ out, int64_t N, int64_t ldo, RowGrid grid) {
+  int64_t t, at;
+  if (!row_place<ONE>(grid, t, at)) return;
+  const int step = ONE ? kBlock : grid.per;
+  at += at / kBlock * (3 * kBlock);
+  uint32_t even[4], odd[4];                      // elements 2 w and the next, 2 w + 1 and the next
+  const uint16_t* row = x + t * ldx;
+  const bool from_odd = (uintptr_t)row & 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t c = 2 * (at + i * step);
+    if (c >= C) break;
+    const uint16_t* p = row + c;
+    if (c + 2 >= C) {
+      even[i] = p[0];
+      odd[i] = c + 1 < C ? p[1] : 0;
+      even[i] |= odd[i] << 16;
+    } else if (from_odd) {
+      odd[i] = *reinterpret_cast<const uint32_t*>(p + 1);
+      even[i] = p[0] | odd[i] << 16;
+    } else {
+      even[i] = *reinterpret_cast<const uint32_t*>(p);
+      odd[i] = even[i] >> 16 | (uint32_t)p[2] << 16;
+    }
+  }
+  for (int j = 0; j < k; ++j) {
+    const int64_t p = places[t * k + j];
+    if (p < 0 || p >= N) continue;
+    uint16_t* to = out + p * ldo;
+    if ((uintptr_t)to & 2) {
+      if (at == 0) to[0] = (uint16_t)even[0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t c = 2 * (at + i * step) + 1;
+        if (c + 1 < C) *reinterpret_cast<uint32_t*>(to + c) = odd[i];
+        else if (c < C) to[c] = (uint16_t)odd[i];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t c = 2 * (at + i * step);
+        if (c + 1 < C) *reinterpret_cast<uint32_t*>(to + c) = even[i];
+        else if (c < C) to[c] = (uint16_t)even[i];
+      }
+    }
   }
 }
 
@@ -799,6 +852,10 @@ hipError_t to_experts(const void* x, int64_t bytes, int64_t ldx, const int32_t* 
     hipLaunchKernelGGL((rows_to_experts_words_kernel<ONE>), grid_of(grid.blocks), dim3(kBlock), 0, stream,
                        static_cast<const uint32_t*>(x), bytes / 4, ldx / 4, places, k,
                        static_cast<uint32_t*>(out), N, ldo / 4, grid);
+  else if (element == 2)
+    hipLaunchKernelGGL((rows_to_experts_halves_kernel<ONE>), grid_of(grid.blocks), dim3(kBlock), 0, stream,
+                       static_cast<const uint16_t*>(x), bytes / 2, ldx / 2, places, k,
+                       static_cast<uint16_t*>(out), N, ldo / 2, grid);
   else
     hipLaunchKernelGGL((rows_to_experts_kernel<false, ONE>), grid_of(grid.blocks), dim3(kBlock), 0, stream, in,
                        bytes, ldx, places, k, to, N, ldo, element, grid);
