@@ -483,7 +483,8 @@ aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int
  *          past C are not used.
  * offsets  int32 [E + 1] or NULL, as above.
  * rows     int32 [T] on the device or NULL: the row of x that row t of y multiplies, such as the token of
- *          a routed slot. Values outside [0, Tx) stand for a row of zeros. NULL: Tx = T.
+ *          a routed slot. Values outside [0, Tx) stand for a row of zeros; with Tx = 0 that is every one, and
+ *          no workspace is used. NULL: Tx = T.
  * x        AAAC_FP8: codes [Tx, ldx bytes] (16-byte aligned, ldx % 16 == 0, C <= ldx < 2^22) with x_scales
  *          fp32 [Tx, ceil(C / 128)]; else AAAC_BF16, AAAC_F16 or AAAC_F32 [Tx, C], any row stride ldx >= C,
  *          x_scales NULL: the call quantizes x as aaac_fp8_quantize does, into ws where it needs one for

@@ -564,6 +564,7 @@ bool fp8_query_args(int64_t E, int64_t R, int64_t C, int64_t T, int y_type, Matm
   a.C = C;
   a.Cp = fp8_blocks(C) * kFp8Block;
   a.T = T;
+  a.Tx = T;
   a.y_type = y_type;
   return true;
 }
@@ -571,14 +572,14 @@ bool fp8_query_args(int64_t E, int64_t R, int64_t C, int64_t T, int y_type, Matm
 // Where an FP8 product's workspace holds what: the parts of split sums, then quantized rows of x (codes
 // [Tx, Cp], zeros past C, and scales a block at a time, [Cp / 128, Tx]) where the product does not
 // quantize them itself.
-MatmulWs fp8_matmul_ws(const MatmulArgs& a, int64_t Tx, bool quantize) {
+MatmulWs fp8_matmul_ws(const MatmulArgs& a, bool quantize) {
   MatmulWs w;
   const MatmulPlan p = plan_matmul(a, kFp8, true);
   const size_t parts = parts_bytes(a, p);
-  quantize = quantize && !p.quantize;
+  quantize = quantize && !p.quantize && a.Tx > 0;
   w.codes = (parts + 255) / 256 * 256;
-  w.scales = w.codes + (size_t)Tx * (size_t)a.Cp;
-  w.bytes = quantize ? w.scales + (size_t)Tx * (size_t)(a.Cp / kFp8Block) * sizeof(float) : parts;
+  w.scales = w.codes + (size_t)a.Tx * (size_t)a.Cp;
+  w.bytes = quantize ? w.scales + (size_t)a.Tx * (size_t)(a.Cp / kFp8Block) * sizeof(float) : parts;
   return w;
 }
 
@@ -1016,7 +1017,8 @@ size_t aaac_fp8_matmul_workspace_bytes(int64_t E, int64_t R, int64_t C, int64_t 
                                        int quantize, int y_type) {
   MatmulArgs a = {};
   if (!fp8_query_args(E, R, C, T, y_type, a) || Tx < 0 || Tx >= ((int64_t)1 << 31)) return 0;
-  return fp8_matmul_ws(a, Tx, quantize != 0).bytes;
+  a.Tx = Tx;
+  return fp8_matmul_ws(a, quantize != 0).bytes;
 }
 
 aaac_status aaac_fp8_matmul_plan(int64_t E, int64_t R, int64_t C, int64_t T, int y_type, int has_ws,
@@ -1090,11 +1092,11 @@ aaac_status aaac_fp8_matmul(const uint8_t* w_codes, int64_t ldw, const float* w_
   a.x_blocks = x_scales;
   a.xs_row = fp8_blocks(C);
   a.xs_blk = 1;
-  a.x_type = x_type;
+  a.x_type = Tx > 0 ? x_type : AAAC_FP8;         // nothing to quantize
   const MatmulPlan p = plan_matmul(a, kFp8, ws != nullptr);
-  const bool first = quantize && !p.quantize;    // x is quantized by a kernel of its own
+  const bool first = a.x_type != AAAC_FP8 && !p.quantize;    // x is quantized by a kernel of its own
   if (ws || first) {
-    const MatmulWs w = fp8_matmul_ws(a, Tx, first);
+    const MatmulWs w = fp8_matmul_ws(a, first);
     if (!ws || !aligned(ws, 256))
       return fail(AAAC_ERR_INVALID_ARG, "%s: ws null or not 256-byte aligned", who);
     if (ws_bytes < w.bytes)

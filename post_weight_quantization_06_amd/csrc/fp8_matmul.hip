@@ -412,7 +412,7 @@ __global__ __launch_bounds__(WR * WT * kWave, 2) void tile_fp8_kernel(MatmulArgs
   const int64_t r0 = (int64_t)rb * BM;
   const int nr = (int)(a.R - r0 < BM ? a.R - r0 : BM), nt = (int)(t1 - t0 < BN ? t1 - t0 : BN);
   const int64_t cb = fp8_blocks(a.C), rbs = fp8_blocks(a.R);
-  // buffers end with the 16-byte piece that holds their last column
+  // buffers end with the 16-byte piece that holds their last column; x has a row (plan_matmul), so none is empty
   const u32x4 wr = rows_buffer(a.codes + ((int64_t)e * a.R + r0) * a.ldw,
                                ((nr - 1) * a.ldw + a.C + 15) & ~(int64_t)15);
   const int64_t x0 = a.pick ? 0 : t0, xn = a.pick ? a.Tx : nt;

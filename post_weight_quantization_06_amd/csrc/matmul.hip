@@ -149,6 +149,13 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
   p.split = 1;
   const int64_t rows = (a.T + a.E - 1) / a.E;    // rows of x an expert, on average
   if (kind == kFp8) {
+    if (a.Tx == 0) {
+      // no row of x: those that are picked are zeros. The few-row kernels read nothing of such an x; the
+      // tiles' buffers of rows hold one row at least.
+      p.rt = 4;
+      p.nt = p.chunks = 1;
+      return p;
+    }
     const bool wide = a.y_type == AAAC_F32;
     const int64_t most = (a.E == 1 ? kFewOne : kFewMean) * (wide ? 2 : 1);
     const int64_t weights = a.E * a.R * a.C;

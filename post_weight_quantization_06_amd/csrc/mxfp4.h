@@ -63,7 +63,7 @@ struct MatmulArgs {
   const uint8_t* x_scales;     // with codes: [T, Cp / 32]
   int64_t T, ldx;
   const int32_t* pick;         // FP8: [T] row of x for each row of y, or NULL
-  int64_t Tx;                  // FP8: rows of x
+  int64_t Tx;                  // FP8: rows of x; the few-row kernels alone take none
   int64_t ldw;                 // FP8: bytes between rows of codes of the weights
   const float* x_blocks;       // FP8: scale of row t, block b at t * xs_row + b * xs_blk
   int64_t xs_row, xs_blk;

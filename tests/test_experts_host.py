@@ -165,6 +165,16 @@ def test_product_workspaces_and_plans(lib):
     assert f(i64(1), i64(16), i64(64), i64(4), FP8, 1, plan) == INVALID
 
 
+@pytest.mark.parametrize("E,R,C,T", [(1, 4096, 4096, 100), (1, 70, 2200, 33), (1, 1024, 8192, 256),
+                                     (8, 1500, 1031, 500), (1, 4000, 896, 2000), (1, 16, 64, 4)])
+def test_an_x_without_rows_needs_no_workspace(lib, E, R, C, T):
+    """Such a product runs without parts and without quantized rows, also where one with rows is split or
+    quantizes them first: the tiles, which take no empty x, are not chosen."""
+    for yt in (BF16, F16, F32):
+        for quantize in (0, 1):
+            assert lib.aaac_fp8_matmul_workspace_bytes(E, R, C, T, 0, quantize, yt) == 0
+
+
 def _route(L, x=FAKE, xt=F32, T=4, E=64, ldl=64, bias=None, score=0, k=4, groups=1, top=1, gt=1, e=FAKE,
            w=FAKE, off=FAKE, rows=FAKE, places=FAKE, work=None, nwork=0):
     return L.aaac_route(x, xt, i64(T), i64(E), i64(ldl), bias, score, i64(k), groups, top, gt, 1,

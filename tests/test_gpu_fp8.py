@@ -513,3 +513,30 @@ def test_refusals_of_the_calls():
         W.matmul(x, rows=torch.zeros(4, dtype=torch.int64, device=DEV))
     with pytest.raises(L.AAACError):             # every row the same memory
         P.fp8_quantize(torch.zeros(1, 64, device=DEV).expand(4, 64))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,R,C,T", [(0, 64, 128, 5), (0, 70, 2100, 33), (0, 4096, 4096, 100), (0, 1024, 8192, 256),
+                                     (0, 4000, 896, 2000), (8, 1500, 1031, 500), (40, 64, 2100, 200)])
+def test_an_x_without_rows_is_rows_of_zeros(E, R, C, T, dtype):
+    """Every index lies outside an x without rows: zeros where the offsets reach, whatever kernel an x with
+    rows would take, and rows of no expert stay."""
+    _say("fp8 no rows of x", E, R, C, T, dtype)
+    g = _gen(E, R, C, T)
+    n = max(E, 1)
+    codes, ws = _aligned(_whole((n, R, C), g), 0x7f), _pow2((n, -(-R // 128), -(-C // 128)), g).to(DEV)
+    if not E:
+        codes, ws = codes[0], ws[0]
+    off = torch.cat([torch.tensor([2]), _offsets(E, T, g)[1:-1].clamp(2, T - 1), torch.tensor([T - 1])]).int() if E else None
+    want = torch.full((T, R), 55.0, dtype=dtype)
+    want[slice(2, T - 1) if E else slice(0, T)] = 0.0
+    rows = torch.randint(-2, 3, (T,), generator=g).int().to(DEV)
+    off = None if off is None else off.to(DEV)
+    none = torch.empty(0, -(-C // 128), device=DEV)
+    for xt in TYPES:
+        out = torch.full((T, R), 55.0, dtype=dtype, device=DEV)
+        P.fp8_matmul(codes, ws, torch.empty(0, C, dtype=xt, device=DEV), off, rows, out=out)
+        assert torch.equal(out.cpu(), want)
+    out = torch.full((T, R), 55.0, dtype=dtype, device=DEV)
+    P.fp8_matmul(codes, ws, torch.empty(0, C, dtype=torch.float8_e4m3fn, device=DEV), off, rows, none, out)
+    assert torch.equal(out.cpu(), want)
