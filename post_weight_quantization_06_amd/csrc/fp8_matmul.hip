@@ -216,7 +216,8 @@ __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
           if (left > 0 && in) x[n][h] = first_bytes(*p, left < 16 ? left : 16);
         }
       }
-      f[n] = b < cb && in ? sx[b * xs_blk] * sw[b] : 0.0f;
+      // a row that is none has the scale 0, as in the tiles: by an infinite scale of weights it is NaN too
+      f[n] = b < cb ? (in ? sx[b * xs_blk] : 0.0f) * sw[b] : 0.0f;
     }
 #pragma unroll
     for (int n = 0; n < U; ++n) {

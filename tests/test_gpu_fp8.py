@@ -540,3 +540,25 @@ def test_an_x_without_rows_is_rows_of_zeros(E, R, C, T, dtype):
     out = torch.full((T, R), 55.0, dtype=dtype, device=DEV)
     P.fp8_matmul(codes, ws, torch.empty(0, C, dtype=torch.float8_e4m3fn, device=DEV), off, rows, none, out)
     assert torch.equal(out.cpu(), want)
+
+
+def test_rows_outside_x_times_infinite_scales():
+    """A row of zeros times a weight of infinite value is NaN in the few-row kernels and in the tiles, for codes
+    as for rows that the call quantizes."""
+    g = _gen(41)
+    codes = _aligned(torch.ones(300, 2200).to(torch.float8_e4m3fn))
+    scales = torch.ones(3, 18, device=DEV)
+    scales[1, 2] = float("inf")
+    x = torch.randn(7, 2200, generator=g).to(DEV)
+    xc, xs = P.fp8_quantize(x)
+    for T in (5, 100):
+        assert (L.fp8_matmul_plan(1, 300, 2200, T)[0] == 0) == (T == 5)
+        _say("fp8 infinite scales", T)
+        rows = torch.randint(0, 7, (T,), generator=g).int()
+        rows[1], rows[3] = -1, 7
+        want = torch.zeros(2, 300)
+        want[:, 128:256] = float("nan")
+        for dt in TYPES:
+            for kw in (dict(x=x), dict(x=xc, x_scales=xs)):
+                y = P.fp8_matmul(codes, scales, rows=rows.to(DEV), dtype=dt, **kw)[[1, 3]].float().cpu()
+                assert torch.equal(torch.isnan(y), torch.isnan(want)) and (y.nan_to_num(0.0) == 0).all()
