@@ -19,10 +19,12 @@ namespace {
 //
 // The FP8 instruction adds eight products at a time, aligned to the largest and cut below 2^-13 of it
 // (measured: 2^16 + 2^2 gives 2^16, 2^16 + 2^3 does not), then in fp32: its sums are off by 2^-19.4 of the
-// sum of magnitudes on average over normal values, 2^-15.8 at most. That is a hundredth of half a step of
-// bf16 and a thirtieth of fp16's, so results of these types use it. fp32 results take the bf16 instruction, whose
-// sums of the same exact products are fp32 sums, at half the rate and with a conversion for every two codes
-// (4096 x 14336 and one row of bf16, in workgroups of eight waves: 17.3 us, with the FP8 instruction 15.5).
+// sum of magnitudes on average over normal values, 2^-15.8 at most. Over a product of normal values that is
+// 1.4e-5 of the result's norm at any number of columns, a 118th of what the rounding to bf16 is off by (1.66e-3),
+// so results of that type use it. It would be a fifteenth of the rounding to fp16 (2.1e-4), and 140 times what
+// fp32 sums are off by (1e-7): those results take the bf16 instruction, whose sums of the same exact products are
+// fp32 sums, at half the rate and with a conversion for every two codes (4096 x 14336 and one row of bf16: 14 us,
+// with the FP8 instruction 13; 14336 x 4096 and 48 rows 25 and 18, 4096 rows 445 and 249 with fp16 results).
 template <bool WIDE> struct Frag;
 template <> struct Frag<false> { u32x4 v[2]; };
 template <> struct Frag<true> { u32x4 v[4]; };
@@ -240,7 +242,7 @@ __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
 
 template <int RT, int U, int W>
 hipError_t few_fp8(MatmulArgs a, hipStream_t stream) {
-  const bool quantize = a.x_type != AAAC_FP8, wide = a.y_type == AAAC_F32;
+  const bool quantize = a.x_type != AAAC_FP8, wide = a.y_type != AAAC_BF16;
   a.row_blocks = (a.R + RT * kMfma - 1) / (RT * kMfma);
   const int64_t grid = a.row_blocks * token_tiles(a, kMfma);
   a.x_rows = (int)(a.T < kMfma ? a.T : kMfma);
@@ -632,7 +634,7 @@ hipError_t launch_few_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t 
 }
 
 hipError_t launch_tile_fp8(const MatmulArgs& a, const MatmulPlan& p, hipStream_t stream) {
-  return a.y_type == AAAC_F32 ? tile_fp8_any<true>(a, p, stream) : tile_fp8_any<false>(a, p, stream);
+  return a.y_type == AAAC_BF16 ? tile_fp8_any<false>(a, p, stream) : tile_fp8_any<true>(a, p, stream);
 }
 
 }  // namespace aaac

@@ -37,7 +37,7 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // FP8, whose tiles stream weights as fast: the few-row kernels where they save more than a second pass over an
 // expert's weights costs. Those of an expert with more than 16 rows are read again, and the tile kernels read
 // x from LDS, so up to kFewOne rows for one matrix and kFewMean rows an expert on average, and twice as many
-// for fp32 results, whose tiles are slower. 64 experts of 2048 x 2048, bf16 x: 33 us with 100 rows (tiles 36),
+// for fp32 and fp16 results, whose tiles are slower. 64 experts of 2048 x 2048, bf16 x: 33 us with 100 rows (tiles 36),
 // 41 with 200 (43), 53 with 400 (46); 4096 x 14336, FP8 x: 16 us with 1 row (tiles 16), 17.6 with 8 (16.6), 21
 // with 16 (17). Up to kFewWeights codes a call is all latency, and no launch for the quantised x or the parts
 // counts more: 4096 x 4096 with 16 rows 15.5 us (17).
@@ -74,7 +74,7 @@ constexpr double kQuantise = 5.0;
 // The MXFP4 step times are those of rows of whole steps; the other form's steps (tile_mxfp4_kernel) take
 // about twice as long in every tile and have no table of their own.
 //
-// The FP8 tiles' times are their own, by results: 16 bits or fp32 (which take another instruction). They
+// The FP8 tiles' times are their own, by results: bf16, or fp32 and fp16 (which take another instruction). They
 // count that a chip at work in part runs faster (kIdle) and, on average over the experts, half a tile that is
 // empty (kLastFp8). Measured: 14336 x 4096 with 300 rows 38 us in 128 wide tiles (128 by 64: 44, 256 wide: 52,
 // split in two: 48), with 1024 rows 65 in 256 wide ones (128 wide: 79); 4096 x 14336 with 512 rows 50 in 128
@@ -89,7 +89,7 @@ constexpr TileCost kMxTiles[] = {{64, 64, 0.45, kTwoMx, kTile}, {128, 64, 0.60, 
                                  {128, 128, 0.75, kTwoMx, kTile}, {256, 256, 1.90, kOne, kTile}};
 constexpr TileCost kFp8Tiles[] = {{64, 64, 0.30, 0.73, 3.5}, {128, 64, 0.46, 0.72, 4.5},
                                   {128, 128, 0.60, 0.79, 6.0}, {256, 256, 1.60, kOne, 12.0}};
-constexpr TileCost kFp8Fp32Tiles[] = {{64, 64, 0.49, 0.73, 3.5}, {128, 64, 0.66, 0.80, 6.0},
+constexpr TileCost kFp8WideTiles[] = {{64, 64, 0.49, 0.73, 3.5}, {128, 64, 0.66, 0.80, 6.0},
                                       {128, 128, 1.00, 0.88, 8.5}};
 constexpr double kPartBytes = 6e6, kIdle = 0.4, kLast = 0.75, kLastFp8 = 0.5;
 
@@ -156,7 +156,7 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
       p.nt = p.chunks = 1;
       return p;
     }
-    const bool wide = a.y_type == AAAC_F32;
+    const bool wide = a.y_type != AAAC_BF16;     // sums by the bf16 instruction
     const int64_t most = (a.E == 1 ? kFewOne : kFewMean) * (wide ? 2 : 1);
     const int64_t weights = a.E * a.R * a.C;
     if (rows <= (a.E == 1 && weights <= kFewWeights ? kMfma : most)) {
@@ -169,7 +169,7 @@ MatmulPlan plan_matmul(const MatmulArgs& a, MatmulKind kind, bool can_split) {
       p.quantize = each * a.C <= kFewQuantize && (a.T < kMfma ? a.T : kMfma) * a.C <= kFewLds;
       return p;
     }
-    const double time = wide ? plan_tiles(a, kFp8Fp32Tiles, kFp8Block, kIdle, kLastFp8, can_split, p)
+    const double time = wide ? plan_tiles(a, kFp8WideTiles, kFp8Block, kIdle, kLastFp8, can_split, p)
                              : plan_tiles(a, kFp8Tiles, kFp8Block, kIdle, kLastFp8, can_split, p);
     int rt;
     if (weights <= (rows <= kMfma ? kFewWeights : kFewAgain) && kMfma * a.C <= kFewQuantize &&

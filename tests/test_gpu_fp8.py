@@ -562,3 +562,14 @@ def test_rows_outside_x_times_infinite_scales():
             for kw in (dict(x=x), dict(x=xc, x_scales=xs)):
                 y = P.fp8_matmul(codes, scales, rows=rows.to(DEV), dtype=dt, **kw)[[1, 3]].float().cpu()
                 assert torch.equal(torch.isnan(y), torch.isnan(want)) and (y.nan_to_num(0.0) == 0).all()
+
+
+@pytest.mark.parametrize("R,C,T", [(515, 4096, 5), (515, 4096, 100), (4096, 8192, 300), (2048, 2048, 700)])
+def test_fp16_results_are_rounded_fp32_sums(R, C, T):
+    """Results of 11 bits come from the same sums as fp32 ones: those rounded once, bit for bit."""
+    _say("fp8 fp16", R, C, T, L.fp8_matmul_plan(1, R, C, T, dtype=torch.float16))
+    g = _gen(R, C, T)
+    W = P.FP8Matrix.quantize(torch.randn(R, C, generator=g).mul_(0.02).to(DEV))
+    x = torch.randn(T, C, generator=g).to(DEV)
+    assert torch.equal(W.matmul(x, dtype=torch.float16), W.matmul(x, dtype=torch.float32).half())
+    assert L.fp8_matmul_plan(1, R, C, T, dtype=torch.float16) == L.fp8_matmul_plan(1, R, C, T, dtype=torch.float32)
