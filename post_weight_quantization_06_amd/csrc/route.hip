@@ -204,11 +204,11 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int64_t t, int lanes_p
   int which[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) which[v] = v;
-  // l or bias -inf: 0, also past the lane's last expert
+  // l or bias -inf, a NaN beside it or not (the minimum is then the other): 0, also past the lane's last expert
   if constexpr (EXACT) {
     auto take = [&](int v, double s) __attribute__((always_inline)) {
       const Key k = key_of(s + (double)bias[v]);
-      key[v] = l[v] != l[v] ? ~(Key)0 : fminf(l[v], bias[v]) == -INFINITY ? 0 : k;
+      key[v] = fminf(l[v], bias[v]) == -INFINITY ? 0 : l[v] != l[v] ? ~(Key)0 : k;
     };
     if (a.sigmoid) {
 #pragma unroll

@@ -269,8 +269,9 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax", bias: Optional[t
     (fp32 [E], for balance), weighted by the score alone: divided by its sum over the chosen ones with
     renormalize, times scale. With groups, the experts form that many groups of neighbours, and only the
     top_groups (default: all) with the largest best value (group_top 1) or sum of the two best (2) take
-    part. Equals go to the lowest index. An expert whose logit or bias is -inf is left out, so a row of
-    -inf (a padded batch's) gets no expert; the type's lowest value is a number like any other."""
+    part. Equals go to the lowest index. An expert whose logit or bias is -inf is left out, whatever the
+    other is, so a row of -inf (a padded batch's) gets no expert; the type's lowest value is a number like
+    any other."""
     if not isinstance(k, int) or k < 1:
         raise ValueError("k must be a positive whole number (got %r)" % (k,))
     inputs = L._route_inputs(logits, bias, score)

@@ -413,3 +413,23 @@ def test_refusals_of_the_calls():
         P.rows_from_experts(x, places, torch.ones(4, 2, device=DEV, requires_grad=True))
     with pytest.raises(ValueError):
         P.rows_from_experts(x, places, torch.ones(4, 2, device=DEV), out=torch.empty(4, 15, device=DEV))
+
+
+def test_nan_logits_of_masked_experts():
+    """A bias of -inf leaves an expert out whatever its logit is, also a NaN."""
+    g = _gen(17)
+    for T in (6, 90):
+        x = torch.randn(T, 48, generator=g)
+        bias = torch.randn(48, generator=g).mul_(0.1)
+        bias[5], bias[17] = -INF, -INF
+        bad = x.clone()
+        bad[:, 5], bad[1::2, 17] = float("nan"), float("nan")
+        for kw in ({}, {"groups": 6, "top_groups": 2, "group_top": 2}, {"groups": 4, "top_groups": 1}):
+            r = _check(x, 7, bias, score="sigmoid", **kw)
+            q = P.route(bad.to(DEV), 7, score="sigmoid", bias=bias.to(DEV), **kw)
+            for a, b in zip(vars(r).values(), vars(q).values()):
+                assert torch.equal(a, b)
+            # and a NaN bias leaves no expert in whose logit is -inf
+            x2, b2 = x.clone(), bias.clone()
+            x2[:, 9], b2[9] = -INF, float("nan")
+            assert not (P.route(x2.to(DEV), 7, score="sigmoid", bias=b2.to(DEV), **kw).experts == 9).any()
