@@ -620,11 +620,11 @@ def _on_gpu(what: str, *tensors):
     return first
 
 
-def _no_grad(what: str, x: torch.Tensor):
+def _no_grad(what: str, x: torch.Tensor, name: str = "x"):
     if x.requires_grad and torch.is_grad_enabled():
-        raise ValueError("%s has no gradient: call it under torch.no_grad() or detach x" % what)
+        raise ValueError("%s has no gradient: call it under torch.no_grad() or detach %s" % (what, name))
     if unpack_dual(x).tangent is not None:     # 0.3 us of a call
-        raise ValueError("%s has no forward-mode gradient: detach x, which carries a tangent" % what)
+        raise ValueError("%s has no forward-mode gradient: detach %s, which carries a tangent" % (what, name))
 
 
 def _launch(name: str, dev: int, stream, *args):
@@ -916,6 +916,8 @@ def aaac_fp8_dequant(codes: torch.Tensor, scales: torch.Tensor, Y: torch.Tensor,
     """Y [M, C] (or [E, M, C], its matrices one after the other) = the values of the codes."""
     what = "aaac_fp8_dequant"
     dev = _on_gpu(what, codes, scales, Y)
+    _no_grad(what, codes, "codes")
+    _no_grad(what, scales, "scales")
     yt = _float_type(Y, "Y")
     E, M, C, ldq = _fp8_codes(codes, "codes")
     Ey, My, Cy, ldy, step = _stacked(Y, "Y")
@@ -959,15 +961,17 @@ def aaac_fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor, 
     None: T = Tx. offsets: int32 [E + 1] (see aaac.h), or None for one matrix."""
     what = "aaac_fp8_matmul"
     dev = _on_gpu(what, codes, scales, x, y, offsets, rows, x_scales, ws)
+    for t, name in ((codes, "codes"), (scales, "scales"), (x, "x")):
+        _no_grad(what, t, name)
     E, R, C, ldw = _fp8_codes(codes, "codes")
     _f32(scales, "scales", E * _blocks(R) * _blocks(C))
     if x.dim() != 2:
         raise ValueError("%s: x must be 2-D (got %d-D)" % (what, x.dim()))
     if x_scales is None:
-        _no_grad(what, x)
         xt, xs = _float_type(x, "x"), None
         Tx, K, ldx = _rows(x, "x")
     else:
+        _no_grad(what, x_scales, "x_scales")
         _, Tx, K, ldx = _fp8_codes(x, "x")
         xt, xs = FP8, x_scales.data_ptr()
         _f32(x_scales, "x_scales", Tx * _blocks(K))

@@ -573,3 +573,26 @@ def test_fp16_results_are_rounded_fp32_sums(R, C, T):
     x = torch.randn(T, C, generator=g).to(DEV)
     assert torch.equal(W.matmul(x, dtype=torch.float16), W.matmul(x, dtype=torch.float32).half())
     assert L.fp8_matmul_plan(1, R, C, T, dtype=torch.float16) == L.fp8_matmul_plan(1, R, C, T, dtype=torch.float32)
+
+
+def test_scales_with_a_gradient_are_refused():
+    W = P.FP8Matrix.quantize(torch.randn(64, 200, device=DEV))
+    x, xs = P.fp8_quantize(torch.randn(4, 200, device=DEV))
+    ws = W.scales.clone().requires_grad_()
+    for call in (lambda: P.fp8_matmul(W.codes, ws, x, x_scales=xs), lambda: P.fp8_dequant(W.codes, ws),
+                 lambda: W.matmul(x, x_scales=xs.clone().requires_grad_()),
+                 lambda: P.fp8_matmul(W.codes, ws, torch.randn(4, 200, device=DEV)),
+                 lambda: P.fp8_matmul(W.codes.detach().requires_grad_(), W.scales, torch.randn(4, 200, device=DEV)),
+                 lambda: P.fp8_matmul(W.codes, W.scales, x.detach().requires_grad_(), x_scales=xs),
+                 lambda: P.fp8_dequant(W.codes.detach().requires_grad_(), W.scales),
+                 lambda: P.fp8_dequant(x, xs.clone().requires_grad_())):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad():
+            call()
+    with torch.autograd.forward_ad.dual_level():
+        dual = torch.autograd.forward_ad.make_dual(W.scales, torch.ones_like(W.scales))
+        with pytest.raises(ValueError, match="tangent"):
+            P.fp8_matmul(W.codes, dual, x, x_scales=xs)
+        with pytest.raises(ValueError, match="tangent"):
+            P.fp8_dequant(W.codes, dual)
