@@ -900,13 +900,21 @@ def _fp8_quantize(X: torch.Tensor, codes: torch.Tensor, ldq: int, scales: torch.
 def aaac_fp8_quantize(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, tile: bool = False,
                       stream=None):
     """codes e4m3 like X [M, C] (or with tile [E, M, C]) in rows whose stride is a multiple of 16, and
-    scales fp32 [M, ceil(C/128)] (with tile [E, ceil(M/128), ceil(C/128)])."""
+    scales fp32 [M, ceil(C/128)] (with tile [E, ceil(M/128), ceil(C/128)]). Each row's columns from C to the
+    next multiple of 16 are zeroed: a single row, too, needs a stride that holds them, and the storage has
+    to reach so far."""
     what = "aaac_fp8_quantize"
     dev = _on_gpu(what, X, codes, scales)
     if codes.shape != X.shape:
         raise ValueError("%s: codes must be shaped as X (got %s and %s)" % (
             what, tuple(codes.shape), tuple(X.shape)))
     E, M, C, ldq = _fp8_codes(codes, "codes")
+    wide = (C + 15) // 16 * 16
+    if wide > C and E * M > 0 and (
+            codes.stride(-2) < wide or
+            codes.storage_offset() + (E * M - 1) * ldq + wide > codes.untyped_storage().nbytes()):
+        raise ValueError("%s: rows of codes are padded to whole 16 bytes, these have no room for it (strides %s)" % (
+            what, codes.stride()))
     _f32(scales, "scales", (E * _blocks(M) if tile else E * M) * _blocks(C))
     _fp8_quantize(X, codes, ldq, scales, tile, dev, stream)
 

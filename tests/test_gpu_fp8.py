@@ -596,3 +596,23 @@ def test_scales_with_a_gradient_are_refused():
             P.fp8_matmul(W.codes, dual, x, x_scales=xs)
         with pytest.raises(ValueError, match="tangent"):
             P.fp8_dequant(W.codes, dual)
+
+
+def test_one_row_of_codes_between_others():
+    """A single row's codes are padded to 16 bytes inside their own row only; where they have no such room the
+    call is refused."""
+    x = torch.randn(1, 100, generator=_gen(23)).to(DEV)
+    scales = torch.empty(1, 1, device=DEV)
+    buf = torch.full((9, 100), 0x55, dtype=torch.uint8, device=DEV)
+    with pytest.raises(ValueError, match="16"):
+        L.aaac_fp8_quantize(x, buf.view(torch.float8_e4m3fn)[4:5], scales)       # starts on 16 bytes
+    assert (buf == 0x55).all()
+    with pytest.raises(ValueError, match="16"):              # the row's padding would lie behind the storage
+        L.aaac_fp8_quantize(x, torch.empty(100, dtype=torch.float8_e4m3fn, device=DEV).as_strided((1, 100), (112, 1)), scales)
+    wide = torch.full((3, 128), 0x55, dtype=torch.uint8, device=DEV)
+    L.aaac_fp8_quantize(x, wide.view(torch.float8_e4m3fn)[1:2, :100], scales)
+    assert np.array_equal(wide[1:2, :100].cpu().numpy(), ref.fp8_encode(x.double().cpu().numpy())[0])
+    assert (wide[1, 100:112] == 0).all() and (wide[1, 112:] == 0x55).all() and (wide[[0, 2]] == 0x55).all()
+    for n in (96, 112):                                      # whole 16 bytes need no room
+        L.aaac_fp8_quantize(x[:, :n] if n < 100 else torch.randn(1, n, device=DEV),
+                            torch.empty(1, n, dtype=torch.float8_e4m3fn, device=DEV), scales)
