@@ -559,10 +559,11 @@ bool fp8_query_args(int64_t E, int64_t R, int64_t C, int64_t T, int y_type, Matm
   if (!type_bytes(y_type) || E < 1 || E > 65535 || R < 1 || R >= ((int64_t)1 << 31) || C < 1 || C >= kMaxMatmulCols || T < 1 ||
       T >= ((int64_t)1 << 31))
     return false;
+  a.Cp = fp8_blocks(C) * kFp8Block;
+  if (R > ((((int64_t)1 << 40) - 1) / a.Cp) / E) return false;
   a.E = (int)E;
   a.R = R;
   a.C = C;
-  a.Cp = fp8_blocks(C) * kFp8Block;
   a.T = T;
   a.Tx = T;
   a.y_type = y_type;

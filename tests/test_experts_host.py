@@ -165,6 +165,18 @@ def test_product_workspaces_and_plans(lib):
     assert f(i64(1), i64(16), i64(64), i64(4), FP8, 1, plan) == INVALID
 
 
+def test_queries_of_weights_past_2_to_40(lib):
+    """The products refuse E * R * C of 2^40 and more, so the queries do: no bytes and no plan."""
+    plan = (ctypes.c_int32 * 6)()
+    for E, R, C in ((65535, (1 << 31) - 1, (1 << 21) - 1), (1, 1 << 30, 1024), (65535, (1 << 13) + 1, 1 << 11)):
+        for T in (4, 40, 4000):
+            for yt in (BF16, F32):
+                assert lib.aaac_fp8_matmul_workspace_bytes(E, R, C, T, T, 1, yt) == 0
+                assert lib.aaac_fp8_matmul_plan(i64(E), i64(R), i64(C), i64(T), yt, 1, plan) == SHAPE
+        assert _mm(lib, E=E, R=R, C=C, ldw=1 << 21, ldx=1 << 21, ldy=R, off=FAKE) == SHAPE
+    assert lib.aaac_fp8_matmul_plan(i64(1), i64(1 << 30), i64(896), i64(4), BF16, 1, plan) == OK
+
+
 @pytest.mark.parametrize("E,R,C,T", [(1, 4096, 4096, 100), (1, 70, 2200, 33), (1, 1024, 8192, 256),
                                      (8, 1500, 1031, 500), (1, 4000, 896, 2000), (1, 16, 64, 4)])
 def test_an_x_without_rows_needs_no_workspace(lib, E, R, C, T):
