@@ -242,6 +242,7 @@ __global__ __launch_bounds__(W * kWave, 1) void few_fp8_kernel(MatmulArgs a) {
 
 template <int RT, int U, int W>
 hipError_t few_fp8(MatmulArgs a, hipStream_t stream) {
+  static_assert(W * kWave <= kGridThreads, "a grid's threads");
   const bool quantize = a.x_type != AAAC_FP8, wide = a.y_type != AAAC_BF16;
   a.row_blocks = (a.R + RT * kMfma - 1) / (RT * kMfma);
   const int64_t grid = a.row_blocks * token_tiles(a, kMfma);

@@ -20,8 +20,10 @@ __host__ __device__ __forceinline__ int64_t mx_blocks(int64_t C) {
 // A grid of `blocks` workgroups numbered by block_id(). A dimension of a grid holds fewer than 2^32
 // threads (a launch of more is cut without an error), so long grids go over two; the last workgroups
 // may then lie past `blocks`.
+constexpr int kGridThreads = 1024;               // of a workgroup at most, those of few_fp8's sixteen waves
 inline dim3 grid_of(int64_t blocks) {
-  constexpr int64_t kRow = (int64_t)1 << 22;     // workgroups of at most 512 threads
+  constexpr int64_t kRow = (int64_t)1 << 21;
+  static_assert(kRow * kGridThreads < (int64_t)1 << 32, "a row's threads");
   if (blocks <= kRow) return dim3((unsigned)blocks);
   return dim3((unsigned)kRow, (unsigned)((blocks + kRow - 1) / kRow));
 }

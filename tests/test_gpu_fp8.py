@@ -616,3 +616,19 @@ def test_one_row_of_codes_between_others():
     for n in (96, 112):                                      # whole 16 bytes need no room
         L.aaac_fp8_quantize(x[:, :n] if n < 100 else torch.randn(1, n, device=DEV),
                             torch.empty(1, n, dtype=torch.float8_e4m3fn, device=DEV), scales)
+
+
+def test_grids_of_two_rows():
+    """More workgroups than one row of a grid holds: every tile of the result is there."""
+    g = _gen(61)
+    R, C, T = 64 * 1024 + 64, 16, 16 * 2048
+    W, x = _whole((R, C), g), _whole((T, C), g)
+    ws, xs = torch.ones(-(-R // 128), 1, device=DEV), torch.ones(T, 1, device=DEV)
+    y = torch.full((T, R), 55.0, dtype=torch.bfloat16, device=DEV)
+    _say("fp8 grid", L.fp8_matmul_plan(1, R, C, T))
+    P.fp8_matmul(W.to(DEV), ws, torch.empty(0, C, device=DEV), rows=torch.zeros(T, dtype=torch.int32, device=DEV), out=y)
+    assert not y.any()                           # (R / 64) (T / 16) workgroups, 2^21 and some
+    P.fp8_matmul(W.to(DEV), ws, x.to(DEV), x_scales=xs, out=y)
+    wf, xf = W.float().to(DEV), x.float().to(DEV)
+    for t in range(0, T, 1024):                  # whole numbers up to 64
+        assert torch.equal(y[t:t + 1024], (xf[t:t + 1024] @ wf.t()).to(torch.bfloat16))
