@@ -632,3 +632,51 @@ def test_grids_of_two_rows():
     wf, xf = W.float().to(DEV), x.float().to(DEV)
     for t in range(0, T, 1024):                  # whole numbers up to 64
         assert torch.equal(y[t:t + 1024], (xf[t:t + 1024] @ wf.t()).to(torch.bfloat16))
+
+
+def test_rows_do_not_depend_on_other_rows():
+    """A result's row is the same whatever the other rows of x hold, in every kernel that a plan picks."""
+    for E, R, C, T, dt in ((0, 515, 4096, 5, torch.bfloat16), (0, 515, 4096, 5, torch.float32), (0, 300, 260, 600, torch.bfloat16),
+                           (0, 1024, 4096, 256, torch.bfloat16), (0, 1024, 4096, 256, torch.float16),
+                           (0, 8192, 384, 64, torch.bfloat16), (0, 4000, 896, 2000, torch.bfloat16),
+                           (0, 4000, 896, 2000, torch.float32), (4, 1030, 8200, 300, torch.bfloat16)):
+        _say("fp8 other rows", E, R, C, T, dt, L.fp8_matmul_plan(max(E, 1), R, C, T, dtype=dt))
+        g = _gen(E, R, C, T)
+        W = P.FP8Matrix.quantize(torch.randn(*([E] if E else []), R, C, generator=g).to(DEV))
+        off = _offsets(E, T, g).to(DEV) if E else None
+        x = torch.randn(T, C, generator=g).to(DEV)
+        other = torch.randn(T, C, generator=g).to(DEV) * 1000
+        other[::7] = float("nan")
+        for same in ([0], [T - 1], list(range(1, T, 2))):
+            mixed = other.clone()
+            mixed[same] = x[same]
+            assert torch.equal(W.matmul(x, off, dtype=dt)[same], W.matmul(mixed, off, dtype=dt)[same])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E,R,C,T", [(0, 70, 300, 5), (0, 8192, 384, 64), (0, 200, 4096, 40), (0, 1024, 8192, 256),
+                                     (0, 4000, 896, 2000), (7, 130, 300, 40), (4, 1030, 8200, 300), (9, 2048, 384, 3000)])
+def test_rows_by_an_index_are_copied_rows(E, R, C, T, dtype):
+    """One row of x for all, few and many, in the few-row kernels, tiles and split tiles: the bits that copied
+    rows give, zeros for indices outside x."""
+    _say("fp8 index", E, R, C, T, dtype, L.fp8_matmul_plan(max(E, 1), R, C, T, dtype=dtype))
+    g = _gen(E, R, C, T)
+    W = P.FP8Matrix.quantize(torch.randn(*([E] if E else []), R, C, generator=g).to(DEV))
+    off = _offsets(E, T, g).to(DEV) if E else None
+    for tokens in (1, 3, T, 2 * T + 1):
+        xc, xs = P.fp8_quantize(torch.randn(tokens, C, generator=g).to(DEV))
+        rows = torch.randint(-1, tokens + 1, (T,), generator=g).int().to(DEV)
+        rows[T // 2] = tokens - 1
+        ok = ((rows >= 0) & (rows < tokens))[:, None]
+        at = rows.long().clamp(0, tokens - 1)
+        copied = _aligned((xc.view(torch.uint8)[at] * ok).view(torch.float8_e4m3fn).cpu())
+        want = W.matmul(copied, off, x_scales=(xs[at] * ok).contiguous(), dtype=dtype)
+        assert torch.equal(W.matmul(xc, off, rows, x_scales=xs, dtype=dtype), want)
+
+
+def test_indexed_rows_reach_every_kind_of_plan():
+    got = {(bm > 0, split > 1) for bm, _, split, *_ in (
+        L.fp8_matmul_plan(max(E, 1), R, C, T) for E, R, C, T in (
+            (0, 70, 300, 5), (0, 8192, 384, 64), (0, 200, 4096, 40), (0, 1024, 8192, 256), (0, 4000, 896, 2000),
+            (7, 130, 300, 40), (4, 1030, 8200, 300), (9, 2048, 384, 3000)))}
+    assert got == {(False, False), (True, False), (True, True)}
