@@ -515,7 +515,7 @@ size_t aaac_route_workspace_bytes(int64_t T, int64_t E);
  * one, where a group has only one left), and only the top_groups largest groups take part. The k largest
  * v are chosen, in descending order; the lower index first among equals, of groups too. Values are
  * compared in 64 bits, and where neither a bias nor a sum over a group enters, by the logits themselves.
- * A NaN ranks above every number.
+ * A NaN ranks above every number: a logit's shows in the weights, a bias's puts its expert first and leaves them.
  * Weights: s of the chosen experts, without the bias, divided by their sum with `renormalize` (a sum of
  * zero gives zeros), times `scale`.
  * logits   [T, E] of type AAAC_BF16, AAAC_F16 or AAAC_F32, row stride ldl >= E elements.

@@ -41,7 +41,7 @@ struct RouteArgs {
   int32_t* offsets;            // [E + 1]
   int32_t* rows;               // [T k]
   int32_t* places;             // [T, k]
-  int32_t* counts;             // [blocks, E]: a block's rows of each expert; unused with one block
+  int32_t* counts;             // [blocks, E up to whole fours]: a block's rows of each expert; unused with one block
   int per_block;               // tokens of a block, set by the launcher
   bool vec;                    // set by the launcher: a lane's logits lie on their whole size
 };

@@ -11,7 +11,7 @@
 // The choice is made on exact keys: scores are monotonous in the logits, so without a bias (and unless
 // scores are added up for groups) the logits themselves are compared; otherwise the values are computed
 // in 64 bits, where a single precision's rounding would reorder neighbours. A NaN ranks above every
-// number and shows in the weights.
+// number; a logit's shows in the weights, which no bias enters.
 #include "aaac.h"
 #include "fp8.h"
 

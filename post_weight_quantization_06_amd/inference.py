@@ -243,7 +243,9 @@ class FP8Matrix:
 
 @dataclasses.dataclass
 class Routing:
-    """Which experts T tokens go to, and the places of their rows in expert order."""
+    """Which experts T tokens go to, and the places of their rows in expert order. `route` makes experts, weights,
+    rows and places as parts of one tensor: one that is kept holds the memory of all four, and one that is saved
+    or has to outlive the others is cloned first."""
     experts: torch.Tensor        # int32 [T, k], best first, -1 where none is left
     weights: torch.Tensor        # float32 [T, k], 0 there
     offsets: torch.Tensor        # int32 [E + 1]: expert e has the places offsets[e] .. offsets[e + 1] - 1

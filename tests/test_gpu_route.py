@@ -433,3 +433,17 @@ def test_nan_logits_of_masked_experts():
             x2, b2 = x.clone(), bias.clone()
             x2[:, 9], b2[9] = -INF, float("nan")
             assert not (P.route(x2.to(DEV), 7, score="sigmoid", bias=b2.to(DEV), **kw).experts == 9).any()
+
+
+def test_nan_bias_ranks_first_and_leaves_the_weights():
+    """A NaN bias puts its expert first for every token; weights are scores, which no bias enters."""
+    x = torch.randn(30, 16, generator=_gen(18))
+    bias = torch.zeros(16)
+    bias[11] = float("nan")
+    for score in ("softmax", "sigmoid"):
+        r = P.route(x.to(DEV), 3, score=score, bias=bias.to(DEV), renormalize=False)
+        assert (r.experts[:, 0] == 11).all()
+        s = torch.sigmoid(x.double()) if score == "sigmoid" else torch.softmax(x.double(), 1)
+        want = s.gather(1, r.experts.long().cpu())
+        # one rounding to fp32, and a softmax's 64-bit sum
+        assert ((r.weights.double().cpu() - want).abs() <= 2 * 2.0 ** -24 * want).all()
