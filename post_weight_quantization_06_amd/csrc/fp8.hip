@@ -26,7 +26,7 @@ __device__ __forceinline__ int64_t divide(int64_t i, int64_t n, int64_t total) {
   return total <= 0xffffffffll ? (int64_t)((uint32_t)i / (uint32_t)n) : i / n;
 }
 
-// Blocks of 1 x 128. 16 columns a lane, so that a store of codes is 16 bytes (4096 x 4096 of bf16: 13 us, 8 of
+// Blocks of 1 x 128. 16 columns a lane, so that a store of codes is 16 bytes (4096 x 4096 of bf16: 13 us, 9.6 of
 // it the bytes' at a copy's rate, with 8 columns a lane 15; 1003 x 5003 of fp32 8.0, with 4 columns 9.6).
 template <int TYPE, bool VEC>
 __global__ __launch_bounds__(kBlock) void fp8_quantize_rows_kernel(

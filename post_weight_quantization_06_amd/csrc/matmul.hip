@@ -38,12 +38,16 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // expert's weights costs. Those of an expert with more than 16 rows are read again, and the tile kernels read
 // x from LDS, so up to kFewOne rows for one matrix and kFewMean rows an expert on average, and twice as many
 // for fp32 and fp16 results, whose tiles are slower. 64 experts of 2048 x 2048, bf16 x: 33 us with 100 rows (tiles 36),
-// 41 with 200 (43), 53 with 400 (46); 4096 x 14336, FP8 x: 16 us with 1 row (tiles 16), 17.6 with 8 (16.6), 21
-// with 16 (17). Up to kFewWeights codes a call is all latency, and no launch for the quantised x or the parts
-// counts more: 4096 x 4096 with 16 rows 15.5 us (17).
+// 41 with 200 (43), 53 with 400 (46). One matrix, calls with FP8 and with bf16 x, three matrices in turn: 4096 x
+// 14336 with 1 row 14.9 and 12.9 us (tiles 17.2 and 20.7), with 8 16.8 and 19.6 (17.4 and 21.0), with 16 20.8 and
+// 21.6 (17.4 and 21.0); 14336 x 4096 with 8 12.9 and 16.6 (13.4 and 17.3); 28672 x 8192 with 8 48 and 52 (55 and
+// 60); 8192 x 28672 with 8 52 and 55 (51 and 54). 8192 x 8192 would be faster in tiles with 2 rows already: 20.3 and
+// 22.2 (17.6 and 21.1). fp32 results with 16 rows: 14336 x 4096 14.4 and 17.9 (20.6 and 24.3), 4096 x 14336 21.2
+// and 22.5 (19.6 and 23.4). Up to kFewWeights codes a call is all latency, and no launch for the quantised x or
+// the parts counts more: 4096 x 4096 with 16 rows 15.5 us (17).
 // 16 weight rows a workgroup of 16 waves where that makes no more workgroups than the CUs, 32 up to twice as
-// many, else 64, the longest run of loads for the time it takes to start and end: 4096 x 14336 with one row
-// 13.4 us (32: 18, 64: 30), 8000 x 8000 14.7 (16: 15.4, 64: 17.6), 14336 x 4096 13.1 (15.7, 14.1), 28672 x 8192
+// many, else 64, the longest run of loads for the time it takes to start and end, in calls of one matrix again and
+// again (some of it stays in the last cache) with one row of bf16: 4096 x 14336 13.4 us (32: 18, 64: 30), 8000 x 8000 14.7 (16: 15.4, 64: 17.6), 14336 x 4096 13.1 (15.7, 14.1), 28672 x 8192
 // 40 (63, 56).
 //
 // FP8 rows of x given in another type: a workgroup of the few-row kernels quantises its own where they have

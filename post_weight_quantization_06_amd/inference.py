@@ -206,7 +206,8 @@ def fp8_matmul(codes: torch.Tensor, scales: torch.Tensor, x: torch.Tensor,
     or codes with x_scales from fp8_quantize. rows: int32 [T], the result's row t multiplies row rows[t]
     of x [Tx, C] (a routing's `rows`: tokens need not be copied to their experts; rows outside x stand
     for zeros). Without `out`, rows outside the offsets hold nothing defined; with it they stay as they
-    were."""
+    were. fp32 and fp16 results are fp32 sums; bf16 ones come faster from sums of fewer bits, off by a
+    hundredth of what the rounding to bf16 is (aaac.h)."""
     if rows is not None:
         if x.dim() != 2:
             raise ValueError("with rows, x must be [Tx, C] (got %d-D)" % x.dim())
