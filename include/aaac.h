@@ -510,8 +510,8 @@ size_t aaac_route_workspace_bytes(int64_t T, int64_t E);
  * Routing of T tokens to k of E experts, and the order of the chosen slots by expert that the grouped
  * products take.
  * Choice: scores s = softmax(logits) over a token's experts or sigmoid(logits); value v = s + bias. An
- * expert whose logit or bias is -inf is left out, also where the other is a NaN. The experts form `groups` groups of E / groups
- * neighbours; a group's value is its largest v (group_top 1) or the sum of its two largest (group_top 2;
+ * expert whose logit or bias is -inf is left out, also where the other is a NaN. The experts form `groups`
+ * groups of E / groups neighbours; a group's value is its largest v (group_top 1) or the sum of its two largest (group_top 2;
  * one, where a group has only one left), and only the top_groups largest groups take part. The k largest
  * v are chosen, in descending order; the lower index first among equals, of groups too. Values are
  * compared in 64 bits, and where neither a bias nor a sum over a group enters, by the logits themselves.

@@ -92,8 +92,8 @@ __device__ __forceinline__ int64_t x_row(const MatmulArgs& a, int64_t t) {
 // QUANTIZE: x is bf16, fp16 or fp32. Its rows are quantised into LDS, eight lanes a block, while the first
 // weights are on their way; the same codes and scales that the quantiser writes.
 // A load takes 64 neighbouring bytes of 16 rows. Measured, the kernel alone: 4096 x 14336 with one row of bf16 11.6
-// to 12.0 us (4.9 TB/s, a copy's rate is 5.2), 64 experts of 2048 x 2048 with 92 rows 33 us. The choice of RT and W stands at the
-// plan; U = 1 with RT = 4 makes the least registers, and two groups of two there take 39 us instead of 34.
+// to 12.0 us (4.9 TB/s, a copy's rate is 5.2), 64 experts of 2048 x 2048 with 92 rows 33 us. The choice of RT and
+// W stands at the plan; U = 1 with RT = 4 makes the least registers, and two groups of two there take 39 us instead of 34.
 // ------------------------------------------------------------------------------------------------
 constexpr int few_x_bytes(int64_t C) { return (int)(fp8_blocks(C) * kFp8Block + 16); }   // of a row in LDS
 
@@ -278,8 +278,8 @@ hipError_t few_fp8(MatmulArgs a, hipStream_t stream) {
 // at once half of a step. Loads past the last step lie outside their buffers, so every step has the same
 // count. A wave with one fragment of weights (FR = 1) has no first half and only point B.
 //
-// Measured, the kernel alone: 4096 rows against 14336 x 4096 237 to 246 us (1.95 PFLOP/s; the matrix instructions alone take 165, with
-// their LDS reads and factors 210, the loads alone 117; 896 tiles are 3.5 rounds of 256 CUs, and a round ends
+// Measured, the kernel alone: 4096 rows against 14336 x 4096 237 to 246 us (1.95 PFLOP/s; the matrix instructions
+// alone take 165, with their LDS reads and factors 210, the loads alone 117; 896 tiles are 3.5 rounds of 256 CUs, and a round ends
 // with 7 us of stores), 16380 rows over 32 experts of 4096 x 2048 187 to 193 us, 48 rows against 14336 x 4096 15.3 us
 // (3.8 TB/s).
 // ------------------------------------------------------------------------------------------------

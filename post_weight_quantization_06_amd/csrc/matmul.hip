@@ -47,8 +47,8 @@ __global__ __launch_bounds__(kBlock) void add_parts_kernel(MatmulArgs a) {
 // the parts counts more: 4096 x 4096 with 16 rows 15.5 us (17).
 // 16 weight rows a workgroup of 16 waves where that makes no more workgroups than the CUs, 32 up to twice as
 // many, else 64, the longest run of loads for the time it takes to start and end, in calls of one matrix again and
-// again (some of it stays in the last cache) with one row of bf16: 4096 x 14336 13.4 us (32: 18, 64: 30), 8000 x 8000 14.7 (16: 15.4, 64: 17.6), 14336 x 4096 13.1 (15.7, 14.1), 28672 x 8192
-// 40 (63, 56).
+// again (some of it stays in the last cache) with one row of bf16: 4096 x 14336 13.4 us (32: 18, 64: 30), 8000 x
+// 8000 14.7 (16: 15.4, 64: 17.6), 14336 x 4096 13.1 (15.7, 14.1), 28672 x 8192 40 (63, 56).
 //
 // FP8 rows of x given in another type: a workgroup of the few-row kernels quantises its own where they have
 // up to kFewQuantize elements, which saves a launch; more take longer than the launch does. An expert may have

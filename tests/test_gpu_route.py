@@ -447,3 +447,19 @@ def test_nan_bias_ranks_first_and_leaves_the_weights():
         want = s.gather(1, r.experts.long().cpu())
         # one rounding to fp32, and a softmax's 64-bit sum
         assert ((r.weights.double().cpu() - want).abs() <= 2 * 2.0 ** -24 * want).all()
+
+
+def test_signalling_nan_logits_of_masked_experts():
+    """The same for a NaN of any bits."""
+    bias = torch.zeros(16, device=DEV)
+    bias[3] = -INF
+    for dt, bits in ((torch.float32, (0x7f800001, -0x7fffff, 0x7fc00000)), (torch.bfloat16, (0x7f81, -0x7f, 0x7fc0)),
+                     (torch.float16, (0x7c01, -0x3ff, 0x7e00))):
+        for b in bits:
+            x = torch.randn(5, 16, generator=_gen(19)).to(dt)
+            x.view(torch.int32 if dt is torch.float32 else torch.int16)[:, 3] = b
+            assert torch.isnan(x[:, 3]).all()
+            r = P.route(x.to(DEV), 4, score="sigmoid", bias=bias)
+            assert not (r.experts == 3).any() and torch.isfinite(r.weights).all()
+            q = P.route(x.to(DEV), 4, score="sigmoid", bias=torch.zeros(16, device=DEV))
+            assert (r.experts >= 0).all() and (q.experts[:, 0] == 3).all() and torch.isnan(q.weights).all()
